@@ -299,6 +299,104 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
                                                size_t workspace_bytes, uint16_t* out, int32_t* err_flag,
                                                w4a16_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * INT4 KV pages.  A pool is uint8 [num_pages][Hkv][W4A16_KV4_SLICE]; a (page,
+ * kv head) slice of 1088 bytes holds 16 rows (tokens) of 128 codes and their
+ * scales, 4.25 bits a value (fp16 pages: 4096 bytes).
+ *   value = q * s, q in [-7, 7] kept as the nibble q + 8 (element d of a row in
+ *   nibble d % 2 of its byte, lowest first); s one byte per 32 elements: the 8
+ *   bits below the sign of an fp16 number (s = the number with bits byte << 7).
+ *   Every value is an fp16 number exactly.
+ *   K: dims 4i..4i+3 of token t at byte 64 t + 2 i, the scale of dims 32c.. at
+ *      1024 + 8 (t % 8) + 2 c + t / 8.
+ *   V: dims 4i..4i+3 of token t at byte 128 (t / 2) + 4 i + 2 (t % 2), the scale
+ *      at 1024 + 16 c + 4 (t % 8 / 2) + 2 (t / 8) + t % 2.
+ * Writing a row: per 32 elements amax = largest magnitude of its fp16 values (k
+ * after RoPE, rounded to fp16), s = the smallest scale with 7 s >= amax (0: all
+ * codes 0), q = x / s rounded to nearest even.  An infinity or a NaN makes its
+ * 32 elements read back as NaN.
+ * RoPE as for kv_append_rope; its two products and their sum are each rounded
+ * to fp32, so that every call here writes the same bytes for the same input.
+ *
+ *   kv_append_rope_int4   kv_append_rope into INT4 pools.
+ *     q_out    fp16 [B][Hq][D] packed: receives the rotated q, and q is only
+ *              read; NULL: q is rotated in place.  Must not overlap q partly.
+ *     row_stride  as for kv_append_rope (elements between the rows of q, k and
+ *              v), a multiple of 8, at least Hq * D.
+ *     Rows name distinct slots (block_table[b][p / 16], p % 16): rows that name
+ *     one slot leave either's bytes there.  A prompt is B = T rows, each with
+ *     the sequence's block-table row and the length after its token.
+ *   kv_read_int4          rows back as fp16 values (K as cached: rotated).
+ *     k_out, v_out  fp16 [B][T][Hkv][D]: row i of sequence b is the token at
+ *              position starts[b] + i if that lies in [0, context_lens[b]);
+ *              other rows are left as they were
+ *     starts   int32 [B] device, or NULL: 0 for every sequence
+ *     err_flag bit 0: a block-table entry outside the pool (its rows are left).
+ *   paged_gqa_decode_int4              paged_gqa_decode over INT4 pools
+ *   paged_gqa_decode_rope_append_int4  the fused form (RoPE, append, attend)
+ *     Arguments as for the fp16 calls, without partition_tokens: the library
+ *     splits each sequence's pages evenly over the CTAs that max_context asks
+ *     for.  Hq/Hkv may be any of 1..8.  workspace:
+ *     paged_gqa_decode_window_workspace_size(.., window = max_context, sinks = 0).
+ *     A length above max_context sets bit 0 of err_flag; the row attends to its
+ *     first max_context tokens, and the fused call appends nothing for it.
+ * Every byte of a page past a sequence's length may hold anything.
+ * Pools must be 128-byte aligned.
+ * ------------------------------------------------------------------------ */
+#define W4A16_KV4_SLICE 1088
+W4A16_API int kv_append_rope_int4(uint16_t* q, const uint16_t* k, const uint16_t* v, int row_stride,
+                                  uint16_t* q_out, uint8_t* k_pool, uint8_t* v_pool, int num_pages,
+                                  const int32_t* block_table, int max_blocks, const int32_t* context_lens, int B,
+                                  int Hq, int Hkv, int D, float theta, int32_t* err_flag, w4a16_stream_t stream);
+W4A16_API int kv_read_int4(const uint8_t* k_pool, const uint8_t* v_pool, int num_pages, const int32_t* block_table,
+                           int max_blocks, const int32_t* starts, const int32_t* context_lens, int T, int B, int Hkv,
+                           int D, uint16_t* k_out, uint16_t* v_out, int32_t* err_flag, w4a16_stream_t stream);
+W4A16_API int paged_gqa_decode_int4(const uint16_t* q, int q_stride, const uint8_t* k_pool, const uint8_t* v_pool,
+                                    int num_pages, const int32_t* block_table, int max_blocks,
+                                    const int32_t* context_lens, int max_context, int B, int Hq, int Hkv, int D,
+                                    float sm_scale, void* workspace, size_t workspace_bytes, uint16_t* out,
+                                    int32_t* err_flag, w4a16_stream_t stream);
+W4A16_API int paged_gqa_decode_rope_append_int4(const uint16_t* qkv, int qkv_stride, uint8_t* k_pool,
+                                                uint8_t* v_pool, int num_pages, const int32_t* block_table,
+                                                int max_blocks, const int32_t* context_lens, int max_context, int B,
+                                                int Hq, int Hkv, int D, float theta, float sm_scale, void* workspace,
+                                                size_t workspace_bytes, uint16_t* out, int32_t* err_flag,
+                                                w4a16_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Sliding window with sinks: paged_gqa_decode where the query, the token at
+ * position context_lens[b] - 1, sees token t < context_lens[b] only if
+ *   t >= context_lens[b] - window   (the last `window` tokens, its own included)
+ *   or t < sinks                    (the first `sinks` tokens stay visible).
+ * window >= 0, sinks >= 0.  Only the pages that hold visible tokens are read
+ * (others may be -1 in the block table, or reused); a query that sees nothing
+ * gives zeros.  FP8 pools: row scales up to 65504 / 448, as appends write them.
+ * Other arguments, the workspace's rules and err_flag as for
+ * paged_gqa_decode_int4 (no partition_tokens, any Hq/Hkv in 1..8); workspace of
+ * paged_gqa_decode_window_workspace_size() bytes with the same sizes.
+ * ------------------------------------------------------------------------ */
+W4A16_API int paged_gqa_decode_window(const uint16_t* q, int q_stride, const uint16_t* k_pool,
+                                      const uint16_t* v_pool, int num_pages, const int32_t* block_table,
+                                      int max_blocks, const int32_t* context_lens, int max_context, int window,
+                                      int sinks, int B, int Hq, int Hkv, int D, float sm_scale, void* workspace,
+                                      size_t workspace_bytes, uint16_t* out, int32_t* err_flag,
+                                      w4a16_stream_t stream);
+W4A16_API int paged_gqa_decode_window_fp8(const uint16_t* q, int q_stride, const uint8_t* k_pool,
+                                          const uint8_t* v_pool, const float* k_scale, const float* v_scale,
+                                          int num_pages, const int32_t* block_table, int max_blocks,
+                                          const int32_t* context_lens, int max_context, int window, int sinks, int B,
+                                          int Hq, int Hkv, int D, float sm_scale, void* workspace,
+                                          size_t workspace_bytes, uint16_t* out, int32_t* err_flag,
+                                          w4a16_stream_t stream);
+W4A16_API int paged_gqa_decode_window_int4(const uint16_t* q, int q_stride, const uint8_t* k_pool,
+                                           const uint8_t* v_pool, int num_pages, const int32_t* block_table,
+                                           int max_blocks, const int32_t* context_lens, int max_context, int window,
+                                           int sinks, int B, int Hq, int Hkv, int D, float sm_scale, void* workspace,
+                                           size_t workspace_bytes, uint16_t* out, int32_t* err_flag,
+                                           w4a16_stream_t stream);
+W4A16_API size_t paged_gqa_decode_window_workspace_size(int B, int Hq, int Hkv, int max_context, int window,
+                                                        int sinks, int D);
+
 /* Bytes of workspace paged_gqa_decode needs for these sizes. */
 W4A16_API size_t paged_gqa_decode_workspace_size(int B, int Hq, int Hkv, int max_context,
                                        int partition_tokens, int D);

@@ -71,6 +71,18 @@ SIGNATURES = {
     "paged_gqa_decode_rope_append_fp8": (I32, [P, I32, P, P, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, F32, F32,
                                                I32, P, SZ, P, P, P]),
     "kv_append_rope_fp8": (I32, [P, P, P, I32, P, P, P, P, I32, P, I32, P, I32, I32, I32, I32, F32, P, P]),
+    "kv_append_rope_int4": (I32, [P, P, P, I32, P, P, P, I32, P, I32, P, I32, I32, I32, I32, F32, P, P]),
+    "kv_read_int4": (I32, [P, P, I32, P, I32, P, P, I32, I32, I32, I32, P, P, P, P]),
+    "paged_gqa_decode_int4": (I32, [P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, F32, P, SZ, P, P, P]),
+    "paged_gqa_decode_rope_append_int4": (I32, [P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, F32, F32, P, SZ,
+                                                P, P, P]),
+    "paged_gqa_decode_window": (I32, [P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, I32, I32, F32, P, SZ, P,
+                                      P, P]),
+    "paged_gqa_decode_window_fp8": (I32, [P, I32, P, P, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, I32, I32, F32,
+                                          P, SZ, P, P, P]),
+    "paged_gqa_decode_window_int4": (I32, [P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, I32, I32, F32, P, SZ,
+                                           P, P, P]),
+    "paged_gqa_decode_window_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
     "paged_gqa_decode_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32]),
     "paged_gqa_decode_default_partition": (I32, [I32, I32, I32]),
     "w4a16_workspace_clear": (I32, [P, SZ, P]),

@@ -15,6 +15,7 @@ from ._lib import LayerWeights, ModelConfig, ModelWeights, check, load
 
 __all__ = ["w4a16_gemv", "w4a16_gemm", "w4a16_gemm_silu_mul", "lm_head_logits_batched", "argmax_rows", "w4a16_gemv_rmsnorm", "w4a16_gemv_silu_mul", "rmsnorm", "kv_append_rope",
            "paged_gqa_decode", "paged_gqa_decode_rope_append", "paged_gqa_decode_workspace_size", "paged_gqa_decode_default_partition",
+           "kv_append_rope_int4", "kv_read_int4", "paged_gqa_decode_int4", "paged_gqa_decode_window", "KV4_SLICE",
            "workspace_clear", "embedding_gather", "lm_head_argmax", "Model", "stream_handle"]
 
 
@@ -351,6 +352,170 @@ def paged_gqa_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, conte
     else:
         check(lib.paged_gqa_decode_fp8(_p(q), 0, _p(k_pool), _p(v_pool), _p(k_scale), _p(v_scale), *common,
                                        float(sm_scale), *tail))
+    return out
+
+
+KV4_SLICE = 1088  # bytes of an INT4 (page, kv head) slice: 1024 of codes, 64 of scales
+
+
+def _paging_int4(k_pool, v_pool, block_table, context_lens):
+    """(pages, Hkv, B) of INT4 pools uint8 [pages][Hkv][1088]."""
+    _arg(k_pool, _U8, "k_pool", (None, None, KV4_SLICE))
+    _arg(v_pool, _U8, "v_pool", tuple(k_pool.shape))
+    _arg(block_table, _I, "block_table", (None, None))
+    B = block_table.shape[0]
+    _arg(context_lens, _I, "context_lens", (B,))
+    return k_pool.shape[0], k_pool.shape[1], B
+
+
+def _same_device(first, **others):
+    """Every tensor on the first one's device, which has to be the current
+    one: the call goes to the current device's stream."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    if first.is_cuda and first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}, the current device is {torch.cuda.current_device()}")
+
+
+def kv_append_rope_int4(q, k, v, k_pool, v_pool, block_table, context_lens, theta, row_stride=0, q_out=None,
+                        err_flag=None, stream=None):
+    """kv_append_rope into INT4 pools [pages][Hkv][KV4_SLICE]: q [B][Hq][128]
+    rotated in place, or into q_out when given (q is then only read); the
+    rotated k row and the v row quantised into their slot.  A row_stride
+    (elements, a multiple of 8) makes q, k and v the starts of rows of that
+    pitch, e.g. views of a q|k|v buffer."""
+    pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
+    D = 128
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t is None or t.dtype != torch.float16 or t.dim() != 3 or t.shape[0] != B or t.shape[2] != D:
+            raise ValueError(f"{name}: expected fp16 ({B}, heads, {D})")
+        pitch = int(row_stride) or t.shape[1] * D
+        if t.stride(2) != 1 or t.stride(1) != D or (B > 1 and t.stride(0) != pitch):
+            raise ValueError(f"{name}: rows must be {pitch} elements apart, heads and dims packed")
+        if not _on_device(t):
+            raise ValueError(f"{name} must be a CUDA tensor")
+    Hq = q.shape[1]
+    if k.shape[1] != Hkv or v.shape[1] != Hkv:
+        raise ValueError(f"k, v: {k.shape[1]} and {v.shape[1]} heads, the pools have {Hkv}")
+    _arg(q_out, _H, "q_out", (B, Hq, D), optional=True)
+    _arg(err_flag, _I, "err_flag", optional=True)
+    _same_device(q, k=k, v=v, q_out=q_out, k_pool=k_pool, v_pool=v_pool, block_table=block_table,
+                 context_lens=context_lens, err_flag=err_flag)
+    check(load().kv_append_rope_int4(_p(q), _p(k), _p(v), int(row_stride), _p(q_out), _p(k_pool), _p(v_pool), pages,
+                                     _p(block_table), block_table.shape[1], _p(context_lens), B, Hq, Hkv, D,
+                                     float(theta), _p(err_flag), stream_handle(stream)))
+    return q if q_out is None else q_out
+
+
+def kv_read_int4(k_pool, v_pool, block_table, context_lens, T, starts=None, k_out=None, v_out=None, err_flag=None,
+                 stream=None):
+    """(k, v) fp16 [B][T][Hkv][128] read back from INT4 pools: row i of
+    sequence b is the token at position starts[b] + i (0 + i without starts)
+    if the sequence holds it; other rows are left as they were (zeros where
+    the call allocates)."""
+    pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
+    T = int(T)
+    if T < 1:
+        raise ValueError(f"T={T}, expected at least 1")
+    _arg(starts, _I, "starts", (B,), optional=True)
+    shape = (B, T, Hkv, 128)
+    _arg(k_out, _H, "k_out", shape, optional=True)
+    _arg(v_out, _H, "v_out", shape, optional=True)
+    _arg(err_flag, _I, "err_flag", optional=True)
+    _same_device(k_pool, v_pool=v_pool, block_table=block_table, context_lens=context_lens, starts=starts,
+                 k_out=k_out, v_out=v_out, err_flag=err_flag)
+    if k_out is None:
+        k_out = torch.zeros(shape, dtype=torch.float16, device=k_pool.device)
+    if v_out is None:
+        v_out = torch.zeros(shape, dtype=torch.float16, device=k_pool.device)
+    check(load().kv_read_int4(_p(k_pool), _p(v_pool), pages, _p(block_table), block_table.shape[1], _p(starts),
+                              _p(context_lens), T, B, Hkv, 128, _p(k_out), _p(v_out), _p(err_flag),
+                              stream_handle(stream)))
+    return k_out, v_out
+
+
+def _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, device):
+    _arg(out, _H, "out", (B, Hq, 128), optional=True)
+    _arg(workspace, _U8, "workspace", optional=True)
+    if workspace is None:
+        nbytes = load().paged_gqa_decode_window_workspace_size(B, Hq, Hkv, max_context, window, sinks, 128)
+        workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if out is None:
+        out = torch.empty((B, Hq, 128), dtype=torch.float16, device=device)
+    return workspace, out
+
+
+def paged_gqa_decode_int4(q, k_pool, v_pool, block_table, context_lens, max_context, sm_scale=None, workspace=None,
+                          out=None, err_flag=None, qkv_theta=None, n_q_heads=None, stream=None):
+    """paged_gqa_decode over INT4 pools [pages][Hkv][KV4_SLICE], q
+    [B][Hq][128].  With qkv_theta given, q holds q|k|v rows (B, (Hq + 2 Hkv)
+    128) and the call is the fused RoPE + INT4 append + attention
+    (paged_gqa_decode_rope_append_int4).  A workspace the caller gives is
+    zeroed once before its first use."""
+    pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
+    D, max_context = 128, int(max_context)
+    fuse = qkv_theta is not None
+    if fuse and n_q_heads is None:
+        raise ValueError("n_q_heads is required with q|k|v rows")
+    Hq = n_q_heads if n_q_heads is not None else q.shape[-2]
+    if fuse:
+        _arg(q, _H, "qkv", (B, None))
+        if q.shape[1] < (Hq + 2 * Hkv) * D:
+            raise ValueError(f"qkv: rows of {q.shape[1]}, need (Hq + 2 Hkv) D = {(Hq + 2 * Hkv) * D}")
+    else:
+        _arg(q, _H, "q", (B, Hq, D))
+    _arg(err_flag, _I, "err_flag", optional=True)
+    _same_device(q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, context_lens=context_lens,
+                 workspace=workspace, out=out, err_flag=err_flag)
+    workspace, out = _window_buffers(B, Hq, Hkv, max_context, max_context, 0, workspace, out, k_pool.device)
+    scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
+    common = (_p(k_pool), _p(v_pool), pages, _p(block_table), block_table.shape[1], _p(context_lens), max_context, B,
+              Hq, Hkv, D)
+    tail = (scale, _p(workspace), workspace.numel(), _p(out), _p(err_flag), stream_handle(stream))
+    if fuse:
+        check(load().paged_gqa_decode_rope_append_int4(_p(q), q.shape[1], *common, float(qkv_theta), *tail))
+    else:
+        check(load().paged_gqa_decode_int4(_p(q), 0, *common, *tail))
+    return out
+
+
+def paged_gqa_decode_window(q, k_pool, v_pool, block_table, context_lens, max_context, window, sinks=0, k_scale=None,
+                            v_scale=None, sm_scale=None, workspace=None, out=None, err_flag=None, stream=None):
+    """Decode attention that sees the last `window` tokens and the first
+    `sinks`: q [B][Hq][128] over pools of any kind -- fp16 [pages][Hkv][16]
+    [128], FP8 (E4M3) codes of that shape with k_scale / v_scale, or INT4
+    [pages][Hkv][KV4_SLICE].  A workspace the caller gives is zeroed once
+    before its first use."""
+    D = 128
+    max_context, window, sinks = int(max_context), int(window), int(sinks)
+    fp8 = k_scale is not None or v_scale is not None
+    if fp8:
+        pages, Hkv, _, B = _paging_fp8(k_pool, v_pool, k_scale, v_scale, block_table, context_lens)
+    elif k_pool.dtype == torch.uint8:
+        pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
+    else:
+        pages, Hkv, _, B = _paging(k_pool, v_pool, block_table, context_lens)
+    if k_pool.dim() == 4:
+        _arg(k_pool, (k_pool.dtype,), "k_pool", (pages, Hkv, 16, D))
+    _arg(q, _H, "q", (B, None, D))
+    Hq = q.shape[1]
+    _arg(err_flag, _I, "err_flag", optional=True)
+    if window < 0 or sinks < 0:
+        raise ValueError(f"window={window}, sinks={sinks}: neither may be negative")
+    _same_device(q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, context_lens=context_lens, k_scale=k_scale,
+                 v_scale=v_scale, workspace=workspace, out=out, err_flag=err_flag)
+    window, sinks = min(window, max_context), min(sinks, max_context)  # (the same tokens, within a C int)
+    workspace, out = _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, k_pool.device)
+    scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
+    args = (pages, _p(block_table), block_table.shape[1], _p(context_lens), max_context, window, sinks, B, Hq, Hkv, D,
+            scale, _p(workspace), workspace.numel(), _p(out), _p(err_flag), stream_handle(stream))
+    if fp8:
+        check(load().paged_gqa_decode_window_fp8(_p(q), 0, _p(k_pool), _p(v_pool), _p(k_scale), _p(v_scale), *args))
+    elif k_pool.dtype == torch.uint8:
+        check(load().paged_gqa_decode_window_int4(_p(q), 0, _p(k_pool), _p(v_pool), *args))
+    else:
+        check(load().paged_gqa_decode_window(_p(q), 0, _p(k_pool), _p(v_pool), *args))
     return out
 
 

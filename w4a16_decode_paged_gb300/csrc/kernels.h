@@ -132,6 +132,56 @@ struct RopeArgs {
 int launch_rope_append(const RopeArgs& a, cudaStream_t s);
 void rope_inv_freq_table(float theta, int D, float* out);
 
+// RoPE + append into INT4 pools (slices of 1088 bytes, kv4.cuh).
+struct Kv4AppendArgs {
+  const __half* q;          // [B][Hq][D] pitch stride_q
+  const __half* k;          // [B][Hkv][D] pitch stride_kv
+  const __half* v;
+  __half* q_out;            // rotated q, pitch stride_qo (q itself: in place)
+  uint8_t* k_pool;          // [pages][Hkv][1088]
+  uint8_t* v_pool;
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  int32_t* err_flag;
+  int stride_q, stride_qo, stride_kv, num_pages, max_blocks, B, Hq, Hkv;
+  float inv_freq[64];
+};
+int launch_rope_append_int4(const Kv4AppendArgs& a, cudaStream_t s);
+
+// Decode attention with tokens as MMA rows (attn_window.cu): INT4 pages, and
+// a sliding window with sinks over any kind of page.
+enum { ATW_F16 = 0, ATW_F8 = 1, ATW_I4 = 2 };
+constexpr int ATW_SMS = 152;             // SMs the split over a long context is sized for
+constexpr int ATW_MAX_PARTITIONS = 64;
+struct AtwArgs {
+  const __half* q;          // [B][Hq][D] pitch q_stride (fused: q | k_new | v_new rows)
+  const void* k;            // this kind's pools (written only by the fused variant)
+  const void* v;
+  const float* ks;          // FP8 row scales
+  const float* vs;
+  const int32_t* block_table;
+  const int32_t* context_lens;
+  __half* out;              // [B][Hq][D]
+  float* ws_o;              // [B][Hq][PC][D]
+  float* ws_ml;             // [B][Hq][PC][2]
+  unsigned int* counters;   // [B][Hkv]
+  int32_t* err_flag;
+  int kind, q_stride, num_pages, max_blocks, max_context, window, sinks, B, Hq, Hkv, G, PC;
+  int fuse_rope_append;     // INT4: rotate q and k_new at len - 1, append k_new / v_new, then attend
+  float scale_log2;         // sm_scale * log2(e)
+  float inv_freq[64];
+  int tag;
+};
+int launch_attn_window(const AtwArgs& a, cudaStream_t s);
+int atw_partitions(int B, int Hkv, int max_context, int window, int sinks);
+inline void atw_workspace(AtwArgs& a, void* ws, int B, int Hq) {  // a.PC set
+  AttnArgs t = {};
+  attention_workspace_layout(t, ws, B, Hq, a.PC);
+  a.ws_o = t.ws_o;
+  a.ws_ml = t.ws_ml;
+  a.counters = t.counters;
+}
+
 int launch_rmsnorm(const __half* x, const __half* gamma, __half* y, int M, int H, float eps, cudaStream_t s,
                    int tag = 0);
 // lens_to_advance (nullable): context_lens[b] += 1; a length above max_len sets bit 0 of err_flag

@@ -1,0 +1,148 @@
+// kv4.cuh -- INT4 KV pages: the format, its quantiser and its unpacking.
+//
+// A (page, kv head) slice is 1088 bytes: 1024 bytes of codes (16 tokens x 128
+// dims, two per byte, element d in nibble d % 2, lowest first, offset binary
+// u = q + 8 with q in [-7, 7]) and 64 scale bytes (one per token and 32 dims).
+//   value = q * s,  s = the fp16 number whose bits are byte << 7
+// so a scale has 5 exponent and 3 fraction bits (4 significant bits, all of
+// fp16's range, byte 0 = 0; bytes from 0xF8 on are not finite).  A code has 3
+// significant bits and a sign: every product is exact in fp16, in fp32 and
+// against a scale that was divided by 64 (multiples of 2^-23).
+// Quantising 32 values: s = the smallest scale with 7 s >= amax, q = x / s
+// rounded to nearest even.  A group with an infinity or a NaN takes byte 0xFF
+// and reads back as NaN throughout.
+//
+// Where the bytes sit follows from the attention's matrix fragments:
+//   K codes   token t, dims 4i..4i+3 at 64 t + 2 i: a lane's 16 bytes are the 32
+//             dims of one scale of one token
+//   K scales  token t, group c at 1024 + 8 (t % 8) + 2 c + t / 8: the bytes of
+//             tokens t and t + 8, which one lane needs, are neighbours
+//   V codes   token t, dims 4i..4i+3 at 128 (t / 2) + 4 i + 2 (t % 2): the two
+//             tokens of a pair alternate by halfwords, so that the nibbles at
+//             one place of a word's two halves are one dim of both tokens
+//   V scales  token t, group c at 1024 + 16 c + 4 (t % 8 / 2) + 2 (t / 8) + t % 2
+// Each token's bytes are its own: appends of different tokens never meet.
+#pragma once
+
+#include "common.cuh"
+
+namespace w4 {
+
+constexpr int KV4_D = 128;
+constexpr int KV4_PAGE = 16;
+constexpr int KV4_GROUP = 32;                       // dims per scale
+constexpr int KV4_CODES = KV4_PAGE * KV4_D / 2;     // 1024
+constexpr int KV4_SLICE = KV4_CODES + KV4_PAGE * KV4_D / KV4_GROUP;  // 1088
+
+// byte offsets in a slice of dims 4i..4i+3 (a halfword) and of group c's scale
+__device__ __forceinline__ int kv4_k_code(int t, int i) { return 64 * t + 2 * i; }
+__device__ __forceinline__ int kv4_v_code(int t, int i) { return 128 * (t >> 1) + 4 * i + 2 * (t & 1); }
+__device__ __forceinline__ int kv4_k_scale(int t, int c) { return KV4_CODES + 8 * (t & 7) + 2 * c + (t >> 3); }
+__device__ __forceinline__ int kv4_v_scale(int t, int c) {
+  return KV4_CODES + 16 * c + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1);
+}
+
+// Scale byte of a group whose largest magnitude has the fp16 bits `bits`.
+__device__ __forceinline__ uint32_t kv4_scale_byte(uint32_t bits) {
+  if (bits >= 0x7C00u) return 0xFFu;  // an infinity or a NaN
+  const float r = __fdiv_rn(__half2float(__ushort_as_half((unsigned short)bits)), 7.0f);
+  // the 3 leading fraction bits rounded up (a carry moves the exponent on);
+  // below fp16's normal range multiples of 2^-17
+  if (r < 0x1p-14f) return (uint32_t)ceilf(r * 0x1p17f);
+  return ((__float_as_uint(r) + 0xFFFFFu) >> 20) - (112u << 3);
+}
+
+__device__ __forceinline__ float kv4_scale_value(uint32_t byte) {
+  return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+}
+
+// One row of 128 fp16 values, four per lane (dims 4 lane .. 4 lane + 3, two
+// packed halves each in x0, x1) -> this lane's four codes and the scale byte
+// of its group of eight lanes.  Warp-wide.
+__device__ __forceinline__ void kv4_quantise(uint32_t x0, uint32_t x1, uint32_t& codes, uint32_t& byte) {
+  // magnitudes compare as integers, NaN and infinity above every number
+  const uint32_t a0 = x0 & 0x7FFF7FFFu, a1 = x1 & 0x7FFF7FFFu;
+  uint32_t m = max(max(a0 & 0xFFFFu, a0 >> 16), max(a1 & 0xFFFFu, a1 >> 16));
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  byte = kv4_scale_byte(m);
+  const float s = kv4_scale_value(byte);
+  const bool live = byte != 0u && byte != 0xFFu;
+  codes = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t h = ((e < 2 ? x0 : x1) >> (16 * (e & 1))) & 0xFFFFu;
+    const float x = __half2float(__ushort_as_half((unsigned short)h));
+    const int q = live ? __float2int_rn(__fdiv_rn(x, s)) : 0;
+    codes |= (uint32_t)(q + 8) << (4 * e);
+  }
+}
+
+// Rotate-half RoPE of a row held four dims per lane (as above): the partner
+// dim i +- 64 sits 16 lanes away.  cs, sn: 64 cosines and sines.  Products and
+// their sum are rounded one by one, so every caller gets the same bits.
+__device__ __forceinline__ float rope_lo(float x0, float x1, float c, float s) {
+  return __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
+}
+__device__ __forceinline__ float rope_hi(float x0, float x1, float c, float s) {
+  return __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
+}
+__device__ __forceinline__ void rope_row4(uint32_t& x0, uint32_t& x1, const float* cs, const float* sn, int lane) {
+  const uint32_t y0 = __shfl_xor_sync(0xffffffffu, x0, 16), y1 = __shfl_xor_sync(0xffffffffu, x1, 16);
+  const int i = 4 * (lane & 15);
+  float r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = __half2float(__ushort_as_half((unsigned short)((e < 2 ? x0 : x1) >> (16 * (e & 1)))));
+    const float y = __half2float(__ushort_as_half((unsigned short)((e < 2 ? y0 : y1) >> (16 * (e & 1)))));
+    r[e] = lane < 16 ? rope_lo(x, y, cs[i + e], sn[i + e]) : rope_hi(y, x, cs[i + e], sn[i + e]);
+  }
+  const __half2 lo = __floats2half2_rn(r[0], r[1]), hi = __floats2half2_rn(r[2], r[3]);
+  x0 = *reinterpret_cast<const uint32_t*>(&lo);
+  x1 = *reinterpret_cast<const uint32_t*>(&hi);
+}
+
+// ---------------------------------------------------------------------------
+// Unpacking.  A nibble u at bits b..b+3 of a half, or-ed under an exponent
+// that makes bit b worth 1, is the fp16 number 2^(10-b) + u; one fused
+// multiply-add takes the bias off and applies the scale:
+//   q s' = (2^(10-b) + u) s' - (2^(10-b) + 8) s',   s' = s / 64
+// exactly, because the bias times a scale still fits fp16's 11 bits at b = 2,
+// 4, 6 (264, 72, 24).  s / 64 keeps 264 s' in fp16's range for every scale;
+// callers multiply by 64 in fp32.
+// ---------------------------------------------------------------------------
+struct Kv4Scale {
+  uint32_t s, c264, c72, c24;  // packed pairs
+};
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// two: the scales' fp16 bits (s, s)
+__device__ __forceinline__ Kv4Scale kv4_scale_pair(uint32_t two) {
+  Kv4Scale r;
+  r.s = hmul2_u(two, 0x24002400u);     // 1 / 64
+  r.c264 = hmul2_u(two, 0xC420C420u);  // -264 / 64
+  r.c72 = hmul2_u(two, 0xBC80BC80u);   // -72 / 64
+  r.c24 = hmul2_u(two, 0xB600B600u);   // -24 / 64
+  return r;
+}
+// (low, high) bytes at bits 0-7 and 16-23 -> the pair's fp16 bits
+__device__ __forceinline__ uint32_t kv4_bytes_to_half2(uint32_t b) { return b << 7; }
+
+// Eight codes of a word: x[n] = nibbles n of the low and of the high half.
+__device__ __forceinline__ void kv4_unpack(uint32_t w, const Kv4Scale& k, uint32_t (&x)[4]) {
+  const uint32_t l = w << 2, r = w >> 6;
+  x[0] = hfma2_u(and_or(l, 0x003C003Cu, 0x5C005C00u), k.s, k.c264);
+  x[1] = hfma2_u(and_or(w, 0x00F000F0u, 0x54005400u), k.s, k.c72);
+  x[2] = hfma2_u(and_or(r, 0x003C003Cu, 0x5C005C00u), k.s, k.c264);
+  x[3] = hfma2_u(and_or(r, 0x03C003C0u, 0x4C004C00u), k.s, k.c24);
+}
+
+}  // namespace w4
