@@ -324,14 +324,15 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
  *     row_stride  as for kv_append_rope (elements between the rows of q, k and
  *              v), a multiple of 8, at least Hq * D.
  *     Rows name distinct slots (block_table[b][p / 16], p % 16): rows that name
- *     one slot leave either's bytes there.  A prompt is B = T rows, each with
+ *     one slot leave either's bytes there; a row of length 0 is skipped.  A prompt is B = T rows, each with
  *     the sequence's block-table row and the length after its token.
  *   kv_read_int4          rows back as fp16 values (K as cached: rotated).
  *     k_out, v_out  fp16 [B][T][Hkv][D]: row i of sequence b is the token at
- *              position starts[b] + i if that lies in [0, context_lens[b]);
- *              other rows are left as they were
+ *              position starts[b] + i if that lies in [0, context_lens[b])
+ *     clear    0: other rows are left as they were; 1: they become zero
  *     starts   int32 [B] device, or NULL: 0 for every sequence
- *     err_flag bit 0: a block-table entry outside the pool (its rows are left).
+ *     err_flag bit 0: a block-table entry outside the pool (its rows count as
+ *              the other rows).
  *   paged_gqa_decode_int4              paged_gqa_decode over INT4 pools
  *   paged_gqa_decode_rope_append_int4  the fused form (RoPE, append, attend)
  *     Arguments as for the fp16 calls, without partition_tokens: the library
@@ -350,7 +351,8 @@ W4A16_API int kv_append_rope_int4(uint16_t* q, const uint16_t* k, const uint16_t
                                   int Hq, int Hkv, int D, float theta, int32_t* err_flag, w4a16_stream_t stream);
 W4A16_API int kv_read_int4(const uint8_t* k_pool, const uint8_t* v_pool, int num_pages, const int32_t* block_table,
                            int max_blocks, const int32_t* starts, const int32_t* context_lens, int T, int B, int Hkv,
-                           int D, uint16_t* k_out, uint16_t* v_out, int32_t* err_flag, w4a16_stream_t stream);
+                           int D, uint16_t* k_out, uint16_t* v_out, int clear, int32_t* err_flag,
+                           w4a16_stream_t stream);
 W4A16_API int paged_gqa_decode_int4(const uint16_t* q, int q_stride, const uint8_t* k_pool, const uint8_t* v_pool,
                                     int num_pages, const int32_t* block_table, int max_blocks,
                                     const int32_t* context_lens, int max_context, int B, int Hq, int Hkv, int D,

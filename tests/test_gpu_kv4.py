@@ -208,6 +208,12 @@ def test_read_back(api, Hkv, lens, T, starts):
         with np.errstate(over="ignore"):
             want = want.astype(np.float16)                       # (a code of -8 at the largest scales passes 65504)
         assert np.array_equal(to_host(out), want, equal_nan=True), which
+    # tensors that the call makes: zeros where the caller's were left alone
+    held = [ko != 7.5, vo != 7.5]
+    torch.full((4 * ko.numel(),), 3.0, dtype=torch.float16, device="cuda")       # (memory that held something)
+    for got, given, h in zip(api.kv_read_int4(dkp, dvp, dbt, dl, T, starts=ds), (ko, vo), held):
+        rows = h.any(-1, keepdim=True)
+        assert torch.equal(got.nan_to_num(9.0), torch.where(rows, given, torch.zeros_like(given)).nan_to_num(9.0))
 
 
 def test_read_reports_bad_pages_and_leaves_their_rows(api):

@@ -87,12 +87,12 @@ def test_append_refusals(lib, bad, code):
     assert _append(lib, **bad) == code and lib.w4a16_last_error()
 
 
-def _read(lib, kp=A, vp=A, pages=8, bt=A, mb=4, starts=None, lens=A, T=5, B=2, Hkv=1, D=128, ko=A, vo=A):
-    return lib.kv_read_int4(kp, vp, pages, bt, mb, starts, lens, T, B, Hkv, D, ko, vo, None, None)
+def _read(lib, kp=A, vp=A, pages=8, bt=A, mb=4, starts=None, lens=A, T=5, B=2, Hkv=1, D=128, ko=A, vo=A, clear=0):
+    return lib.kv_read_int4(kp, vp, pages, bt, mb, starts, lens, T, B, Hkv, D, ko, vo, clear, None, None)
 
 
 @pytest.mark.parametrize("bad,code", [
-    (dict(kp=None), 1), (dict(vo=None), 1), (dict(T=0), 1), (dict(B=0), 1), (dict(Hkv=0), 1), (dict(D=96), 3),
+    (dict(kp=None), 1), (dict(vo=None), 1), (dict(T=0), 1), (dict(B=0), 1), (dict(Hkv=0), 1), (dict(clear=2), 1), (dict(D=96), 3),
     (dict(B=65536), 3), (dict(ko=MIS), 2), (dict(kp=MIS), 2)])
 def test_read_refusals(lib, bad, code):
     assert _read(lib, **bad) == code and lib.w4a16_last_error()
@@ -172,7 +172,7 @@ def test_binding_append(rec):
     name, a = r.calls[-1]
     assert name == "kv_append_rope_int4" and a[3] == 9 * 128 and a[11:15] == (2, 7, 1, 128)
     n = len(r.calls)
-    for bad, what in ((dict(q=_h(2, 7, 64)), "q"), (dict(k=_h(2, 2, 128)), "heads"), (dict(v=_h(3, 1, 128)), "v"),
+    for bad, what in ((dict(q=_h(2, 7, 64)), "q"), (dict(k=_h(2, 2, 128)), "k: shape"), (dict(v=_h(3, 1, 128)), "v"),
                       (dict(q=v3[:, :7]), "q"), (dict(q_out=_h(2, 6, 128)), "q_out"),
                       (dict(k_pool=torch.zeros((8, 1, 1024), dtype=torch.uint8)), "k_pool"),
                       (dict(block_table=torch.zeros((2, 4), dtype=torch.int64)), "block_table"),
@@ -190,7 +190,9 @@ def test_binding_read(rec):
     k, v = api.kv_read_int4(**_base(), T=5)
     assert tuple(k.shape) == tuple(v.shape) == (2, 5, 1, 128)
     for bad, what in ((dict(T=0), "T="), (dict(starts=torch.zeros(3, dtype=torch.int32)), "starts"),
-                      (dict(k_out=_h(2, 4, 1, 128)), "k_out"), (dict(v_out=_h(2, 5, 1, 128).float()), "v_out")):
+                      (dict(k_out=_h(2, 4, 1, 128), v_out=_h(2, 5, 1, 128)), "k_out"),
+                      (dict(k_out=_h(2, 5, 1, 128), v_out=_h(2, 5, 1, 128).float()), "v_out"),
+                      (dict(v_out=_h(2, 5, 1, 128)), "k_out is required")):
         with pytest.raises(ValueError, match=what):
             api.kv_read_int4(**{**_base(), "T": 5, **bad})
 

@@ -72,7 +72,7 @@ SIGNATURES = {
                                                I32, P, SZ, P, P, P]),
     "kv_append_rope_fp8": (I32, [P, P, P, I32, P, P, P, P, I32, P, I32, P, I32, I32, I32, I32, F32, P, P]),
     "kv_append_rope_int4": (I32, [P, P, P, I32, P, P, P, I32, P, I32, P, I32, I32, I32, I32, F32, P, P]),
-    "kv_read_int4": (I32, [P, P, I32, P, I32, P, P, I32, I32, I32, I32, P, P, P, P]),
+    "kv_read_int4": (I32, [P, P, I32, P, I32, P, P, I32, I32, I32, I32, P, P, I32, P, P]),
     "paged_gqa_decode_int4": (I32, [P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, F32, P, SZ, P, P, P]),
     "paged_gqa_decode_rope_append_int4": (I32, [P, I32, P, P, I32, P, I32, P, I32, I32, I32, I32, I32, F32, F32, P, SZ,
                                                 P, P, P]),

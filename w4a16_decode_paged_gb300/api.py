@@ -356,26 +356,62 @@ def paged_gqa_decode_fp8(q, k_pool, v_pool, k_scale, v_scale, block_table, conte
 
 
 KV4_SLICE = 1088  # bytes of an INT4 (page, kv head) slice: 1024 of codes, 64 of scales
+_SCALE_128 = 1.0 / math.sqrt(128)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _paging_int4(k_pool, v_pool, block_table, context_lens):
-    """(pages, Hkv, B) of INT4 pools uint8 [pages][Hkv][1088]."""
-    _arg(k_pool, _U8, "k_pool", (None, None, KV4_SLICE))
-    _arg(v_pool, _U8, "v_pool", tuple(k_pool.shape))
-    _arg(block_table, _I, "block_table", (None, None))
-    B = block_table.shape[0]
-    _arg(context_lens, _I, "context_lens", (B,))
-    return k_pool.shape[0], k_pool.shape[1], B
+# The calls below are a few microseconds on the GPU at their smallest, so their
+# checks take one comparison chain per tensor and only a tensor that fails it
+# goes through _arg for the message.
+def _is(t, dtype, shape, dev, name):
+    """t is a contiguous tensor of this dtype and exact shape on device `dev`."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
+    _arg(t, (dtype,), name, shape)
+    raise ValueError(f"{name} is on {t.device}, expected device {dev}")
 
 
-def _same_device(first, **others):
-    """Every tensor on the first one's device, which has to be the current
-    one: the call goes to the current device's stream."""
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-    if first.is_cuda and first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {first.device}, the current device is {torch.cuda.current_device()}")
+def _device_of(t, name):
+    """Index of the device that t is on, which has to be the current one (the
+    call goes to one of its streams)."""
+    dev = t.get_device()
+    if dev < 0:
+        if not _on_device(t):
+            raise ValueError(f"{name} must be a CUDA tensor")
+    elif dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is {torch.cuda.current_device()}")
+    return dev
+
+
+def _stream_on(stream, dev):
+    return _raw_stream(dev) if stream is None and dev >= 0 and _raw_stream is not None else stream_handle(stream)
+
+
+def _paging_of(kind, k_pool, v_pool, block_table, context_lens):
+    """(pages, Hkv, B, device) of a pool of this kind and its paging."""
+    dtype = torch.float16 if kind == "fp16" else torch.uint8
+    if k_pool is None or k_pool.dim() != (3 if kind == "int4" else 4):
+        _arg(k_pool, (dtype,), "k_pool", (None, None, KV4_SLICE) if kind == "int4" else (None, None, 16, 128))
+    pages, Hkv = k_pool.shape[:2]
+    shape = (pages, Hkv, KV4_SLICE) if kind == "int4" else (pages, Hkv, 16, 128)
+    dev = _device_of(k_pool, "k_pool")
+    _is(k_pool, dtype, shape, dev, "k_pool")
+    _is(v_pool, dtype, shape, dev, "v_pool")
+    if block_table is None or block_table.dim() != 2:
+        _arg(block_table, _I, "block_table", (None, None))
+    B, blocks = block_table.shape
+    _is(block_table, torch.int32, (B, blocks), dev, "block_table")
+    _is(context_lens, torch.int32, (B,), dev, "context_lens")
+    return pages, Hkv, B, blocks, dev
+
+
+def _err_flag(t, dev):
+    if t is not None:
+        _is(t, torch.int32, t.shape, dev, "err_flag")
+        if t.numel() < 1:
+            raise ValueError("err_flag is empty")
+        return t.data_ptr()
+    return None
 
 
 def kv_append_rope_int4(q, k, v, k_pool, v_pool, block_table, context_lens, theta, row_stride=0, q_out=None,
@@ -385,64 +421,66 @@ def kv_append_rope_int4(q, k, v, k_pool, v_pool, block_table, context_lens, thet
     rotated k row and the v row quantised into their slot.  A row_stride
     (elements, a multiple of 8) makes q, k and v the starts of rows of that
     pitch, e.g. views of a q|k|v buffer."""
-    pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
-    D = 128
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t is None or t.dtype != torch.float16 or t.dim() != 3 or t.shape[0] != B or t.shape[2] != D:
-            raise ValueError(f"{name}: expected fp16 ({B}, heads, {D})")
-        pitch = int(row_stride) or t.shape[1] * D
-        if t.stride(2) != 1 or t.stride(1) != D or (B > 1 and t.stride(0) != pitch):
-            raise ValueError(f"{name}: rows must be {pitch} elements apart, heads and dims packed")
-        if not _on_device(t):
-            raise ValueError(f"{name} must be a CUDA tensor")
+    pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
+    row_stride = int(row_stride)
+    if q is None or q.dim() != 3:
+        _arg(q, _H, "q", (B, None, 128))
     Hq = q.shape[1]
-    if k.shape[1] != Hkv or v.shape[1] != Hkv:
-        raise ValueError(f"k, v: {k.shape[1]} and {v.shape[1]} heads, the pools have {Hkv}")
-    _arg(q_out, _H, "q_out", (B, Hq, D), optional=True)
-    _arg(err_flag, _I, "err_flag", optional=True)
-    _same_device(q, k=k, v=v, q_out=q_out, k_pool=k_pool, v_pool=v_pool, block_table=block_table,
-                 context_lens=context_lens, err_flag=err_flag)
-    check(load().kv_append_rope_int4(_p(q), _p(k), _p(v), int(row_stride), _p(q_out), _p(k_pool), _p(v_pool), pages,
-                                     _p(block_table), block_table.shape[1], _p(context_lens), B, Hq, Hkv, D,
-                                     float(theta), _p(err_flag), stream_handle(stream)))
+    if row_stride == 0:
+        _is(q, torch.float16, (B, Hq, 128), dev, "q")
+        _is(k, torch.float16, (B, Hkv, 128), dev, "k")
+        _is(v, torch.float16, (B, Hkv, 128), dev, "v")
+    else:
+        for t, n, name in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v")):
+            if t is None or t.dtype != torch.float16 or t.shape != (B, n, 128) or t.get_device() != dev:
+                raise ValueError(f"{name}: expected fp16 ({B}, {n}, 128) on the pools' device")
+            if t.stride(2) != 1 or (n > 1 and t.stride(1) != 128) or (B > 1 and t.stride(0) != row_stride):
+                raise ValueError(f"{name}: rows must be {row_stride} elements apart, heads and dims packed")
+    if q_out is not None:
+        _is(q_out, torch.float16, (B, Hq, 128), dev, "q_out")
+    check(load().kv_append_rope_int4(q.data_ptr(), k.data_ptr(), v.data_ptr(), row_stride, _p(q_out),
+                                     k_pool.data_ptr(), v_pool.data_ptr(), pages, block_table.data_ptr(), blocks,
+                                     context_lens.data_ptr(), B, Hq, Hkv, 128, float(theta), _err_flag(err_flag, dev),
+                                     _stream_on(stream, dev)))
     return q if q_out is None else q_out
 
 
 def kv_read_int4(k_pool, v_pool, block_table, context_lens, T, starts=None, k_out=None, v_out=None, err_flag=None,
                  stream=None):
     """(k, v) fp16 [B][T][Hkv][128] read back from INT4 pools: row i of
-    sequence b is the token at position starts[b] + i (0 + i without starts)
-    if the sequence holds it; other rows are left as they were (zeros where
-    the call allocates)."""
-    pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
+    sequence b is the token at position starts[b] + i (i without starts) if
+    the sequence holds it.  Other rows of a k_out, v_out pair that the caller
+    gives are left as they were; of tensors that the call makes, they are zero."""
+    pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
     T = int(T)
     if T < 1:
         raise ValueError(f"T={T}, expected at least 1")
-    _arg(starts, _I, "starts", (B,), optional=True)
+    if starts is not None:
+        _is(starts, torch.int32, (B,), dev, "starts")
     shape = (B, T, Hkv, 128)
-    _arg(k_out, _H, "k_out", shape, optional=True)
-    _arg(v_out, _H, "v_out", shape, optional=True)
-    _arg(err_flag, _I, "err_flag", optional=True)
-    _same_device(k_pool, v_pool=v_pool, block_table=block_table, context_lens=context_lens, starts=starts,
-                 k_out=k_out, v_out=v_out, err_flag=err_flag)
-    if k_out is None:
-        k_out = torch.zeros(shape, dtype=torch.float16, device=k_pool.device)
-    if v_out is None:
-        v_out = torch.zeros(shape, dtype=torch.float16, device=k_pool.device)
-    check(load().kv_read_int4(_p(k_pool), _p(v_pool), pages, _p(block_table), block_table.shape[1], _p(starts),
-                              _p(context_lens), T, B, Hkv, 128, _p(k_out), _p(v_out), _p(err_flag),
-                              stream_handle(stream)))
+    fresh = k_out is None and v_out is None
+    if fresh:
+        k_out = k_pool.new_empty(shape, dtype=torch.float16)
+        v_out = k_pool.new_empty(shape, dtype=torch.float16)
+    else:
+        _is(k_out, torch.float16, shape, dev, "k_out")
+        _is(v_out, torch.float16, shape, dev, "v_out")
+    check(load().kv_read_int4(k_pool.data_ptr(), v_pool.data_ptr(), pages, block_table.data_ptr(), blocks, _p(starts),
+                              context_lens.data_ptr(), T, B, Hkv, 128, k_out.data_ptr(), v_out.data_ptr(), fresh,
+                              _err_flag(err_flag, dev), _stream_on(stream, dev)))
     return k_out, v_out
 
 
-def _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, device):
-    _arg(out, _H, "out", (B, Hq, 128), optional=True)
-    _arg(workspace, _U8, "workspace", optional=True)
+def _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, like, dev):
     if workspace is None:
         nbytes = load().paged_gqa_decode_window_workspace_size(B, Hq, Hkv, max_context, window, sinks, 128)
-        workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=like.device)
+    else:
+        _is(workspace, torch.uint8, workspace.shape, dev, "workspace")
     if out is None:
-        out = torch.empty((B, Hq, 128), dtype=torch.float16, device=device)
+        out = like.new_empty((B, Hq, 128))
+    else:
+        _is(out, torch.float16, (B, Hq, 128), dev, "out")
     return workspace, out
 
 
@@ -453,30 +491,39 @@ def paged_gqa_decode_int4(q, k_pool, v_pool, block_table, context_lens, max_cont
     128) and the call is the fused RoPE + INT4 append + attention
     (paged_gqa_decode_rope_append_int4).  A workspace the caller gives is
     zeroed once before its first use."""
-    pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
-    D, max_context = 128, int(max_context)
+    pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
+    max_context = int(max_context)
     fuse = qkv_theta is not None
-    if fuse and n_q_heads is None:
-        raise ValueError("n_q_heads is required with q|k|v rows")
-    Hq = n_q_heads if n_q_heads is not None else q.shape[-2]
     if fuse:
-        _arg(q, _H, "qkv", (B, None))
-        if q.shape[1] < (Hq + 2 * Hkv) * D:
-            raise ValueError(f"qkv: rows of {q.shape[1]}, need (Hq + 2 Hkv) D = {(Hq + 2 * Hkv) * D}")
+        if n_q_heads is None:
+            raise ValueError("n_q_heads is required with q|k|v rows")
+        Hq = int(n_q_heads)
+        if q is None or q.dim() != 2:
+            _arg(q, _H, "qkv", (B, None))
+        pitch = q.shape[1]
+        _is(q, torch.float16, (B, pitch), dev, "qkv")
+        if pitch < (Hq + 2 * Hkv) * 128:
+            raise ValueError(f"qkv: rows of {pitch}, need (Hq + 2 Hkv) D = {(Hq + 2 * Hkv) * 128}")
     else:
-        _arg(q, _H, "q", (B, Hq, D))
-    _arg(err_flag, _I, "err_flag", optional=True)
-    _same_device(q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, context_lens=context_lens,
-                 workspace=workspace, out=out, err_flag=err_flag)
-    workspace, out = _window_buffers(B, Hq, Hkv, max_context, max_context, 0, workspace, out, k_pool.device)
-    scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-    common = (_p(k_pool), _p(v_pool), pages, _p(block_table), block_table.shape[1], _p(context_lens), max_context, B,
-              Hq, Hkv, D)
-    tail = (scale, _p(workspace), workspace.numel(), _p(out), _p(err_flag), stream_handle(stream))
+        if q is None or q.dim() != 3:
+            _arg(q, _H, "q", (B, None, 128))
+        Hq = q.shape[1]
+        if n_q_heads is not None and n_q_heads != Hq:
+            raise ValueError(f"q has {Hq} heads, n_q_heads={n_q_heads}")
+        _is(q, torch.float16, (B, Hq, 128), dev, "q")
+    workspace, out = _window_buffers(B, Hq, Hkv, max_context, max_context, 0, workspace, out, q, dev)
+    scale = _SCALE_128 if sm_scale is None else float(sm_scale)
+    lib, err, sh = load(), _err_flag(err_flag, dev), _stream_on(stream, dev)
     if fuse:
-        check(load().paged_gqa_decode_rope_append_int4(_p(q), q.shape[1], *common, float(qkv_theta), *tail))
+        check(lib.paged_gqa_decode_rope_append_int4(
+            q.data_ptr(), pitch, k_pool.data_ptr(), v_pool.data_ptr(), pages, block_table.data_ptr(), blocks,
+            context_lens.data_ptr(), max_context, B, Hq, Hkv, 128, float(qkv_theta), scale, workspace.data_ptr(),
+            workspace.numel(), out.data_ptr(), err, sh))
     else:
-        check(load().paged_gqa_decode_int4(_p(q), 0, *common, *tail))
+        check(lib.paged_gqa_decode_int4(
+            q.data_ptr(), 0, k_pool.data_ptr(), v_pool.data_ptr(), pages, block_table.data_ptr(), blocks,
+            context_lens.data_ptr(), max_context, B, Hq, Hkv, 128, scale, workspace.data_ptr(), workspace.numel(),
+            out.data_ptr(), err, sh))
     return out
 
 
@@ -487,35 +534,32 @@ def paged_gqa_decode_window(q, k_pool, v_pool, block_table, context_lens, max_co
     [128], FP8 (E4M3) codes of that shape with k_scale / v_scale, or INT4
     [pages][Hkv][KV4_SLICE].  A workspace the caller gives is zeroed once
     before its first use."""
-    D = 128
-    max_context, window, sinks = int(max_context), int(window), int(sinks)
     fp8 = k_scale is not None or v_scale is not None
+    kind = "fp8" if fp8 else "int4" if k_pool is not None and k_pool.dtype is torch.uint8 else "fp16"
+    pages, Hkv, B, blocks, dev = _paging_of(kind, k_pool, v_pool, block_table, context_lens)
     if fp8:
-        pages, Hkv, _, B = _paging_fp8(k_pool, v_pool, k_scale, v_scale, block_table, context_lens)
-    elif k_pool.dtype == torch.uint8:
-        pages, Hkv, B = _paging_int4(k_pool, v_pool, block_table, context_lens)
-    else:
-        pages, Hkv, _, B = _paging(k_pool, v_pool, block_table, context_lens)
-    if k_pool.dim() == 4:
-        _arg(k_pool, (k_pool.dtype,), "k_pool", (pages, Hkv, 16, D))
-    _arg(q, _H, "q", (B, None, D))
-    Hq = q.shape[1]
-    _arg(err_flag, _I, "err_flag", optional=True)
+        _is(k_scale, torch.float32, (pages, Hkv, 16), dev, "k_scale")
+        _is(v_scale, torch.float32, (pages, Hkv, 16), dev, "v_scale")
+    max_context, window, sinks = int(max_context), int(window), int(sinks)
     if window < 0 or sinks < 0:
         raise ValueError(f"window={window}, sinks={sinks}: neither may be negative")
-    _same_device(q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, context_lens=context_lens, k_scale=k_scale,
-                 v_scale=v_scale, workspace=workspace, out=out, err_flag=err_flag)
     window, sinks = min(window, max_context), min(sinks, max_context)  # (the same tokens, within a C int)
-    workspace, out = _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, k_pool.device)
-    scale = 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale)
-    args = (pages, _p(block_table), block_table.shape[1], _p(context_lens), max_context, window, sinks, B, Hq, Hkv, D,
-            scale, _p(workspace), workspace.numel(), _p(out), _p(err_flag), stream_handle(stream))
+    if q is None or q.dim() != 3:
+        _arg(q, _H, "q", (B, None, 128))
+    Hq = q.shape[1]
+    _is(q, torch.float16, (B, Hq, 128), dev, "q")
+    workspace, out = _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, q, dev)
+    args = (pages, block_table.data_ptr(), blocks, context_lens.data_ptr(), max_context, window, sinks, B, Hq, Hkv, 128,
+            _SCALE_128 if sm_scale is None else float(sm_scale), workspace.data_ptr(), workspace.numel(),
+            out.data_ptr(), _err_flag(err_flag, dev), _stream_on(stream, dev))
+    lib = load()
     if fp8:
-        check(load().paged_gqa_decode_window_fp8(_p(q), 0, _p(k_pool), _p(v_pool), _p(k_scale), _p(v_scale), *args))
-    elif k_pool.dtype == torch.uint8:
-        check(load().paged_gqa_decode_window_int4(_p(q), 0, _p(k_pool), _p(v_pool), *args))
+        check(lib.paged_gqa_decode_window_fp8(q.data_ptr(), 0, k_pool.data_ptr(), v_pool.data_ptr(),
+                                              k_scale.data_ptr(), v_scale.data_ptr(), *args))
+    elif kind == "int4":
+        check(lib.paged_gqa_decode_window_int4(q.data_ptr(), 0, k_pool.data_ptr(), v_pool.data_ptr(), *args))
     else:
-        check(load().paged_gqa_decode_window(_p(q), 0, _p(k_pool), _p(v_pool), *args))
+        check(lib.paged_gqa_decode_window(q.data_ptr(), 0, k_pool.data_ptr(), v_pool.data_ptr(), *args))
     return out
 
 

@@ -53,6 +53,11 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+__device__ __forceinline__ float ex2(float x) {
+  float d;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -68,6 +73,19 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 template <int KIND>
 struct Page;
 
+// Where a lane reads in slice 0 of this (kv head's) pools, and the bytes from
+// one page to the next; kc / vc codes or values, ks / vs scales.
+struct LanePtrs {
+  const uint8_t *kc, *vc, *ks, *vs;
+  uint32_t pitch, spitch;
+  __device__ __forceinline__ const uint8_t* at(const uint8_t* p, int page) const {
+    return p + (uint64_t)(uint32_t)page * pitch;
+  }
+  __device__ __forceinline__ const uint8_t* at_scale(const uint8_t* p, int page) const {
+    return p + (uint64_t)(uint32_t)page * spitch;
+  }
+};
+
 template <>
 struct Page<ATW_F16> {
   static constexpr int BATCH = 1;  // pages per step of a warp
@@ -77,33 +95,30 @@ struct Page<ATW_F16> {
     return 32 * (st >> 1) + 8 * t4 + 4 * (st & 1) + 2 * r + e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 64 * (mt >> 2) + 8 * g + 2 * (mt & 3); }
-  __device__ __forceinline__ void load_k(const AtwArgs& a, size_t slice, int g, int t4) {
-    const __half* p = static_cast<const __half*>(a.k) + slice * ATT_SLICE + g * ATT_D + 8 * t4;
+  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int g, int t4) {
+    const uint8_t* k = static_cast<const uint8_t*>(a.k) + (size_t)kvh * ATT_SLICE * 2;
+    const uint8_t* v = static_cast<const uint8_t*>(a.v) + (size_t)kvh * ATT_SLICE * 2;
+    return {k + g * 256 + 16 * t4, v + 2 * t4 * 256 + 16 * g, nullptr, nullptr, (uint32_t)(a.Hkv * ATT_SLICE * 2), 0u};
+  }
+  __device__ __forceinline__ void load_k(const LanePtrs& lp, int page) {
+    const uint8_t* p = lp.at(lp.kc, page);
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k[r][i] = ldcg16(p + r * 8 * ATT_D + 32 * i);
+      for (int i = 0; i < 4; ++i) k[r][i] = ldcg16(p + r * 2048 + 64 * i);
   }
-  __device__ __forceinline__ void load_v(const AtwArgs& a, size_t slice, int g, int t4) {
-    const __half* p = static_cast<const __half*>(a.v) + slice * ATT_SLICE + 2 * t4 * ATT_D + 8 * g;
+  __device__ __forceinline__ void load_v(const LanePtrs& lp, int page) {
+    const uint8_t* p = lp.at(lp.vc, page);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[r][i] = ldcg16(p + ((r & 1) + 8 * (r >> 1)) * ATT_D + 64 * i);
+      for (int i = 0; i < 2; ++i) v[r][i] = ldcg16(p + ((r & 1) + 8 * (r >> 1)) * 256 + 128 * i);
   }
-  __device__ __forceinline__ void clear_k() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) k[i >> 2][i & 3] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  __device__ __forceinline__ void clear_v() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i >> 1][i & 1] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  // V rows of tokens that do not count (bit r: row r of this lane's four does) become zero
-  __device__ __forceinline__ void mask_v(uint32_t live) {
+  // V rows of tokens that are not seen (bit r of live: token r is) become zero
+  __device__ __forceinline__ void mask_v(uint32_t live, int, int t4) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (!((live >> r) & 1u)) v[r][0] = v[r][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) v[r][0] = v[r][1] = make_uint4(0u, 0u, 0u, 0u);
   }
   __device__ __forceinline__ void scores(const uint32_t (&qb)[8][2], float (&s)[4]) const {
 #pragma unroll
@@ -114,7 +129,7 @@ struct Page<ATW_F16> {
     }
   }
   __device__ __forceinline__ void score_scale(float (&)[4]) const {}
-  __device__ __forceinline__ void p_scale(float (&)[4], bool, bool) const {}
+  __device__ __forceinline__ void p_scale(float (&)[4]) const {}
   __device__ __forceinline__ void output(uint32_t b0, uint32_t b1, float (&o)[8][4]) const {
 #pragma unroll
     for (int mt = 0; mt < 8; ++mt) {
@@ -134,34 +149,38 @@ struct Page<ATW_F8> {
     return 64 * (st >> 2) + 16 * t4 + 4 * (st & 3) + 2 * r + e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 16 * g + 2 * mt; }
-  __device__ __forceinline__ void load_k(const AtwArgs& a, size_t slice, int g, int t4) {
-    const uint8_t* p = static_cast<const uint8_t*>(a.k) + slice * ATT_SLICE + g * ATT_D + 16 * t4;
+  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int g, int t4) {
+    const uint8_t* k = static_cast<const uint8_t*>(a.k) + (size_t)kvh * ATT_SLICE;
+    const uint8_t* v = static_cast<const uint8_t*>(a.v) + (size_t)kvh * ATT_SLICE;
+    return {k + g * 128 + 16 * t4, v + 2 * t4 * 128 + 16 * g,
+            reinterpret_cast<const uint8_t*>(a.ks + (size_t)kvh * ATT_PAGE + g),
+            reinterpret_cast<const uint8_t*>(a.vs + (size_t)kvh * ATT_PAGE + g), (uint32_t)(a.Hkv * ATT_SLICE),
+            (uint32_t)(a.Hkv * ATT_PAGE * 4)};
+  }
+  __device__ __forceinline__ void load_k(const LanePtrs& lp, int page) {
+    const uint8_t* p = lp.at(lp.kc, page);
+    const float* q = reinterpret_cast<const float*>(lp.at_scale(lp.ks, page));
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) k[r][i] = ldcg16(p + r * 8 * ATT_D + 64 * i);
-      ks[r] = __ldcg(a.ks + slice * ATT_PAGE + g + 8 * r);
+      for (int i = 0; i < 2; ++i) k[r][i] = ldcg16(p + r * 1024 + 64 * i);
+      ks[r] = __ldcg(q + 8 * r);
     }
   }
-  __device__ __forceinline__ void load_v(const AtwArgs& a, size_t slice, int g, int t4) {
-    const uint8_t* p = static_cast<const uint8_t*>(a.v) + slice * ATT_SLICE + 2 * t4 * ATT_D + 16 * g;
+  __device__ __forceinline__ void load_v(const LanePtrs& lp, int page) {
+    const uint8_t* p = lp.at(lp.vc, page);
+    const float* q = reinterpret_cast<const float*>(lp.at_scale(lp.vs, page));
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = ldcg16(p + ((r & 1) + 8 * (r >> 1)) * ATT_D);
+    for (int r = 0; r < 4; ++r) v[r] = ldcg16(p + ((r & 1) + 8 * (r >> 1)) * 128);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) vs[r] = __ldcg(a.vs + slice * ATT_PAGE + g + 8 * r);
+    for (int r = 0; r < 2; ++r) vs[r] = __ldcg(q + 8 * r);
   }
-  __device__ __forceinline__ void clear_k() {
-    k[0][0] = k[0][1] = k[1][0] = k[1][1] = make_uint4(0u, 0u, 0u, 0u);
-    ks[0] = ks[1] = 0.f;
-  }
-  __device__ __forceinline__ void clear_v() {
-    v[0] = v[1] = v[2] = v[3] = make_uint4(0u, 0u, 0u, 0u);
-    vs[0] = vs[1] = 0.f;
-  }
-  __device__ __forceinline__ void mask_v(uint32_t live) {
+  __device__ __forceinline__ void mask_v(uint32_t live, int g, int t4) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (!((live >> r) & 1u)) v[r] = make_uint4(0u, 0u, 0u, 0u);
+      if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) v[r] = make_uint4(0u, 0u, 0u, 0u);
+    if (!((live >> g) & 1u)) vs[0] = 0.f;
+    if (!((live >> (g + 8)) & 1u)) vs[1] = 0.f;
   }
   __device__ __forceinline__ void scores(const uint32_t (&qb)[8][2], float (&s)[4]) const {
 #pragma unroll
@@ -178,9 +197,9 @@ struct Page<ATW_F8> {
     s[2] *= ks[1];
     s[3] *= ks[1];
   }
-  // V row scales go into P before its rounding (masked tokens: p = 0 whatever their scale holds)
-  __device__ __forceinline__ void p_scale(float (&p)[4], bool live0, bool live1) const {
-    const float f0 = live0 ? vs[0] * ATW_V8 : 0.f, f1 = live1 ? vs[1] * ATW_V8 : 0.f;
+  // V row scales go into P before its rounding
+  __device__ __forceinline__ void p_scale(float (&p)[4]) const {
+    const float f0 = vs[0] * ATW_V8, f1 = vs[1] * ATW_V8;
     p[0] *= f0;
     p[1] *= f0;
     p[2] *= f1;
@@ -210,31 +229,29 @@ struct Page<ATW_I4> {
     return 32 * t4 + 8 * (st >> 1) + 2 * (st & 1) + r + 4 * e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 16 * g + 2 * mt; }
-  __device__ __forceinline__ void load_k(const AtwArgs& a, size_t slice, int g, int t4) {
-    const uint8_t* p = static_cast<const uint8_t*>(a.k) + slice * KV4_SLICE;
-    k[0] = ldcg16(p + kv4_k_code(g, 8 * t4));
-    k[1] = ldcg16(p + kv4_k_code(g + 8, 8 * t4));
-    ks = __ldcg(reinterpret_cast<const unsigned short*>(p + kv4_k_scale(g, t4)));
+  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int g, int t4) {
+    const uint8_t* k = static_cast<const uint8_t*>(a.k) + (size_t)kvh * KV4_SLICE;
+    const uint8_t* v = static_cast<const uint8_t*>(a.v) + (size_t)kvh * KV4_SLICE;
+    return {k + kv4_k_code(g, 8 * t4), v + kv4_v_code(2 * t4, 4 * g), k + kv4_k_scale(g, t4),
+            v + kv4_v_scale(2 * t4, g >> 1), (uint32_t)(a.Hkv * KV4_SLICE), (uint32_t)(a.Hkv * KV4_SLICE)};
   }
-  __device__ __forceinline__ void load_v(const AtwArgs& a, size_t slice, int g, int t4) {
-    const uint8_t* p = static_cast<const uint8_t*>(a.v) + slice * KV4_SLICE;
-    v[0] = ldcg16(p + kv4_v_code(2 * t4, 4 * g));
-    v[1] = ldcg16(p + kv4_v_code(2 * t4 + 8, 4 * g));
-    vs = __ldcg(reinterpret_cast<const unsigned int*>(p + kv4_v_scale(2 * t4, g >> 1)));
+  __device__ __forceinline__ void load_k(const LanePtrs& lp, int page) {
+    const uint8_t* p = lp.at(lp.kc, page);
+    k[0] = ldcg16(p);
+    k[1] = ldcg16(p + 512);
+    ks = __ldcg(reinterpret_cast<const unsigned short*>(lp.at(lp.ks, page)));
   }
-  __device__ __forceinline__ void clear_k() {
-    k[0] = k[1] = make_uint4(0u, 0u, 0u, 0u);
-    ks = 0u;
-  }
-  __device__ __forceinline__ void clear_v() {
-    v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u);
-    vs = 0u;
+  __device__ __forceinline__ void load_v(const LanePtrs& lp, int page) {
+    const uint8_t* p = lp.at(lp.vc, page);
+    v[0] = ldcg16(p);
+    v[1] = ldcg16(p + 512);
+    vs = __ldcg(reinterpret_cast<const unsigned int*>(lp.at(lp.vs, page)));
   }
   // a zero scale makes every code zero
-  __device__ __forceinline__ void mask_v(uint32_t live) {
+  __device__ __forceinline__ void mask_v(uint32_t live, int, int t4) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (!((live >> r) & 1u)) vs &= ~(0xFFu << (8 * r));
+      if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) vs &= ~(0xFFu << (8 * r));
   }
   __device__ __forceinline__ void scores(const uint32_t (&qb)[8][2], float (&s)[4]) const {
     const Kv4Scale s0 = kv4_scale_pair((ks & 0xFFu) * 0x00800080u), s1 = kv4_scale_pair((ks >> 8) * 0x00800080u);
@@ -248,7 +265,7 @@ struct Page<ATW_I4> {
     }
   }
   __device__ __forceinline__ void score_scale(float (&)[4]) const {}
-  __device__ __forceinline__ void p_scale(float (&)[4], bool, bool) const {}
+  __device__ __forceinline__ void p_scale(float (&)[4]) const {}
   __device__ __forceinline__ void output(uint32_t b0, uint32_t b1, float (&o)[8][4]) const {
     const Kv4Scale s0 = kv4_scale_pair(prmt(vs, 0u, 0x4140) << 7), s1 = kv4_scale_pair(prmt(vs, 0u, 0x4342) << 7);
 #pragma unroll
@@ -336,41 +353,36 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
     const int v = wv0 + (i / BATCH) * NW * BATCH + i % BATCH;
     if (v >= v1) return -1;
     const int pn = page_no(v);
-    const int pg = pn < a.max_blocks ? __ldcg(&bt[pn]) : -1;
-    if (pg < 0 || pg >= a.num_pages) {
+    const int id = pn < a.max_blocks ? __ldcg(&bt[pn]) : -1;
+    if (id < 0 || id >= a.num_pages) {
       if (a.err_flag) atomicOr(a.err_flag, 1);
       return -1;
     }
-    return pg;
+    return id;
   };
   // 32 page ids at a time, one per lane
   int ids = table(lane), ids_next = -1;
+  const LanePtrs lp = Page<KIND>::lane_ptrs(a, kvh, g, t4);
 
+  // (a missing page loads page 0 in its place: its tokens are masked)
   Page<KIND> pg[BATCH];
-  int cur[BATCH], nxt[BATCH];
-  auto fetch_ids = [&](int step, int (&out)[BATCH]) {
+  int cur[BATCH];
+  auto fetch_ids = [&](int step) {
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) out[j] = __shfl_sync(0xffffffffu, ids, (step * BATCH + j) & 31);
-  };
-  auto load_k = [&](const int (&id)[BATCH]) {
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      if (id[j] >= 0) pg[j].load_k(a, (size_t)id[j] * a.Hkv + kvh, g, t4);
-      else pg[j].clear_k();
-    }
-  };
-  auto load_v = [&](const int (&id)[BATCH]) {
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      if (id[j] >= 0) pg[j].load_v(a, (size_t)id[j] * a.Hkv + kvh, g, t4);
-      else pg[j].clear_v();
-    }
+    for (int j = 0; j < BATCH; ++j) cur[j] = __shfl_sync(0xffffffffu, ids, (step * BATCH + j) & 31);
   };
   if (steps > 0) {
-    fetch_ids(0, cur);
-    load_k(cur);
-    load_v(cur);
+    fetch_ids(0);
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) pg[j].load_k(lp, max(cur[j], 0));
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) pg[j].load_v(lp, max(cur[j], 0));
   }
+  // pages some of whose tokens are masked: the last of the sinks, the first of
+  // the window, the last of the sequence (-1: none)
+  const int part_s = S % ATT_PAGE ? nsp - 1 : -1;
+  const int part_w = nsp < n && wp * ATT_PAGE < w0 ? nsp : -1;
+  const int part_l = L % ATT_PAGE ? n - 1 : -1;
 
   // ---- queries ----------------------------------------------------------------
   const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
@@ -415,12 +427,13 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const __half lo = s_q[g][Page<KIND>::qdim(st, t4, r, 0)], hi = s_q[g][Page<KIND>::qdim(st, t4, r, 1)];
-      qb[st][r] = (uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16);
+      qb[st][r] = ((uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16)) ^
+                  (a.scale_log2 < 0.f ? 0x80008000u : 0u);
     }
   W4_TRACE_MARK(0);
 
   // ---- pages --------------------------------------------------------------------
-  const float scale = a.scale_log2 * atw_s_factor<KIND>();
+  const float scale = fabsf(a.scale_log2) * atw_s_factor<KIND>();  // (its sign is in the queries)
   float m0 = -INFINITY, m1 = -INFINITY;  // references of heads 2 t4 and 2 t4 + 1 (log2 domain)
   float l0 = 0.f, l1 = 0.f;              // this lane's part of their sums
   float o[8][4];                         // rows: dims odim(mt, g) + {0, 1}, columns: the two heads
@@ -428,44 +441,51 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
   for (int step = 0; step < steps; ++step) {
-    const int nstep = step + 1;
-    if (((nstep * BATCH) & 31) == 0) ids = ids_next;
-    if (((nstep * BATCH) & 31) == BATCH) ids_next = table((nstep * BATCH & ~31) + 32 + lane);
-    fetch_ids(nstep, nxt);
-    if (nstep >= steps) {
+    const int v = wv0 + step * NW * BATCH;  // first visible page of this step
+    // does any of these pages have masked tokens?
+    bool masked = false;
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) nxt[j] = -1;
-    }
-    // visibility of the tokens of these pages: full pages need no test
-    int tok0[BATCH];
-    bool full[BATCH];
+    for (int j = 0; j < BATCH; ++j)
+      masked |= cur[j] < 0 || v + j == part_s || v + j == part_w || v + j == part_l;
+    uint32_t live[BATCH];  // bit r: token r of the page is seen
+    if (masked) {
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      tok0[j] = page_no(wv0 + step * NW * BATCH + j) * ATT_PAGE;
-      full[j] = cur[j] >= 0 && tok0[j] + ATT_PAGE <= L && (tok0[j] >= w0 || tok0[j] + ATT_PAGE <= S);
+      for (int j = 0; j < BATCH; ++j) {
+        live[j] = 0u;
+        const int t0 = page_no(v + j) * ATT_PAGE;
+        if (cur[j] >= 0) {
+          for (int r = 0; r < ATT_PAGE; ++r)
+            live[j] |= (t0 + r < L && (t0 + r >= w0 || t0 + r < S) ? 1u : 0u) << r;
+        }
+      }
     }
-    auto seen = [&](int j, int r) {  // token r of page j
-      const int t = tok0[j] + r;
-      return full[j] || (cur[j] >= 0 && t < L && (t >= w0 || t < S));
-    };
+    bool fresh[BATCH];  // fused: the page of the new token
     float s[BATCH][4];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
       if constexpr (FUSE) {
-        if (cur[j] >= 0 && tok0[j] == (pos & ~(ATT_PAGE - 1))) pg[j].patch_k(s_new[0], s_news[0], pos & 15, g, t4);
+        fresh[j] = v + j == n - 1 && pos >= 0;
+        if (fresh[j]) pg[j].patch_k(s_new[0], s_news[0], pos & 15, g, t4);
       }
       s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
       pg[j].scores(qb, s[j]);
       pg[j].score_scale(s[j]);
     }
-    load_k(nxt);
+    const bool more = step + 1 < steps;
+    if (more) {
+      const int i = (step + 1) * BATCH;
+      if ((i & 31) == 0) ids = ids_next;
+      if ((i & 31) == BATCH) ids_next = table((i & ~31) + 32 + lane);
+      fetch_ids(step + 1);
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const bool a0 = seen(j, g), a1 = seen(j, g + 8);
-      s[j][0] = a0 ? s[j][0] * scale : -INFINITY;
-      s[j][1] = a0 ? s[j][1] * scale : -INFINITY;
-      s[j][2] = a1 ? s[j][2] * scale : -INFINITY;
-      s[j][3] = a1 ? s[j][3] * scale : -INFINITY;
+      for (int j = 0; j < BATCH; ++j) pg[j].load_k(lp, max(cur[j], 0));
+    }
+    if (masked) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) {
+        if (!((live[j] >> g) & 1u)) s[j][0] = s[j][1] = -INFINITY;
+        if (!((live[j] >> (g + 8)) & 1u)) s[j][2] = s[j][3] = -INFINITY;
+      }
     }
     float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
 #pragma unroll
@@ -473,6 +493,8 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
       x0 = fmaxf(x0, fmaxf(s[j][0], s[j][2]));
       x1 = fmaxf(x1, fmaxf(s[j][1], s[j][3]));
     }
+    x0 *= scale;
+    x1 *= scale;
     if (__any_sync(0xffffffffu, x0 > m0 + ATW_SLACK || x1 > m1 + ATW_SLACK)) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
@@ -481,7 +503,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
       }
       x0 = fmaxf(m0, x0);
       x1 = fmaxf(m1, x1);
-      const float c0 = x0 == m0 ? 1.f : exp2f(m0 - x0), c1 = x1 == m1 ? 1.f : exp2f(m1 - x1);
+      const float c0 = x0 == m0 ? 1.f : ex2(m0 - x0), c1 = x1 == m1 ? 1.f : ex2(m1 - x1);
       m0 = x0;
       m1 = x1;
       l0 *= c0;
@@ -496,31 +518,40 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
     }
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      const bool a0 = seen(j, g), a1 = seen(j, g + 8);
-      // (a masked token's -inf under a reference still at -inf is no number)
-      float p[4];
-      p[0] = a0 ? exp2f(s[j][0] - m0) : 0.f;
-      p[1] = a0 ? exp2f(s[j][1] - m1) : 0.f;
-      p[2] = a1 ? exp2f(s[j][2] - m0) : 0.f;
-      p[3] = a1 ? exp2f(s[j][3] - m1) : 0.f;
-      l0 += p[0] + p[2];
-      l1 += p[1] + p[3];
-      if constexpr (FUSE) {
-        if (cur[j] >= 0 && tok0[j] == (pos & ~(ATT_PAGE - 1))) pg[j].patch_v(s_new[1], s_news[1], pos & 15, g, t4);
-      }
-      if (!full[j]) {
-        uint32_t live = 0u;
+      s[j][0] = ex2(fmaf(s[j][0], scale, -m0));
+      s[j][1] = ex2(fmaf(s[j][1], scale, -m1));
+      s[j][2] = ex2(fmaf(s[j][2], scale, -m0));
+      s[j][3] = ex2(fmaf(s[j][3], scale, -m1));
+    }
+    if (masked) {  // (-inf under a reference still at -inf is no number)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) live |= (seen(j, 2 * t4 + (r & 1) + 8 * (r >> 1)) ? 1u : 0u) << r;
-        pg[j].mask_v(live);
+      for (int j = 0; j < BATCH; ++j) {
+        if (!((live[j] >> g) & 1u)) s[j][0] = s[j][1] = 0.f;
+        if (!((live[j] >> (g + 8)) & 1u)) s[j][2] = s[j][3] = 0.f;
       }
-      pg[j].p_scale(p, a0, a1);
-      const uint32_t b0 = movmatrix_trans(pack_h2(p[0], p[1])), b1 = movmatrix_trans(pack_h2(p[2], p[3]));
+    }
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      l0 += s[j][0] + s[j][2];
+      l1 += s[j][1] + s[j][3];
+      if constexpr (FUSE) {
+        if (fresh[j]) pg[j].patch_v(s_new[1], s_news[1], pos & 15, g, t4);
+      }
+    }
+    if (masked) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j) pg[j].mask_v(live[j], g, t4);
+    }
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      pg[j].p_scale(s[j]);
+      const uint32_t b0 = movmatrix_trans(pack_h2(s[j][0], s[j][1])), b1 = movmatrix_trans(pack_h2(s[j][2], s[j][3]));
       pg[j].output(b0, b1, o);
     }
-    load_v(nxt);
+    if (more) {
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) cur[j] = nxt[j];
+      for (int j = 0; j < BATCH; ++j) pg[j].load_v(lp, max(cur[j], 0));
+    }
   }
   W4_TRACE_MARK(1);
 

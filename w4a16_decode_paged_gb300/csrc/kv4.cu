@@ -59,6 +59,7 @@ struct Kv4ReadArgs {
   __half *k_out, *v_out;  // [B][T][Hkv][D]
   int32_t* err_flag;
   int num_pages, max_blocks, T, Hkv, pages_max;  // pages_max: pages that T rows can touch
+  int clear;  // rows that hold no token become zero
 };
 
 // eight dims of one token (two code halfwords) times their scale, as 16 bytes
@@ -80,44 +81,45 @@ __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv
   const int h = (int)(item % a.Hkv);
   const long long pi = item / a.Hkv;
   if (pi >= a.pages_max) return;
-  const int L = __ldcg(&a.context_lens[b]);
+  const long long L = __ldcg(&a.context_lens[b]);
   const long long first = a.starts ? __ldcg(&a.starts[b]) : 0;
-  const long long lo = first > 0 ? first : 0;
-  const long long hi = first + a.T < (long long)L ? first + a.T : (long long)L;  // tokens [lo, hi)
-  const long long blk = lo / KV4_PAGE + pi;
-  if (blk * KV4_PAGE >= hi) return;
-  const int page = blk < a.max_blocks ? __ldcg(&a.block_table[(size_t)b * a.max_blocks + blk]) : -1;
-  if (page < 0 || page >= a.num_pages) {
+  const long long blk = (first >> 4) + pi;  // (rounds down for negative starts too)
+  const long long lo = blk * KV4_PAGE, hi = lo + KV4_PAGE;
+  if (lo >= first + a.T) return;
+  const bool live = lo < L && hi > 0;  // the page holds a token of the sequence
+  if (!live && !a.clear) return;
+  const int page = live && blk < a.max_blocks ? __ldcg(&a.block_table[(size_t)b * a.max_blocks + blk]) : -1;
+  const bool ok = page >= 0 && page < a.num_pages;
+  if (live && !ok) {
     if (lane == 0 && a.err_flag) atomicOr(a.err_flag, 1);
-    return;
+    if (!a.clear) return;
   }
-  const size_t off = ((size_t)page * a.Hkv + h) * KV4_SLICE;
+  const size_t off = ((size_t)(ok ? page : 0) * a.Hkv + h) * KV4_SLICE;
   const uint8_t* ks = a.k_pool + off;
   const uint8_t* vs = a.v_pool + off;
   const int c = lane & 15, half = lane >> 4;  // dims 8 c .. 8 c + 7
   const size_t pitch = (size_t)a.Hkv * KV4_D;
   const size_t out0 = ((size_t)b * a.T * a.Hkv + h) * KV4_D + 8 * c;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  // row of token t of the page: the token's value, zero, or left alone
+  auto put = [&](__half* out, int t, uint4 value) {
+    const long long tok = lo + t, row = tok - first;
+    if (row < 0 || row >= a.T) return;
+    const bool holds = ok && tok >= 0 && tok < L;
+    if (holds || a.clear) *reinterpret_cast<uint4*>(out + out0 + (size_t)row * pitch) = holds ? value : zero;
+  };
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int t = 2 * i + half;  // K: two tokens per step
-    const long long tok = blk * KV4_PAGE + t;
-    if (tok >= lo && tok < hi) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + kv4_k_code(t, 2 * c));
-      const uint4 o = kv4_eight(w & 0xFFFFu, w >> 16, kv4_scale_value(ks[kv4_k_scale(t, c >> 2)]));
-      *reinterpret_cast<uint4*>(a.k_out + out0 + (size_t)(tok - first) * pitch) = o;
-    }
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + kv4_k_code(t, 2 * c));
+    put(a.k_out, t, kv4_eight(w & 0xFFFFu, w >> 16, kv4_scale_value(ks[kv4_k_scale(t, c >> 2)])));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = 4 * i + 2 * half;  // V: two token pairs per step
-    const long long tok = blk * KV4_PAGE + t;
     const uint2 w = *reinterpret_cast<const uint2*>(vs + kv4_v_code(t, 2 * c));
-    if (tok >= lo && tok < hi)
-      *reinterpret_cast<uint4*>(a.v_out + out0 + (size_t)(tok - first) * pitch) =
-          kv4_eight(w.x & 0xFFFFu, w.y & 0xFFFFu, kv4_scale_value(vs[kv4_v_scale(t, c >> 2)]));
-    if (tok + 1 >= lo && tok + 1 < hi)
-      *reinterpret_cast<uint4*>(a.v_out + out0 + (size_t)(tok + 1 - first) * pitch) =
-          kv4_eight(w.x >> 16, w.y >> 16, kv4_scale_value(vs[kv4_v_scale(t + 1, c >> 2)]));
+    put(a.v_out, t, kv4_eight(w.x & 0xFFFFu, w.y & 0xFFFFu, kv4_scale_value(vs[kv4_v_scale(t, c >> 2)])));
+    put(a.v_out, t + 1, kv4_eight(w.x >> 16, w.y >> 16, kv4_scale_value(vs[kv4_v_scale(t + 1, c >> 2)])));
   }
 }
 
@@ -166,7 +168,9 @@ extern "C" int kv_append_rope_int4(uint16_t* q, const uint16_t* k, const uint16_
 
 extern "C" int kv_read_int4(const uint8_t* k_pool, const uint8_t* v_pool, int num_pages, const int32_t* block_table,
                             int max_blocks, const int32_t* starts, const int32_t* context_lens, int T, int B, int Hkv,
-                            int D, uint16_t* k_out, uint16_t* v_out, int32_t* err_flag, w4a16_stream_t stream) {
+                            int D, uint16_t* k_out, uint16_t* v_out, int clear, int32_t* err_flag,
+                            w4a16_stream_t stream) {
+  W4_CHECK_ARG(clear == 0 || clear == 1, "kv_read_int4: clear=%d", clear);
   W4_CHECK_ARG(k_pool && v_pool && block_table && context_lens && k_out && v_out, "kv_read_int4: null pointer");
   W4_CHECK_ARG(T >= 1 && B >= 1 && Hkv >= 1 && num_pages >= 1 && max_blocks >= 1, "kv_read_int4: sizes");
   W4_CHECK_SHAPE(D == KV4_D, "kv_read_int4: D=%d, only 128 is built", D);
@@ -188,9 +192,8 @@ extern "C" int kv_read_int4(const uint8_t* k_pool, const uint8_t* v_pool, int nu
   a.max_blocks = max_blocks;
   a.T = T;
   a.Hkv = Hkv;
-  // pages that T consecutive tokens can touch; the block table holds max_blocks
-  const long long pages = ((long long)T + KV4_PAGE - 2) / KV4_PAGE + 1;
-  a.pages_max = (int)(pages < max_blocks ? pages : max_blocks);
+  a.clear = clear;
+  a.pages_max = (int)(((long long)T + KV4_PAGE - 2) / KV4_PAGE + 1);  // that T consecutive tokens can touch
   const long long ctas = ((long long)a.pages_max * Hkv + 7) / 8;
   W4_CHECK_SHAPE(ctas <= 0x7FFFFFFFll, "kv_read_int4: T=%d x Hkv=%d is too large", T, Hkv);
   cudaError_t e = launch_pdl(w4pg_read_int4, dim3((unsigned)ctas, (unsigned)B), dim3(256), 0, (cudaStream_t)stream, a);
