@@ -70,72 +70,65 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 // k_frag gives the A fragments of MMA step st (st of 8), v_frag those of the
 // 16 dims of block mt (mt of 8).
 // ---------------------------------------------------------------------------
+// One bulk copy (16-byte aligned both ends, bytes a multiple of 16) that
+// completes on the mbarrier.
+__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 template <int KIND>
 struct Page;
 
-// Where a lane reads in slice 0 of this (kv head's) pools, and the bytes from
-// one page to the next; kc / vc codes or values, ks / vs scales.
-struct LanePtrs {
-  const uint8_t *kc, *vc, *ks, *vs;
-  uint32_t pitch, spitch;
-  __device__ __forceinline__ const uint8_t* at(const uint8_t* p, int page) const {
-    return p + (uint64_t)(uint32_t)page * pitch;
-  }
-  __device__ __forceinline__ const uint8_t* at_scale(const uint8_t* p, int page) const {
-    return p + (uint64_t)(uint32_t)page * spitch;
-  }
-};
-
 template <>
 struct Page<ATW_F16> {
-  static constexpr int BATCH = 1;  // pages per step of a warp
-  uint4 k[2][4], v[4][2];
+  static constexpr int BATCH = 1;   // pages per step of a warp
+  static constexpr int STAGES = 3;  // steps in flight per warp
+  static constexpr int MIN_CTAS = 1;
+  static constexpr int V = 4096;    // V's offset in a page's slot
+  static constexpr int SLOT = 8192;
   // dim of element e (0, 1) of query register r (0, 1) in step st
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
     return 32 * (st >> 1) + 8 * t4 + 4 * (st & 1) + 2 * r + e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 64 * (mt >> 2) + 8 * g + 2 * (mt & 3); }
-  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int g, int t4) {
-    const uint8_t* k = static_cast<const uint8_t*>(a.k) + (size_t)kvh * ATT_SLICE * 2;
-    const uint8_t* v = static_cast<const uint8_t*>(a.v) + (size_t)kvh * ATT_SLICE * 2;
-    return {k + g * 256 + 16 * t4, v + 2 * t4 * 256 + 16 * g, nullptr, nullptr, (uint32_t)(a.Hkv * ATT_SLICE * 2), 0u};
+  // the copies of one page (one lane issues them)
+  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, uint32_t bar) {
+    bulk_g2s(slot, static_cast<const __half*>(a.k) + slice * ATT_SLICE, 4096, bar);
+    bulk_g2s(slot + V, static_cast<const __half*>(a.v) + slice * ATT_SLICE, 4096, bar);
   }
-  __device__ __forceinline__ void load_k(const LanePtrs& lp, int page) {
-    const uint8_t* p = lp.at(lp.kc, page);
+  // S^T += K Q^T of one page, scaled where the kind has K row scales
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const uint32_t (&qb)[8][2],
+                                                float (&s)[4]) {
+    const unsigned char* p = slot + 256 * g + 16 * t4;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) k[r][i] = ldcg16(p + r * 2048 + 64 * i);
-  }
-  __device__ __forceinline__ void load_v(const LanePtrs& lp, int page) {
-    const uint8_t* p = lp.at(lp.vc, page);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) v[r][i] = ldcg16(p + ((r & 1) + 8 * (r >> 1)) * 256 + 128 * i);
-  }
-  // V rows of tokens that are not seen (bit r of live: token r is) become zero
-  __device__ __forceinline__ void mask_v(uint32_t live, int, int t4) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) v[r][0] = v[r][1] = make_uint4(0u, 0u, 0u, 0u);
-  }
-  __device__ __forceinline__ void scores(const uint32_t (&qb)[8][2], float (&s)[4]) const {
-#pragma unroll
-    for (int st = 0; st < 8; ++st) {
-      const uint32_t* k0 = &k[0][st >> 1].x + 2 * (st & 1);
-      const uint32_t* k1 = &k[1][st >> 1].x + 2 * (st & 1);
-      mma_16816_full(s, k0[0], k1[0], k0[1], k1[1], qb[st][0], qb[st][1]);
+    for (int i = 0; i < 4; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + 64 * i), y = *reinterpret_cast<const uint4*>(p + 2048 + 64 * i);
+      mma_16816_full(s, x.x, y.x, x.y, y.y, qb[2 * i][0], qb[2 * i][1]);
+      mma_16816_full(s, x.z, y.z, x.w, y.w, qb[2 * i + 1][0], qb[2 * i + 1][1]);
     }
   }
-  __device__ __forceinline__ void score_scale(float (&)[4]) const {}
-  __device__ __forceinline__ void p_scale(float (&)[4]) const {}
-  __device__ __forceinline__ void output(uint32_t b0, uint32_t b1, float (&o)[8][4]) const {
+  // factors of P that come before its rounding
+  static __device__ __forceinline__ void p_scale(const unsigned char*, int, uint32_t, float (&)[4]) {}
+  // O^T += V^T P^T; bit r of live: token r is seen, V rows of others count as zero whatever they hold
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, bool masked, uint32_t live,
+                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
+    const unsigned char* p = slot + V + 512 * t4 + 16 * g;
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt) {
-      const int i = mt >> 2, j = mt & 3;
-      const uint32_t a = (&v[0][i].x)[j], b = (&v[1][i].x)[j], c = (&v[2][i].x)[j], d = (&v[3][i].x)[j];
-      mma_16816_full(o[mt], prmt(a, b, 0x5410), prmt(a, b, 0x7632), prmt(c, d, 0x5410), prmt(c, d, 0x7632), b0, b1);
+    for (int i = 0; i < 2; ++i) {
+      uint4 w[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        w[r] = *reinterpret_cast<const uint4*>(p + 256 * (r & 1) + 2048 * (r >> 1) + 128 * i);
+        if (masked && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t a = (&w[0].x)[j], b = (&w[1].x)[j], c = (&w[2].x)[j], d = (&w[3].x)[j];
+        mma_16816_full(o[4 * i + j], prmt(a, b, 0x5410), prmt(a, b, 0x7632), prmt(c, d, 0x5410), prmt(c, d, 0x7632), b0,
+                       b1);
+      }
     }
   }
 };
@@ -143,72 +136,62 @@ struct Page<ATW_F16> {
 template <>
 struct Page<ATW_F8> {
   static constexpr int BATCH = 1;
-  uint4 k[2][2], v[4];
-  float ks[2], vs[2];
+  static constexpr int STAGES = 3;
+  static constexpr int MIN_CTAS = 2;
+  static constexpr int V = 2048, KS = 4096, VS = 4160;
+  static constexpr int SLOT = 4224;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
     return 64 * (st >> 2) + 16 * t4 + 4 * (st & 3) + 2 * r + e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 16 * g + 2 * mt; }
-  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int g, int t4) {
-    const uint8_t* k = static_cast<const uint8_t*>(a.k) + (size_t)kvh * ATT_SLICE;
-    const uint8_t* v = static_cast<const uint8_t*>(a.v) + (size_t)kvh * ATT_SLICE;
-    return {k + g * 128 + 16 * t4, v + 2 * t4 * 128 + 16 * g,
-            reinterpret_cast<const uint8_t*>(a.ks + (size_t)kvh * ATT_PAGE + g),
-            reinterpret_cast<const uint8_t*>(a.vs + (size_t)kvh * ATT_PAGE + g), (uint32_t)(a.Hkv * ATT_SLICE),
-            (uint32_t)(a.Hkv * ATT_PAGE * 4)};
+  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, uint32_t bar) {
+    bulk_g2s(slot, static_cast<const uint8_t*>(a.k) + slice * ATT_SLICE, 2048, bar);
+    bulk_g2s(slot + V, static_cast<const uint8_t*>(a.v) + slice * ATT_SLICE, 2048, bar);
+    bulk_g2s(slot + KS, a.ks + slice * ATT_PAGE, 64, bar);
+    bulk_g2s(slot + VS, a.vs + slice * ATT_PAGE, 64, bar);
   }
-  __device__ __forceinline__ void load_k(const LanePtrs& lp, int page) {
-    const uint8_t* p = lp.at(lp.kc, page);
-    const float* q = reinterpret_cast<const float*>(lp.at_scale(lp.ks, page));
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const uint32_t (&qb)[8][2],
+                                                float (&s)[4]) {
+    const unsigned char* p = slot + 128 * g + 16 * t4;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+    for (int i = 0; i < 2; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + 64 * i), y = *reinterpret_cast<const uint4*>(p + 1024 + 64 * i);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) k[r][i] = ldcg16(p + r * 1024 + 64 * i);
-      ks[r] = __ldcg(q + 8 * r);
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_h2x2((&x.x)[w], a0, a2);
+        e4m3x4_to_h2x2((&y.x)[w], a1, a3);
+        mma_16816_full(s, a0, a1, a2, a3, qb[4 * i + w][0], qb[4 * i + w][1]);
+      }
     }
-  }
-  __device__ __forceinline__ void load_v(const LanePtrs& lp, int page) {
-    const uint8_t* p = lp.at(lp.vc, page);
-    const float* q = reinterpret_cast<const float*>(lp.at_scale(lp.vs, page));
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = ldcg16(p + ((r & 1) + 8 * (r >> 1)) * 128);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) vs[r] = __ldcg(q + 8 * r);
-  }
-  __device__ __forceinline__ void mask_v(uint32_t live, int g, int t4) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) v[r] = make_uint4(0u, 0u, 0u, 0u);
-    if (!((live >> g) & 1u)) vs[0] = 0.f;
-    if (!((live >> (g + 8)) & 1u)) vs[1] = 0.f;
-  }
-  __device__ __forceinline__ void scores(const uint32_t (&qb)[8][2], float (&s)[4]) const {
-#pragma unroll
-    for (int st = 0; st < 8; ++st) {
-      uint32_t a0, a1, a2, a3;
-      e4m3x4_to_h2x2((&k[0][st >> 2].x)[st & 3], a0, a2);
-      e4m3x4_to_h2x2((&k[1][st >> 2].x)[st & 3], a1, a3);
-      mma_16816_full(s, a0, a1, a2, a3, qb[st][0], qb[st][1]);
-    }
-  }
-  __device__ __forceinline__ void score_scale(float (&s)[4]) const {
-    s[0] *= ks[0];
-    s[1] *= ks[0];
-    s[2] *= ks[1];
-    s[3] *= ks[1];
+    const float* ks = reinterpret_cast<const float*>(slot + KS);
+    const float f0 = ks[g], f1 = ks[g + 8];
+    s[0] *= f0;
+    s[1] *= f0;
+    s[2] *= f1;
+    s[3] *= f1;
   }
   // V row scales go into P before its rounding
-  __device__ __forceinline__ void p_scale(float (&p)[4]) const {
-    const float f0 = vs[0] * ATW_V8, f1 = vs[1] * ATW_V8;
+  static __device__ __forceinline__ void p_scale(const unsigned char* slot, int g, uint32_t live, float (&p)[4]) {
+    const float* vs = reinterpret_cast<const float*>(slot + VS);
+    const float f0 = (live >> g) & 1u ? vs[g] * ATW_V8 : 0.f, f1 = (live >> (g + 8)) & 1u ? vs[g + 8] * ATW_V8 : 0.f;
     p[0] *= f0;
     p[1] *= f0;
     p[2] *= f1;
     p[3] *= f1;
   }
-  __device__ __forceinline__ void output(uint32_t b0, uint32_t b1, float (&o)[8][4]) const {
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, bool masked, uint32_t live,
+                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
+    const unsigned char* p = slot + V + 256 * t4 + 16 * g;
+    uint4 w[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      w[r] = *reinterpret_cast<const uint4*>(p + 128 * (r & 1) + 1024 * (r >> 1));
+      if (masked && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t a = (&v[0].x)[j], b = (&v[1].x)[j], c = (&v[2].x)[j], d = (&v[3].x)[j];
+      const uint32_t a = (&w[0].x)[j], b = (&w[1].x)[j], c = (&w[2].x)[j], d = (&w[3].x)[j];
       uint32_t x[4], y[4];
       e4m3x4_to_h2x2(prmt(a, b, 0x5140), x[0], x[1]);
       e4m3x4_to_h2x2(prmt(a, b, 0x7362), x[2], x[3]);
@@ -223,80 +206,62 @@ struct Page<ATW_F8> {
 template <>
 struct Page<ATW_I4> {
   static constexpr int BATCH = 2;
-  uint4 k[2], v[2];
-  uint32_t ks, vs;  // scale bytes: K tokens g, g + 8; V tokens 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4
+  static constexpr int STAGES = 3;
+  static constexpr int MIN_CTAS = 2;
+  static constexpr int V = KV4_SLICE;
+  static constexpr int SLOT = 2 * KV4_SLICE;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
     return 32 * t4 + 8 * (st >> 1) + 2 * (st & 1) + r + 4 * e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 16 * g + 2 * mt; }
-  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int g, int t4) {
-    const uint8_t* k = static_cast<const uint8_t*>(a.k) + (size_t)kvh * KV4_SLICE;
-    const uint8_t* v = static_cast<const uint8_t*>(a.v) + (size_t)kvh * KV4_SLICE;
-    return {k + kv4_k_code(g, 8 * t4), v + kv4_v_code(2 * t4, 4 * g), k + kv4_k_scale(g, t4),
-            v + kv4_v_scale(2 * t4, g >> 1), (uint32_t)(a.Hkv * KV4_SLICE), (uint32_t)(a.Hkv * KV4_SLICE)};
+  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, uint32_t bar) {
+    bulk_g2s(slot, static_cast<const uint8_t*>(a.k) + slice * KV4_SLICE, KV4_SLICE, bar);
+    bulk_g2s(slot + V, static_cast<const uint8_t*>(a.v) + slice * KV4_SLICE, KV4_SLICE, bar);
   }
-  __device__ __forceinline__ void load_k(const LanePtrs& lp, int page) {
-    const uint8_t* p = lp.at(lp.kc, page);
-    k[0] = ldcg16(p);
-    k[1] = ldcg16(p + 512);
-    ks = __ldcg(reinterpret_cast<const unsigned short*>(lp.at(lp.ks, page)));
-  }
-  __device__ __forceinline__ void load_v(const LanePtrs& lp, int page) {
-    const uint8_t* p = lp.at(lp.vc, page);
-    v[0] = ldcg16(p);
-    v[1] = ldcg16(p + 512);
-    vs = __ldcg(reinterpret_cast<const unsigned int*>(lp.at(lp.vs, page)));
-  }
-  // a zero scale makes every code zero
-  __device__ __forceinline__ void mask_v(uint32_t live, int, int t4) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) vs &= ~(0xFFu << (8 * r));
-  }
-  __device__ __forceinline__ void scores(const uint32_t (&qb)[8][2], float (&s)[4]) const {
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const uint32_t (&qb)[8][2],
+                                                float (&s)[4]) {
+    const uint4 k0 = *reinterpret_cast<const uint4*>(slot + kv4_k_code(g, 8 * t4));
+    const uint4 k1 = *reinterpret_cast<const uint4*>(slot + kv4_k_code(g + 8, 8 * t4));
+    const uint32_t ks = *reinterpret_cast<const uint16_t*>(slot + kv4_k_scale(g, t4));  // tokens g and g + 8
     const Kv4Scale s0 = kv4_scale_pair((ks & 0xFFu) * 0x00800080u), s1 = kv4_scale_pair((ks >> 8) * 0x00800080u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t x[4], y[4];
-      kv4_unpack((&k[0].x)[i], s0, x);
-      kv4_unpack((&k[1].x)[i], s1, y);
+      kv4_unpack((&k0.x)[i], s0, x);
+      kv4_unpack((&k1.x)[i], s1, y);
       mma_16816_full(s, x[0], y[0], x[1], y[1], qb[2 * i][0], qb[2 * i][1]);
       mma_16816_full(s, x[2], y[2], x[3], y[3], qb[2 * i + 1][0], qb[2 * i + 1][1]);
     }
   }
-  __device__ __forceinline__ void score_scale(float (&)[4]) const {}
-  __device__ __forceinline__ void p_scale(float (&)[4]) const {}
-  __device__ __forceinline__ void output(uint32_t b0, uint32_t b1, float (&o)[8][4]) const {
+  static __device__ __forceinline__ void p_scale(const unsigned char*, int, uint32_t, float (&)[4]) {}
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, bool masked, uint32_t live,
+                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
+    const uint4 v0 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4, 4 * g));
+    const uint4 v1 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4 + 8, 4 * g));
+    // scale bytes of tokens 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4; a zero scale makes every code zero
+    uint32_t vs = *reinterpret_cast<const uint32_t*>(slot + V + kv4_v_scale(2 * t4, g >> 1));
+    if (masked) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) vs &= ~(0xFFu << (8 * r));
+    }
     const Kv4Scale s0 = kv4_scale_pair(prmt(vs, 0u, 0x4140) << 7), s1 = kv4_scale_pair(prmt(vs, 0u, 0x4342) << 7);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t x[4], y[4];
-      kv4_unpack((&v[0].x)[j], s0, x);
-      kv4_unpack((&v[1].x)[j], s1, y);
+      kv4_unpack((&v0.x)[j], s0, x);
+      kv4_unpack((&v1.x)[j], s1, y);
       mma_16816_full(o[2 * j], x[0], x[1], y[0], y[1], b0, b1);
       mma_16816_full(o[2 * j + 1], x[2], x[3], y[2], y[3], b0, b1);
     }
   }
-  // the new token's row (codes and scales in shared memory) over what was loaded
-  __device__ __forceinline__ void patch_k(const uint16_t* codes, const uint8_t* scale, int slot, int g, int t4) {
-    if ((slot & 7) != g) return;
-    const uint4 w = *reinterpret_cast<const uint4*>(codes + 8 * t4);
-    if (slot < 8) k[0] = w;
-    else k[1] = w;
-    const int sh = 8 * (slot >> 3);
-    ks = (ks & ~(0xFFu << sh)) | ((uint32_t)scale[t4] << sh);
-  }
-  __device__ __forceinline__ void patch_v(const uint16_t* codes, const uint8_t* scale, int slot, int g, int t4) {
-    if (((slot & 7) >> 1) != t4) return;
-    const uint32_t sel = (slot & 1) ? 0x5410u : 0x3254u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t c = codes[4 * g + j];
-      if (slot < 8) (&v[0].x)[j] = prmt((&v[0].x)[j], c, sel);
-      else (&v[1].x)[j] = prmt((&v[1].x)[j], c, sel);
-    }
-    const int sh = 8 * (2 * (slot >> 3) + (slot & 1));
-    vs = (vs & ~(0xFFu << sh)) | ((uint32_t)scale[g >> 1] << sh);
+  // the new token's rows over what was copied (warp-wide)
+  static __device__ __forceinline__ void patch(unsigned char* slot, const uint16_t (&codes)[2][32],
+                                               const uint8_t (&scales)[2][4], int t, int lane) {
+    *reinterpret_cast<uint16_t*>(slot + kv4_k_code(t, lane)) = codes[0][lane];
+    *reinterpret_cast<uint16_t*>(slot + V + kv4_v_code(t, lane)) = codes[1][lane];
+    if (lane < 4) slot[kv4_k_scale(t, lane)] = scales[0][lane];
+    else if (lane < 8) slot[V + kv4_v_scale(t, lane - 4)] = scales[1][lane - 4];
   }
 };
 
@@ -306,24 +271,43 @@ __device__ __forceinline__ constexpr float atw_s_factor() { return KIND == ATW_I
 template <int KIND>
 __device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I4 ? 64.f : (KIND == ATW_F8 ? 1.f / ATW_V8 : 1.f); }
 
+template <int KIND>
+constexpr size_t atw_ring_bytes() { return (size_t)ATW_NW * Page<KIND>::STAGES * Page<KIND>::BATCH * Page<KIND>::SLOT; }
+constexpr size_t ATW_MERGE_BYTES = (size_t)ATW_NW * 8 * ATW_PITCH * 4;
+template <int KIND>
+constexpr size_t atw_smem() { return std::max(atw_ring_bytes<KIND>(), ATW_MERGE_BYTES); }
+constexpr uint32_t ATW_WAIT_POLLS = 1u << 20;  // bound of a wait for copies
+
 template <int KIND, bool FUSE>
-__global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_attn_window(const __grid_constant__ AtwArgs a) {
-  constexpr int NW = ATW_NW, BATCH = Page<KIND>::BATCH;
+__global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
+    w4pg_attn_window(const __grid_constant__ AtwArgs a) {
+  using PG = Page<KIND>;
+  constexpr int NW = ATW_NW, BATCH = PG::BATCH, STAGES = PG::STAGES;
+  extern __shared__ __align__(128) unsigned char smraw[];  // the warps' rings, then their merge
   __shared__ __align__(16) __half s_q[8][ATT_D + 8];
-  __shared__ __align__(16) float s_o[NW * 8 * ATW_PITCH];  // [warp][head][128 + 4], dims in the order (mt, g, e)
   __shared__ float s_ml[NW * 8 * 2];
   __shared__ float s_cos[FUSE ? ATT_D / 2 : 1], s_sin[FUSE ? ATT_D / 2 : 1];
-  __shared__ __align__(16) uint16_t s_new[FUSE ? 2 : 1][32];  // codes of the new K and V rows
-  __shared__ uint8_t s_news[FUSE ? 2 : 1][4];
+  __shared__ __align__(16) uint16_t s_new[2][32];  // codes of the new K and V rows (fused)
+  __shared__ uint8_t s_news[2][4];
+  __shared__ __align__(8) uint64_t s_bar[NW * STAGES];
+  __shared__ float2 s_part[ATW_MAX_PARTITIONS * 8];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int pc = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int G = a.G;
+  uint64_t* bar = s_bar + warp * STAGES;
+  if (lane < STAGES) mbar_init(&bar[lane], 1);
+  fence_mbar_init();
   W4_TRACE_SCOPE(a.tag);
   pdl_wait_then_trigger();
   W4_TRACE_WAITED();
+
+  // the queries are asked for first: their latency passes under the lengths' and the table's
+  const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
+  uint4 qw = make_uint4(0u, 0u, 0u, 0u);
+  if (!FUSE && tid < 8 * ATT_D / 8 && tid / (ATT_D / 8) < G) qw = ldcg16(qrow + 8 * tid);
 
   // ---- the visible pages and this CTA's share -------------------------------
   int L = __ldcg(&a.context_lens[b]);
@@ -360,24 +344,29 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
     }
     return id;
   };
-  // 32 page ids at a time, one per lane
+  // 32 page ids at a time, one per lane: `ids` holds those of the steps being
+  // copied (pages 32 c .. of the list), ids_next the 32 after
   int ids = table(lane), ids_next = -1;
-  const LanePtrs lp = Page<KIND>::lane_ptrs(a, kvh, g, t4);
-
-  // (a missing page loads page 0 in its place: its tokens are masked)
-  Page<KIND> pg[BATCH];
-  int cur[BATCH];
-  auto fetch_ids = [&](int step) {
+  unsigned have = 0;  // bit (stage * BATCH + j): that page was copied
+  unsigned char* ring = smraw + (size_t)warp * STAGES * BATCH * PG::SLOT;
+  // copies step `st`'s pages into its stage (warp-wide; steps come in order)
+  auto issue = [&](int st) {
+    const int i = st * BATCH, stage = st % STAGES;
+    if (i > 0 && (i & 31) == 0) ids = ids_next;
+    if ((i & 31) == BATCH && st + 1 < steps) ids_next = table((i & ~31) + 32 + lane);
+    unsigned got = 0;
 #pragma unroll
-    for (int j = 0; j < BATCH; ++j) cur[j] = __shfl_sync(0xffffffffu, ids, (step * BATCH + j) & 31);
+    for (int j = 0; j < BATCH; ++j) got |= (__shfl_sync(0xffffffffu, ids, (i + j) & 31) >= 0 ? 1u : 0u) << j;
+    have = (have & ~(((1u << BATCH) - 1u) << (stage * BATCH))) | (got << (stage * BATCH));
+    // lane j of the warp's first BATCH lanes copies page j
+    if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(got) * PG::SLOT);
+    __syncwarp();
+    const int id = __shfl_sync(0xffffffffu, ids, (i + min(lane, BATCH - 1)) & 31);
+    if (lane < BATCH && id >= 0)
+      PG::fetch(a, (size_t)id * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + lane) * PG::SLOT, smem_u32(&bar[stage]));
   };
-  if (steps > 0) {
-    fetch_ids(0);
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) pg[j].load_k(lp, max(cur[j], 0));
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) pg[j].load_v(lp, max(cur[j], 0));
-  }
+  __syncwarp();
+  for (int st = 0; st < STAGES && st < steps; ++st) issue(st);
   // pages some of whose tokens are masked: the last of the sinks, the first of
   // the window, the last of the sequence (-1: none)
   const int part_s = S % ATT_PAGE ? nsp - 1 : -1;
@@ -385,7 +374,6 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
   const int part_l = L % ATT_PAGE ? n - 1 : -1;
 
   // ---- queries ----------------------------------------------------------------
-  const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
   const int pos = fits ? L - 1 : -1;  // the new token's (fused); a length past the bound appends nothing
   if (FUSE) {
     if (tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
@@ -417,8 +405,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
       }
     }
   } else if (tid < 8 * ATT_D / 8) {
-    const int h = tid / (ATT_D / 8), c = tid % (ATT_D / 8);
-    *reinterpret_cast<uint4*>(&s_q[h][8 * c]) = h < G ? ldcg16(qrow + h * ATT_D + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4*>(&s_q[tid / (ATT_D / 8)][8 * (tid % (ATT_D / 8))]) = qw;
   }
   __syncthreads();
   uint32_t qb[8][2];
@@ -426,7 +413,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
   for (int st = 0; st < 8; ++st)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const __half lo = s_q[g][Page<KIND>::qdim(st, t4, r, 0)], hi = s_q[g][Page<KIND>::qdim(st, t4, r, 1)];
+      const __half lo = s_q[g][PG::qdim(st, t4, r, 0)], hi = s_q[g][PG::qdim(st, t4, r, 1)];
       qb[st][r] = ((uint32_t)__half_as_ushort(lo) | ((uint32_t)__half_as_ushort(hi) << 16)) ^
                   (a.scale_log2 < 0.f ? 0x80008000u : 0u);
     }
@@ -440,45 +427,44 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
+  bool landed = true;  // no wait for copies has run out
+  int stage = 0;
+  uint32_t parity = 0;
   for (int step = 0; step < steps; ++step) {
     const int v = wv0 + step * NW * BATCH;  // first visible page of this step
+    unsigned char* slot = ring + stage * BATCH * PG::SLOT;
+    const unsigned got = have >> (stage * BATCH);
     // does any of these pages have masked tokens?
     bool masked = false;
 #pragma unroll
     for (int j = 0; j < BATCH; ++j)
-      masked |= cur[j] < 0 || v + j == part_s || v + j == part_w || v + j == part_l;
+      masked |= !((got >> j) & 1u) || v + j == part_s || v + j == part_w || v + j == part_l;
     uint32_t live[BATCH];  // bit r: token r of the page is seen
-    if (masked) {
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
+    for (int j = 0; j < BATCH; ++j) {
+      live[j] = 0xFFFFu;
+      if (masked) {
         live[j] = 0u;
         const int t0 = page_no(v + j) * ATT_PAGE;
-        if (cur[j] >= 0) {
+        if ((got >> j) & 1u) {
           for (int r = 0; r < ATT_PAGE; ++r)
             live[j] |= (t0 + r < L && (t0 + r >= w0 || t0 + r < S) ? 1u : 0u) << r;
         }
       }
     }
-    bool fresh[BATCH];  // fused: the page of the new token
+    landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, ATW_WAIT_POLLS));
+    if (!landed) break;
+    if constexpr (FUSE) {
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (v + j == n - 1 && pos >= 0) PG::patch(slot + j * PG::SLOT, s_new, s_news, pos & 15, lane);
+      __syncwarp();
+    }
     float s[BATCH][4];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      if constexpr (FUSE) {
-        fresh[j] = v + j == n - 1 && pos >= 0;
-        if (fresh[j]) pg[j].patch_k(s_new[0], s_news[0], pos & 15, g, t4);
-      }
       s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      pg[j].scores(qb, s[j]);
-      pg[j].score_scale(s[j]);
-    }
-    const bool more = step + 1 < steps;
-    if (more) {
-      const int i = (step + 1) * BATCH;
-      if ((i & 31) == 0) ids = ids_next;
-      if ((i & 31) == BATCH) ids_next = table((i & ~31) + 32 + lane);
-      fetch_ids(step + 1);
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) pg[j].load_k(lp, max(cur[j], 0));
+      PG::scores(slot + j * PG::SLOT, g, t4, qb, s[j]);
     }
     if (masked) {
 #pragma unroll
@@ -534,28 +520,31 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
     for (int j = 0; j < BATCH; ++j) {
       l0 += s[j][0] + s[j][2];
       l1 += s[j][1] + s[j][3];
-      if constexpr (FUSE) {
-        if (fresh[j]) pg[j].patch_v(s_new[1], s_news[1], pos & 15, g, t4);
-      }
-    }
-    if (masked) {
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) pg[j].mask_v(live[j], g, t4);
     }
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      pg[j].p_scale(s[j]);
+      PG::p_scale(slot + j * PG::SLOT, g, live[j], s[j]);
       const uint32_t b0 = movmatrix_trans(pack_h2(s[j][0], s[j][1])), b1 = movmatrix_trans(pack_h2(s[j][2], s[j][3]));
-      pg[j].output(b0, b1, o);
+      PG::output(slot + j * PG::SLOT, g, t4, masked, live[j], b0, b1, o);
     }
-    if (more) {
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) pg[j].load_v(lp, max(cur[j], 0));
+    __syncwarp();  // every lane has read the stage
+    if (step + STAGES < steps) issue(step + STAGES);
+    if (++stage == STAGES) {
+      stage = 0;
+      parity ^= 1u;
     }
   }
+  if (!landed) {
+    // a wait ran out: report it, and give the copies still in flight their
+    // time before the ring's memory changes hands
+    if (lane == 0 && a.err_flag) atomicOr(a.err_flag, 2);
+    for (int st = 0; st < STAGES; ++st) mbar_wait_bounded(&bar[st], parity ^ (st < stage ? 1u : 0u), ATW_WAIT_POLLS >> 4);
+  }
+  __syncthreads();  // the rings become the merge's buffer
   W4_TRACE_MARK(1);
 
   // ---- the warps' states, merged in shared memory ------------------------------------
+  float* s_o = reinterpret_cast<float*>(smraw);  // [warp][head][128 + 4], dims in the order (mt, g, e)
 #pragma unroll
   for (int d = 4; d < 32; d <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, d);
@@ -579,12 +568,13 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
   auto write_out = [&](int h, int i4, float4 acc) {  // positions 4 i4 .. 4 i4 + 3 of the order (mt, g, e)
     const int mt = i4 >> 2, g0 = 2 * (i4 & 3);
     __half* out = a.out + (qh0 + h) * ATT_D;
-    *reinterpret_cast<__half2*>(out + Page<KIND>::odim(mt, g0)) = __floats2half2_rn(acc.x, acc.y);
-    *reinterpret_cast<__half2*>(out + Page<KIND>::odim(mt, g0 + 1)) = __floats2half2_rn(acc.z, acc.w);
+    *reinterpret_cast<__half2*>(out + PG::odim(mt, g0)) = __floats2half2_rn(acc.x, acc.y);
+    *reinterpret_cast<__half2*>(out + PG::odim(mt, g0 + 1)) = __floats2half2_rn(acc.z, acc.w);
   };
+  static_assert(8 * 32 <= NW * 32, "a thread per (head, four dims)");
+  const int h = tid >> 5, i4 = lane;
   const bool single = active == 1;
-  for (int idx = tid; idx < G * 32; idx += NW * 32) {
-    const int h = idx >> 5, i4 = idx & 31;
+  if (h < G) {
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[(w * 8 + h) * 2]);
@@ -593,7 +583,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float mw = s_ml[(w * 8 + h) * 2], lw = s_ml[(w * 8 + h) * 2 + 1];
-      const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : exp2f(mw - M);
+      const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : ex2(mw - M);
       const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + h) * ATW_PITCH + 4 * i4);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
@@ -605,59 +595,80 @@ __global__ void __launch_bounds__(ATW_NW * 32, KIND == ATW_F16 ? 1 : 2) w4pg_att
       const float inv = den == 0.f ? 0.f : atw_o_factor<KIND>() / den;
       write_out(h, i4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     } else {
-      *reinterpret_cast<float4*>(a.ws_o + ((qh0 + h) * a.PC + pc) * ATT_D + 4 * i4) = acc;
-      if (i4 == 0) *reinterpret_cast<float2*>(a.ws_ml + ((qh0 + h) * a.PC + pc) * 2) = make_float2(M, den);
+      __stcg(reinterpret_cast<float4*>(a.ws_o + ((qh0 + h) * a.PC + pc) * ATT_D + 4 * i4), acc);
+      if (i4 == 0) __stcg(reinterpret_cast<float2*>(a.ws_ml + ((qh0 + h) * a.PC + pc) * 2), make_float2(M, den));
     }
   }
   if (single) return;
+  W4_TRACE_MARK(2);
 
   // ---- the CTAs' partials: the last to finish adds them up, in order ----------------
-  __threadfence();
   __syncthreads();
-  if (tid == 0) s_last = atomicAdd(&a.counters[(size_t)b * a.Hkv + kvh], 1u) == (unsigned)(active - 1);
+  if (tid == 0) {
+    __threadfence();  // the CTA's partial (ordered before by the barrier) before its ticket
+    s_last = atomicAdd(&a.counters[(size_t)b * a.Hkv + kvh], 1u) == (unsigned)(active - 1);
+    __threadfence();
+  }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
-  for (int idx = tid; idx < G * 32; idx += NW * 32) {
-    const int h = idx >> 5, i4 = idx & 31;
-    const float2* ml = reinterpret_cast<const float2*>(a.ws_ml + (qh0 + h) * a.PC * 2);
+  // one round trip for the first partials and all (max, sum) pairs
+  constexpr int FLIGHT = 16;
+  float4 pv[FLIGHT];
+  const float4* src = reinterpret_cast<const float4*>(a.ws_o + (qh0 + min(h, G - 1)) * a.PC * ATT_D) + i4;
+#pragma unroll
+  for (int j = 0; j < FLIGHT; ++j)
+    if (j < active) pv[j] = __ldcg(src + (size_t)j * (ATT_D / 4));
+  for (int idx = tid; idx < G * active; idx += NW * 32) {
+    const int hh = idx / active, j = idx - hh * active;
+    s_part[hh * ATW_MAX_PARTITIONS + j] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + (qh0 + hh) * a.PC + j);
+  }
+  __syncthreads();
+  if (h < G) {
+    const float2* ml = s_part + h * ATW_MAX_PARTITIONS;
     float M = -INFINITY;
-    for (int j = 0; j < active; ++j) M = fmaxf(M, __ldcg(ml + j).x);
+    for (int j = 0; j < active; ++j) M = fmaxf(M, ml[j].x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float den = 0.f;
-    const float4* src = reinterpret_cast<const float4*>(a.ws_o + (qh0 + h) * a.PC * ATT_D) + i4;
-#pragma unroll 4
-    for (int j = 0; j < active; ++j) {
-      const float2 e = __ldcg(ml + j);
-      const float f = e.x == -INFINITY ? (e.y == 0.f ? 0.f : 1.f) : exp2f(e.x - M);
-      const float4 v = __ldcg(src + (size_t)j * (ATT_D / 4));
+    auto add = [&](int j, float4 v) {
+      const float2 e = ml[j];
+      const float f = e.x == -INFINITY ? (e.y == 0.f ? 0.f : 1.f) : ex2(e.x - M);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
       acc.z = fmaf(v.z, f, acc.z);
       acc.w = fmaf(v.w, f, acc.w);
       den = fmaf(e.y, f, den);
-    }
+    };
+#pragma unroll
+    for (int j = 0; j < FLIGHT; ++j)
+      if (j < active) add(j, pv[j]);
+#pragma unroll 8
+    for (int j = FLIGHT; j < active; ++j) add(j, __ldcg(src + (size_t)j * (ATT_D / 4)));
     const float inv = den == 0.f ? 0.f : atw_o_factor<KIND>() / den;
     write_out(h, i4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   }
   if (tid == 0) a.counters[(size_t)b * a.Hkv + kvh] = 0u;  // ready for the next call
 }
 
-// CTAs per (sequence, kv head): enough for two per SM over the batch, no more
-// than the visible pages can feed with a step for every warp.
-int atw_partitions(int B, int Hkv, int max_context, int window, int sinks) {
+// CTAs per (sequence, kv head): enough for what fits the SMs at once over the
+// batch, no more than the visible pages can feed with a page for every warp.
+int atw_partitions(int kind, int B, int Hkv, int max_context, int window, int sinks) {
   const long long all = ((long long)max_context + ATT_PAGE - 1) / ATT_PAGE;
   const long long seen = ((long long)std::min(sinks, max_context) + ATT_PAGE - 1) / ATT_PAGE +
                          ((long long)window + ATT_PAGE - 2) / ATT_PAGE + 1;
   const long long n = std::min(all, seen);
-  const long long want = (2ll * ATW_SMS + (long long)B * Hkv - 1) / ((long long)B * Hkv);
+  const long long ctas = kind == ATW_F16 ? ATW_SMS : 2ll * ATW_SMS;  // (fp16 pages: one CTA's rings fill an SM)
+  const long long want = (ctas + (long long)B * Hkv - 1) / ((long long)B * Hkv);
   const long long most = (n + ATW_NW - 1) / ATW_NW;
   return (int)std::max(1ll, std::min(std::min(want, most), (long long)ATW_MAX_PARTITIONS));
 }
 
 template <int KIND, bool FUSE>
 static int launch_atw(const AtwArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_pdl(w4pg_attn_window<KIND, FUSE>, dim3(a.PC, a.Hkv, a.B), dim3(ATW_NW * 32), 0, s, a);
+  static PerDeviceOnce once;
+  constexpr size_t smem = atw_smem<KIND>();
+  auto kern = w4pg_attn_window<KIND, FUSE>;
+  once_per_device(once, [&] { cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
+  cudaError_t e = launch_pdl(kern, dim3(a.PC, a.Hkv, a.B), dim3(ATW_NW * 32), smem, s, a);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }
@@ -695,7 +706,7 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
   W4_CHECK_ALIGN(a.k, 128, "k_pool");
   W4_CHECK_ALIGN(a.v, 128, "v_pool");
   W4_CHECK_ALIGN(out, 128, "out");
-  a.PC = atw_partitions(B, Hkv, max_context, window, sinks);
+  a.PC = atw_partitions(a.kind, B, Hkv, max_context, window, sinks);
   if (a.PC > 1) {
     const size_t need = attention_workspace_bytes(B, Hq, Hkv, a.PC);
     W4_CHECK_ARG(workspace != nullptr && workspace_bytes >= need, "%s: workspace of %zu bytes needed", who, need);
@@ -726,7 +737,7 @@ extern "C" size_t paged_gqa_decode_window_workspace_size(int B, int Hq, int Hkv,
                                                          int sinks, int D) {
   (void)D;
   if (B < 1 || Hq < 1 || Hkv < 1 || max_context < 1 || window < 0 || sinks < 0) return 0;
-  return attention_workspace_bytes(B, Hq, Hkv, atw_partitions(B, Hkv, max_context, window, sinks));
+  return attention_workspace_bytes(B, Hq, Hkv, atw_partitions(ATW_I4, B, Hkv, max_context, window, sinks));
 }
 
 extern "C" int paged_gqa_decode_window(const uint16_t* q, int q_stride, const uint16_t* k_pool, const uint16_t* v_pool,

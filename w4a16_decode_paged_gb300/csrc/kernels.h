@@ -173,7 +173,7 @@ struct AtwArgs {
   int tag;
 };
 int launch_attn_window(const AtwArgs& a, cudaStream_t s);
-int atw_partitions(int B, int Hkv, int max_context, int window, int sinks);
+int atw_partitions(int kind, int B, int Hkv, int max_context, int window, int sinks);
 inline void atw_workspace(AtwArgs& a, void* ws, int B, int Hq) {  // a.PC set
   AttnArgs t = {};
   attention_workspace_layout(t, ws, B, Hq, a.PC);
