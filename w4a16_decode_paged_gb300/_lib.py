@@ -8,6 +8,7 @@ calls raise instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -147,6 +148,29 @@ def load() -> ctypes.CDLL:
                 lib.w4a16_trace_count.argtypes = []
             _lib = lib
     return _lib
+
+
+_native = None
+_NATIVE_ENTRIES = ("kv_append_rope_int4", "kv_read_int4", "paged_gqa_decode_int4", "paged_gqa_decode_rope_append_int4",
+                   "paged_gqa_decode_window", "paged_gqa_decode_window_fp8", "paged_gqa_decode_window_int4")
+
+
+def native():
+    """The native argument marshalling (csrc/torch_args.cpp) bound to the
+    library's entries; raises if it has not been built."""
+    global _native
+    if _native is None:
+        lib = load()
+        if not os.path.exists(_build.ARGS_LIB):
+            raise RuntimeError(f"{_build.ARGS_LIB} is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        import torch  # noqa: F401  (its libraries have to be in the process first)
+        spec = importlib.util.spec_from_file_location("_w4a16_torch", _build.ARGS_LIB)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_ENTRIES))
+        _native = mod
+    return _native
 
 
 def check(rc: int) -> None:

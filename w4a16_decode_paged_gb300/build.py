@@ -3,16 +3,21 @@
 Each .cu file under csrc/ is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into one shared
 library with a plain C ABI (include/w4a16.h).  The output goes to
-``w4a16_decode_paged_gb300/_build/``.
+``w4a16_decode_paged_gb300/_build/``.  Beside it goes _w4a16_torch.so, the
+argument marshalling of the short calls (csrc/torch_args.cpp, g++ against
+torch's headers; it holds no kernel and is given the library's entries by
+address).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +29,10 @@ LIB = os.path.join(BUILD, "libw4a16_gb300.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
+
+
+ARGS_SRC = os.path.join(CSRC, "torch_args.cpp")
+ARGS_LIB = os.path.join(BUILD, "_w4a16_torch.so")
 
 
 def nvcc() -> str:
@@ -65,6 +74,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str
     lib = out or LIB
     bdir = os.path.dirname(lib)
     if not force and os.path.exists(lib) and all(os.path.getmtime(p) <= os.path.getmtime(lib) for p in _deps()):
+        if lib == LIB:
+            build_args()
         return lib
     os.makedirs(bdir, exist_ok=True)
     cc = nvcc()
@@ -81,8 +92,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(10, len(srcs) + 1)) as ex:
+        args = ex.submit(build_args, force) if lib == LIB else None
         objs = list(ex.map(compile_one, srcs))
+        if args is not None:
+            args.result()
     tmp = lib + f".tmp{os.getpid()}"
     rdc = ["-rdc=true"] if "-rdc=true" in flags else []
     cmd = [cc, *ARCH, *rdc, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
@@ -91,6 +105,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
     return lib
+
+
+def build_args(force: bool = False) -> str:
+    """The native argument marshalling (a CPython module, host code only)."""
+    deps = [ARGS_SRC, os.path.join(INCLUDE, "w4a16.h")]
+    if not force and os.path.exists(ARGS_LIB) and all(os.path.getmtime(p) <= os.path.getmtime(ARGS_LIB) for p in deps):
+        return ARGS_LIB
+    os.makedirs(BUILD, exist_ok=True)
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include")]
+    lib = os.path.join(torch_dir, "lib")
+    tmp = ARGS_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", ARGS_SRC, "-o", tmp,
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], *[x for p in inc for x in ("-isystem", p)],
+           "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {ARGS_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ARGS_LIB)
+    return ARGS_LIB
 
 
 if __name__ == "__main__":
