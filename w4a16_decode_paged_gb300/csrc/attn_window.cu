@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   extern __shared__ __align__(128) unsigned char smraw[];  // the warps' rings, then their merge
   __shared__ __align__(16) __half s_q[8][ATT_D + 8];
   __shared__ float s_ml[NW * 8 * 2];
-  __shared__ float s_cos[FUSE ? ATT_D / 2 : 1], s_sin[FUSE ? ATT_D / 2 : 1];
+  __shared__ __align__(16) float s_cos[FUSE ? ATT_D / 2 : 4], s_sin[FUSE ? ATT_D / 2 : 4];
   __shared__ __align__(16) uint16_t s_new[2][32];  // codes of the new K and V rows (fused)
   __shared__ uint8_t s_news[2][4];
   __shared__ __align__(8) uint64_t s_bar[NW * STAGES];
@@ -378,30 +378,31 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   if (FUSE) {
     if (tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
     __syncthreads();
-    // a warp per query head; the CTA of the last page also takes the new K and V rows
+    // two rows per warp: eight query heads (those from G on are zero), and in
+    // the CTA of the last page the new K and V rows
     const bool last = pc == active - 1;
-    for (int r = warp; r < 8 + (last ? 2 : 0); r += NW) {
-      uint2 x = make_uint2(0u, 0u);
+    const int r = 2 * warp + (lane >> 4), c = lane & 15;
+    if (warp < (last ? 5 : 4)) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
       const __half* src = r < 8 ? qrow + r * ATT_D
                                 : a.q + (size_t)b * a.q_stride + (size_t)(a.Hq + (r - 8) * a.Hkv + kvh) * ATT_D;
-      if (r < G || r >= 8) x = __ldcg(reinterpret_cast<const uint2*>(src) + lane);
-      if (r != 9) rope_row4(x.x, x.y, s_cos, s_sin, lane);
+      if (r < G || r >= 8) x = ldcg16(src + 8 * c);
+      uint4 w = x;
+      rope_rows(w, s_cos, s_sin, lane);
       if (r < 8) {
-        *reinterpret_cast<uint2*>(&s_q[r][4 * lane]) = x;
+        *reinterpret_cast<uint4*>(&s_q[r][8 * c]) = w;
       } else {
+        const bool is_k = r == 8;
+        if (!is_k) w = x;
         uint32_t codes, byte;
-        kv4_quantise(x.x, x.y, codes, byte);
-        s_new[r - 8][lane] = (uint16_t)codes;
-        if ((lane & 7) == 0) s_news[r - 8][lane >> 3] = (uint8_t)byte;
-        const int blk = max(pos, 0) / ATT_PAGE, slot = max(pos, 0) % ATT_PAGE;
+        kv4_quantise(w, codes, byte);
+        *reinterpret_cast<uint32_t*>(&s_new[r - 8][2 * c]) = codes;
+        if ((c & 3) == 0) s_news[r - 8][c >> 2] = (uint8_t)byte;
+        const int blk = max(pos, 0) / ATT_PAGE;
         const int id = pos >= 0 && blk < a.max_blocks ? __ldcg(&bt[blk]) : -1;
-        if (id >= 0 && id < a.num_pages) {
-          uint8_t* sl = static_cast<uint8_t*>(const_cast<void*>(r == 8 ? a.k : a.v)) +
-                        ((size_t)id * a.Hkv + kvh) * KV4_SLICE;
-          *reinterpret_cast<uint16_t*>(sl + (r == 8 ? kv4_k_code(slot, lane) : kv4_v_code(slot, lane))) = (uint16_t)codes;
-          if ((lane & 7) == 0)
-            sl[r == 8 ? kv4_k_scale(slot, lane >> 3) : kv4_v_scale(slot, lane >> 3)] = (uint8_t)byte;
-        }
+        if (id >= 0 && id < a.num_pages)
+          kv4_put(static_cast<uint8_t*>(const_cast<void*>(is_k ? a.k : a.v)) + ((size_t)id * a.Hkv + kvh) * KV4_SLICE,
+                  is_k, pos % ATT_PAGE, c, codes, byte);
       }
     }
   } else if (tid < 8 * ATT_D / 8) {

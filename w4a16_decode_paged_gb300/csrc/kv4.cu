@@ -6,45 +6,67 @@
 namespace w4 {
 
 // ---------------------------------------------------------------------------
-// RoPE + INT4 append: one CTA per row.
+// RoPE + INT4 append: one CTA per row (of the batch or the prompt).  Its head
+// rows -- q (rotated), k (rotated, quantised), v (quantised) -- are taken two
+// at a time by a warp, eight dims per lane.  The values do not depend on the
+// position, so they are asked for before the length and the table entry are
+// read and the sines computed.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256) w4pg_rope_append_int4(const __grid_constant__ Kv4AppendArgs a) {
-  __shared__ float s_cos[KV4_D / 2], s_sin[KV4_D / 2];
+constexpr int APPEND_WARPS = 8;
+constexpr int APPEND_AHEAD = 3;  // row pairs a warp loads ahead (3 x 16 rows: 28 + 2 x 4 heads in one go)
+
+__global__ void __launch_bounds__(APPEND_WARPS * 32) w4pg_rope_append_int4(const __grid_constant__ Kv4AppendArgs a) {
+  __shared__ __align__(16) float s_cos[KV4_D / 2], s_sin[KV4_D / 2];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = lane & 15, half = lane >> 4;
+  const int rows = a.Hq + 2 * a.Hkv;
+  const __half* qb = a.q + (size_t)b * a.stride_q;
+  const __half* kb = a.k + (size_t)b * a.stride_kv;
+  const __half* vb = a.v + (size_t)b * a.stride_kv;
+  auto load = [&](int r) -> uint4 {
+    if (r >= rows) return make_uint4(0u, 0u, 0u, 0u);
+    const __half* src = r < a.Hq ? qb + (size_t)r * KV4_D
+                                 : (r < a.Hq + a.Hkv ? kb + (size_t)(r - a.Hq) * KV4_D
+                                                     : vb + (size_t)(r - a.Hq - a.Hkv) * KV4_D);
+    return __ldcg(reinterpret_cast<const uint4*>(src) + c);
+  };
   pdl_wait_then_trigger();
+  uint4 x[APPEND_AHEAD];
+#pragma unroll
+  for (int u = 0; u < APPEND_AHEAD; ++u) x[u] = load(2 * (warp + u * APPEND_WARPS) + half);
   const int pos = __ldcg(&a.context_lens[b]) - 1;
   if (pos < 0) return;
-  if (tid < KV4_D / 2) sincosf(__fmul_rn((float)pos, a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
   const int blk = pos / KV4_PAGE, slot = pos % KV4_PAGE;
   const int page = blk < a.max_blocks ? __ldcg(&a.block_table[(size_t)b * a.max_blocks + blk]) : -1;
+  if (tid < KV4_D / 2) sincosf(__fmul_rn((float)pos, a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
   const bool ok = page >= 0 && page < a.num_pages;
   if (!ok && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
   __syncthreads();
-  // rows: q heads (rotated), k heads (rotated, quantised), v heads (quantised),
-  // one warp each, four dims per lane
-  const int rows = a.Hq + 2 * a.Hkv;
-  for (int r = warp; r < rows; r += 8) {
-    const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
-    if (!is_q && !ok) break;
-    const int h = is_q ? r : (is_k ? r - a.Hq : r - a.Hq - a.Hkv);
-    const __half* src = is_q ? a.q + (size_t)b * a.stride_q : (is_k ? a.k : a.v) + (size_t)b * a.stride_kv;
-    uint2 x = *reinterpret_cast<const uint2*>(src + (size_t)h * KV4_D + 4 * lane);
-    if (is_q || is_k) rope_row4(x.x, x.y, s_cos, s_sin, lane);
-    if (is_q) {
-      *reinterpret_cast<uint2*>(a.q_out + (size_t)b * a.stride_qo + (size_t)h * KV4_D + 4 * lane) = x;
-      continue;
+  for (int r0 = 2 * warp; r0 < rows; r0 += 2 * APPEND_WARPS * APPEND_AHEAD) {
+#pragma unroll
+    for (int u = 0; u < APPEND_AHEAD; ++u) {
+      const int r = r0 + 2 * u * APPEND_WARPS + half;
+      if (r - half >= rows) break;
+      const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
+      const uint4 raw = x[u];
+      uint4 w = raw;
+      rope_rows(w, s_cos, s_sin, lane);
+      if (!is_q && !is_k) w = raw;  // (the two rows of a warp may be of different kinds)
+      uint32_t codes, byte;
+      if (r - half + 1 >= a.Hq) kv4_quantise(w, codes, byte);
+      if (is_q) {
+        *reinterpret_cast<uint4*>(a.q_out + (size_t)b * a.stride_qo + (size_t)r * KV4_D + 8 * c) = w;
+      } else if (ok && r < rows) {
+        const int h = is_k ? r - a.Hq : r - a.Hq - a.Hkv;
+        kv4_put((is_k ? a.k_pool : a.v_pool) + ((size_t)page * a.Hkv + h) * KV4_SLICE, is_k, slot, c, codes, byte);
+      }
+      x[u] = load(r + 2 * APPEND_WARPS * APPEND_AHEAD);
     }
-    uint32_t codes, byte;
-    kv4_quantise(x.x, x.y, codes, byte);
-    uint8_t* sl = (is_k ? a.k_pool : a.v_pool) + ((size_t)page * a.Hkv + h) * KV4_SLICE;
-    *reinterpret_cast<uint16_t*>(sl + (is_k ? kv4_k_code(slot, lane) : kv4_v_code(slot, lane))) = (uint16_t)codes;
-    if ((lane & 7) == 0)
-      sl[is_k ? kv4_k_scale(slot, lane >> 3) : kv4_v_scale(slot, lane >> 3)] = (uint8_t)byte;
   }
 }
 
 int launch_rope_append_int4(const Kv4AppendArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_pdl(w4pg_rope_append_int4, dim3(a.B), dim3(256), 0, s, a);
+  cudaError_t e = launch_pdl(w4pg_rope_append_int4, dim3(a.B), dim3(APPEND_WARPS * 32), 0, s, a);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "int4 rope/append launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }
@@ -62,17 +84,15 @@ struct Kv4ReadArgs {
   int clear;  // rows that hold no token become zero
 };
 
-// eight dims of one token (two code halfwords) times their scale, as 16 bytes
-__device__ __forceinline__ uint4 kv4_eight(uint32_t lo4, uint32_t hi4, float s) {
-  uint32_t w[4];
+// a word of codes times its scale(s): the pairs (n, n + 4) of its nibbles as
+// fp16 values.  two: the fp16 bits of the low and the high half's scale.
+__device__ __forceinline__ void kv4_values(uint32_t word, const Kv4Scale& k, uint32_t (&x)[4]) {
+  kv4_unpack(word, k, x);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = ((i < 2 ? lo4 : hi4) >> (8 * (i & 1))) & 0xFFu;
-    const __half2 h = __floats2half2_rn(((int)(c & 15u) - 8) * s, ((int)(c >> 4) - 8) * s);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) x[i] = hmul2_u(x[i], 0x54005400u);  // 64: the unpacking's scales are s / 64
 }
+__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
 __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv4ReadArgs a) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
@@ -110,16 +130,24 @@ __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv
   };
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int t = 2 * i + half;  // K: two tokens per step
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(ks + kv4_k_code(t, 2 * c));
-    put(a.k_out, t, kv4_eight(w & 0xFFFFu, w >> 16, kv4_scale_value(ks[kv4_k_scale(t, c >> 2)])));
+    const int t = 2 * i + half;  // K: two tokens per step, a word of eight dims per lane
+    const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(ks + kv4_k_code(t, 2 * c)));
+    const uint32_t s = __ldcg(ks + kv4_k_scale(t, c >> 2));
+    uint32_t x[4];
+    kv4_values(w, kv4_scale_pair(s * 0x00800080u), x);
+    put(a.k_out, t, make_uint4(lows(x[0], x[1]), lows(x[2], x[3]), highs(x[0], x[1]), highs(x[2], x[3])));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = 4 * i + 2 * half;  // V: two token pairs per step
-    const uint2 w = *reinterpret_cast<const uint2*>(vs + kv4_v_code(t, 2 * c));
-    put(a.v_out, t, kv4_eight(w.x & 0xFFFFu, w.y & 0xFFFFu, kv4_scale_value(vs[kv4_v_scale(t, c >> 2)])));
-    put(a.v_out, t + 1, kv4_eight(w.x >> 16, w.y >> 16, kv4_scale_value(vs[kv4_v_scale(t + 1, c >> 2)])));
+    const int t = 4 * i + 2 * half;  // V: two token pairs per step, two words of four dims of both tokens
+    const uint2 w = __ldcg(reinterpret_cast<const uint2*>(vs + kv4_v_code(t, 2 * c)));
+    const uint32_t s = __ldcg(reinterpret_cast<const unsigned short*>(vs + kv4_v_scale(t, c >> 2)));
+    const Kv4Scale k = kv4_scale_pair(((s & 0xFFu) << 7) | ((s >> 8) << 23));
+    uint32_t x[4], y[4];
+    kv4_values(w.x, k, x);
+    kv4_values(w.y, k, y);
+    put(a.v_out, t, make_uint4(lows(x[0], x[1]), lows(x[2], x[3]), lows(y[0], y[1]), lows(y[2], y[3])));
+    put(a.v_out, t + 1, make_uint4(highs(x[0], x[1]), highs(x[2], x[3]), highs(y[0], y[1]), highs(y[2], y[3])));
   }
 }
 

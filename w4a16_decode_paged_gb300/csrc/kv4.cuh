@@ -56,50 +56,69 @@ __device__ __forceinline__ float kv4_scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
 
-// One row of 128 fp16 values, four per lane (dims 4 lane .. 4 lane + 3, two
-// packed halves each in x0, x1) -> this lane's four codes and the scale byte
-// of its group of eight lanes.  Warp-wide.
-__device__ __forceinline__ void kv4_quantise(uint32_t x0, uint32_t x1, uint32_t& codes, uint32_t& byte) {
+// Rows of 128 fp16 values, eight per lane (dims 8 c .. 8 c + 7 of lane c of a
+// half-warp, packed in x) -> this lane's eight codes, lowest nibble first, and
+// the scale byte of its group of four lanes.  Warp-wide: two rows at once.
+__device__ __forceinline__ void kv4_quantise(const uint4& x, uint32_t& codes, uint32_t& byte) {
   // magnitudes compare as integers, NaN and infinity above every number
-  const uint32_t a0 = x0 & 0x7FFF7FFFu, a1 = x1 & 0x7FFF7FFFu;
-  uint32_t m = max(max(a0 & 0xFFFFu, a0 >> 16), max(a1 & 0xFFFFu, a1 >> 16));
+  uint32_t m = 0u;
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, (&x.x)[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   byte = kv4_scale_byte(m);
   const float s = kv4_scale_value(byte);
   const bool live = byte != 0u && byte != 0xFFu;
   codes = 0u;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t h = ((e < 2 ? x0 : x1) >> (16 * (e & 1))) & 0xFFFFu;
-    const float x = __half2float(__ushort_as_half((unsigned short)h));
-    const int q = live ? __float2int_rn(__fdiv_rn(x, s)) : 0;
+  for (int e = 0; e < 8; ++e) {
+    const float v = __half2float(__ushort_as_half((unsigned short)((&x.x)[e >> 1] >> (16 * (e & 1)))));
+    const int q = live ? __float2int_rn(__fdiv_rn(v, s)) : 0;
     codes |= (uint32_t)(q + 8) << (4 * e);
   }
 }
 
-// Rotate-half RoPE of a row held four dims per lane (as above): the partner
-// dim i +- 64 sits 16 lanes away.  cs, sn: 64 cosines and sines.  Products and
-// their sum are rounded one by one, so every caller gets the same bits.
+// This lane's codes and (first lane of a group) scale into token t of a slice.
+__device__ __forceinline__ void kv4_put(uint8_t* slice, bool is_k, int t, int c, uint32_t codes, uint32_t byte) {
+  if (is_k) {
+    *reinterpret_cast<uint32_t*>(slice + kv4_k_code(t, 2 * c)) = codes;
+  } else {
+    *reinterpret_cast<uint16_t*>(slice + kv4_v_code(t, 2 * c)) = (uint16_t)codes;
+    *reinterpret_cast<uint16_t*>(slice + kv4_v_code(t, 2 * c + 1)) = (uint16_t)(codes >> 16);
+  }
+  if ((c & 3) == 0) slice[is_k ? kv4_k_scale(t, c >> 2) : kv4_v_scale(t, c >> 2)] = (uint8_t)byte;
+}
+
+// Rotate-half RoPE of rows held eight dims per lane (as above): the partner
+// dims i +- 64 sit eight lanes away.  cs, sn: 64 cosines and sines.  Products
+// and their sum are rounded one by one, so every caller gets the same bits.
 __device__ __forceinline__ float rope_lo(float x0, float x1, float c, float s) {
   return __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
 }
 __device__ __forceinline__ float rope_hi(float x0, float x1, float c, float s) {
   return __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
 }
-__device__ __forceinline__ void rope_row4(uint32_t& x0, uint32_t& x1, const float* cs, const float* sn, int lane) {
-  const uint32_t y0 = __shfl_xor_sync(0xffffffffu, x0, 16), y1 = __shfl_xor_sync(0xffffffffu, x1, 16);
-  const int i = 4 * (lane & 15);
-  float r[4];
+__device__ __forceinline__ void rope_rows(uint4& x, const float* cs, const float* sn, int lane) {
+  const int i = 8 * (lane & 7);
+  const bool low = (lane & 8) == 0;
+  const float4 c0 = *reinterpret_cast<const float4*>(cs + i), c1 = *reinterpret_cast<const float4*>(cs + i + 4);
+  const float4 s0 = *reinterpret_cast<const float4*>(sn + i), s1 = *reinterpret_cast<const float4*>(sn + i + 4);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float x = __half2float(__ushort_as_half((unsigned short)((e < 2 ? x0 : x1) >> (16 * (e & 1)))));
-    const float y = __half2float(__ushort_as_half((unsigned short)((e < 2 ? y0 : y1) >> (16 * (e & 1)))));
-    r[e] = lane < 16 ? rope_lo(x, y, cs[i + e], sn[i + e]) : rope_hi(y, x, cs[i + e], sn[i + e]);
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, (&x.x)[w], 8);
+    float r[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = 2 * w + e;
+      const float c = k < 4 ? (&c0.x)[k] : (&c1.x)[k - 4], s = k < 4 ? (&s0.x)[k] : (&s1.x)[k - 4];
+      const float own = __half2float(__ushort_as_half((unsigned short)((&x.x)[w] >> (16 * e))));
+      const float other = __half2float(__ushort_as_half((unsigned short)(y >> (16 * e))));
+      r[e] = low ? rope_lo(own, other, c, s) : rope_hi(other, own, c, s);
+    }
+    const __half2 h = __floats2half2_rn(r[0], r[1]);
+    (&x.x)[w] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  const __half2 lo = __floats2half2_rn(r[0], r[1]), hi = __floats2half2_rn(r[2], r[3]);
-  x0 = *reinterpret_cast<const uint32_t*>(&lo);
-  x1 = *reinterpret_cast<const uint32_t*>(&hi);
 }
 
 // ---------------------------------------------------------------------------
