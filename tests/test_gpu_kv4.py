@@ -178,6 +178,32 @@ def test_prompt_append_equals_token_by_token(api):
     assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
 
 
+def test_long_prompt_append(api):
+    """More rows than are appended one per CTA, an odd number of them, some of
+    length 0 and one with a page outside the pool: the bytes of smaller calls."""
+    r = np.random.default_rng(11)
+    T, Hq, Hkv = 611, 6, 3
+    bt, pages = _table(r, [T])
+    q, k, v = dev(*(synth.normal_fp16(r, (T, n, D)) for n in (Hq, Hkv, Hkv)))
+    table = np.repeat(bt, T, 0)
+    table[100] = pages
+    lens = np.arange(1, T + 1, dtype=np.int32)
+    lens[[7, 200]] = 0
+    dbt, dl = dev(table, lens)
+    mark = torch.full_like(q, 5.0)
+    pools = [torch.zeros((pages, Hkv, 1088), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q1 = api.kv_append_rope_int4(q, k, v, pools[0], pools[1], dbt, dl, THETA, q_out=mark.clone(), err_flag=err)
+    assert int(err.item()) == 1
+    q2 = mark.clone()
+    for i in range(0, T, 200):
+        j = min(i + 200, T)
+        part = [x[i:j].clone() for x in (q, k, v, dbt, dl)]
+        q2[i:j] = api.kv_append_rope_int4(*part[:3], pools[2], pools[3], part[3], part[4], THETA, q_out=mark[i:j].clone())
+    assert torch.equal(q1, q2) and torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+    assert bool((q1[[7, 200]] == 5.0).all()) and not bool((q1[100] == 5.0).any())
+
+
 # ---- read -----------------------------------------------------------------------
 @pytest.mark.parametrize("Hkv,lens,T,starts", [
     (1, [1], 1, None), (4, [37, 16, 0], 40, None), (2, [100, 31, 250], 19, [3, 16, 240]), (8, [17, 64], 64, [-5, 63]),
@@ -259,6 +285,27 @@ def test_attention(api, G, Hkv, lens):
     want = ref.attend(q, lambda p: ref.unpack(kp[p], "k"), lambda p: ref.unpack(vp[p], "v"), bt, lens, 1 / math.sqrt(D))
     ref.check_attention(to_host(out), want, int(lens.max()), f"G={G}")
     assert np.all(to_host(out)[lens <= 0] == 0)
+
+
+@pytest.mark.parametrize("B,Hkv,lens", [(300, 2, [33, 1, 0, 700]), (2100, 2, [17]), (5, 1, [9000, 10, 10, 10, 8000])])
+def test_attention_shares_a_batch_out(api, B, Hkv, lens):
+    """Batches that take several rounds of the prefix sum over the lengths,
+    that have more pairs than tickets, that are very uneven."""
+    r = np.random.default_rng(600 + B)
+    lens = np.resize(np.asarray(lens, np.int32), B)
+    bt, pages = _table(r, lens)
+    kp, vp = ref.random_pool(r, pages, Hkv), ref.random_pool(r, pages, Hkv)
+    q = synth.normal_fp16(r, (B, 3 * Hkv, D))
+    mc = int(lens.max())
+    out = to_host(api.paged_gqa_decode_int4(*dev(q, kp, vp, bt, lens), max_context=mc))
+    some = list(range(min(B, 8))) + [B // 2, B - 2, B - 1]
+    want = ref.attend(q[some], lambda p: ref.unpack(kp[p], "k"), lambda p: ref.unpack(vp[p], "v"), bt[some], lens[some],
+                      1 / math.sqrt(D))
+    ref.check_attention(out[some], want, mc)
+    # every row alone gives what the batch gave, to the order of the sums
+    for b in (1, B // 2 + 1):
+        alone = to_host(api.paged_gqa_decode_int4(*dev(q[b:b + 1], kp, vp, bt[b:b + 1], lens[b:b + 1]), max_context=mc))
+        assert np.abs(alone[0].astype(np.float64) - out[b].astype(np.float64)).max() <= 2.0 ** -8
 
 
 @pytest.mark.parametrize("spread,qstd", [(2.0 ** -12, 1.0), (600.0, 0.004), (9000.0, 2.0 ** -12)])

@@ -98,7 +98,7 @@ def test_read_refusals(lib, bad, code):
     assert _read(lib, **bad) == code and lib.w4a16_last_error()
 
 
-def _attn(lib, form, q=A, qs=0, kp=A, vp=A, ks=A, vs=A, pages=8, bt=A, mb=64, lens=A, mc=1024, window=100, sinks=4, B=2,
+def _attn(lib, form, q=A, qs=0, kp=A, vp=A, ks=A, vs=A, pages=8, bt=A, mb=4096, lens=A, mc=65536, window=60000, sinks=4, B=2,
           Hq=7, Hkv=1, D=128, theta=1e6, ws=A, wsb=1 << 30, out=A):
     head = (q, qs, kp, vp) + ((ks, vs) if form == "window_fp8" else ()) + (pages, bt, mb, lens, mc)
     head += (window, sinks) if "window" in form else ()
@@ -113,7 +113,7 @@ FORMS = ["int4", "rope_append_int4", "window", "window_fp8", "window_int4"]
 @pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("bad,code", [
     (dict(q=None), 1), (dict(kp=None), 1), (dict(bt=None), 1), (dict(out=None), 1), (dict(B=0), 1), (dict(mc=0), 1),
-    (dict(mc=1025), 3), (dict(D=64), 3), (dict(Hq=9), 3), (dict(Hq=7, Hkv=2), 3), (dict(B=65536), 3), (dict(qs=100), 1),
+    (dict(mc=65537), 3), (dict(D=64), 3), (dict(Hq=9), 3), (dict(Hq=7, Hkv=2), 3), (dict(B=(1 << 24) + 1), 3), (dict(qs=100), 1),
     (dict(qs=4097), 1), (dict(q=MIS), 2), (dict(vp=MIS), 2), (dict(out=MIS), 2), (dict(ws=None), 1),
     (dict(wsb=1000), 1), (dict(ws=MIS), 2)])
 def test_attention_refusals(lib, form, bad, code):

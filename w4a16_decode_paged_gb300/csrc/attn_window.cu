@@ -29,6 +29,7 @@
 // tokens of a visible page take no part whatever their bytes hold: their
 // scores are -inf and their V rows are zeroed.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "attn_core.cuh"
@@ -86,6 +87,7 @@ struct Page<ATW_F16> {
   static constexpr int BATCH = 1;   // pages per step of a warp
   static constexpr int STAGES = 3;  // steps in flight per warp
   static constexpr int MIN_CTAS = 1;
+  static constexpr int MIN_PAGES = 8;
   static constexpr int V = 4096;    // V's offset in a page's slot
   static constexpr int SLOT = 8192;
   // dim of element e (0, 1) of query register r (0, 1) in step st
@@ -138,6 +140,7 @@ struct Page<ATW_F8> {
   static constexpr int BATCH = 1;
   static constexpr int STAGES = 3;
   static constexpr int MIN_CTAS = 2;
+  static constexpr int MIN_PAGES = 16;
   static constexpr int V = 2048, KS = 4096, VS = 4160;
   static constexpr int SLOT = 4224;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
@@ -208,6 +211,7 @@ struct Page<ATW_I4> {
   static constexpr int BATCH = 2;
   static constexpr int STAGES = 3;
   static constexpr int MIN_CTAS = 2;
+  static constexpr int MIN_PAGES = 64;
   static constexpr int V = KV4_SLICE;
   static constexpr int SLOT = 2 * KV4_SLICE;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
@@ -271,6 +275,141 @@ __device__ __forceinline__ constexpr float atw_s_factor() { return KIND == ATW_I
 template <int KIND>
 __device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I4 ? 64.f : (KIND == ATW_F8 ? 1.f / ATW_V8 : 1.f); }
 
+// ---------------------------------------------------------------------------
+// Which pages a CTA takes.  A (sequence, kv head) pair with n visible pages is
+// cut into ceil(n / per) equal parts, one CTA each, where `per` is what the
+// whole batch's pages come to per CTA that fits the GPU at once (at least
+// min_pages: below that a second CTA costs more than it saves).  CTAs are
+// numbered in the order (sequence, kv head, part), so a CTA finds its place by
+// a prefix sum over the sequences' part counts, which follow from the lengths.
+// With equal lengths parts come out whole for a number of CTAs that is a
+// multiple of the pairs (fit); where that leaves more parts than fit at once
+// (slots), lengths are mixed and a pair rounds up by half a part on average.
+// ---------------------------------------------------------------------------
+struct AtwShare {
+  int b, kvh, part, parts;  // b -1: nothing to do
+  int L, w0, S, nsp, wp, n;
+  bool fits;
+};
+
+// the visible pages of a sequence of this length
+__device__ __forceinline__ AtwShare atw_visible(const AtwArgs& a, int len) {
+  AtwShare r;
+  r.fits = len <= a.max_context;
+  r.L = max(min(len, a.max_context), 0);
+  r.w0 = a.window >= r.L ? 0 : r.L - a.window;  // first token of the window
+  r.S = min(a.sinks, r.L);                      // sinks
+  if (r.w0 <= r.S) r.w0 = r.S = 0;              // they meet: everything is seen
+  r.nsp = (r.S + ATT_PAGE - 1) / ATT_PAGE;
+  r.wp = max(r.w0 / ATT_PAGE, r.nsp);           // the window's first page that is not a sink page
+  r.n = r.nsp + (r.w0 < r.L ? max((r.L + ATT_PAGE - 1) / ATT_PAGE - r.wp, 0) : 0);
+  return r;
+}
+
+__device__ __forceinline__ int atw_parts(int n, int per) { return min(max((n + per - 1) / per, 1), ATW_MAX_PARTITIONS); }
+__device__ __forceinline__ int atw_per(long long pages, int fit, int min_pages) {
+  return (int)min(max((pages + fit - 1) / fit, (long long)min_pages), (long long)INT_MAX / 2);
+}
+
+// Up to 32 sequences: every warp works it out for itself.
+__device__ __forceinline__ AtwShare atw_share_warp(const AtwArgs& a, int min_pages) {
+  const int lane = threadIdx.x & 31, cta = blockIdx.x;
+  const int len = lane < a.B ? __ldcg(&a.context_lens[lane]) : 0;
+  const int n = lane < a.B ? atw_visible(a, len).n : 0;
+  const int pages = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+  const long long all = (long long)pages * a.Hkv;
+  int per = atw_per(all, a.fit, min_pages);
+  int p = lane < a.B ? atw_parts(n, per) : 0;
+  if (__reduce_add_sync(0xffffffffu, (unsigned)p) * (unsigned)a.Hkv > (unsigned)a.slots) {
+    per = atw_per(all, a.fit_mixed, min_pages);
+    p = lane < a.B ? atw_parts(n, per) : 0;
+  }
+  int hi = p * a.Hkv;  // inclusive prefix sum
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, hi, d);
+    if (lane >= d) hi += t;
+  }
+  AtwShare r;
+  const unsigned past = __ballot_sync(0xffffffffu, lane < a.B && hi > cta);  // sequences that end behind this CTA
+  if (past == 0u) {
+    r.b = -1;
+    return r;
+  }
+  const int b = __ffs(past) - 1;
+  r = atw_visible(a, __shfl_sync(0xffffffffu, len, b));
+  r.b = b;
+  r.parts = __shfl_sync(0xffffffffu, p, b);
+  const int i = cta - (__shfl_sync(0xffffffffu, hi, b) - r.parts * a.Hkv);
+  r.kvh = i / r.parts;
+  r.part = i - r.kvh * r.parts;
+  return r;
+}
+
+// More: CTA-wide; s: 2 * ATW_NW + 8 ints of shared memory.
+__device__ __noinline__ AtwShare atw_share_cta(const AtwArgs& a, int min_pages, int* s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = blockIdx.x;
+  long long* s64 = reinterpret_cast<long long*>(s);
+  auto sum_over = [&](auto term) {  // of every sequence
+    long long v = 0;
+    for (int i = tid; i < a.B; i += ATW_NW * 32) v += term(atw_visible(a, __ldcg(&a.context_lens[i])).n);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (lane == 0) s64[warp] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < ATW_NW; ++w) v += s64[w];
+    __syncthreads();
+    return v;
+  };
+  const long long all = sum_over([](int n) { return n; }) * a.Hkv;
+  int per = atw_per(all, a.fit, min_pages);
+  if (sum_over([&](int n) { return atw_parts(n, per); }) * a.Hkv > a.slots) per = atw_per(all, a.fit_mixed, min_pages);
+  // the sequence whose CTAs hold this one
+  int base = 0;  // CTAs of the sequences before this round's
+  int* found = s + 2 * ATW_NW;  // b, first CTA of b, parts
+  if (tid == 0) found[0] = -1;
+  for (int i0 = 0; i0 < a.B; i0 += ATW_NW * 32) {
+    const int i = i0 + tid;
+    const int p = i < a.B ? atw_parts(atw_visible(a, __ldcg(&a.context_lens[i])).n, per) : 0;
+    int sum = p * a.Hkv;  // inclusive prefix sum over the threads
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += t;
+    }
+    if (lane == 31) s[warp] = sum;
+    __syncthreads();
+    int before = base, after = base;
+#pragma unroll
+    for (int w = 0; w < ATW_NW; ++w) {
+      if (w < warp) before += s[w];
+      after += s[w];
+    }
+    const int hi = before + sum, lo = hi - p * a.Hkv;
+    if (p > 0 && cta >= lo && cta < hi) {
+      found[0] = i;
+      found[1] = lo;
+      found[2] = p;
+    }
+    __syncthreads();
+    base = after;
+    if (cta < base) break;
+  }
+  AtwShare r;
+  r.b = found[0];
+  if (r.b < 0) return r;
+  const int b = found[0], lo = found[1], p = found[2];
+  r = atw_visible(a, __ldcg(&a.context_lens[b]));
+  r.b = b;
+  r.parts = p;
+  r.kvh = (cta - lo) / p;
+  r.part = (cta - lo) - r.kvh * p;
+  return r;
+}
+
 template <int KIND>
 constexpr size_t atw_ring_bytes() { return (size_t)ATW_NW * Page<KIND>::STAGES * Page<KIND>::BATCH * Page<KIND>::SLOT; }
 constexpr size_t ATW_MERGE_BYTES = (size_t)ATW_NW * 8 * ATW_PITCH * 4;
@@ -291,11 +430,11 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   __shared__ uint8_t s_news[2][4];
   __shared__ __align__(8) uint64_t s_bar[NW * STAGES];
   __shared__ float2 s_part[ATW_MAX_PARTITIONS * 8];
+  __shared__ __align__(8) int s_scan[2 * NW + 8];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const int pc = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
   const int G = a.G;
   uint64_t* bar = s_bar + warp * STAGES;
   if (lane < STAGES) mbar_init(&bar[lane], 1);
@@ -304,28 +443,17 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   pdl_wait_then_trigger();
   W4_TRACE_WAITED();
 
-  // the queries are asked for first: their latency passes under the lengths' and the table's
+  // ---- which (sequence, kv head) and which part of its pages ------------------
+  const AtwShare sh = a.B <= 32 ? atw_share_warp(a, PG::MIN_PAGES) : atw_share_cta(a, PG::MIN_PAGES, s_scan);
+  if (sh.b < 0) return;
+  const int b = sh.b, kvh = sh.kvh, pc = sh.part, active = sh.parts;
+  const int L = sh.L, w0 = sh.w0, S = sh.S, n = sh.n, nsp = sh.nsp, wp = sh.wp;
+  const bool fits = sh.fits;
+  if (!fits && pc == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
   const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
   uint4 qw = make_uint4(0u, 0u, 0u, 0u);
   if (!FUSE && tid < 8 * ATT_D / 8 && tid / (ATT_D / 8) < G) qw = ldcg16(qrow + 8 * tid);
-
-  // ---- the visible pages and this CTA's share -------------------------------
-  int L = __ldcg(&a.context_lens[b]);
-  const bool fits = L <= a.max_context;
-  if (!fits) {
-    if (pc == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
-    L = a.max_context;
-  }
-  L = max(L, 0);
-  int w0 = a.window >= L ? 0 : L - a.window;  // first token of the window
-  int S = min(a.sinks, L);                    // sinks
-  if (w0 <= S) w0 = S = 0;                    // they meet: everything is seen
-  const int nsp = (S + ATT_PAGE - 1) / ATT_PAGE;
-  const int wp = max(w0 / ATT_PAGE, nsp);     // the window's first page that is not a sink page
-  const int n = nsp + (w0 < L ? max((L + ATT_PAGE - 1) / ATT_PAGE - wp, 0) : 0);
-  const int chunk = max((n + a.PC - 1) / a.PC, NW * BATCH);
-  const int active = max((n + chunk - 1) / chunk, 1);
-  if (pc >= active) return;
+  const int chunk = (n + active - 1) / active;
   const int v0 = pc * chunk, v1 = min(n, v0 + chunk);
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
   auto page_no = [&](int v) { return v < nsp ? v : v - nsp + wp; };
@@ -345,28 +473,31 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     return id;
   };
   // 32 page ids at a time, one per lane: `ids` holds those of the steps being
-  // copied (pages 32 c .. of the list), ids_next the 32 after
+  // copied (pages 32 c .. of the list), ids_next the 32 after; the lane that
+  // holds an id issues that page's copies
+  static_assert(32 % BATCH == 0, "a step's ids sit in one group of 32");
   int ids = table(lane), ids_next = -1;
+  unsigned ids_ok = __ballot_sync(0xffffffffu, ids >= 0);
   unsigned have = 0;  // bit (stage * BATCH + j): that page was copied
   unsigned char* ring = smraw + (size_t)warp * STAGES * BATCH * PG::SLOT;
   // copies step `st`'s pages into its stage (warp-wide; steps come in order)
-  auto issue = [&](int st) {
-    const int i = st * BATCH, stage = st % STAGES;
-    if (i > 0 && (i & 31) == 0) ids = ids_next;
-    if ((i & 31) == BATCH && st + 1 < steps) ids_next = table((i & ~31) + 32 + lane);
-    unsigned got = 0;
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) got |= (__shfl_sync(0xffffffffu, ids, (i + j) & 31) >= 0 ? 1u : 0u) << j;
+  auto issue = [&](int st, int stage) {
+    const int i = (st * BATCH) & 31;
+    if (i == 0 && st > 0) {
+      ids = ids_next;
+      ids_ok = __ballot_sync(0xffffffffu, ids >= 0);
+    }
+    if (i == BATCH) ids_next = table(st * BATCH - BATCH + 32 + lane);
+    const unsigned got = (ids_ok >> i) & ((1u << BATCH) - 1u);
     have = (have & ~(((1u << BATCH) - 1u) << (stage * BATCH))) | (got << (stage * BATCH));
-    // lane j of the warp's first BATCH lanes copies page j
     if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(got) * PG::SLOT);
     __syncwarp();
-    const int id = __shfl_sync(0xffffffffu, ids, (i + min(lane, BATCH - 1)) & 31);
-    if (lane < BATCH && id >= 0)
-      PG::fetch(a, (size_t)id * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + lane) * PG::SLOT, smem_u32(&bar[stage]));
+    const int j = lane - i;
+    if (j >= 0 && j < BATCH && ids >= 0)
+      PG::fetch(a, (size_t)ids * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, smem_u32(&bar[stage]));
   };
   __syncwarp();
-  for (int st = 0; st < STAGES && st < steps; ++st) issue(st);
+  for (int st = 0; st < STAGES && st < steps; ++st) issue(st, st);
   // pages some of whose tokens are masked: the last of the sinks, the first of
   // the window, the last of the sequence (-1: none)
   const int part_s = S % ATT_PAGE ? nsp - 1 : -1;
@@ -380,7 +511,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     __syncthreads();
     // two rows per warp: eight query heads (those from G on are zero), and in
     // the CTA of the last page the new K and V rows
-    const bool last = pc == active - 1;
+    const bool last = v0 < n && v1 == n;
     const int r = 2 * warp + (lane >> 4), c = lane & 15;
     if (warp < (last ? 5 : 4)) {
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -529,7 +660,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
       PG::output(slot + j * PG::SLOT, g, t4, masked, live[j], b0, b1, o);
     }
     __syncwarp();  // every lane has read the stage
-    if (step + STAGES < steps) issue(step + STAGES);
+    if (step + STAGES < steps) issue(step + STAGES, stage);
     if (++stage == STAGES) {
       stage = 0;
       parity ^= 1u;
@@ -596,8 +727,8 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
       const float inv = den == 0.f ? 0.f : atw_o_factor<KIND>() / den;
       write_out(h, i4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     } else {
-      __stcg(reinterpret_cast<float4*>(a.ws_o + ((qh0 + h) * a.PC + pc) * ATT_D + 4 * i4), acc);
-      if (i4 == 0) __stcg(reinterpret_cast<float2*>(a.ws_ml + ((qh0 + h) * a.PC + pc) * 2), make_float2(M, den));
+      __stcg(reinterpret_cast<float4*>(a.ws_o + ((size_t)blockIdx.x * G + h) * ATT_D + 4 * i4), acc);
+      if (i4 == 0) __stcg(reinterpret_cast<float2*>(a.ws_ml + ((size_t)blockIdx.x * G + h) * 2), make_float2(M, den));
     }
   }
   if (single) return;
@@ -607,7 +738,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   __syncthreads();
   if (tid == 0) {
     __threadfence();  // the CTA's partial (ordered before by the barrier) before its ticket
-    s_last = atomicAdd(&a.counters[(size_t)b * a.Hkv + kvh], 1u) == (unsigned)(active - 1);
+    s_last = atomicAdd(&a.counters[b * a.Hkv + kvh], 1u) == (unsigned)(active - 1);
     __threadfence();
   }
   __syncthreads();
@@ -615,13 +746,15 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   // one round trip for the first partials and all (max, sum) pairs
   constexpr int FLIGHT = 16;
   float4 pv[FLIGHT];
-  const float4* src = reinterpret_cast<const float4*>(a.ws_o + (qh0 + min(h, G - 1)) * a.PC * ATT_D) + i4;
+  const size_t first = blockIdx.x - pc;  // the parts are consecutive CTAs
+  const float4* src = reinterpret_cast<const float4*>(a.ws_o + (first * G + min(h, G - 1)) * ATT_D) + i4;
+  const size_t pitch = (size_t)G * (ATT_D / 4);
 #pragma unroll
   for (int j = 0; j < FLIGHT; ++j)
-    if (j < active) pv[j] = __ldcg(src + (size_t)j * (ATT_D / 4));
+    if (j < active) pv[j] = __ldcg(src + (size_t)j * pitch);
   for (int idx = tid; idx < G * active; idx += NW * 32) {
-    const int hh = idx / active, j = idx - hh * active;
-    s_part[hh * ATW_MAX_PARTITIONS + j] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + (qh0 + hh) * a.PC + j);
+    const int j = idx / G, hh = idx - j * G;
+    s_part[hh * ATW_MAX_PARTITIONS + j] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + first * G + idx);
   }
   __syncthreads();
   if (h < G) {
@@ -643,24 +776,33 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     for (int j = 0; j < FLIGHT; ++j)
       if (j < active) add(j, pv[j]);
 #pragma unroll 8
-    for (int j = FLIGHT; j < active; ++j) add(j, __ldcg(src + (size_t)j * (ATT_D / 4)));
+    for (int j = FLIGHT; j < active; ++j) add(j, __ldcg(src + (size_t)j * pitch));
     const float inv = den == 0.f ? 0.f : atw_o_factor<KIND>() / den;
     write_out(h, i4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   }
-  if (tid == 0) a.counters[(size_t)b * a.Hkv + kvh] = 0u;  // ready for the next call
+  if (tid == 0) a.counters[b * a.Hkv + kvh] = 0u;  // ready for the next call
 }
 
-// CTAs per (sequence, kv head): enough for what fits the SMs at once over the
-// batch, no more than the visible pages can feed with a page for every warp.
-int atw_partitions(int kind, int B, int Hkv, int max_context, int window, int sinks) {
+// The split's figures (see above) and the CTAs of the grid: no more than either
+// every pair's pages in parts of min_pages, or the shared-out parts and one
+// part of rounding up per pair, can need.
+static void atw_plan(AtwArgs& a, int kind, int B, int Hkv, int max_context, int window, int sinks) {
+  const long long groups = (long long)B * Hkv;
   const long long all = ((long long)max_context + ATT_PAGE - 1) / ATT_PAGE;
   const long long seen = ((long long)std::min(sinks, max_context) + ATT_PAGE - 1) / ATT_PAGE +
                          ((long long)window + ATT_PAGE - 2) / ATT_PAGE + 1;
   const long long n = std::min(all, seen);
-  const long long ctas = kind == ATW_F16 ? ATW_SMS : 2ll * ATW_SMS;  // (fp16 pages: one CTA's rings fill an SM)
-  const long long want = (ctas + (long long)B * Hkv - 1) / ((long long)B * Hkv);
-  const long long most = (n + ATW_NW - 1) / ATW_NW;
-  return (int)std::max(1ll, std::min(std::min(want, most), (long long)ATW_MAX_PARTITIONS));
+  const int min_pages = kind == ATW_F16 ? Page<ATW_F16>::MIN_PAGES
+                                        : (kind == ATW_F8 ? Page<ATW_F8>::MIN_PAGES : Page<ATW_I4>::MIN_PAGES);
+  a.slots = kind == ATW_F16 ? ATW_SMS : 2 * ATW_SMS;  // (fp16 pages: one CTA's rings fill an SM)
+  a.fit = groups <= a.slots ? (int)(a.slots / groups * groups) : a.slots;
+  a.fit_mixed = (int)std::max(a.slots - groups / 2, a.slots / 2ll);
+  a.ctas = (int)std::min(groups * std::min((n + min_pages - 1) / min_pages, (long long)ATW_MAX_PARTITIONS),
+                         std::max(a.fit, a.fit_mixed) + groups);
+  if (groups * 4 > (long long)ATT_TICKET_BYTES) {  // no ticket for every pair: no splitting
+    a.fit = a.fit_mixed = 1;
+    a.ctas = (int)groups;
+  }
 }
 
 template <int KIND, bool FUSE>
@@ -669,7 +811,7 @@ static int launch_atw(const AtwArgs& a, cudaStream_t s) {
   constexpr size_t smem = atw_smem<KIND>();
   auto kern = w4pg_attn_window<KIND, FUSE>;
   once_per_device(once, [&] { cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
-  cudaError_t e = launch_pdl(kern, dim3(a.PC, a.Hkv, a.B), dim3(ATW_NW * 32), smem, s, a);
+  cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(ATW_NW * 32), smem, s, a);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }
@@ -695,7 +837,7 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
   W4_CHECK_ARG(window >= 0 && sinks >= 0, "%s: window=%d sinks=%d", who, window, sinks);
   W4_CHECK_SHAPE(D == ATT_D, "%s: D=%d, only 128 is built", who, D);
   W4_CHECK_SHAPE(Hq % Hkv == 0 && Hq / Hkv <= 8, "%s: Hq=%d Hkv=%d", who, Hq, Hkv);
-  W4_CHECK_SHAPE(B <= 65535 && Hkv <= 65535, "%s: B=%d Hkv=%d", who, B, Hkv);
+  W4_CHECK_SHAPE((long long)B * Hkv <= (1 << 24), "%s: B=%d Hkv=%d", who, B, Hkv);
   W4_CHECK_SHAPE((long long)max_context <= (long long)max_blocks * ATT_PAGE, "%s: max_context %d > max_blocks*16", who,
                  max_context);
   const bool fuse = a.fuse_rope_append;
@@ -707,12 +849,12 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
   W4_CHECK_ALIGN(a.k, 128, "k_pool");
   W4_CHECK_ALIGN(a.v, 128, "v_pool");
   W4_CHECK_ALIGN(out, 128, "out");
-  a.PC = atw_partitions(a.kind, B, Hkv, max_context, window, sinks);
-  if (a.PC > 1) {
-    const size_t need = attention_workspace_bytes(B, Hq, Hkv, a.PC);
+  atw_plan(a, a.kind, B, Hkv, max_context, window, sinks);
+  if (a.ctas > B * Hkv) {
+    const size_t need = atw_workspace_bytes(a.ctas, Hq / Hkv);
     W4_CHECK_ARG(workspace != nullptr && workspace_bytes >= need, "%s: workspace of %zu bytes needed", who, need);
     W4_CHECK_ALIGN(workspace, 128, "workspace");
-    atw_workspace(a, workspace, B, Hq);
+    atw_workspace(a, workspace, a.ctas, Hq / Hkv);
   }
   a.q = reinterpret_cast<const __half*>(q);
   a.block_table = block_table;
@@ -737,8 +879,16 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
 extern "C" size_t paged_gqa_decode_window_workspace_size(int B, int Hq, int Hkv, int max_context, int window,
                                                          int sinks, int D) {
   (void)D;
-  if (B < 1 || Hq < 1 || Hkv < 1 || max_context < 1 || window < 0 || sinks < 0) return 0;
-  return attention_workspace_bytes(B, Hq, Hkv, atw_partitions(ATW_I4, B, Hkv, max_context, window, sinks));
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_context < 1 || window < 0 || sinks < 0 ||
+      (long long)B * Hkv > (1 << 24))
+    return 0;
+  int most = 0;  // (whichever kind of page the call is about)
+  for (int kind : {ATW_F16, ATW_F8, ATW_I4}) {
+    AtwArgs a = {};
+    atw_plan(a, kind, B, Hkv, max_context, window, sinks);
+    if (a.ctas > B * Hkv) most = std::max(most, a.ctas);
+  }
+  return most ? atw_workspace_bytes(most, Hq / Hkv) : ATT_TICKET_BYTES;
 }
 
 extern "C" int paged_gqa_decode_window(const uint16_t* q, int q_stride, const uint16_t* k_pool, const uint16_t* v_pool,

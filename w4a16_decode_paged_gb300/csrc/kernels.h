@@ -162,24 +162,24 @@ struct AtwArgs {
   const int32_t* block_table;
   const int32_t* context_lens;
   __half* out;              // [B][Hq][D]
-  float* ws_o;              // [B][Hq][PC][D]
-  float* ws_ml;             // [B][Hq][PC][2]
+  float* ws_o;              // [ctas][G][D] partial outputs
+  float* ws_ml;             // [ctas][G][2] their maxima and sums
   unsigned int* counters;   // [B][Hkv]
   int32_t* err_flag;
-  int kind, q_stride, num_pages, max_blocks, max_context, window, sinks, B, Hq, Hkv, G, PC;
+  int kind, q_stride, num_pages, max_blocks, max_context, window, sinks, B, Hq, Hkv, G;
+  int slots, fit, fit_mixed, ctas;  // the split over CTAs (attn_window.cu); ctas: of the grid
   int fuse_rope_append;     // INT4: rotate q and k_new at len - 1, append k_new / v_new, then attend
   float scale_log2;         // sm_scale * log2(e)
   float inv_freq[64];
   int tag;
 };
 int launch_attn_window(const AtwArgs& a, cudaStream_t s);
-int atw_partitions(int kind, int B, int Hkv, int max_context, int window, int sinks);
-inline void atw_workspace(AtwArgs& a, void* ws, int B, int Hq) {  // a.PC set
-  AttnArgs t = {};
-  attention_workspace_layout(t, ws, B, Hq, a.PC);
-  a.ws_o = t.ws_o;
-  a.ws_ml = t.ws_ml;
-  a.counters = t.counters;
+inline size_t atw_workspace_bytes(int ctas, int G) { return ATT_TICKET_BYTES + (size_t)ctas * G * (128 + 2) * 4; }
+inline void atw_workspace(AtwArgs& a, void* ws, int ctas, int G) {  // tickets first, as for the other workspaces
+  char* w = static_cast<char*>(ws);
+  a.counters = reinterpret_cast<unsigned int*>(w);
+  a.ws_o = reinterpret_cast<float*>(w + ATT_TICKET_BYTES);
+  a.ws_ml = a.ws_o + (size_t)ctas * G * 128;
 }
 
 int launch_rmsnorm(const __half* x, const __half* gamma, __half* y, int M, int H, float eps, cudaStream_t s,

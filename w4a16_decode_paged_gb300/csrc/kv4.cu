@@ -6,67 +6,85 @@
 namespace w4 {
 
 // ---------------------------------------------------------------------------
-// RoPE + INT4 append: one CTA per row (of the batch or the prompt).  Its head
+// RoPE + INT4 append: R rows (of the batch or the prompt) per CTA.  Their head
 // rows -- q (rotated), k (rotated, quantised), v (quantised) -- are taken two
 // at a time by a warp, eight dims per lane.  The values do not depend on the
-// position, so they are asked for before the length and the table entry are
-// read and the sines computed.
+// positions, so the first of them are asked for before the lengths and the
+// table entries are read and the sines computed; the next are asked for as
+// these are finished.
 // ---------------------------------------------------------------------------
 constexpr int APPEND_WARPS = 8;
-constexpr int APPEND_AHEAD = 3;  // row pairs a warp loads ahead (3 x 16 rows: 28 + 2 x 4 heads in one go)
+constexpr int APPEND_AHEAD = 3;  // row pairs a warp loads ahead
 
+template <int R>
 __global__ void __launch_bounds__(APPEND_WARPS * 32) w4pg_rope_append_int4(const __grid_constant__ Kv4AppendArgs a) {
-  __shared__ __align__(16) float s_cos[KV4_D / 2], s_sin[KV4_D / 2];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ __align__(16) float s_cos[R][KV4_D / 2], s_sin[R][KV4_D / 2];
+  __shared__ int s_slot[R], s_page[R];  // page -1: none; slot -1: a row of length 0
+  const int b0 = blockIdx.x * R, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = lane & 15, half = lane >> 4;
-  const int rows = a.Hq + 2 * a.Hkv;
-  const __half* qb = a.q + (size_t)b * a.stride_q;
-  const __half* kb = a.k + (size_t)b * a.stride_kv;
-  const __half* vb = a.v + (size_t)b * a.stride_kv;
-  auto load = [&](int r) -> uint4 {
-    if (r >= rows) return make_uint4(0u, 0u, 0u, 0u);
-    const __half* src = r < a.Hq ? qb + (size_t)r * KV4_D
-                                 : (r < a.Hq + a.Hkv ? kb + (size_t)(r - a.Hq) * KV4_D
-                                                     : vb + (size_t)(r - a.Hq - a.Hkv) * KV4_D);
+  const int per = a.Hq + 2 * a.Hkv;          // head rows per row
+  const int rows = min(R, a.B - b0) * per;
+  auto load = [&](int i) -> uint4 {
+    if (i >= rows) return make_uint4(0u, 0u, 0u, 0u);
+    const int u = R == 1 ? 0 : i / per, r = i - u * per;
+    const size_t b = b0 + u;
+    const __half* src = r < a.Hq ? a.q + b * a.stride_q + (size_t)r * KV4_D
+                                 : (r < a.Hq + a.Hkv ? a.k + b * a.stride_kv + (size_t)(r - a.Hq) * KV4_D
+                                                     : a.v + b * a.stride_kv + (size_t)(r - a.Hq - a.Hkv) * KV4_D);
     return __ldcg(reinterpret_cast<const uint4*>(src) + c);
   };
   pdl_wait_then_trigger();
   uint4 x[APPEND_AHEAD];
 #pragma unroll
   for (int u = 0; u < APPEND_AHEAD; ++u) x[u] = load(2 * (warp + u * APPEND_WARPS) + half);
-  const int pos = __ldcg(&a.context_lens[b]) - 1;
-  if (pos < 0) return;
-  const int blk = pos / KV4_PAGE, slot = pos % KV4_PAGE;
-  const int page = blk < a.max_blocks ? __ldcg(&a.block_table[(size_t)b * a.max_blocks + blk]) : -1;
-  if (tid < KV4_D / 2) sincosf(__fmul_rn((float)pos, a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
-  const bool ok = page >= 0 && page < a.num_pages;
-  if (!ok && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
+  for (int i = tid; i < R * (KV4_D / 2); i += APPEND_WARPS * 32) {
+    const int u = i / (KV4_D / 2), f = i % (KV4_D / 2), b = b0 + u;
+    const int pos = b < a.B ? __ldcg(&a.context_lens[b]) - 1 : -1;
+    if (f == 0) {
+      const int blk = pos / KV4_PAGE;
+      const int page = pos >= 0 && blk < a.max_blocks ? __ldcg(&a.block_table[(size_t)b * a.max_blocks + blk]) : -1;
+      const bool ok = page >= 0 && page < a.num_pages;
+      if (pos >= 0 && !ok && a.err_flag) atomicOr(a.err_flag, 1);
+      s_page[u] = ok ? page : -1;
+      s_slot[u] = pos >= 0 ? pos % KV4_PAGE : -1;
+    }
+    sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[f]), &s_sin[u][f], &s_cos[u][f]);
+  }
   __syncthreads();
-  for (int r0 = 2 * warp; r0 < rows; r0 += 2 * APPEND_WARPS * APPEND_AHEAD) {
+  for (int i0 = 2 * warp; i0 < rows; i0 += 2 * APPEND_WARPS * APPEND_AHEAD) {
 #pragma unroll
-    for (int u = 0; u < APPEND_AHEAD; ++u) {
-      const int r = r0 + 2 * u * APPEND_WARPS + half;
-      if (r - half >= rows) break;
+    for (int k = 0; k < APPEND_AHEAD; ++k) {
+      const int i = i0 + 2 * k * APPEND_WARPS + half;
+      if (i - half >= rows) break;
+      const int u = R == 1 ? 0 : min(i, rows - 1) / per, r = i - u * per;
       const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
-      const uint4 raw = x[u];
+      const uint4 raw = x[k];
       uint4 w = raw;
-      rope_rows(w, s_cos, s_sin, lane);
-      if (!is_q && !is_k) w = raw;  // (the two rows of a warp may be of different kinds)
-      uint32_t codes, byte;
-      if (r - half + 1 >= a.Hq) kv4_quantise(w, codes, byte);
-      if (is_q) {
-        *reinterpret_cast<uint4*>(a.q_out + (size_t)b * a.stride_qo + (size_t)r * KV4_D + 8 * c) = w;
-      } else if (ok && r < rows) {
-        const int h = is_k ? r - a.Hq : r - a.Hq - a.Hkv;
-        kv4_put((is_k ? a.k_pool : a.v_pool) + ((size_t)page * a.Hkv + h) * KV4_SLICE, is_k, slot, c, codes, byte);
+      rope_rows(w, s_cos[u], s_sin[u], lane);
+      if (!is_q && !is_k) w = raw;
+      uint32_t codes = 0u, byte = 0u;
+      if (__any_sync(0xffffffffu, !is_q)) kv4_quantise(w, codes, byte);  // (a warp's two rows may be of two kinds)
+      const int slot = s_slot[u], page = s_page[u];
+      if (i < rows && slot >= 0) {
+        if (is_q) {
+          *reinterpret_cast<uint4*>(a.q_out + (size_t)(b0 + u) * a.stride_qo + (size_t)r * KV4_D + 8 * c) = w;
+        } else if (page >= 0) {
+          const int h = is_k ? r - a.Hq : r - a.Hq - a.Hkv;
+          kv4_put((is_k ? a.k_pool : a.v_pool) + ((size_t)page * a.Hkv + h) * KV4_SLICE, is_k, slot, c, codes, byte);
+        }
       }
-      x[u] = load(r + 2 * APPEND_WARPS * APPEND_AHEAD);
+      x[k] = load(i + 2 * APPEND_WARPS * APPEND_AHEAD);
     }
   }
 }
 
+// One row per CTA as long as a wave of CTAs holds them (a decode batch: the
+// shortest chain of latencies); four where a prompt's rows would queue (2048
+// rows of 28 + 2 x 4 heads: @@).
 int launch_rope_append_int4(const Kv4AppendArgs& a, cudaStream_t s) {
-  cudaError_t e = launch_pdl(w4pg_rope_append_int4, dim3(a.B), dim3(APPEND_WARPS * 32), 0, s, a);
+  cudaError_t e;
+  if (a.B <= 2 * num_sms()) e = launch_pdl(w4pg_rope_append_int4<1>, dim3(a.B), dim3(APPEND_WARPS * 32), 0, s, a);
+  else e = launch_pdl(w4pg_rope_append_int4<4>, dim3((a.B + 3) / 4), dim3(APPEND_WARPS * 32), 0, s, a);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "int4 rope/append launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }
@@ -120,6 +138,20 @@ __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv
   const int c = lane & 15, half = lane >> 4;  // dims 8 c .. 8 c + 7
   const size_t pitch = (size_t)a.Hkv * KV4_D;
   const size_t out0 = ((size_t)b * a.T * a.Hkv + h) * KV4_D + 8 * c;
+  // everything the lane needs of the page, in one go: K words of eight dims of
+  // tokens 2 i + half, V word pairs of the token pairs 4 i + 2 half, and the
+  // scale bytes (K: those of tokens t and t + 8; V: of two token pairs)
+  uint32_t kw[8], ksc[4], vsc[2];
+  uint2 vw[4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) kw[i] = __ldcg(reinterpret_cast<const uint32_t*>(ks + kv4_k_code(2 * i + half, 2 * c)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) vw[i] = __ldcg(reinterpret_cast<const uint2*>(vs + kv4_v_code(4 * i + 2 * half, 2 * c)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    ksc[i] = __ldcg(reinterpret_cast<const unsigned short*>(ks + kv4_k_scale(2 * i + half, c >> 2)));
+#pragma unroll
+  for (int i = 0; i < 2; ++i) vsc[i] = __ldcg(reinterpret_cast<const uint32_t*>(vs + kv4_v_scale(4 * i + 2 * half, c >> 2)));
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   // row of token t of the page: the token's value, zero, or left alone
   auto put = [&](__half* out, int t, uint4 value) {
@@ -130,22 +162,19 @@ __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv
   };
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int t = 2 * i + half;  // K: two tokens per step, a word of eight dims per lane
-    const uint32_t w = __ldcg(reinterpret_cast<const uint32_t*>(ks + kv4_k_code(t, 2 * c)));
-    const uint32_t s = __ldcg(ks + kv4_k_scale(t, c >> 2));
+    const uint32_t s = i < 4 ? ksc[i] & 0xFFu : ksc[i - 4] >> 8;
     uint32_t x[4];
-    kv4_values(w, kv4_scale_pair(s * 0x00800080u), x);
-    put(a.k_out, t, make_uint4(lows(x[0], x[1]), lows(x[2], x[3]), highs(x[0], x[1]), highs(x[2], x[3])));
+    kv4_values(kw[i], kv4_scale_pair(s * 0x00800080u), x);
+    put(a.k_out, 2 * i + half, make_uint4(lows(x[0], x[1]), lows(x[2], x[3]), highs(x[0], x[1]), highs(x[2], x[3])));
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = 4 * i + 2 * half;  // V: two token pairs per step, two words of four dims of both tokens
-    const uint2 w = __ldcg(reinterpret_cast<const uint2*>(vs + kv4_v_code(t, 2 * c)));
-    const uint32_t s = __ldcg(reinterpret_cast<const unsigned short*>(vs + kv4_v_scale(t, c >> 2)));
-    const Kv4Scale k = kv4_scale_pair(((s & 0xFFu) << 7) | ((s >> 8) << 23));
+    const int t = 4 * i + 2 * half;
+    const uint32_t s = vsc[i & 1] >> (i < 2 ? 0 : 16);
+    const Kv4Scale k = kv4_scale_pair(((s & 0xFFu) << 7) | ((s & 0xFF00u) << 15));
     uint32_t x[4], y[4];
-    kv4_values(w.x, k, x);
-    kv4_values(w.y, k, y);
+    kv4_values(vw[i].x, k, x);
+    kv4_values(vw[i].y, k, y);
     put(a.v_out, t, make_uint4(lows(x[0], x[1]), lows(x[2], x[3]), lows(y[0], y[1]), lows(y[2], y[3])));
     put(a.v_out, t + 1, make_uint4(highs(x[0], x[1]), highs(x[2], x[3]), highs(y[0], y[1]), highs(y[2], y[3])));
   }
