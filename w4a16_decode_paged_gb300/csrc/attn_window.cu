@@ -14,11 +14,10 @@
 //   O^T[128 dims][8 heads]  += V^T P^T
 // so both products use all 16 rows (heads as rows would leave half of them
 // zero), the accumulators of 8 heads x 128 dims are 32 registers a lane, and a
-// lane's K rows and V dims are contiguous in memory: the cache goes from global
-// memory to registers with 16-byte loads and is widened there, without shared
-// memory.  The next page's K is requested when the scores have consumed this
-// page's, its V after the second product.  P^T is the scores' accumulator
-// transposed 8x8 by 8x8 with movmatrix.
+// lane's K rows and V dims are contiguous: a page's (page, kv head) slices are
+// copied whole, by bulk copies, into the warp's ring in shared memory, read
+// back with 16-byte loads and widened in registers.  P^T is the scores'
+// accumulator transposed 8x8 by 8x8 with movmatrix.
 //
 // Softmax: p = exp2(s - m) with a reference m per head that is the running
 // maximum as of the last time a score passed it by more than 2^ATW_SLACK;
@@ -31,6 +30,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_core.cuh"
 #include "kernels.h"
@@ -112,10 +112,13 @@ struct Page<ATW_F16> {
     }
   }
   // factors of P that come before its rounding
+  template <bool MASK>
   static __device__ __forceinline__ void p_scale(const unsigned char*, int, uint32_t, float (&)[4]) {}
-  // O^T += V^T P^T; bit r of live: token r is seen, V rows of others count as zero whatever they hold
-  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, bool masked, uint32_t live,
-                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
+  // O^T += V^T P^T; MASK: bit r of live says that token r is seen, V rows of
+  // others count as zero whatever they hold
+  template <bool MASK>
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, uint32_t live, uint32_t b0,
+                                                uint32_t b1, float (&o)[8][4]) {
     const unsigned char* p = slot + V + 512 * t4 + 16 * g;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -123,7 +126,7 @@ struct Page<ATW_F16> {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         w[r] = *reinterpret_cast<const uint4*>(p + 256 * (r & 1) + 2048 * (r >> 1) + 128 * i);
-        if (masked && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
+        if (MASK && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -175,22 +178,26 @@ struct Page<ATW_F8> {
     s[3] *= f1;
   }
   // V row scales go into P before its rounding
+  template <bool MASK>
   static __device__ __forceinline__ void p_scale(const unsigned char* slot, int g, uint32_t live, float (&p)[4]) {
     const float* vs = reinterpret_cast<const float*>(slot + VS);
-    const float f0 = (live >> g) & 1u ? vs[g] * ATW_V8 : 0.f, f1 = (live >> (g + 8)) & 1u ? vs[g + 8] * ATW_V8 : 0.f;
+    float f0 = vs[g] * ATW_V8, f1 = vs[g + 8] * ATW_V8;
+    if (MASK && !((live >> g) & 1u)) f0 = 0.f;
+    if (MASK && !((live >> (g + 8)) & 1u)) f1 = 0.f;
     p[0] *= f0;
     p[1] *= f0;
     p[2] *= f1;
     p[3] *= f1;
   }
-  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, bool masked, uint32_t live,
-                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
+  template <bool MASK>
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, uint32_t live, uint32_t b0,
+                                                uint32_t b1, float (&o)[8][4]) {
     const unsigned char* p = slot + V + 256 * t4 + 16 * g;
     uint4 w[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       w[r] = *reinterpret_cast<const uint4*>(p + 128 * (r & 1) + 1024 * (r >> 1));
-      if (masked && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
+      if (MASK && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -237,14 +244,16 @@ struct Page<ATW_I4> {
       mma_16816_full(s, x[2], y[2], x[3], y[3], qb[2 * i + 1][0], qb[2 * i + 1][1]);
     }
   }
+  template <bool MASK>
   static __device__ __forceinline__ void p_scale(const unsigned char*, int, uint32_t, float (&)[4]) {}
-  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, bool masked, uint32_t live,
-                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
+  template <bool MASK>
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, uint32_t live, uint32_t b0,
+                                                uint32_t b1, float (&o)[8][4]) {
     const uint4 v0 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4, 4 * g));
     const uint4 v1 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4 + 8, 4 * g));
     // scale bytes of tokens 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4; a zero scale makes every code zero
     uint32_t vs = *reinterpret_cast<const uint32_t*>(slot + V + kv4_v_scale(2 * t4, g >> 1));
-    if (masked) {
+    if (MASK) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (!((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) vs &= ~(0xFFu << (8 * r));
@@ -415,6 +424,7 @@ constexpr size_t atw_ring_bytes() { return (size_t)ATW_NW * Page<KIND>::STAGES *
 constexpr size_t ATW_MERGE_BYTES = (size_t)ATW_NW * 8 * ATW_PITCH * 4;
 template <int KIND>
 constexpr size_t atw_smem() { return std::max(atw_ring_bytes<KIND>(), ATW_MERGE_BYTES); }
+
 constexpr uint32_t ATW_WAIT_POLLS = 1u << 20;  // bound of a wait for copies
 
 template <int KIND, bool FUSE>
@@ -473,36 +483,39 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     return id;
   };
   // 32 page ids at a time, one per lane: `ids` holds those of the steps being
-  // copied (pages 32 c .. of the list), ids_next the 32 after; the lane that
-  // holds an id issues that page's copies
+  // copied (pages 32 c .. of the list), ids_next the 32 after
   static_assert(32 % BATCH == 0, "a step's ids sit in one group of 32");
   int ids = table(lane), ids_next = -1;
-  unsigned ids_ok = __ballot_sync(0xffffffffu, ids >= 0);
   unsigned have = 0;  // bit (stage * BATCH + j): that page was copied
   unsigned char* ring = smraw + (size_t)warp * STAGES * BATCH * PG::SLOT;
   // copies step `st`'s pages into its stage (warp-wide; steps come in order)
   auto issue = [&](int st, int stage) {
     const int i = (st * BATCH) & 31;
-    if (i == 0 && st > 0) {
-      ids = ids_next;
-      ids_ok = __ballot_sync(0xffffffffu, ids >= 0);
-    }
+    if (i == 0 && st > 0) ids = ids_next;
     if (i == BATCH) ids_next = table(st * BATCH - BATCH + 32 + lane);
-    const unsigned got = (ids_ok >> i) & ((1u << BATCH) - 1u);
+    int id[BATCH];
+    unsigned got = 0;
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
+      id[j] = __shfl_sync(0xffffffffu, ids, i + j);
+      got |= (id[j] >= 0 ? 1u : 0u) << j;
+    }
     have = (have & ~(((1u << BATCH) - 1u) << (stage * BATCH))) | (got << (stage * BATCH));
-    if (lane == 0) mbar_arrive_expect_tx(&bar[stage], __popc(got) * PG::SLOT);
-    __syncwarp();
-    const int j = lane - i;
-    if (j >= 0 && j < BATCH && ids >= 0)
-      PG::fetch(a, (size_t)ids * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, smem_u32(&bar[stage]));
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bar[stage], __popc(got) * PG::SLOT);
+#pragma unroll
+      for (int j = 0; j < BATCH; ++j)
+        if (id[j] >= 0)
+          PG::fetch(a, (size_t)id[j] * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, smem_u32(&bar[stage]));
+    }
   };
   __syncwarp();
   for (int st = 0; st < STAGES && st < steps; ++st) issue(st, st);
   // pages some of whose tokens are masked: the last of the sinks, the first of
-  // the window, the last of the sequence (-1: none)
+  // the window, the last of the sequence (-1: none; fused: the new token's)
   const int part_s = S % ATT_PAGE ? nsp - 1 : -1;
   const int part_w = nsp < n && wp * ATT_PAGE < w0 ? nsp : -1;
-  const int part_l = L % ATT_PAGE ? n - 1 : -1;
+  const int part_l = FUSE || L % ATT_PAGE ? n - 1 : -1;
 
   // ---- queries ----------------------------------------------------------------
   const int pos = fits ? L - 1 : -1;  // the new token's (fused); a length past the bound appends nothing
@@ -559,48 +572,39 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
+  float t0 = -INFINITY, t1 = -INFINITY;  // m0, m1 plus the slack
   bool landed = true;  // no wait for copies has run out
   int stage = 0;
   uint32_t parity = 0;
-  for (int step = 0; step < steps; ++step) {
-    const int v = wv0 + step * NW * BATCH;  // first visible page of this step
+  // one step; MASK: some token of its pages is not seen
+  auto attend = [&](auto mask, int v) {
+    constexpr bool MASK = decltype(mask)::value;
     unsigned char* slot = ring + stage * BATCH * PG::SLOT;
-    const unsigned got = have >> (stage * BATCH);
-    // does any of these pages have masked tokens?
-    bool masked = false;
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j)
-      masked |= !((got >> j) & 1u) || v + j == part_s || v + j == part_w || v + j == part_l;
     uint32_t live[BATCH];  // bit r: token r of the page is seen
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      live[j] = 0xFFFFu;
-      if (masked) {
-        live[j] = 0u;
-        const int t0 = page_no(v + j) * ATT_PAGE;
-        if ((got >> j) & 1u) {
-          for (int r = 0; r < ATT_PAGE; ++r)
-            live[j] |= (t0 + r < L && (t0 + r >= w0 || t0 + r < S) ? 1u : 0u) << r;
-        }
+      live[j] = 0u;
+      if (MASK && (have >> (stage * BATCH + j)) & 1u) {
+        // t < L, and t >= w0 or t < S
+        const int first = page_no(v + j) * ATT_PAGE;
+        auto below = [&](int t) { return (1u << min(max(t - first, 0), ATT_PAGE)) - 1u; };
+        live[j] = below(L) & (~below(w0) | below(S));
       }
     }
-    landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, ATW_WAIT_POLLS));
-    if (!landed) break;
     if constexpr (FUSE) {
+      if constexpr (MASK) {  // (the new token's page counts as masked)
 #pragma unroll
-      for (int j = 0; j < BATCH; ++j)
-        if (v + j == n - 1 && pos >= 0) PG::patch(slot + j * PG::SLOT, s_new, s_news, pos & 15, lane);
-      __syncwarp();
+        for (int j = 0; j < BATCH; ++j)
+          if (v + j == n - 1 && pos >= 0) PG::patch(slot + j * PG::SLOT, s_new, s_news, pos & 15, lane);
+        __syncwarp();
+      }
     }
     float s[BATCH][4];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
       s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
       PG::scores(slot + j * PG::SLOT, g, t4, qb, s[j]);
-    }
-    if (masked) {
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
+      if (MASK) {
         if (!((live[j] >> g) & 1u)) s[j][0] = s[j][1] = -INFINITY;
         if (!((live[j] >> (g + 8)) & 1u)) s[j][2] = s[j][3] = -INFINITY;
       }
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     }
     x0 *= scale;
     x1 *= scale;
-    if (__any_sync(0xffffffffu, x0 > m0 + ATW_SLACK || x1 > m1 + ATW_SLACK)) {
+    if (__any_sync(0xffffffffu, x0 > t0 || x1 > t1)) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
@@ -624,6 +628,8 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
       const float c0 = x0 == m0 ? 1.f : ex2(m0 - x0), c1 = x1 == m1 ? 1.f : ex2(m1 - x1);
       m0 = x0;
       m1 = x1;
+      t0 = m0 + ATW_SLACK;
+      t1 = m1 + ATW_SLACK;
       l0 *= c0;
       l1 *= c1;
 #pragma unroll
@@ -636,29 +642,31 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     }
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      s[j][0] = ex2(fmaf(s[j][0], scale, -m0));
-      s[j][1] = ex2(fmaf(s[j][1], scale, -m1));
-      s[j][2] = ex2(fmaf(s[j][2], scale, -m0));
-      s[j][3] = ex2(fmaf(s[j][3], scale, -m1));
-    }
-    if (masked) {  // (-inf under a reference still at -inf is no number)
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j) {
-        if (!((live[j] >> g) & 1u)) s[j][0] = s[j][1] = 0.f;
-        if (!((live[j] >> (g + 8)) & 1u)) s[j][2] = s[j][3] = 0.f;
+      float p[4];
+      p[0] = ex2(fmaf(s[j][0], scale, -m0));
+      p[1] = ex2(fmaf(s[j][1], scale, -m1));
+      p[2] = ex2(fmaf(s[j][2], scale, -m0));
+      p[3] = ex2(fmaf(s[j][3], scale, -m1));
+      if (MASK) {  // (-inf under a reference still at -inf is no number)
+        if (!((live[j] >> g) & 1u)) p[0] = p[1] = 0.f;
+        if (!((live[j] >> (g + 8)) & 1u)) p[2] = p[3] = 0.f;
       }
+      l0 += p[0] + p[2];
+      l1 += p[1] + p[3];
+      PG::template p_scale<MASK>(slot + j * PG::SLOT, g, live[j], p);
+      const uint32_t b0 = movmatrix_trans(pack_h2(p[0], p[1])), b1 = movmatrix_trans(pack_h2(p[2], p[3]));
+      PG::template output<MASK>(slot + j * PG::SLOT, g, t4, live[j], b0, b1, o);
     }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      l0 += s[j][0] + s[j][2];
-      l1 += s[j][1] + s[j][3];
-    }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      PG::p_scale(slot + j * PG::SLOT, g, live[j], s[j]);
-      const uint32_t b0 = movmatrix_trans(pack_h2(s[j][0], s[j][1])), b1 = movmatrix_trans(pack_h2(s[j][2], s[j][3]));
-      PG::output(slot + j * PG::SLOT, g, t4, masked, live[j], b0, b1, o);
-    }
+  };
+  for (int step = 0; step < steps; ++step) {
+    const int v = wv0 + step * NW * BATCH;  // first visible page of this step
+    landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, ATW_WAIT_POLLS));
+    if (!landed) break;
+    const bool whole = ((have >> (stage * BATCH)) & ((1u << BATCH) - 1u)) == (1u << BATCH) - 1u &&
+                       (unsigned)(part_s - v) >= (unsigned)BATCH && (unsigned)(part_w - v) >= (unsigned)BATCH &&
+                       (unsigned)(part_l - v) >= (unsigned)BATCH;
+    if (whole) attend(std::false_type{}, v);
+    else attend(std::true_type{}, v);
     __syncwarp();  // every lane has read the stage
     if (step + STAGES < steps) issue(step + STAGES, stage);
     if (++stage == STAGES) {
