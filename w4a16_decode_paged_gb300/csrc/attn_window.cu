@@ -51,8 +51,16 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// D (16 x 8) += A (16 x 16) B (16 x 8), fp16 in, fp32 accumulate (registers as
+// mma_16816_full; free to move, so that independent chains interleave).
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ float ex2(float x) {
   float d;
@@ -101,14 +109,14 @@ struct Page<ATW_F16> {
     bulk_g2s(slot + V, static_cast<const __half*>(a.v) + slice * ATT_SLICE, 4096, bar);
   }
   // S^T += K Q^T of one page, scaled where the kind has K row scales
-  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const uint32_t (&qb)[8][2],
-                                                float (&s)[4]) {
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias& bias,
+                                                const uint32_t (&qb)[8][2], float (&s)[4]) {
     const unsigned char* p = slot + 256 * g + 16 * t4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint4 x = *reinterpret_cast<const uint4*>(p + 64 * i), y = *reinterpret_cast<const uint4*>(p + 2048 + 64 * i);
-      mma_16816_full(s, x.x, y.x, x.y, y.y, qb[2 * i][0], qb[2 * i][1]);
-      mma_16816_full(s, x.z, y.z, x.w, y.w, qb[2 * i + 1][0], qb[2 * i + 1][1]);
+      mma(s, x.x, y.x, x.y, y.y, qb[2 * i][0], qb[2 * i][1]);
+      mma(s, x.z, y.z, x.w, y.w, qb[2 * i + 1][0], qb[2 * i + 1][1]);
     }
   }
   // factors of P that come before its rounding
@@ -117,8 +125,8 @@ struct Page<ATW_F16> {
   // O^T += V^T P^T; MASK: bit r of live says that token r is seen, V rows of
   // others count as zero whatever they hold
   template <bool MASK>
-  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, uint32_t live, uint32_t b0,
-                                                uint32_t b1, float (&o)[8][4]) {
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
+                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
     const unsigned char* p = slot + V + 512 * t4 + 16 * g;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -131,7 +139,7 @@ struct Page<ATW_F16> {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t a = (&w[0].x)[j], b = (&w[1].x)[j], c = (&w[2].x)[j], d = (&w[3].x)[j];
-        mma_16816_full(o[4 * i + j], prmt(a, b, 0x5410), prmt(a, b, 0x7632), prmt(c, d, 0x5410), prmt(c, d, 0x7632), b0,
+        mma(o[4 * i + j], prmt(a, b, 0x5410), prmt(a, b, 0x7632), prmt(c, d, 0x5410), prmt(c, d, 0x7632), b0,
                        b1);
       }
     }
@@ -156,8 +164,8 @@ struct Page<ATW_F8> {
     bulk_g2s(slot + KS, a.ks + slice * ATT_PAGE, 64, bar);
     bulk_g2s(slot + VS, a.vs + slice * ATT_PAGE, 64, bar);
   }
-  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const uint32_t (&qb)[8][2],
-                                                float (&s)[4]) {
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias& bias,
+                                                const uint32_t (&qb)[8][2], float (&s)[4]) {
     const unsigned char* p = slot + 128 * g + 16 * t4;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -167,7 +175,7 @@ struct Page<ATW_F8> {
         uint32_t a0, a1, a2, a3;
         e4m3x4_to_h2x2((&x.x)[w], a0, a2);
         e4m3x4_to_h2x2((&y.x)[w], a1, a3);
-        mma_16816_full(s, a0, a1, a2, a3, qb[4 * i + w][0], qb[4 * i + w][1]);
+        mma(s, a0, a1, a2, a3, qb[4 * i + w][0], qb[4 * i + w][1]);
       }
     }
     const float* ks = reinterpret_cast<const float*>(slot + KS);
@@ -190,8 +198,8 @@ struct Page<ATW_F8> {
     p[3] *= f1;
   }
   template <bool MASK>
-  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, uint32_t live, uint32_t b0,
-                                                uint32_t b1, float (&o)[8][4]) {
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
+                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
     const unsigned char* p = slot + V + 256 * t4 + 16 * g;
     uint4 w[4];
 #pragma unroll
@@ -207,8 +215,8 @@ struct Page<ATW_F8> {
       e4m3x4_to_h2x2(prmt(a, b, 0x7362), x[2], x[3]);
       e4m3x4_to_h2x2(prmt(c, d, 0x5140), y[0], y[1]);
       e4m3x4_to_h2x2(prmt(c, d, 0x7362), y[2], y[3]);
-      mma_16816_full(o[2 * j], x[0], x[1], y[0], y[1], b0, b1);
-      mma_16816_full(o[2 * j + 1], x[2], x[3], y[2], y[3], b0, b1);
+      mma(o[2 * j], x[0], x[1], y[0], y[1], b0, b1);
+      mma(o[2 * j + 1], x[2], x[3], y[2], y[3], b0, b1);
     }
   }
 };
@@ -229,8 +237,8 @@ struct Page<ATW_I4> {
     bulk_g2s(slot, static_cast<const uint8_t*>(a.k) + slice * KV4_SLICE, KV4_SLICE, bar);
     bulk_g2s(slot + V, static_cast<const uint8_t*>(a.v) + slice * KV4_SLICE, KV4_SLICE, bar);
   }
-  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const uint32_t (&qb)[8][2],
-                                                float (&s)[4]) {
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias& bias,
+                                                const uint32_t (&qb)[8][2], float (&s)[4]) {
     const uint4 k0 = *reinterpret_cast<const uint4*>(slot + kv4_k_code(g, 8 * t4));
     const uint4 k1 = *reinterpret_cast<const uint4*>(slot + kv4_k_code(g + 8, 8 * t4));
     const uint32_t ks = *reinterpret_cast<const uint16_t*>(slot + kv4_k_scale(g, t4));  // tokens g and g + 8
@@ -238,17 +246,17 @@ struct Page<ATW_I4> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t x[4], y[4];
-      kv4_unpack((&k0.x)[i], s0, x);
-      kv4_unpack((&k1.x)[i], s1, y);
-      mma_16816_full(s, x[0], y[0], x[1], y[1], qb[2 * i][0], qb[2 * i][1]);
-      mma_16816_full(s, x[2], y[2], x[3], y[3], qb[2 * i + 1][0], qb[2 * i + 1][1]);
+      kv4_unpack((&k0.x)[i], s0, bias, x);
+      kv4_unpack((&k1.x)[i], s1, bias, y);
+      mma(s, x[0], y[0], x[1], y[1], qb[2 * i][0], qb[2 * i][1]);
+      mma(s, x[2], y[2], x[3], y[3], qb[2 * i + 1][0], qb[2 * i + 1][1]);
     }
   }
   template <bool MASK>
   static __device__ __forceinline__ void p_scale(const unsigned char*, int, uint32_t, float (&)[4]) {}
   template <bool MASK>
-  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, uint32_t live, uint32_t b0,
-                                                uint32_t b1, float (&o)[8][4]) {
+  static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
+                                                uint32_t b0, uint32_t b1, float (&o)[8][4]) {
     const uint4 v0 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4, 4 * g));
     const uint4 v1 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4 + 8, 4 * g));
     // scale bytes of tokens 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4; a zero scale makes every code zero
@@ -262,10 +270,10 @@ struct Page<ATW_I4> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t x[4], y[4];
-      kv4_unpack((&v0.x)[j], s0, x);
-      kv4_unpack((&v1.x)[j], s1, y);
-      mma_16816_full(o[2 * j], x[0], x[1], y[0], y[1], b0, b1);
-      mma_16816_full(o[2 * j + 1], x[2], x[3], y[2], y[3], b0, b1);
+      kv4_unpack((&v0.x)[j], s0, bias, x);
+      kv4_unpack((&v1.x)[j], s1, bias, y);
+      mma(o[2 * j], x[0], x[1], y[0], y[1], b0, b1);
+      mma(o[2 * j + 1], x[2], x[3], y[2], y[3], b0, b1);
     }
   }
   // the new token's rows over what was copied (warp-wide)
@@ -297,13 +305,14 @@ __device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I
 // ---------------------------------------------------------------------------
 struct AtwShare {
   int b, kvh, part, parts;  // b -1: nothing to do
-  int L, w0, S, nsp, wp, n;
+  int len, L, w0, S, nsp, wp, n;
   bool fits;
 };
 
 // the visible pages of a sequence of this length
 __device__ __forceinline__ AtwShare atw_visible(const AtwArgs& a, int len) {
   AtwShare r;
+  r.len = len;
   r.fits = len <= a.max_context;
   r.L = max(min(len, a.max_context), 0);
   r.w0 = a.window >= r.L ? 0 : r.L - a.window;  // first token of the window
@@ -320,7 +329,8 @@ __device__ __forceinline__ int atw_per(long long pages, int fit, int min_pages) 
   return (int)min(max((pages + fit - 1) / fit, (long long)min_pages), (long long)INT_MAX / 2);
 }
 
-// Up to 32 sequences: every warp works it out for itself.
+// Up to 32 sequences: one warp's work (every warp's own would be eight times
+// the requests for the same line of lengths).
 __device__ __forceinline__ AtwShare atw_share_warp(const AtwArgs& a, int min_pages) {
   const int lane = threadIdx.x & 31, cta = blockIdx.x;
   const int len = lane < a.B ? __ldcg(&a.context_lens[lane]) : 0;
@@ -454,7 +464,27 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   W4_TRACE_WAITED();
 
   // ---- which (sequence, kv head) and which part of its pages ------------------
-  const AtwShare sh = a.B <= 32 ? atw_share_warp(a, PG::MIN_PAGES) : atw_share_cta(a, PG::MIN_PAGES, s_scan);
+  AtwShare sh;
+  if (a.B <= 32) {
+    if (warp == 0) {
+      const AtwShare r = atw_share_warp(a, PG::MIN_PAGES);
+      if (lane == 0) {
+        s_scan[0] = r.b;
+        s_scan[1] = r.kvh;
+        s_scan[2] = r.part;
+        s_scan[3] = r.parts;
+        s_scan[4] = r.len;
+      }
+    }
+    __syncthreads();
+    sh = atw_visible(a, s_scan[4]);
+    sh.b = s_scan[0];
+    sh.kvh = s_scan[1];
+    sh.part = s_scan[2];
+    sh.parts = s_scan[3];
+  } else {
+    sh = atw_share_cta(a, PG::MIN_PAGES, s_scan);
+  }
   if (sh.b < 0) return;
   const int b = sh.b, kvh = sh.kvh, pc = sh.part, active = sh.parts;
   const int L = sh.L, w0 = sh.w0, S = sh.S, n = sh.n, nsp = sh.nsp, wp = sh.wp;
@@ -572,6 +602,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
+  const Kv4Bias bias;
   float t0 = -INFINITY, t1 = -INFINITY;  // m0, m1 plus the slack
   bool landed = true;  // no wait for copies has run out
   int stage = 0;
@@ -603,7 +634,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
       s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      PG::scores(slot + j * PG::SLOT, g, t4, qb, s[j]);
+      PG::scores(slot + j * PG::SLOT, g, t4, bias, qb, s[j]);
       if (MASK) {
         if (!((live[j] >> g) & 1u)) s[j][0] = s[j][1] = -INFINITY;
         if (!((live[j] >> (g + 8)) & 1u)) s[j][2] = s[j][3] = -INFINITY;
@@ -655,7 +686,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
       l1 += p[1] + p[3];
       PG::template p_scale<MASK>(slot + j * PG::SLOT, g, live[j], p);
       const uint32_t b0 = movmatrix_trans(pack_h2(p[0], p[1])), b1 = movmatrix_trans(pack_h2(p[2], p[3]));
-      PG::template output<MASK>(slot + j * PG::SLOT, g, t4, live[j], b0, b1, o);
+      PG::template output<MASK>(slot + j * PG::SLOT, g, t4, bias, live[j], b0, b1, o);
     }
   };
   for (int step = 0; step < steps; ++step) {
@@ -745,9 +776,14 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   // ---- the CTAs' partials: the last to finish adds them up, in order ----------------
   __syncthreads();
   if (tid == 0) {
-    __threadfence();  // the CTA's partial (ordered before by the barrier) before its ticket
-    s_last = atomicAdd(&a.counters[b * a.Hkv + kvh], 1u) == (unsigned)(active - 1);
-    __threadfence();
+    // releases the CTA's partial (ordered before by the barrier) with the
+    // ticket, and for the last acquires the others'
+    unsigned ticket;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                 : "=r"(ticket)
+                 : "l"(a.counters + b * a.Hkv + kvh)
+                 : "memory");
+    s_last = ticket == (unsigned)(active - 1);
   }
   __syncthreads();
   if (!s_last) return;

@@ -104,8 +104,8 @@ struct Kv4ReadArgs {
 
 // a word of codes times its scale(s): the pairs (n, n + 4) of its nibbles as
 // fp16 values.  two: the fp16 bits of the low and the high half's scale.
-__device__ __forceinline__ void kv4_values(uint32_t word, const Kv4Scale& k, uint32_t (&x)[4]) {
-  kv4_unpack(word, k, x);
+__device__ __forceinline__ void kv4_values(uint32_t word, const Kv4Scale& k, const Kv4Bias& e, uint32_t (&x)[4]) {
+  kv4_unpack(word, k, e, x);
 #pragma unroll
   for (int i = 0; i < 4; ++i) x[i] = hmul2_u(x[i], 0x54005400u);  // 64: the unpacking's scales are s / 64
 }
@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv
     ksc[i] = __ldcg(reinterpret_cast<const unsigned short*>(ks + kv4_k_scale(2 * i + half, c >> 2)));
 #pragma unroll
   for (int i = 0; i < 2; ++i) vsc[i] = __ldcg(reinterpret_cast<const uint32_t*>(vs + kv4_v_scale(4 * i + 2 * half, c >> 2)));
+  const Kv4Bias bias;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   // row of token t of the page: the token's value, zero, or left alone
   auto put = [&](__half* out, int t, uint4 value) {
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv
   for (int i = 0; i < 8; ++i) {
     const uint32_t s = i < 4 ? ksc[i] & 0xFFu : ksc[i - 4] >> 8;
     uint32_t x[4];
-    kv4_values(kw[i], kv4_scale_pair(s * 0x00800080u), x);
+    kv4_values(kw[i], kv4_scale_pair(s * 0x00800080u), bias, x);
     put(a.k_out, 2 * i + half, make_uint4(lows(x[0], x[1]), lows(x[2], x[3]), highs(x[0], x[1]), highs(x[2], x[3])));
   }
 #pragma unroll
@@ -173,8 +174,8 @@ __global__ void __launch_bounds__(256) w4pg_read_int4(const __grid_constant__ Kv
     const uint32_t s = vsc[i & 1] >> (i < 2 ? 0 : 16);
     const Kv4Scale k = kv4_scale_pair(((s & 0xFFu) << 7) | ((s & 0xFF00u) << 15));
     uint32_t x[4], y[4];
-    kv4_values(vw[i].x, k, x);
-    kv4_values(vw[i].y, k, y);
+    kv4_values(vw[i].x, k, bias, x);
+    kv4_values(vw[i].y, k, bias, y);
     put(a.v_out, t, make_uint4(lows(x[0], x[1]), lows(x[2], x[3]), lows(y[0], y[1]), lows(y[2], y[3])));
     put(a.v_out, t + 1, make_uint4(highs(x[0], x[1]), highs(x[2], x[3]), highs(y[0], y[1]), highs(y[2], y[3])));
   }

@@ -155,13 +155,24 @@ __device__ __forceinline__ Kv4Scale kv4_scale_pair(uint32_t two) {
 // (low, high) bytes at bits 0-7 and 16-23 -> the pair's fp16 bits
 __device__ __forceinline__ uint32_t kv4_bytes_to_half2(uint32_t b) { return b << 7; }
 
+// The exponents, kept in registers: an instruction takes one immediate, which
+// the mask is, and a compiler that may re-create a constant does so at each use.
+struct Kv4Bias {
+  uint32_t e256, e64, e16;
+  __device__ __forceinline__ Kv4Bias() {
+    asm volatile("mov.u32 %0, 0x5C005C00;" : "=r"(e256));
+    asm volatile("mov.u32 %0, 0x54005400;" : "=r"(e64));
+    asm volatile("mov.u32 %0, 0x4C004C00;" : "=r"(e16));
+  }
+};
+
 // Eight codes of a word: x[n] = nibbles n of the low and of the high half.
-__device__ __forceinline__ void kv4_unpack(uint32_t w, const Kv4Scale& k, uint32_t (&x)[4]) {
+__device__ __forceinline__ void kv4_unpack(uint32_t w, const Kv4Scale& k, const Kv4Bias& e, uint32_t (&x)[4]) {
   const uint32_t l = w << 2, r = w >> 6;
-  x[0] = hfma2_u(and_or(l, 0x003C003Cu, 0x5C005C00u), k.s, k.c264);
-  x[1] = hfma2_u(and_or(w, 0x00F000F0u, 0x54005400u), k.s, k.c72);
-  x[2] = hfma2_u(and_or(r, 0x003C003Cu, 0x5C005C00u), k.s, k.c264);
-  x[3] = hfma2_u(and_or(r, 0x03C003C0u, 0x4C004C00u), k.s, k.c24);
+  x[0] = hfma2_u(and_or(l, 0x003C003Cu, e.e256), k.s, k.c264);
+  x[1] = hfma2_u(and_or(w, 0x00F000F0u, e.e64), k.s, k.c72);
+  x[2] = hfma2_u(and_or(r, 0x003C003Cu, e.e256), k.s, k.c264);
+  x[3] = hfma2_u(and_or(r, 0x03C003C0u, e.e16), k.s, k.c24);
 }
 
 }  // namespace w4
