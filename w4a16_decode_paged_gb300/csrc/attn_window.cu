@@ -93,7 +93,7 @@ struct Page;
 template <>
 struct Page<ATW_F16> {
   static constexpr int BATCH = 1;   // pages per step of a warp
-  static constexpr int STAGES = 3;  // steps in flight per warp
+  static constexpr int STAGES = 2;  // steps in flight per warp
   static constexpr int MIN_CTAS = 1;
   static constexpr int MIN_PAGES = 8;
   static constexpr int V = 4096;    // V's offset in a page's slot
@@ -149,7 +149,7 @@ struct Page<ATW_F16> {
 template <>
 struct Page<ATW_F8> {
   static constexpr int BATCH = 1;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 16;
   static constexpr int V = 2048, KS = 4096, VS = 4160;
@@ -224,9 +224,9 @@ struct Page<ATW_F8> {
 template <>
 struct Page<ATW_I4> {
   static constexpr int BATCH = 2;
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
-  static constexpr int MIN_PAGES = 64;
+  static constexpr int MIN_PAGES = 32;
   static constexpr int V = KV4_SLICE;
   static constexpr int SLOT = 2 * KV4_SLICE;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
@@ -492,9 +492,17 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   if (!fits && pc == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
   const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
   uint4 qw = make_uint4(0u, 0u, 0u, 0u);
-  if (!FUSE && tid < 8 * ATT_D / 8 && tid / (ATT_D / 8) < G) qw = ldcg16(qrow + 8 * tid);
   const int chunk = (n + active - 1) / active;
   const int v0 = pc * chunk, v1 = min(n, v0 + chunk);
+  // The rows that become queries, and (fused, in the CTA of the last page) the
+  // new K and V rows 8 and 9: half a warp per row.  They are asked for before
+  // any page: behind the first pages' copies they would wait for them all.
+  const int r = 2 * warp + (lane >> 4), c = lane & 15;
+  const bool last = v0 < n && v1 == n;
+  if (r < G) qw = ldcg16(qrow + r * ATT_D + 8 * c);
+  else if (FUSE && last && (r == 8 || r == 9))
+    qw = ldcg16(a.q + (size_t)b * a.q_stride + (size_t)(a.Hq + (r - 8) * a.Hkv + kvh) * ATT_D + 8 * c);
+  const int pos = fits ? L - 1 : -1;  // the new token's (fused); a length past the bound appends nothing
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
   auto page_no = [&](int v) { return v < nsp ? v : v - nsp + wp; };
 
@@ -539,6 +547,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
           PG::fetch(a, (size_t)id[j] * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, smem_u32(&bar[stage]));
     }
   };
+  if (FUSE && tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
   __syncwarp();
   for (int st = 0; st < STAGES && st < steps; ++st) issue(st, st);
   // pages some of whose tokens are masked: the last of the sinks, the first of
@@ -548,26 +557,16 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   const int part_l = FUSE || L % ATT_PAGE ? n - 1 : -1;
 
   // ---- queries ----------------------------------------------------------------
-  const int pos = fits ? L - 1 : -1;  // the new token's (fused); a length past the bound appends nothing
   if (FUSE) {
-    if (tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
-    __syncthreads();
-    // two rows per warp: eight query heads (those from G on are zero), and in
-    // the CTA of the last page the new K and V rows
-    const bool last = v0 < n && v1 == n;
-    const int r = 2 * warp + (lane >> 4), c = lane & 15;
+    __syncthreads();  // the sines and cosines
     if (warp < (last ? 5 : 4)) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      const __half* src = r < 8 ? qrow + r * ATT_D
-                                : a.q + (size_t)b * a.q_stride + (size_t)(a.Hq + (r - 8) * a.Hkv + kvh) * ATT_D;
-      if (r < G || r >= 8) x = ldcg16(src + 8 * c);
-      uint4 w = x;
+      uint4 w = qw;
       rope_rows(w, s_cos, s_sin, lane);
       if (r < 8) {
         *reinterpret_cast<uint4*>(&s_q[r][8 * c]) = w;
       } else {
         const bool is_k = r == 8;
-        if (!is_k) w = x;
+        if (!is_k) w = qw;
         uint32_t codes, byte;
         kv4_quantise(w, codes, byte);
         *reinterpret_cast<uint32_t*>(&s_new[r - 8][2 * c]) = codes;
@@ -579,8 +578,8 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
                   is_k, pos % ATT_PAGE, c, codes, byte);
       }
     }
-  } else if (tid < 8 * ATT_D / 8) {
-    *reinterpret_cast<uint4*>(&s_q[tid / (ATT_D / 8)][8 * (tid % (ATT_D / 8))]) = qw;
+  } else if (r < 8) {
+    *reinterpret_cast<uint4*>(&s_q[r][8 * c]) = qw;
   }
   __syncthreads();
   uint32_t qb[8][2];
@@ -743,7 +742,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     *reinterpret_cast<__half2*>(out + PG::odim(mt, g0 + 1)) = __floats2half2_rn(acc.z, acc.w);
   };
   static_assert(8 * 32 <= NW * 32, "a thread per (head, four dims)");
-  const int h = tid >> 5, i4 = lane;
+  const int h = warp, i4 = lane;
   const bool single = active == 1;
   if (h < G) {
     float M = -INFINITY;
@@ -788,7 +787,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   __syncthreads();
   if (!s_last) return;
   // one round trip for the first partials and all (max, sum) pairs
-  constexpr int FLIGHT = 16;
+  constexpr int FLIGHT = 20;
   float4 pv[FLIGHT];
   const size_t first = blockIdx.x - pc;  // the parts are consecutive CTAs
   const float4* src = reinterpret_cast<const float4*>(a.ws_o + (first * G + min(h, G - 1)) * ATT_D) + i4;
