@@ -325,8 +325,9 @@ __device__ __forceinline__ AtwShare atw_visible(const AtwArgs& a, int len) {
 }
 
 __device__ __forceinline__ int atw_parts(int n, int per) { return min(max((n + per - 1) / per, 1), ATW_MAX_PARTITIONS); }
-__device__ __forceinline__ int atw_per(long long pages, int fit, int min_pages) {
-  return (int)min(max((pages + fit - 1) / fit, (long long)min_pages), (long long)INT_MAX / 2);
+// (the host refuses batches whose pages, times the kv heads, pass 2^30)
+__device__ __forceinline__ int atw_per(unsigned pages, unsigned fit, int min_pages) {
+  return max((int)((pages + fit - 1) / fit), min_pages);
 }
 
 // Up to 32 sequences: one warp's work (every warp's own would be eight times
@@ -335,8 +336,7 @@ __device__ __forceinline__ AtwShare atw_share_warp(const AtwArgs& a, int min_pag
   const int lane = threadIdx.x & 31, cta = blockIdx.x;
   const int len = lane < a.B ? __ldcg(&a.context_lens[lane]) : 0;
   const int n = lane < a.B ? atw_visible(a, len).n : 0;
-  const int pages = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
-  const long long all = (long long)pages * a.Hkv;
+  const unsigned all = __reduce_add_sync(0xffffffffu, (unsigned)n) * (unsigned)a.Hkv;
   int per = atw_per(all, a.fit, min_pages);
   int p = lane < a.B ? atw_parts(n, per) : 0;
   if (__reduce_add_sync(0xffffffffu, (unsigned)p) * (unsigned)a.Hkv > (unsigned)a.slots) {
@@ -369,23 +369,22 @@ __device__ __forceinline__ AtwShare atw_share_warp(const AtwArgs& a, int min_pag
 __device__ __noinline__ AtwShare atw_share_cta(const AtwArgs& a, int min_pages, int* s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x;
-  long long* s64 = reinterpret_cast<long long*>(s);
   auto sum_over = [&](auto term) {  // of every sequence
-    long long v = 0;
+    unsigned v = 0;
     for (int i = tid; i < a.B; i += ATW_NW * 32) v += term(atw_visible(a, __ldcg(&a.context_lens[i])).n);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (lane == 0) s64[warp] = v;
+    v = __reduce_add_sync(0xffffffffu, v);
+    if (lane == 0) s[warp] = (int)v;
     __syncthreads();
     v = 0;
 #pragma unroll
-    for (int w = 0; w < ATW_NW; ++w) v += s64[w];
+    for (int w = 0; w < ATW_NW; ++w) v += (unsigned)s[w];
     __syncthreads();
     return v;
   };
-  const long long all = sum_over([](int n) { return n; }) * a.Hkv;
+  const unsigned all = sum_over([](int n) { return (unsigned)n; }) * (unsigned)a.Hkv;
   int per = atw_per(all, a.fit, min_pages);
-  if (sum_over([&](int n) { return atw_parts(n, per); }) * a.Hkv > a.slots) per = atw_per(all, a.fit_mixed, min_pages);
+  if (sum_over([&](int n) { return (unsigned)atw_parts(n, per); }) * (unsigned)a.Hkv > (unsigned)a.slots)
+    per = atw_per(all, a.fit_mixed, min_pages);
   // the sequence whose CTAs hold this one
   int base = 0;  // CTAs of the sequences before this round's
   int* found = s + 2 * ATW_NW;  // b, first CTA of b, parts
@@ -561,7 +560,9 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     __syncthreads();  // the sines and cosines
     if (warp < (last ? 5 : 4)) {
       uint4 w = qw;
-      rope_rows(w, s_cos, s_sin, lane);
+      RopeLane rope;
+      rope.load(s_cos, s_sin, lane);
+      rope_rows(w, rope);
       if (r < 8) {
         *reinterpret_cast<uint4*>(&s_q[r][8 * c]) = w;
       } else {
@@ -880,7 +881,8 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
   W4_CHECK_ARG(window >= 0 && sinks >= 0, "%s: window=%d sinks=%d", who, window, sinks);
   W4_CHECK_SHAPE(D == ATT_D, "%s: D=%d, only 128 is built", who, D);
   W4_CHECK_SHAPE(Hq % Hkv == 0 && Hq / Hkv <= 8, "%s: Hq=%d Hkv=%d", who, Hq, Hkv);
-  W4_CHECK_SHAPE((long long)B * Hkv <= (1 << 24), "%s: B=%d Hkv=%d", who, B, Hkv);
+  W4_CHECK_SHAPE((long long)B * Hkv <= (1 << 24) && (long long)B * Hkv * (max_context / ATT_PAGE + 1) <= (1 << 30),
+                 "%s: B=%d x Hkv=%d x max_context %d is too large", who, B, Hkv, max_context);
   W4_CHECK_SHAPE((long long)max_context <= (long long)max_blocks * ATT_PAGE, "%s: max_context %d > max_blocks*16", who,
                  max_context);
   const bool fuse = a.fuse_rope_append;

@@ -6,74 +6,77 @@
 namespace w4 {
 
 // ---------------------------------------------------------------------------
-// RoPE + INT4 append: R rows (of the batch or the prompt) per CTA.  Their head
-// rows -- q (rotated), k (rotated, quantised), v (quantised) -- are taken two
-// at a time by a warp, eight dims per lane.  The values do not depend on the
-// positions, so the first of them are asked for before the lengths and the
-// table entries are read and the sines computed; the next are asked for as
-// these are finished.
+// RoPE + INT4 append: R rows (of the batch or the prompt) per CTA, 8 / R warps
+// each.  A row's head rows -- q (rotated), k (rotated, quantised), v
+// (quantised) -- are taken two at a time by a warp, eight dims per lane.  The
+// values do not depend on the position, so the first of them are asked for
+// before the length and the table entry are read and the sines computed; the
+// next are asked for as these are finished.
 // ---------------------------------------------------------------------------
 constexpr int APPEND_WARPS = 8;
 constexpr int APPEND_AHEAD = 3;  // row pairs a warp loads ahead
 
 template <int R>
 __global__ void __launch_bounds__(APPEND_WARPS * 32) w4pg_rope_append_int4(const __grid_constant__ Kv4AppendArgs a) {
+  constexpr int PER = APPEND_WARPS / R;  // warps per row
   __shared__ __align__(16) float s_cos[R][KV4_D / 2], s_sin[R][KV4_D / 2];
   __shared__ int s_slot[R], s_page[R];  // page -1: none; slot -1: a row of length 0
-  const int b0 = blockIdx.x * R, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = warp / PER, w0 = warp % PER;
   const int c = lane & 15, half = lane >> 4;
-  const int per = a.Hq + 2 * a.Hkv;          // head rows per row
-  const int rows = min(R, a.B - b0) * per;
-  auto load = [&](int i) -> uint4 {
-    if (i >= rows) return make_uint4(0u, 0u, 0u, 0u);
-    const int u = R == 1 ? 0 : i / per, r = i - u * per;
-    const size_t b = b0 + u;
-    const __half* src = r < a.Hq ? a.q + b * a.stride_q + (size_t)r * KV4_D
-                                 : (r < a.Hq + a.Hkv ? a.k + b * a.stride_kv + (size_t)(r - a.Hq) * KV4_D
-                                                     : a.v + b * a.stride_kv + (size_t)(r - a.Hq - a.Hkv) * KV4_D);
-    return __ldcg(reinterpret_cast<const uint4*>(src) + c);
+  const size_t b = (size_t)blockIdx.x * R + u;
+  const int rows = b < (size_t)a.B ? a.Hq + 2 * a.Hkv : 0;
+  const __half* qb = a.q + b * a.stride_q + 8 * c;
+  const __half* kb = a.k + b * a.stride_kv + 8 * c;
+  const __half* vb = a.v + b * a.stride_kv + 8 * c;
+  auto load = [&](int r) -> uint4 {
+    if (r >= rows) return make_uint4(0u, 0u, 0u, 0u);
+    const __half* src = r < a.Hq ? qb + (size_t)r * KV4_D
+                                 : (r < a.Hq + a.Hkv ? kb + (size_t)(r - a.Hq) * KV4_D
+                                                     : vb + (size_t)(r - a.Hq - a.Hkv) * KV4_D);
+    return __ldcg(reinterpret_cast<const uint4*>(src));
   };
   pdl_wait_then_trigger();
   uint4 x[APPEND_AHEAD];
 #pragma unroll
-  for (int u = 0; u < APPEND_AHEAD; ++u) x[u] = load(2 * (warp + u * APPEND_WARPS) + half);
+  for (int k = 0; k < APPEND_AHEAD; ++k) x[k] = load(2 * (w0 + k * PER) + half);
   for (int i = tid; i < R * (KV4_D / 2); i += APPEND_WARPS * 32) {
-    const int u = i / (KV4_D / 2), f = i % (KV4_D / 2), b = b0 + u;
-    const int pos = b < a.B ? __ldcg(&a.context_lens[b]) - 1 : -1;
+    const int v = i / (KV4_D / 2), f = i % (KV4_D / 2), bv = blockIdx.x * R + v;
+    const int pos = bv < a.B ? __ldcg(&a.context_lens[bv]) - 1 : -1;
     if (f == 0) {
       const int blk = pos / KV4_PAGE;
-      const int page = pos >= 0 && blk < a.max_blocks ? __ldcg(&a.block_table[(size_t)b * a.max_blocks + blk]) : -1;
+      const int page = pos >= 0 && blk < a.max_blocks ? __ldcg(&a.block_table[(size_t)bv * a.max_blocks + blk]) : -1;
       const bool ok = page >= 0 && page < a.num_pages;
       if (pos >= 0 && !ok && a.err_flag) atomicOr(a.err_flag, 1);
-      s_page[u] = ok ? page : -1;
-      s_slot[u] = pos >= 0 ? pos % KV4_PAGE : -1;
+      s_page[v] = ok ? page : -1;
+      s_slot[v] = pos >= 0 ? pos % KV4_PAGE : -1;
     }
-    sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[f]), &s_sin[u][f], &s_cos[u][f]);
+    sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[f]), &s_sin[v][f], &s_cos[v][f]);
   }
   __syncthreads();
-  for (int i0 = 2 * warp; i0 < rows; i0 += 2 * APPEND_WARPS * APPEND_AHEAD) {
+  const int slot = s_slot[u], page = s_page[u];
+  if (slot < 0) return;
+  RopeLane rope;
+  rope.load(s_cos[u], s_sin[u], lane);
+  for (int r0 = 2 * w0; r0 < rows; r0 += 2 * PER * APPEND_AHEAD) {
 #pragma unroll
     for (int k = 0; k < APPEND_AHEAD; ++k) {
-      const int i = i0 + 2 * k * APPEND_WARPS + half;
-      if (i - half >= rows) break;
-      const int u = R == 1 ? 0 : min(i, rows - 1) / per, r = i - u * per;
+      const int pair = r0 + 2 * k * PER, r = pair + half;
+      if (pair >= rows) break;
       const bool is_q = r < a.Hq, is_k = !is_q && r < a.Hq + a.Hkv;
-      const uint4 raw = x[k];
-      uint4 w = raw;
-      rope_rows(w, s_cos[u], s_sin[u], lane);
-      if (!is_q && !is_k) w = raw;
+      // (a warp's two rows may be of two kinds)
+      uint4 w = x[k];
+      if (pair < a.Hq + a.Hkv) rope_rows(w, rope);
+      if (!is_q && !is_k) w = x[k];
       uint32_t codes = 0u, byte = 0u;
-      if (__any_sync(0xffffffffu, !is_q)) kv4_quantise(w, codes, byte);  // (a warp's two rows may be of two kinds)
-      const int slot = s_slot[u], page = s_page[u];
-      if (i < rows && slot >= 0) {
-        if (is_q) {
-          *reinterpret_cast<uint4*>(a.q_out + (size_t)(b0 + u) * a.stride_qo + (size_t)r * KV4_D + 8 * c) = w;
-        } else if (page >= 0) {
-          const int h = is_k ? r - a.Hq : r - a.Hq - a.Hkv;
-          kv4_put((is_k ? a.k_pool : a.v_pool) + ((size_t)page * a.Hkv + h) * KV4_SLICE, is_k, slot, c, codes, byte);
-        }
+      if (pair + 1 >= a.Hq) kv4_quantise(w, codes, byte);
+      if (is_q) {
+        *reinterpret_cast<uint4*>(a.q_out + b * a.stride_qo + (size_t)r * KV4_D + 8 * c) = w;
+      } else if (page >= 0 && r < rows) {
+        const int h = is_k ? r - a.Hq : r - a.Hq - a.Hkv;
+        kv4_put((is_k ? a.k_pool : a.v_pool) + ((size_t)page * a.Hkv + h) * KV4_SLICE, is_k, slot, c, codes, byte);
       }
-      x[k] = load(i + 2 * APPEND_WARPS * APPEND_AHEAD);
+      x[k] = load(r + 2 * PER * APPEND_AHEAD);
     }
   }
 }

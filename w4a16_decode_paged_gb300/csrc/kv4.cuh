@@ -42,10 +42,13 @@ __device__ __forceinline__ int kv4_v_scale(int t, int c) {
   return KV4_CODES + 16 * c + 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1);
 }
 
-// Scale byte of a group whose largest magnitude has the fp16 bits `bits`.
+// Scale byte of a group whose largest magnitude has the fp16 bits `bits`: the
+// smallest scale s with 7 s >= amax.  amax / 7 is taken a little too small
+// (times 1/7 rounded down): where it is a scale exactly, rounding up brings it
+// back; elsewhere amax, of 11 bits, is 2^-12 or more away from 7 s, of 7 bits.
 __device__ __forceinline__ uint32_t kv4_scale_byte(uint32_t bits) {
   if (bits >= 0x7C00u) return 0xFFu;  // an infinity or a NaN
-  const float r = __fdiv_rn(__half2float(__ushort_as_half((unsigned short)bits)), 7.0f);
+  const float r = __half2float(__ushort_as_half((unsigned short)bits)) * __uint_as_float(0x3E124924u);
   // the 3 leading fraction bits rounded up (a carry moves the exponent on);
   // below fp16's normal range multiples of 2^-17
   if (r < 0x1p-14f) return (uint32_t)ceilf(r * 0x1p17f);
@@ -68,14 +71,20 @@ __device__ __forceinline__ void kv4_quantise(const uint4& x, uint32_t& codes, ui
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   byte = kv4_scale_byte(m);
-  const float s = kv4_scale_value(byte);
   const bool live = byte != 0u && byte != 0xFFu;
-  codes = 0u;
+  // q = x / s to nearest even, without a division per value: y = x (1/s) is off
+  // by 2^-21 at most.  x / s is a tie n + 1/2 exactly or 2^-12 or more away from
+  // one (x has 11 bits, (n + 1/2) s has 8), so rounding y to multiples of 2^-14
+  // first (the sum with 768 and back) makes ties exact and moves no other
+  // across.  The sum with 1.5 * 2^23 then leaves q in the low bits.
+  const float inv = live ? __frcp_rn(kv4_scale_value(byte)) : 0.f;
+  codes = 0x88888888u - 0x4B400000u * 0x11111111u;  // (q + 8) 16^e, summed modulo 2^32
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float v = __half2float(__ushort_as_half((unsigned short)((&x.x)[e >> 1] >> (16 * (e & 1)))));
-    const int q = live ? __float2int_rn(__fdiv_rn(v, s)) : 0;
-    codes |= (uint32_t)(q + 8) << (4 * e);
+    float y = live ? __fmul_rn(v, inv) : 0.f;
+    y = __fsub_rn(__fadd_rn(y, 768.0f), 768.0f);
+    codes += __float_as_uint(__fadd_rn(y, 12582912.0f)) << (4 * e);
   }
 }
 
@@ -93,28 +102,31 @@ __device__ __forceinline__ void kv4_put(uint8_t* slice, bool is_k, int t, int c,
 // Rotate-half RoPE of rows held eight dims per lane (as above): the partner
 // dims i +- 64 sit eight lanes away.  cs, sn: 64 cosines and sines.  Products
 // and their sum are rounded one by one, so every caller gets the same bits.
-__device__ __forceinline__ float rope_lo(float x0, float x1, float c, float s) {
-  return __fsub_rn(__fmul_rn(x0, c), __fmul_rn(x1, s));
-}
-__device__ __forceinline__ float rope_hi(float x0, float x1, float c, float s) {
-  return __fadd_rn(__fmul_rn(x1, c), __fmul_rn(x0, s));
-}
-__device__ __forceinline__ void rope_rows(uint4& x, const float* cs, const float* sn, int lane) {
-  const int i = 8 * (lane & 7);
-  const bool low = (lane & 8) == 0;
-  const float4 c0 = *reinterpret_cast<const float4*>(cs + i), c1 = *reinterpret_cast<const float4*>(cs + i + 4);
-  const float4 s0 = *reinterpret_cast<const float4*>(sn + i), s1 = *reinterpret_cast<const float4*>(sn + i + 4);
+// This lane's eight cosines and sines of one position, the sines with the sign
+// that the lane's half of the row takes them with: the low half rotates to
+// x c - y s, the high half to x c + y s (x its own, y the partner's).
+struct RopeLane {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const float* cs, const float* sn, int lane) {
+    const int i = 8 * (lane & 7);
+    const float sign = (lane & 8) == 0 ? -1.f : 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      c[e] = cs[i + e];
+      s[e] = sign * sn[i + e];
+    }
+  }
+};
+__device__ __forceinline__ void rope_rows(uint4& x, const RopeLane& t) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const uint32_t y = __shfl_xor_sync(0xffffffffu, (&x.x)[w], 8);
     float r[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int k = 2 * w + e;
-      const float c = k < 4 ? (&c0.x)[k] : (&c1.x)[k - 4], s = k < 4 ? (&s0.x)[k] : (&s1.x)[k - 4];
       const float own = __half2float(__ushort_as_half((unsigned short)((&x.x)[w] >> (16 * e))));
       const float other = __half2float(__ushort_as_half((unsigned short)(y >> (16 * e))));
-      r[e] = low ? rope_lo(own, other, c, s) : rope_hi(other, own, c, s);
+      r[e] = __fadd_rn(__fmul_rn(own, t.c[2 * w + e]), __fmul_rn(other, t.s[2 * w + e]));
     }
     const __half2 h = __floats2half2_rn(r[0], r[1]);
     (&x.x)[w] = *reinterpret_cast<const uint32_t*>(&h);
