@@ -38,7 +38,6 @@
 
 namespace w4 {
 
-constexpr int ATW_NW = 8;              // warps per CTA
 constexpr int ATW_PITCH = ATT_D + 4;   // floats per head in the warps' merge
 constexpr float ATW_SLACK = 2.0f;
 constexpr float ATW_V8 = 64.0f;        // FP8: factor that keeps p * (V row scale) in fp16's normal range
@@ -92,6 +91,7 @@ struct Page;
 
 template <>
 struct Page<ATW_F16> {
+  static constexpr int NW = 8;      // warps per CTA
   static constexpr int BATCH = 1;   // pages per step of a warp
   static constexpr int STAGES = 2;  // steps in flight per warp
   static constexpr int MIN_CTAS = 1;
@@ -148,6 +148,7 @@ struct Page<ATW_F16> {
 
 template <>
 struct Page<ATW_F8> {
+  static constexpr int NW = 8;
   static constexpr int BATCH = 1;
   static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
@@ -223,6 +224,7 @@ struct Page<ATW_F8> {
 
 template <>
 struct Page<ATW_I4> {
+  static constexpr int NW = 8;
   static constexpr int BATCH = 2;
   static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
@@ -365,19 +367,20 @@ __device__ __forceinline__ AtwShare atw_share_warp(const AtwArgs& a, int min_pag
   return r;
 }
 
-// More: CTA-wide; s: 2 * ATW_NW + 8 ints of shared memory.
+// More: CTA-wide; s: 24 ints of shared memory.
+template <int NW>
 __device__ __noinline__ AtwShare atw_share_cta(const AtwArgs& a, int min_pages, int* s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x;
   auto sum_over = [&](auto term) {  // of every sequence
     unsigned v = 0;
-    for (int i = tid; i < a.B; i += ATW_NW * 32) v += term(atw_visible(a, __ldcg(&a.context_lens[i])).n);
+    for (int i = tid; i < a.B; i += NW * 32) v += term(atw_visible(a, __ldcg(&a.context_lens[i])).n);
     v = __reduce_add_sync(0xffffffffu, v);
     if (lane == 0) s[warp] = (int)v;
     __syncthreads();
     v = 0;
 #pragma unroll
-    for (int w = 0; w < ATW_NW; ++w) v += (unsigned)s[w];
+    for (int w = 0; w < NW; ++w) v += (unsigned)s[w];
     __syncthreads();
     return v;
   };
@@ -387,9 +390,9 @@ __device__ __noinline__ AtwShare atw_share_cta(const AtwArgs& a, int min_pages, 
     per = atw_per(all, a.fit_mixed, min_pages);
   // the sequence whose CTAs hold this one
   int base = 0;  // CTAs of the sequences before this round's
-  int* found = s + 2 * ATW_NW;  // b, first CTA of b, parts
+  int* found = s + 16;  // b, first CTA of b, parts
   if (tid == 0) found[0] = -1;
-  for (int i0 = 0; i0 < a.B; i0 += ATW_NW * 32) {
+  for (int i0 = 0; i0 < a.B; i0 += NW * 32) {
     const int i = i0 + tid;
     const int p = i < a.B ? atw_parts(atw_visible(a, __ldcg(&a.context_lens[i])).n, per) : 0;
     int sum = p * a.Hkv;  // inclusive prefix sum over the threads
@@ -402,7 +405,7 @@ __device__ __noinline__ AtwShare atw_share_cta(const AtwArgs& a, int min_pages, 
     __syncthreads();
     int before = base, after = base;
 #pragma unroll
-    for (int w = 0; w < ATW_NW; ++w) {
+    for (int w = 0; w < NW; ++w) {
       if (w < warp) before += s[w];
       after += s[w];
     }
@@ -429,18 +432,17 @@ __device__ __noinline__ AtwShare atw_share_cta(const AtwArgs& a, int min_pages, 
 }
 
 template <int KIND>
-constexpr size_t atw_ring_bytes() { return (size_t)ATW_NW * Page<KIND>::STAGES * Page<KIND>::BATCH * Page<KIND>::SLOT; }
-constexpr size_t ATW_MERGE_BYTES = (size_t)ATW_NW * 8 * ATW_PITCH * 4;
+constexpr size_t atw_ring_bytes() { return (size_t)Page<KIND>::NW * Page<KIND>::STAGES * Page<KIND>::BATCH * Page<KIND>::SLOT; }
 template <int KIND>
-constexpr size_t atw_smem() { return std::max(atw_ring_bytes<KIND>(), ATW_MERGE_BYTES); }
+constexpr size_t atw_smem() { return std::max(atw_ring_bytes<KIND>(), (size_t)Page<KIND>::NW * 8 * ATW_PITCH * 4); }
 
 constexpr uint32_t ATW_WAIT_POLLS = 1u << 20;  // bound of a wait for copies
 
 template <int KIND, bool FUSE>
-__global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
+__global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     w4pg_attn_window(const __grid_constant__ AtwArgs a) {
   using PG = Page<KIND>;
-  constexpr int NW = ATW_NW, BATCH = PG::BATCH, STAGES = PG::STAGES;
+  constexpr int NW = PG::NW, BATCH = PG::BATCH, STAGES = PG::STAGES;
   extern __shared__ __align__(128) unsigned char smraw[];  // the warps' rings, then their merge
   __shared__ __align__(16) __half s_q[8][ATT_D + 8];
   __shared__ float s_ml[NW * 8 * 2];
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   __shared__ uint8_t s_news[2][4];
   __shared__ __align__(8) uint64_t s_bar[NW * STAGES];
   __shared__ float2 s_part[ATW_MAX_PARTITIONS * 8];
-  __shared__ __align__(8) int s_scan[2 * NW + 8];
+  __shared__ int s_scan[24];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -482,7 +484,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     sh.part = s_scan[2];
     sh.parts = s_scan[3];
   } else {
-    sh = atw_share_cta(a, PG::MIN_PAGES, s_scan);
+    sh = atw_share_cta<NW>(a, PG::MIN_PAGES, s_scan);
   }
   if (sh.b < 0) return;
   const int b = sh.b, kvh = sh.kvh, pc = sh.part, active = sh.parts;
@@ -742,10 +744,10 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     *reinterpret_cast<__half2*>(out + PG::odim(mt, g0)) = __floats2half2_rn(acc.x, acc.y);
     *reinterpret_cast<__half2*>(out + PG::odim(mt, g0 + 1)) = __floats2half2_rn(acc.z, acc.w);
   };
-  static_assert(8 * 32 <= NW * 32, "a thread per (head, four dims)");
-  const int h = warp, i4 = lane;
+  static_assert(8 % NW == 0, "a warp per head, or for a few heads");
+  const int i4 = lane;
   const bool single = active == 1;
-  if (h < G) {
+  for (int h = warp; h < G; h += NW) {
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[(w * 8 + h) * 2]);
@@ -789,19 +791,23 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
   if (!s_last) return;
   // one round trip for the first partials and all (max, sum) pairs
   constexpr int FLIGHT = 20;
-  float4 pv[FLIGHT];
   const size_t first = blockIdx.x - pc;  // the parts are consecutive CTAs
-  const float4* src = reinterpret_cast<const float4*>(a.ws_o + (first * G + min(h, G - 1)) * ATT_D) + i4;
   const size_t pitch = (size_t)G * (ATT_D / 4);
+  const float4* src = reinterpret_cast<const float4*>(a.ws_o + first * G * ATT_D) + i4;
+  float4 pv[FLIGHT];
+  auto ask = [&](int h) {
 #pragma unroll
-  for (int j = 0; j < FLIGHT; ++j)
-    if (j < active) pv[j] = __ldcg(src + (size_t)j * pitch);
+    for (int j = 0; j < FLIGHT; ++j)
+      if (j < active) pv[j] = __ldcg(src + (size_t)h * (ATT_D / 4) + (size_t)j * pitch);
+  };
+  if (warp < G) ask(warp);
   for (int idx = tid; idx < G * active; idx += NW * 32) {
     const int j = idx / G, hh = idx - j * G;
     s_part[hh * ATW_MAX_PARTITIONS + j] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + first * G + idx);
   }
   __syncthreads();
-  if (h < G) {
+  for (int h = warp; h < G; h += NW) {
+    if (h != warp) ask(h);
     const float2* ml = s_part + h * ATW_MAX_PARTITIONS;
     float M = -INFINITY;
     for (int j = 0; j < active; ++j) M = fmaxf(M, ml[j].x);
@@ -820,7 +826,7 @@ __global__ void __launch_bounds__(ATW_NW * 32, Page<KIND>::MIN_CTAS)
     for (int j = 0; j < FLIGHT; ++j)
       if (j < active) add(j, pv[j]);
 #pragma unroll 8
-    for (int j = FLIGHT; j < active; ++j) add(j, __ldcg(src + (size_t)j * pitch));
+    for (int j = FLIGHT; j < active; ++j) add(j, __ldcg(src + (size_t)h * (ATT_D / 4) + (size_t)j * pitch));
     const float inv = den == 0.f ? 0.f : atw_o_factor<KIND>() / den;
     write_out(h, i4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   }
@@ -838,7 +844,8 @@ static void atw_plan(AtwArgs& a, int kind, int B, int Hkv, int max_context, int 
   const long long n = std::min(all, seen);
   const int min_pages = kind == ATW_F16 ? Page<ATW_F16>::MIN_PAGES
                                         : (kind == ATW_F8 ? Page<ATW_F8>::MIN_PAGES : Page<ATW_I4>::MIN_PAGES);
-  a.slots = kind == ATW_F16 ? ATW_SMS : 2 * ATW_SMS;  // (fp16 pages: one CTA's rings fill an SM)
+  a.slots = ATW_SMS * (kind == ATW_F16 ? Page<ATW_F16>::MIN_CTAS
+                                       : (kind == ATW_F8 ? Page<ATW_F8>::MIN_CTAS : Page<ATW_I4>::MIN_CTAS));
   a.fit = groups <= a.slots ? (int)(a.slots / groups * groups) : a.slots;
   a.fit_mixed = (int)std::max(a.slots - groups / 2, a.slots / 2ll);
   a.ctas = (int)std::min(groups * std::min((n + min_pages - 1) / min_pages, (long long)ATW_MAX_PARTITIONS),
@@ -855,7 +862,7 @@ static int launch_atw(const AtwArgs& a, cudaStream_t s) {
   constexpr size_t smem = atw_smem<KIND>();
   auto kern = w4pg_attn_window<KIND, FUSE>;
   once_per_device(once, [&] { cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
-  cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(ATW_NW * 32), smem, s, a);
+  cudaError_t e = launch_pdl(kern, dim3(a.ctas), dim3(Page<KIND>::NW * 32), smem, s, a);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }

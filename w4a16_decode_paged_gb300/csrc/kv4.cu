@@ -17,7 +17,7 @@ constexpr int APPEND_WARPS = 8;
 constexpr int APPEND_AHEAD = 3;  // row pairs a warp loads ahead
 
 template <int R>
-__global__ void __launch_bounds__(APPEND_WARPS * 32) w4pg_rope_append_int4(const __grid_constant__ Kv4AppendArgs a) {
+__global__ void __launch_bounds__(APPEND_WARPS * 32, 4) w4pg_rope_append_int4(const __grid_constant__ Kv4AppendArgs a) {
   constexpr int PER = APPEND_WARPS / R;  // warps per row
   __shared__ __align__(16) float s_cos[R][KV4_D / 2], s_sin[R][KV4_D / 2];
   __shared__ int s_slot[R], s_page[R];  // page -1: none; slot -1: a row of length 0
