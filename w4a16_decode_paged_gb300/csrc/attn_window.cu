@@ -86,6 +86,12 @@ __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t
                : "memory");
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// BULK: one lane's fetch() issues the copies of a page, which complete on an
+// mbarrier; else all lanes' fetch() does, as a group of asynchronous copies.
 template <int KIND>
 struct Page;
 
@@ -96,25 +102,37 @@ struct Page<ATW_F16> {
   static constexpr int STAGES = 2;  // steps in flight per warp
   static constexpr int MIN_CTAS = 1;
   static constexpr int MIN_PAGES = 8;
+  static constexpr bool BULK = false;
   static constexpr int V = 4096;    // V's offset in a page's slot
   static constexpr int SLOT = 8192;
   // dim of element e (0, 1) of query register r (0, 1) in step st
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
-    return 32 * (st >> 1) + 8 * t4 + 4 * (st & 1) + 2 * r + e;
+    return 64 * (st >> 2) + 16 * t4 + 8 * ((st >> 1) & 1) + 4 * (st & 1) + 2 * r + e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 64 * (mt >> 2) + 8 * g + 2 * (mt & 3); }
-  // the copies of one page (one lane issues them)
-  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, uint32_t bar) {
-    bulk_g2s(slot, static_cast<const __half*>(a.k) + slice * ATT_SLICE, 4096, bar);
-    bulk_g2s(slot + V, static_cast<const __half*>(a.v) + slice * ATT_SLICE, 4096, bar);
+  // Rows of 256 bytes, copied 512 bytes per instruction; the 16-byte chunks of
+  // each half row are permuted by the row (chunk ^ row % 8), so that neither
+  // the K reads (two rows, every other chunk) nor the V reads (four rows, one
+  // chunk) of eight lanes meet in a bank.
+  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, int lane) {
+    const unsigned char* k = static_cast<const unsigned char*>(a.k) + slice * 4096 + 16 * lane;
+    const unsigned char* v = static_cast<const unsigned char*>(a.v) + slice * 4096 + 16 * lane;
+    const int row = lane >> 4, c = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t at = slot + 512 * i + 256 * row + 16 * (c ^ ((2 * i + row) & 7));
+      copy16(at, k + 512 * i);
+      copy16(at + V, v + 512 * i);
+    }
   }
   // S^T += K Q^T of one page, scaled where the kind has K row scales
-  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias& bias,
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias&,
                                                 const uint32_t (&qb)[8][2], float (&s)[4]) {
-    const unsigned char* p = slot + 256 * g + 16 * t4;
+    const unsigned char* p = slot + 256 * g;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p + 64 * i), y = *reinterpret_cast<const uint4*>(p + 2048 + 64 * i);
+      const int at = 128 * (i >> 1) + 16 * ((2 * t4 + (i & 1)) ^ g);
+      const uint4 x = *reinterpret_cast<const uint4*>(p + at), y = *reinterpret_cast<const uint4*>(p + 2048 + at);
       mma(s, x.x, y.x, x.y, y.y, qb[2 * i][0], qb[2 * i][1]);
       mma(s, x.z, y.z, x.w, y.w, qb[2 * i + 1][0], qb[2 * i + 1][1]);
     }
@@ -127,13 +145,14 @@ struct Page<ATW_F16> {
   template <bool MASK>
   static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
                                                 uint32_t b0, uint32_t b1, float (&o)[8][4]) {
-    const unsigned char* p = slot + V + 512 * t4 + 16 * g;
+    const unsigned char* p = slot + V + 512 * t4;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       uint4 w[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        w[r] = *reinterpret_cast<const uint4*>(p + 256 * (r & 1) + 2048 * (r >> 1) + 128 * i);
+        w[r] = *reinterpret_cast<const uint4*>(p + 256 * (r & 1) + 2048 * (r >> 1) + 128 * i +
+                                               16 * (g ^ (2 * t4 + (r & 1))));
         if (MASK && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
@@ -153,24 +172,34 @@ struct Page<ATW_F8> {
   static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 16;
+  static constexpr bool BULK = false;
   static constexpr int V = 2048, KS = 4096, VS = 4160;
   static constexpr int SLOT = 4224;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
-    return 64 * (st >> 2) + 16 * t4 + 4 * (st & 3) + 2 * r + e;
+    return 32 * t4 + 16 * (st >> 2) + 4 * (st & 3) + 2 * r + e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 16 * g + 2 * mt; }
-  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, uint32_t bar) {
-    bulk_g2s(slot, static_cast<const uint8_t*>(a.k) + slice * ATT_SLICE, 2048, bar);
-    bulk_g2s(slot + V, static_cast<const uint8_t*>(a.v) + slice * ATT_SLICE, 2048, bar);
-    bulk_g2s(slot + KS, a.ks + slice * ATT_PAGE, 64, bar);
-    bulk_g2s(slot + VS, a.vs + slice * ATT_PAGE, 64, bar);
+  // (rows of 128 bytes, their chunks permuted as those of fp16 pages)
+  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, int lane) {
+    const unsigned char* k = static_cast<const unsigned char*>(a.k) + slice * 2048 + 16 * lane;
+    const unsigned char* v = static_cast<const unsigned char*>(a.v) + slice * 2048 + 16 * lane;
+    const int row = lane >> 3, c = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = slot + 512 * i + 128 * row + 16 * (c ^ ((4 * i + row) & 7));
+      copy16(at, k + 512 * i);
+      copy16(at + V, v + 512 * i);
+    }
+    if (lane < 8)
+      copy16(slot + KS + 16 * lane, (lane < 4 ? a.ks + slice * ATT_PAGE : a.vs + slice * ATT_PAGE) + 4 * (lane & 3));
   }
-  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias& bias,
+  static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias&,
                                                 const uint32_t (&qb)[8][2], float (&s)[4]) {
-    const unsigned char* p = slot + 128 * g + 16 * t4;
+    const unsigned char* p = slot + 128 * g;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p + 64 * i), y = *reinterpret_cast<const uint4*>(p + 1024 + 64 * i);
+      const int at = 16 * ((2 * t4 + i) ^ g);
+      const uint4 x = *reinterpret_cast<const uint4*>(p + at), y = *reinterpret_cast<const uint4*>(p + 1024 + at);
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t a0, a1, a2, a3;
@@ -201,11 +230,11 @@ struct Page<ATW_F8> {
   template <bool MASK>
   static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
                                                 uint32_t b0, uint32_t b1, float (&o)[8][4]) {
-    const unsigned char* p = slot + V + 256 * t4 + 16 * g;
+    const unsigned char* p = slot + V + 256 * t4;
     uint4 w[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      w[r] = *reinterpret_cast<const uint4*>(p + 128 * (r & 1) + 1024 * (r >> 1));
+      w[r] = *reinterpret_cast<const uint4*>(p + 128 * (r & 1) + 1024 * (r >> 1) + 16 * (g ^ (2 * t4 + (r & 1))));
       if (MASK && !((live >> (2 * t4 + (r & 1) + 8 * (r >> 1))) & 1u)) w[r] = make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
@@ -229,6 +258,7 @@ struct Page<ATW_I4> {
   static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 32;
+  static constexpr bool BULK = true;
   static constexpr int V = KV4_SLICE;
   static constexpr int SLOT = 2 * KV4_SLICE;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
@@ -540,17 +570,29 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
       got |= (id[j] >= 0 ? 1u : 0u) << j;
     }
     have = (have & ~(((1u << BATCH) - 1u) << (stage * BATCH))) | (got << (stage * BATCH));
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&bar[stage], __popc(got) * PG::SLOT);
+    if constexpr (PG::BULK) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar[stage], __popc(got) * PG::SLOT);
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+          if (id[j] >= 0)
+            PG::fetch(a, (size_t)id[j] * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT,
+                      smem_u32(&bar[stage]));
+      }
+    } else {
 #pragma unroll
       for (int j = 0; j < BATCH; ++j)
         if (id[j] >= 0)
-          PG::fetch(a, (size_t)id[j] * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, smem_u32(&bar[stage]));
+          PG::fetch(a, (size_t)id[j] * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, lane);
     }
   };
   if (FUSE && tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
   __syncwarp();
-  for (int st = 0; st < STAGES && st < steps; ++st) issue(st, st);
+#pragma unroll
+  for (int st = 0; st < STAGES; ++st) {
+    if (st < steps) issue(st, st);
+    if (!PG::BULK) cp_async_commit();
+  }
   // pages some of whose tokens are masked: the last of the sinks, the first of
   // the window, the last of the sequence (-1: none; fused: the new token's)
   const int part_s = S % ATT_PAGE ? nsp - 1 : -1;
@@ -693,8 +735,13 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   };
   for (int step = 0; step < steps; ++step) {
     const int v = wv0 + step * NW * BATCH;  // first visible page of this step
-    landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, ATW_WAIT_POLLS));
-    if (!landed) break;
+    if constexpr (PG::BULK) {
+      landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, ATW_WAIT_POLLS));
+      if (!landed) break;
+    } else {
+      cp_async_wait<STAGES - 1>();  // this lane's copies,
+      __syncwarp();                 // and every other's
+    }
     const bool whole = ((have >> (stage * BATCH)) & ((1u << BATCH) - 1u)) == (1u << BATCH) - 1u &&
                        (unsigned)(part_s - v) >= (unsigned)BATCH && (unsigned)(part_w - v) >= (unsigned)BATCH &&
                        (unsigned)(part_l - v) >= (unsigned)BATCH;
@@ -702,11 +749,13 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     else attend(std::true_type{}, v);
     __syncwarp();  // every lane has read the stage
     if (step + STAGES < steps) issue(step + STAGES, stage);
+    if (!PG::BULK) cp_async_commit();
     if (++stage == STAGES) {
       stage = 0;
       parity ^= 1u;
     }
   }
+  if (!PG::BULK) cp_async_wait<0>();
   if (!landed) {
     // a wait ran out: report it, and give the copies still in flight their
     // time before the ring's memory changes hands
