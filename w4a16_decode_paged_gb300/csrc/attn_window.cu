@@ -14,10 +14,13 @@
 //   O^T[128 dims][8 heads]  += V^T P^T
 // so both products use all 16 rows (heads as rows would leave half of them
 // zero), the accumulators of 8 heads x 128 dims are 32 registers a lane, and a
-// lane's K rows and V dims are contiguous: a page's (page, kv head) slices are
-// copied whole, by bulk copies, into the warp's ring in shared memory, read
-// back with 16-byte loads and widened in registers.  P^T is the scores'
-// accumulator transposed 8x8 by 8x8 with movmatrix.
+// lane's K rows and V dims are contiguous: a page's (page, kv head) slices go
+// whole, 512 bytes per asynchronous copy, into the warp's ring in shared memory,
+// are read back with 16-byte loads free of bank conflicts, and are widened in
+// registers.  (Bulk copies to mbarriers measured the same for INT4 pages, and
+// slower for the others, whose rows they cannot permute; copies straight to
+// registers had too little in flight.)  P^T is the scores' accumulator
+// transposed 8x8 by 8x8 with movmatrix.
 //
 // Softmax: p = exp2(s - m) with a reference m per head that is the running
 // maximum as of the last time a score passed it by more than 2^ATW_SLACK;
@@ -78,20 +81,10 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
 // k_frag gives the A fragments of MMA step st (st of 8), v_frag those of the
 // 16 dims of block mt (mt of 8).
 // ---------------------------------------------------------------------------
-// One bulk copy (16-byte aligned both ends, bytes a multiple of 16) that
-// completes on the mbarrier.
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
-
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// BULK: one lane's fetch() issues the copies of a page, which complete on an
-// mbarrier; else all lanes' fetch() does, as a group of asynchronous copies.
 template <int KIND>
 struct Page;
 
@@ -102,7 +95,6 @@ struct Page<ATW_F16> {
   static constexpr int STAGES = 2;  // steps in flight per warp
   static constexpr int MIN_CTAS = 1;
   static constexpr int MIN_PAGES = 8;
-  static constexpr bool BULK = false;
   static constexpr int V = 4096;    // V's offset in a page's slot
   static constexpr int SLOT = 8192;
   // dim of element e (0, 1) of query register r (0, 1) in step st
@@ -172,7 +164,6 @@ struct Page<ATW_F8> {
   static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 16;
-  static constexpr bool BULK = false;
   static constexpr int V = 2048, KS = 4096, VS = 4160;
   static constexpr int SLOT = 4224;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
@@ -258,22 +249,31 @@ struct Page<ATW_I4> {
   static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 32;
-  static constexpr bool BULK = true;
-  static constexpr int V = KV4_SLICE;
+  static constexpr int V = 1024, KS = 2048, VS = 2112;
   static constexpr int SLOT = 2 * KV4_SLICE;
   static __device__ __forceinline__ int qdim(int st, int t4, int r, int e) {
     return 32 * t4 + 8 * (st >> 1) + 2 * (st & 1) + r + 4 * e;
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 16 * g + 2 * mt; }
-  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, uint32_t bar) {
-    bulk_g2s(slot, static_cast<const uint8_t*>(a.k) + slice * KV4_SLICE, KV4_SLICE, bar);
-    bulk_g2s(slot + V, static_cast<const uint8_t*>(a.v) + slice * KV4_SLICE, KV4_SLICE, bar);
+  // K rows as they are (a lane reads the chunks it copied); the 16-byte chunks
+  // of a V pair's 128 bytes permuted by the pair, so that the reads of eight
+  // lanes (four pairs, two chunks) do not meet in a bank
+  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, int lane) {
+    const uint8_t* k = static_cast<const uint8_t*>(a.k) + slice * KV4_SLICE + 16 * lane;
+    const uint8_t* v = static_cast<const uint8_t*>(a.v) + slice * KV4_SLICE + 16 * lane;
+    const int pair = lane >> 3, c = lane & 7;
+    const uint32_t kd = slot + 16 * lane, vd = slot + V + 128 * pair + 16 * (c ^ (2 * pair));
+    copy16(kd, k);
+    copy16(kd + 512, k + 512);
+    copy16(vd, v);
+    copy16(vd + 512, v + 512);
+    if (lane < 8) copy16(slot + KS + 16 * lane, (lane < 4 ? k : v - 64) + KV4_CODES);
   }
   static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias& bias,
                                                 const uint32_t (&qb)[8][2], float (&s)[4]) {
     const uint4 k0 = *reinterpret_cast<const uint4*>(slot + kv4_k_code(g, 8 * t4));
     const uint4 k1 = *reinterpret_cast<const uint4*>(slot + kv4_k_code(g + 8, 8 * t4));
-    const uint32_t ks = *reinterpret_cast<const uint16_t*>(slot + kv4_k_scale(g, t4));  // tokens g and g + 8
+    const uint32_t ks = *reinterpret_cast<const uint16_t*>(slot + KS - KV4_CODES + kv4_k_scale(g, t4));  // tokens g and g + 8
     const Kv4Scale s0 = kv4_scale_pair((ks & 0xFFu) * 0x00800080u), s1 = kv4_scale_pair((ks >> 8) * 0x00800080u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -289,10 +289,10 @@ struct Page<ATW_I4> {
   template <bool MASK>
   static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
                                                 uint32_t b0, uint32_t b1, float (&o)[8][4]) {
-    const uint4 v0 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4, 4 * g));
-    const uint4 v1 = *reinterpret_cast<const uint4*>(slot + V + kv4_v_code(2 * t4 + 8, 4 * g));
+    const unsigned char* p = slot + V + 128 * t4 + 16 * (g ^ (2 * t4));
+    const uint4 v0 = *reinterpret_cast<const uint4*>(p), v1 = *reinterpret_cast<const uint4*>(p + 512);
     // scale bytes of tokens 2 t4, 2 t4 + 1, 8 + 2 t4, 9 + 2 t4; a zero scale makes every code zero
-    uint32_t vs = *reinterpret_cast<const uint32_t*>(slot + V + kv4_v_scale(2 * t4, g >> 1));
+    uint32_t vs = *reinterpret_cast<const uint32_t*>(slot + VS - KV4_CODES + kv4_v_scale(2 * t4, g >> 1));
     if (MASK) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -312,9 +312,11 @@ struct Page<ATW_I4> {
   static __device__ __forceinline__ void patch(unsigned char* slot, const uint16_t (&codes)[2][32],
                                                const uint8_t (&scales)[2][4], int t, int lane) {
     *reinterpret_cast<uint16_t*>(slot + kv4_k_code(t, lane)) = codes[0][lane];
-    *reinterpret_cast<uint16_t*>(slot + V + kv4_v_code(t, lane)) = codes[1][lane];
-    if (lane < 4) slot[kv4_k_scale(t, lane)] = scales[0][lane];
-    else if (lane < 8) slot[V + kv4_v_scale(t, lane - 4)] = scales[1][lane - 4];
+    const int pair = t >> 1;  // (dims 4 lane .. are in chunk lane / 4 of the pair)
+    *reinterpret_cast<uint16_t*>(slot + V + 128 * pair + 16 * ((lane >> 2) ^ (2 * pair & 7)) + 4 * (lane & 3) +
+                                 2 * (t & 1)) = codes[1][lane];
+    if (lane < 4) slot[KS - KV4_CODES + kv4_k_scale(t, lane)] = scales[0][lane];
+    else if (lane < 8) slot[VS - KV4_CODES + kv4_v_scale(t, lane - 4)] = scales[1][lane - 4];
   }
 };
 
@@ -466,8 +468,6 @@ constexpr size_t atw_ring_bytes() { return (size_t)Page<KIND>::NW * Page<KIND>::
 template <int KIND>
 constexpr size_t atw_smem() { return std::max(atw_ring_bytes<KIND>(), (size_t)Page<KIND>::NW * 8 * ATW_PITCH * 4); }
 
-constexpr uint32_t ATW_WAIT_POLLS = 1u << 20;  // bound of a wait for copies
-
 template <int KIND, bool FUSE>
 __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     w4pg_attn_window(const __grid_constant__ AtwArgs a) {
@@ -479,7 +479,6 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   __shared__ __align__(16) float s_cos[FUSE ? ATT_D / 2 : 4], s_sin[FUSE ? ATT_D / 2 : 4];
   __shared__ __align__(16) uint16_t s_new[2][32];  // codes of the new K and V rows (fused)
   __shared__ uint8_t s_news[2][4];
-  __shared__ __align__(8) uint64_t s_bar[NW * STAGES];
   __shared__ float2 s_part[ATW_MAX_PARTITIONS * 8];
   __shared__ int s_scan[24];
   __shared__ int s_last;
@@ -487,9 +486,6 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int G = a.G;
-  uint64_t* bar = s_bar + warp * STAGES;
-  if (lane < STAGES) mbar_init(&bar[lane], 1);
-  fence_mbar_init();
   W4_TRACE_SCOPE(a.tag);
   pdl_wait_then_trigger();
   W4_TRACE_WAITED();
@@ -562,36 +558,21 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     const int i = (st * BATCH) & 31;
     if (i == 0 && st > 0) ids = ids_next;
     if (i == BATCH) ids_next = table(st * BATCH - BATCH + 32 + lane);
-    int id[BATCH];
-    unsigned got = 0;
+    have &= ~(((1u << BATCH) - 1u) << (stage * BATCH));
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      id[j] = __shfl_sync(0xffffffffu, ids, i + j);
-      got |= (id[j] >= 0 ? 1u : 0u) << j;
-    }
-    have = (have & ~(((1u << BATCH) - 1u) << (stage * BATCH))) | (got << (stage * BATCH));
-    if constexpr (PG::BULK) {
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar[stage], __popc(got) * PG::SLOT);
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j)
-          if (id[j] >= 0)
-            PG::fetch(a, (size_t)id[j] * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT,
-                      smem_u32(&bar[stage]));
+      const int id = __shfl_sync(0xffffffffu, ids, i + j);
+      if (id >= 0) {
+        PG::fetch(a, (size_t)id * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, lane);
+        have |= 1u << (stage * BATCH + j);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < BATCH; ++j)
-        if (id[j] >= 0)
-          PG::fetch(a, (size_t)id[j] * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, lane);
     }
   };
   if (FUSE && tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
-  __syncwarp();
 #pragma unroll
   for (int st = 0; st < STAGES; ++st) {
     if (st < steps) issue(st, st);
-    if (!PG::BULK) cp_async_commit();
+    cp_async_commit();  // (a group per step, empty behind the last)
   }
   // pages some of whose tokens are masked: the last of the sinks, the first of
   // the window, the last of the sequence (-1: none; fused: the new token's)
@@ -648,9 +629,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 
   const Kv4Bias bias;
   float t0 = -INFINITY, t1 = -INFINITY;  // m0, m1 plus the slack
-  bool landed = true;  // no wait for copies has run out
   int stage = 0;
-  uint32_t parity = 0;
   // one step; MASK: some token of its pages is not seen
   auto attend = [&](auto mask, int v) {
     constexpr bool MASK = decltype(mask)::value;
@@ -735,13 +714,8 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   };
   for (int step = 0; step < steps; ++step) {
     const int v = wv0 + step * NW * BATCH;  // first visible page of this step
-    if constexpr (PG::BULK) {
-      landed = __all_sync(0xffffffffu, mbar_wait_bounded(&bar[stage], parity, ATW_WAIT_POLLS));
-      if (!landed) break;
-    } else {
-      cp_async_wait<STAGES - 1>();  // this lane's copies,
-      __syncwarp();                 // and every other's
-    }
+    cp_async_wait<STAGES - 1>();  // this lane's copies,
+    __syncwarp();                 // and every other's
     const bool whole = ((have >> (stage * BATCH)) & ((1u << BATCH) - 1u)) == (1u << BATCH) - 1u &&
                        (unsigned)(part_s - v) >= (unsigned)BATCH && (unsigned)(part_w - v) >= (unsigned)BATCH &&
                        (unsigned)(part_l - v) >= (unsigned)BATCH;
@@ -749,19 +723,10 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     else attend(std::true_type{}, v);
     __syncwarp();  // every lane has read the stage
     if (step + STAGES < steps) issue(step + STAGES, stage);
-    if (!PG::BULK) cp_async_commit();
-    if (++stage == STAGES) {
-      stage = 0;
-      parity ^= 1u;
-    }
+    cp_async_commit();
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
-  if (!PG::BULK) cp_async_wait<0>();
-  if (!landed) {
-    // a wait ran out: report it, and give the copies still in flight their
-    // time before the ring's memory changes hands
-    if (lane == 0 && a.err_flag) atomicOr(a.err_flag, 2);
-    for (int st = 0; st < STAGES; ++st) mbar_wait_bounded(&bar[st], parity ^ (st < stage ? 1u : 0u), ATW_WAIT_POLLS >> 4);
-  }
+  cp_async_wait<0>();
   __syncthreads();  // the rings become the merge's buffer
   W4_TRACE_MARK(1);
 
