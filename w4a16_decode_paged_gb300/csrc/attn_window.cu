@@ -479,9 +479,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   __shared__ __align__(16) float s_cos[FUSE ? ATT_D / 2 : 4], s_sin[FUSE ? ATT_D / 2 : 4];
   __shared__ __align__(16) uint16_t s_new[2][32];  // codes of the new K and V rows (fused)
   __shared__ uint8_t s_news[2][4];
-  __shared__ float2 s_part[ATW_MAX_PARTITIONS * 8];
   __shared__ int s_scan[24];
-  __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -781,76 +779,68 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     if (single) {
       const float inv = den == 0.f ? 0.f : atw_o_factor<KIND>() / den;
       write_out(h, i4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    } else {
-      __stcg(reinterpret_cast<float4*>(a.ws_o + ((size_t)blockIdx.x * G + h) * ATT_D + 4 * i4), acc);
-      if (i4 == 0) __stcg(reinterpret_cast<float2*>(a.ws_ml + ((size_t)blockIdx.x * G + h) * 2), make_float2(M, den));
+      continue;
     }
-  }
-  if (single) return;
-  W4_TRACE_MARK(2);
-
-  // ---- the CTAs' partials: the last to finish adds them up, in order ----------------
-  __syncthreads();
-  if (tid == 0) {
-    // releases the CTA's partial (ordered before by the barrier) with the
-    // ticket, and for the last acquires the others'
-    unsigned ticket;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                 : "=r"(ticket)
-                 : "l"(a.counters + b * a.Hkv + kvh)
-                 : "memory");
-    s_last = ticket == (unsigned)(active - 1);
-  }
-  __syncthreads();
-  if (!s_last) return;
-  // one round trip for the first partials and all (max, sum) pairs
-  constexpr int FLIGHT = 20;
-  const size_t first = blockIdx.x - pc;  // the parts are consecutive CTAs
-  const size_t pitch = (size_t)G * (ATT_D / 4);
-  const float4* src = reinterpret_cast<const float4*>(a.ws_o + first * G * ATT_D) + i4;
-  float4 pv[FLIGHT];
-  auto ask = [&](int h) {
+    // ---- this head's partials of all the parts: the last warp to finish its
+    // adds them up, in the order of the parts ---------------------------------
+    const size_t mine = (size_t)blockIdx.x * G + h;
+    __stcg(reinterpret_cast<float4*>(a.ws_o + mine * ATT_D) + i4, acc);
+    if (lane == 0) __stcg(reinterpret_cast<float2*>(a.ws_ml) + mine, make_float2(M, den));
+    __syncwarp();
+    unsigned* counter = a.counters + qh0 + h;
+    unsigned ticket = 0;
+    if (lane == 0)  // releases the warp's partial with the ticket; for the last, acquires the others'
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(ticket) : "l"(counter) : "memory");
+    ticket = __shfl_sync(0xffffffffu, ticket, 0);
+    if (ticket != (unsigned)(active - 1)) continue;
+    if (lane == 0) *counter = 0u;  // ready for the next call
+    // one round trip for the first partials and all (max, sum) pairs
+    constexpr int FLIGHT = 20;
+    const size_t first = (size_t)(blockIdx.x - pc) * G + h;  // the parts are consecutive CTAs
+    const float4* src = reinterpret_cast<const float4*>(a.ws_o) + first * (ATT_D / 4) + i4;
+    const size_t pitch = (size_t)G * (ATT_D / 4);
+    float4 pv[FLIGHT];
 #pragma unroll
     for (int j = 0; j < FLIGHT; ++j)
-      if (j < active) pv[j] = __ldcg(src + (size_t)h * (ATT_D / 4) + (size_t)j * pitch);
-  };
-  if (warp < G) ask(warp);
-  for (int idx = tid; idx < G * active; idx += NW * 32) {
-    const int j = idx / G, hh = idx - j * G;
-    s_part[hh * ATW_MAX_PARTITIONS + j] = __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + first * G + idx);
-  }
-  __syncthreads();
-  for (int h = warp; h < G; h += NW) {
-    if (h != warp) ask(h);
-    const float2* ml = s_part + h * ATW_MAX_PARTITIONS;
-    float M = -INFINITY;
-    for (int j = 0; j < active; ++j) M = fmaxf(M, ml[j].x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f;
+      if (j < active) pv[j] = __ldcg(src + (size_t)j * pitch);
+    static_assert(ATW_MAX_PARTITIONS == 64, "two parts per lane");
+    float2 e[2];  // of parts lane and 32 + lane
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      e[k] = 32 * k + lane < active ? __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + first + (size_t)(32 * k + lane) * G)
+                                    : make_float2(-INFINITY, 0.f);
+    float top = fmaxf(e[0].x, e[1].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float f[2], sum = 0.f;  // weights
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      f[k] = e[k].x == -INFINITY ? (e[k].y == 0.f ? 0.f : 1.f) : ex2(e[k].x - top);
+      sum = fmaf(e[k].y, f[k], sum);
+    }
+    sum = warp_sum(sum);
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](int j, float4 v) {
-      const float2 e = ml[j];
-      const float f = e.x == -INFINITY ? (e.y == 0.f ? 0.f : 1.f) : ex2(e.x - M);
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
-      den = fmaf(e.y, f, den);
+      const float w = __shfl_sync(0xffffffffu, j < 32 ? f[0] : f[1], j & 31);
+      acc.x = fmaf(v.x, w, acc.x);
+      acc.y = fmaf(v.y, w, acc.y);
+      acc.z = fmaf(v.z, w, acc.z);
+      acc.w = fmaf(v.w, w, acc.w);
     };
 #pragma unroll
     for (int j = 0; j < FLIGHT; ++j)
       if (j < active) add(j, pv[j]);
 #pragma unroll 8
-    for (int j = FLIGHT; j < active; ++j) add(j, __ldcg(src + (size_t)h * (ATT_D / 4) + (size_t)j * pitch));
-    const float inv = den == 0.f ? 0.f : atw_o_factor<KIND>() / den;
+    for (int j = FLIGHT; j < active; ++j) add(j, __ldcg(src + (size_t)j * pitch));
+    const float inv = sum == 0.f ? 0.f : atw_o_factor<KIND>() / sum;
     write_out(h, i4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   }
-  if (tid == 0) a.counters[b * a.Hkv + kvh] = 0u;  // ready for the next call
 }
 
 // The split's figures (see above) and the CTAs of the grid: no more than either
 // every pair's pages in parts of min_pages, or the shared-out parts and one
 // part of rounding up per pair, can need.
-static void atw_plan(AtwArgs& a, int kind, int B, int Hkv, int max_context, int window, int sinks) {
+static void atw_plan(AtwArgs& a, int kind, int B, int Hq, int Hkv, int max_context, int window, int sinks) {
   const long long groups = (long long)B * Hkv;
   const long long all = ((long long)max_context + ATT_PAGE - 1) / ATT_PAGE;
   const long long seen = ((long long)std::min(sinks, max_context) + ATT_PAGE - 1) / ATT_PAGE +
@@ -864,7 +854,7 @@ static void atw_plan(AtwArgs& a, int kind, int B, int Hkv, int max_context, int 
   a.fit_mixed = (int)std::max(a.slots - groups / 2, a.slots / 2ll);
   a.ctas = (int)std::min(groups * std::min((n + min_pages - 1) / min_pages, (long long)ATW_MAX_PARTITIONS),
                          std::max(a.fit, a.fit_mixed) + groups);
-  if (groups * 4 > (long long)ATT_TICKET_BYTES) {  // no ticket for every pair: no splitting
+  if ((long long)B * Hq * 4 > (long long)ATT_TICKET_BYTES) {  // no ticket for every query head: no splitting
     a.fit = a.fit_mixed = 1;
     a.ctas = (int)groups;
   }
@@ -915,7 +905,7 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
   W4_CHECK_ALIGN(a.k, 128, "k_pool");
   W4_CHECK_ALIGN(a.v, 128, "v_pool");
   W4_CHECK_ALIGN(out, 128, "out");
-  atw_plan(a, a.kind, B, Hkv, max_context, window, sinks);
+  atw_plan(a, a.kind, B, Hq, Hkv, max_context, window, sinks);
   if (a.ctas > B * Hkv) {
     const size_t need = atw_workspace_bytes(a.ctas, Hq / Hkv);
     W4_CHECK_ARG(workspace != nullptr && workspace_bytes >= need, "%s: workspace of %zu bytes needed", who, need);
@@ -951,7 +941,7 @@ extern "C" size_t paged_gqa_decode_window_workspace_size(int B, int Hq, int Hkv,
   int most = 0;  // (whichever kind of page the call is about)
   for (int kind : {ATW_F16, ATW_F8, ATW_I4}) {
     AtwArgs a = {};
-    atw_plan(a, kind, B, Hkv, max_context, window, sinks);
+    atw_plan(a, kind, B, Hq, Hkv, max_context, window, sinks);
     if (a.ctas > B * Hkv) most = std::max(most, a.ctas);
   }
   return most ? atw_workspace_bytes(most, Hq / Hkv) : ATT_TICKET_BYTES;

@@ -164,7 +164,7 @@ struct AtwArgs {
   __half* out;              // [B][Hq][D]
   float* ws_o;              // [ctas][G][D] partial outputs
   float* ws_ml;             // [ctas][G][2] their maxima and sums
-  unsigned int* counters;   // [B][Hkv]
+  unsigned int* counters;   // [B][Hq]
   int32_t* err_flag;
   int kind, q_stride, num_pages, max_blocks, max_context, window, sinks, B, Hq, Hkv, G;
   int slots, fit, fit_mixed, ctas;  // the split over CTAs (attn_window.cu); ctas: of the grid

@@ -138,12 +138,12 @@ __device__ __forceinline__ void rope_rows(uint4& x, const RopeLane& t) {
 // that makes bit b worth 1, is the fp16 number 2^(10-b) + u; one fused
 // multiply-add takes the bias off and applies the scale:
 //   q s' = (2^(10-b) + u) s' - (2^(10-b) + 8) s',   s' = s / 64
-// exactly, because the bias times a scale still fits fp16's 11 bits at b = 2,
-// 4, 6 (264, 72, 24).  s / 64 keeps 264 s' in fp16's range for every scale;
+// exactly, because the bias times a scale still fits fp16's 11 bits at b = 2
+// and 6 (264 and 24).  s / 64 keeps 264 s' in fp16's range for every scale;
 // callers multiply by 64 in fp32.
 // ---------------------------------------------------------------------------
 struct Kv4Scale {
-  uint32_t s, c264, c72, c24;  // packed pairs
+  uint32_t s, c264, c24;  // packed pairs
 };
 __device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -160,7 +160,6 @@ __device__ __forceinline__ Kv4Scale kv4_scale_pair(uint32_t two) {
   Kv4Scale r;
   r.s = hmul2_u(two, 0x24002400u);     // 1 / 64
   r.c264 = hmul2_u(two, 0xC420C420u);  // -264 / 64
-  r.c72 = hmul2_u(two, 0xBC80BC80u);   // -72 / 64
   r.c24 = hmul2_u(two, 0xB600B600u);   // -24 / 64
   return r;
 }
@@ -170,19 +169,18 @@ __device__ __forceinline__ uint32_t kv4_bytes_to_half2(uint32_t b) { return b <<
 // The exponents, kept in registers: an instruction takes one immediate, which
 // the mask is, and a compiler that may re-create a constant does so at each use.
 struct Kv4Bias {
-  uint32_t e256, e64, e16;
+  uint32_t e256, e16;
   __device__ __forceinline__ Kv4Bias() {
     asm volatile("mov.u32 %0, 0x5C005C00;" : "=r"(e256));
-    asm volatile("mov.u32 %0, 0x54005400;" : "=r"(e64));
     asm volatile("mov.u32 %0, 0x4C004C00;" : "=r"(e16));
   }
 };
 
 // Eight codes of a word: x[n] = nibbles n of the low and of the high half.
 __device__ __forceinline__ void kv4_unpack(uint32_t w, const Kv4Scale& k, const Kv4Bias& e, uint32_t (&x)[4]) {
-  const uint32_t l = w << 2, r = w >> 6;
+  const uint32_t l = w << 2, r = w >> 6;  // nibbles 0, 1 and 2, 3 at bits 2 and 6
   x[0] = hfma2_u(and_or(l, 0x003C003Cu, e.e256), k.s, k.c264);
-  x[1] = hfma2_u(and_or(w, 0x00F000F0u, e.e64), k.s, k.c72);
+  x[1] = hfma2_u(and_or(l, 0x03C003C0u, e.e16), k.s, k.c24);
   x[2] = hfma2_u(and_or(r, 0x003C003Cu, e.e256), k.s, k.c264);
   x[3] = hfma2_u(and_or(r, 0x03C003C0u, e.e16), k.s, k.c24);
 }
