@@ -486,6 +486,11 @@ typedef struct {
    * over the codes; the persistent decode path is not built for them. */
   uint8_t *k8, *v8;
   float *k_scale, *v_scale;
+  /* INT4 KV pages instead (every layer or none; the other pools then NULL):
+   * uint8 [num_pages][Hkv][W4A16_KV4_SLICE], as paged_gqa_decode_int4 takes
+   * them.  decode_step (the kernels' path) and w4a16_prefill append and attend
+   * as paged_gqa_decode_rope_append_int4 and kv_append_rope_int4 do. */
+  uint8_t *k4, *v4;
 } w4a16_layer_weights;
 
 typedef struct {

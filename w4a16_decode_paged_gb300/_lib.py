@@ -41,7 +41,7 @@ class ModelConfig(ctypes.Structure):
 class LayerWeights(ctypes.Structure):
     _fields_ = [(n, P) for n in ("ln1", "ln2", "wq", "wk", "wv", "wo", "wg", "wu", "wd", "sq", "sk", "sv", "so",
                                  "sg", "su", "sd", "bq", "bk", "bv", "k_pool", "v_pool",
-                                 "k8", "v8", "k_scale", "v_scale")]
+                                 "k8", "v8", "k_scale", "v_scale", "k4", "v4")]
 
 
 class ModelWeights(ctypes.Structure):

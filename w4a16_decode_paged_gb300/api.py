@@ -630,7 +630,7 @@ class Model:
     (torch tensors kept alive here), the library owns its activation arena."""
 
     LAYER_KEYS = ("ln1", "ln2", "wq", "wk", "wv", "wo", "wg", "wu", "wd", "sq", "sk", "sv", "so", "sg", "su",
-                  "sd", "bq", "bk", "bv", "k_pool", "v_pool", "k8", "v8", "k_scale", "v_scale")
+                  "sd", "bq", "bk", "bv", "k_pool", "v_pool", "k8", "v8", "k_scale", "v_scale", "k4", "v4")
 
     def __init__(self, cfg: dict, layers: list, embed=None, final_norm=None, lm_head=None, max_batch=1,
                  max_context=4096, num_pages=None, partition_tokens=0):
@@ -823,14 +823,15 @@ def device_pool(case: dict, layer: int, which: str, device="cuda"):
 
 
 def _layer_pool(layer: dict):
-    return layer["k_pool"] if layer.get("k_pool") is not None else layer["k8"]
+    return next(layer[n] for n in ("k_pool", "k8", "k4") if layer.get(n) is not None)
 
 
 def device_layer(w: dict, k_pool, v_pool, device="cuda") -> dict:
     """Move one layer's numpy weights (as drawn by ``synth``) and its pools to
     the device as torch tensors (uint32 words travel as int32).  A pool given
     as a (codes uint8, scales fp32) pair makes the layer's KV cache FP8
-    (E4M3) pages."""
+    (E4M3) pages; a pool given as uint8 [pages][Hkv][KV4_SLICE] makes it INT4
+    pages."""
     import numpy as np
 
     out = {}
@@ -852,6 +853,12 @@ def device_layer(w: dict, k_pool, v_pool, device="cuda") -> dict:
             if out[key].dtype != dt or not out[key].is_contiguous():
                 raise ValueError(f"{key}: {dt} contiguous expected")
         return out
-    for key, a in (("k_pool", k_pool), ("v_pool", v_pool)):
-        out[key] = dev(a)
+    k, v = dev(k_pool), dev(v_pool)
+    if k.dtype == torch.uint8 or v.dtype == torch.uint8:
+        for name, t in (("k_pool", k), ("v_pool", v)):
+            _arg(t, _U8, name, (None, k.shape[1], KV4_SLICE))
+        out["k_pool"] = out["v_pool"] = None
+        out["k4"], out["v4"] = k, v
+        return out
+    out["k_pool"], out["v_pool"] = k, v
     return out

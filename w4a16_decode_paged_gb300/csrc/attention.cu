@@ -30,10 +30,12 @@
 #include <cmath>
 #include <cstdio>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_core.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
 
 namespace w4 {
 
@@ -586,16 +588,53 @@ int launch_paged_attention(const AttnArgs& a_in, cudaStream_t s) {
 // takes 16 consecutive rows and one kv head; every K/V page of its range is
 // copied once into a ring shared by the CTA's 8 warps, and warp w works on
 // rows 2w and 2w + 1 together (the MMA's rows 0-7 and 8-15), so each page
-// feeds 16 query tokens x G heads.  KV8: FP8 (E4M3) pages, codes and row
-// scales, in the dim orders of the FP8 decode step (attn8_qdim, attn8_odim).
+// feeds 16 query tokens x G heads.  KV: the pages' kind (PF_F16, PF_F8, PF_I4).
+// FP8 (E4M3) pages: codes and row scales, in the dim orders of the FP8 decode
+// step (attn8_qdim, attn8_odim).  INT4 pages are unpacked to fp16 rows on their
+// way into the ring: each thread loads a page's words two pages ahead and
+// stores their values one page ahead.
 // ---------------------------------------------------------------------------
 constexpr int PF_ROWS = 16;    // query rows per CTA
 constexpr int PF_WARPS = 8;
 constexpr int PF_STAGES = 3;   // page slots of the CTA's ring
 constexpr size_t pf_slot_bytes(bool kv8) { return kv8 ? (size_t)ATT8_SLOT : (size_t)2 * ATT_SSLICE * 2; }
 
-template <int G, bool KV8>
+enum { PF_F16 = 0, PF_F8 = 1, PF_I4 = 2 };
+
+// One thread's words of an INT4 page: K dims 8 (i % 16) .. of token i / 16, V
+// dims 4 (i % 32) .. of the token pair i / 32, with their scale bytes.
+struct PfWords {
+  uint32_t k, v, ks, vs;
+  __device__ __forceinline__ void load(const uint8_t* kp, const uint8_t* vp, int i) {
+    k = __ldcg(reinterpret_cast<const unsigned int*>(kp) + i);
+    v = __ldcg(reinterpret_cast<const unsigned int*>(vp) + i);
+    ks = __ldcg(kp + kv4_k_scale(i >> 4, (i & 15) >> 2));
+    vs = __ldcg(reinterpret_cast<const unsigned short*>(vp + kv4_v_scale(2 * (i >> 5), (i & 31) >> 3)));
+  }
+  // values into the page's fp16 rows; tokens from `tokens` on count as zero in V, whatever they hold
+  __device__ __forceinline__ void store(__half* kr, __half* vr, int i, int tokens, const Kv4Bias& bias) const {
+    uint32_t x[4];
+    kv4_unpack(k, kv4_scale_pair(ks * 0x00800080u), bias, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = hmul2_u(x[e], 0x54005400u);  // 64: the unpacking's scales are s / 64
+    *reinterpret_cast<uint4*>(kr + (i >> 4) * ATT_PITCH + 8 * (i & 15)) =
+        make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                   __byte_perm(x[2], x[3], 0x7632));
+    const int t = 2 * (i >> 5);
+    const uint32_t s = t >= tokens ? 0u : (t + 1 >= tokens ? vs & 0xFFu : vs);
+    kv4_unpack(v, kv4_scale_pair(((s & 0xFFu) << 7) | ((s & 0xFF00u) << 15)), bias, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = hmul2_u(x[e], 0x54005400u);
+    __half* row = vr + t * ATT_PITCH + 4 * (i & 31);
+    *reinterpret_cast<uint2*>(row) = make_uint2(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
+    *reinterpret_cast<uint2*>(row + ATT_PITCH) =
+        make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+  }
+};
+
+template <int G, int KV>
 __global__ void __launch_bounds__(PF_WARPS * 32) w4pg_prefill_attn(const __grid_constant__ AttnArgs a) {
+  constexpr bool KV8 = KV == PF_F8;
   extern __shared__ __align__(16) unsigned char smraw[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kvh = blockIdx.y;
@@ -644,7 +683,21 @@ __global__ void __launch_bounds__(PF_WARPS * 32) w4pg_prefill_attn(const __grid_
   };
   // page li into slot li % PF_STAGES: 2 x 16 rows of 256 bytes, 512 16-byte
   // copies over the CTA's 256 threads; one commit group per page
+  PfWords words;
+  struct None {};
+  const std::conditional_t<KV == PF_I4, Kv4Bias, None> bias;
   auto issue = [&](int li) {
+    if (KV == PF_I4) {
+      // the words of page li into registers (their values: unpack())
+      const int pg = li < npages ? page_id(li) : -1;
+      if (pg >= 0) {
+        const size_t off = ((size_t)pg * a.Hkv + kvh) * KV4_SLICE;
+        words.load(a.k8 + off, a.v8 + off, tid);
+      } else if (li < npages && tid == 0 && a.err_flag) {
+        atomicOr(a.err_flag, 1);
+      }
+      return;
+    }
     if (li < npages) {
       const int pg = page_id(li);
       if (pg >= 0 && KV8) {
@@ -674,17 +727,38 @@ __global__ void __launch_bounds__(PF_WARPS * 32) w4pg_prefill_attn(const __grid_
     }
     cp_async_commit();
   };
+  // INT4: the values of page li, whose words are loaded, into slot li % PF_STAGES
+  auto unpack = [&](int li) {
+    if constexpr (KV == PF_I4) {
+      if (li < npages && page_id(li) >= 0) {
+        __half* kr = reinterpret_cast<__half*>(smraw + (size_t)(li % PF_STAGES) * SLOT);
+        words.store(kr, kr + ATT_SSLICE, tid, L - li * ATT_PAGE, bias);
+      }
+    }
+  };
   float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
   float o[16][4];
 #pragma unroll
   for (int nb = 0; nb < 16; ++nb) o[nb][0] = o[nb][1] = o[nb][2] = o[nb][3] = 0.f;
   const uint32_t k_off = attn_k_off(lane), v_off = attn_v_off(lane);
+  if (KV == PF_I4) {
+    issue(0);
+    unpack(0);
+    issue(1);
+  } else {
 #pragma unroll
-  for (int i = 0; i < PF_STAGES - 1; ++i) issue(i);
+    for (int i = 0; i < PF_STAGES - 1; ++i) issue(i);
+  }
   for (int li = 0; li < npages; ++li) {
-    cp_async_wait<PF_STAGES - 2>();  // this thread's copies of page li landed
-    __syncthreads();                 // everyone's; and every warp is done with page li - 1
-    issue(li + PF_STAGES - 1);       // into the slot page li - 1 used
+    if (KV == PF_I4) {
+      __syncthreads();  // page li is stored; every warp is done with page li - 2's slot
+      unpack(li + 1);
+      issue(li + 2);
+    } else {
+      cp_async_wait<PF_STAGES - 2>();  // this thread's copies of page li landed
+      __syncthreads();                 // everyone's; and every warp is done with page li - 1
+      issue(li + PF_STAGES - 1);       // into the slot page li - 1 used
+    }
     const int tok0 = li * ATT_PAGE;
     // rows whose position is before this page see nothing in it (posB is -1
     // when the warp has only row A)
@@ -723,10 +797,10 @@ __global__ void __launch_bounds__(PF_WARPS * 32) w4pg_prefill_attn(const __grid_
   }
 }
 
-template <int G, bool KV8>
-static int launch_prefill_attn_g(const AttnArgs& a, cudaStream_t s) {
-  constexpr size_t smem = (size_t)PF_STAGES * pf_slot_bytes(KV8);
-  auto kern = w4pg_prefill_attn<G, KV8>;
+template <int G, int KV>
+static int launch_prefill_attn_gk(const AttnArgs& a, cudaStream_t s) {
+  constexpr size_t smem = (size_t)PF_STAGES * pf_slot_bytes(KV == PF_F8);
+  auto kern = w4pg_prefill_attn<G, KV>;
   static PerDeviceOnce once;
   once_per_device(once, [&] { cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem); });
   const dim3 grid((a.B + PF_ROWS - 1) / PF_ROWS, a.Hkv);
@@ -735,13 +809,19 @@ static int launch_prefill_attn_g(const AttnArgs& a, cudaStream_t s) {
   return W4A16_OK;
 }
 
+template <int G>
+static int launch_prefill_attn_g(const AttnArgs& a, cudaStream_t s) {
+  if (a.kv4) return launch_prefill_attn_gk<G, PF_I4>(a, s);
+  return a.kv8 ? launch_prefill_attn_gk<G, PF_F8>(a, s) : launch_prefill_attn_gk<G, PF_F16>(a, s);
+}
+
 int launch_prefill_attention(const AttnArgs& a, cudaStream_t s) {
   switch (a.Hq / a.Hkv) {
-    case 1: return a.kv8 ? launch_prefill_attn_g<1, true>(a, s) : launch_prefill_attn_g<1, false>(a, s);
-    case 2: return a.kv8 ? launch_prefill_attn_g<2, true>(a, s) : launch_prefill_attn_g<2, false>(a, s);
-    case 4: return a.kv8 ? launch_prefill_attn_g<4, true>(a, s) : launch_prefill_attn_g<4, false>(a, s);
-    case 7: return a.kv8 ? launch_prefill_attn_g<7, true>(a, s) : launch_prefill_attn_g<7, false>(a, s);
-    case 8: return a.kv8 ? launch_prefill_attn_g<8, true>(a, s) : launch_prefill_attn_g<8, false>(a, s);
+    case 1: return launch_prefill_attn_g<1>(a, s);
+    case 2: return launch_prefill_attn_g<2>(a, s);
+    case 4: return launch_prefill_attn_g<4>(a, s);
+    case 7: return launch_prefill_attn_g<7>(a, s);
+    case 8: return launch_prefill_attn_g<8>(a, s);
     default:
       return set_error(W4A16_ERR_SHAPE, "prefill attention: Hq/Hkv=%d not built (1, 2, 4, 7, 8)", a.Hq / a.Hkv);
   }

@@ -840,7 +840,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 // The split's figures (see above) and the CTAs of the grid: no more than either
 // every pair's pages in parts of min_pages, or the shared-out parts and one
 // part of rounding up per pair, can need.
-static void atw_plan(AtwArgs& a, int kind, int B, int Hq, int Hkv, int max_context, int window, int sinks) {
+void atw_plan(AtwArgs& a, int kind, int B, int Hq, int Hkv, int max_context, int window, int sinks) {
   const long long groups = (long long)B * Hkv;
   const long long all = ((long long)max_context + ATT_PAGE - 1) / ATT_PAGE;
   const long long seen = ((long long)std::min(sinks, max_context) + ATT_PAGE - 1) / ATT_PAGE +
@@ -872,6 +872,7 @@ static int launch_atw(const AtwArgs& a, cudaStream_t s) {
 }
 
 int launch_attn_window(const AtwArgs& a, cudaStream_t s) {
+  if (a.G > 8) return set_error(W4A16_ERR_SHAPE, "paged attention: Hq/Hkv=%d > 8", a.G);
   if (a.kind == ATW_F16) return launch_atw<ATW_F16, false>(a, s);
   if (a.kind == ATW_F8) return launch_atw<ATW_F8, false>(a, s);
   return a.fuse_rope_append ? launch_atw<ATW_I4, true>(a, s) : launch_atw<ATW_I4, false>(a, s);

@@ -102,6 +102,7 @@ struct AttnArgs {
   uint8_t* v8;
   float* ks;
   float* vs;
+  int kv4;                  // prompt attention only: k8 / v8 are INT4 pools [pages][Hkv][1088]
 };
 int launch_paged_attention(const AttnArgs& a, cudaStream_t s);
 // Causal prompt attention: rows 0..B-1 of q are tokens of one sequence at
@@ -174,6 +175,8 @@ struct AtwArgs {
   int tag;
 };
 int launch_attn_window(const AtwArgs& a, cudaStream_t s);
+// sets the split and the grid (a.kind, B, Hq, Hkv and the limits given)
+void atw_plan(AtwArgs& a, int kind, int B, int Hq, int Hkv, int max_context, int window, int sinks);
 inline size_t atw_workspace_bytes(int ctas, int G) { return ATT_TICKET_BYTES + (size_t)ctas * G * (128 + 2) * 4; }
 inline void atw_workspace(AtwArgs& a, void* ws, int ctas, int G) {  // tickets first, as for the other workspaces
   char* w = static_cast<char*>(ws);

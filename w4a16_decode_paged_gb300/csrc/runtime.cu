@@ -54,6 +54,7 @@ struct w4a16_model {
   const __half *embed = nullptr, *final_norm = nullptr, *lm_head = nullptr;
   int max_batch = 0, max_context = 0, part_tokens = 0, P = 0;
   bool kv8 = false;  // the layers' KV pools are FP8 (E4M3) codes + row scales
+  bool kv4 = false;  // the layers' KV pools are INT4 slices
   char* arena = nullptr;
   size_t arena_bytes = 0;
   __half *x = nullptr, *qkv = nullptr, *att = nullptr, *h = nullptr, *mlp = nullptr;
@@ -119,17 +120,21 @@ extern "C" int w4a16_model_create(const w4a16_model_config* cfg, const w4a16_mod
   m->cfg = c;
   m->layers.assign(w->layers, w->layers + c.n_layers);
   m->kv8 = c.n_layers > 0 && m->layers[0].k8 != nullptr;
+  m->kv4 = c.n_layers > 0 && !m->kv8 && m->layers[0].k4 != nullptr;
   for (int l = 0; l < c.n_layers; ++l) {
     const w4a16_layer_weights& L = m->layers[l];
-    const bool pools = m->kv8 ? (L.k8 && L.v8 && L.k_scale && L.v_scale) : (L.k_pool && L.v_pool && !L.k8);
+    const bool pools = m->kv4   ? (L.k4 && L.v4 && !L.k8 && !L.k_pool)
+                       : m->kv8 ? (L.k8 && L.v8 && L.k_scale && L.v_scale && !L.k4)
+                                : (L.k_pool && L.v_pool && !L.k8 && !L.k4);
     if (!(L.ln1 && L.ln2 && L.wq && L.wk && L.wv && L.wo && L.wg && L.wu && L.wd && L.sq && L.sk && L.sv && L.so &&
           L.sg && L.su && L.sd && pools)) {
       delete m;
       return set_error(W4A16_ERR_INVALID_ARG,
-                       "model_create: layer %d has a null weight or pool (FP8 pools: every layer or none)", l);
+                       "model_create: layer %d has a null weight or pool (FP8 or INT4 pools: every layer or none)", l);
     }
     const void* ptrs[] = {L.ln1, L.ln2, L.wq, L.wk, L.wv, L.wo, L.wg, L.wu, L.wd, L.sq, L.sk, L.sv, L.so, L.sg,
-                          L.su,  L.sd,  L.bq, L.bk, L.bv, L.k_pool, L.v_pool, L.k8, L.v8, L.k_scale, L.v_scale};
+                          L.su,  L.sd,  L.bq, L.bk, L.bv, L.k_pool, L.v_pool, L.k8, L.v8, L.k_scale, L.v_scale,
+                          L.k4, L.v4};
     for (const void* p : ptrs) {
       if (p && !aligned(p, 128)) {
         delete m;
@@ -162,6 +167,17 @@ extern "C" int w4a16_model_create(const w4a16_model_config* cfg, const w4a16_mod
   const size_t o_h = off; off += up256((size_t)max_batch * c.hidden * 2);
   const size_t o_mlp = off; off += up256((size_t)max_batch * c.inter * 2);
   m->attn_ws_bytes = attention_workspace_bytes(max_batch, c.n_q_heads, c.n_kv_heads, m->P);
+  if (m->kv4) {
+    if ((long long)max_batch * c.n_kv_heads * (max_context / 16 + 1) > (1 << 30)) {
+      delete m;
+      return set_error(W4A16_ERR_SHAPE, "model_create: max_context %d is too large for INT4 pools", max_context);
+    }
+    for (int b = 1; b <= max_batch; ++b) {
+      AtwArgs t = {};
+      atw_plan(t, ATW_I4, b, c.n_q_heads, c.n_kv_heads, max_context, max_context, 0);
+      m->attn_ws_bytes = std::max(m->attn_ws_bytes, atw_workspace_bytes(t.ctas, c.n_q_heads / c.n_kv_heads));
+    }
+  }
   const size_t o_aws = off; off += up256(m->attn_ws_bytes);
   m->lm_ws_bytes = lm_head_workspace_bytes(max_batch, c.vocab);
   const size_t o_lws = off; off += up256(m->lm_ws_bytes);
@@ -183,7 +199,7 @@ extern "C" int w4a16_model_create(const w4a16_model_config* cfg, const w4a16_mod
   // the persistent path: one sequence, the Qwen2-style 7:1 GQA shapes, contexts
   // its attention merge covers
   m->pk_ok = persistent_supported(c.hidden, c.n_q_heads, c.n_kv_heads, c.head_dim, c.inter, c.n_layers, max_context) &&
-             c.vocab >= 2 && c.vocab % 2 == 0 && !m->kv8;
+             c.vocab >= 2 && c.vocab % 2 == 0 && !m->kv8 && !m->kv4;
   size_t o_pk = off;
   if (m->pk_ok) {
     m->pk_P = (max_context + PK_PARTITION_TOKENS - 1) / PK_PARTITION_TOKENS;
@@ -371,35 +387,63 @@ static int run_layer(w4a16_model* m, int l, __half* x, const int32_t* bt, int ma
 
   // RoPE of q and the new k, the KV append and the paged attention are one
   // kernel: it prefetches this partition's pages while the q|k|v GEMV runs.
-  AttnArgs a = {};
-  a.q = m->qkv;
-  a.q_stride = nqkv;
-  a.k_pool = reinterpret_cast<__half*>(L.k_pool);
-  a.v_pool = reinterpret_cast<__half*>(L.v_pool);
-  if (m->kv8) {
-    a.kv8 = 1;
-    a.k8 = L.k8;
-    a.v8 = L.v8;
-    a.ks = L.k_scale;
-    a.vs = L.v_scale;
+  if (m->kv4) {
+    AtwArgs a = {};
+    a.kind = ATW_I4;
+    a.fuse_rope_append = 1;
+    a.q = m->qkv;
+    a.q_stride = nqkv;
+    a.k = L.k4;
+    a.v = L.v4;
+    a.block_table = bt;
+    a.context_lens = lens;
+    a.out = m->att;
+    a.err_flag = m->err_flag;
+    a.num_pages = c.num_pages;
+    a.max_blocks = max_blocks;
+    a.max_context = m->max_context;
+    a.window = m->max_context;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.scale_log2 = (1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+    std::memcpy(a.inv_freq, m->inv_freq, sizeof(a.inv_freq));
+    atw_plan(a, ATW_I4, B, Hq, Hkv, m->max_context, m->max_context, 0);
+    atw_workspace(a, m->attn_ws, a.ctas, a.G);
+    a.tag = tag++;
+    if ((rc = launch_attn_window(a, s))) return rc;
+  } else {
+    AttnArgs a = {};
+    a.q = m->qkv;
+    a.q_stride = nqkv;
+    a.k_pool = reinterpret_cast<__half*>(L.k_pool);
+    a.v_pool = reinterpret_cast<__half*>(L.v_pool);
+    if (m->kv8) {
+      a.kv8 = 1;
+      a.k8 = L.k8;
+      a.v8 = L.v8;
+      a.ks = L.k_scale;
+      a.vs = L.v_scale;
+    }
+    a.block_table = bt;
+    a.context_lens = lens;
+    a.out = m->att;
+    attention_workspace_layout(a, m->attn_ws, m->max_batch, Hq, m->P);
+    a.err_flag = m->err_flag;
+    a.num_pages = c.num_pages;
+    a.max_blocks = max_blocks;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.P = m->P;
+    a.part_tokens = m->part_tokens;
+    a.scale_log2 = (1.0f / sqrtf((float)D)) * 1.4426950408889634f;
+    a.fuse_rope_append = 1;
+    std::memcpy(a.inv_freq, m->inv_freq, sizeof(a.inv_freq));
+    a.tag = tag++;
+    if ((rc = launch_paged_attention(a, s))) return rc;
   }
-  a.block_table = bt;
-  a.context_lens = lens;
-  a.out = m->att;
-  attention_workspace_layout(a, m->attn_ws, m->max_batch, Hq, m->P);
-  a.err_flag = m->err_flag;
-  a.num_pages = c.num_pages;
-  a.max_blocks = max_blocks;
-  a.B = B;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.P = m->P;
-  a.part_tokens = m->part_tokens;
-  a.scale_log2 = (1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-  a.fuse_rope_append = 1;
-  std::memcpy(a.inv_freq, m->inv_freq, sizeof(a.inv_freq));
-  a.tag = tag++;
-  if ((rc = launch_paged_attention(a, s))) return rc;
 
   GemvArgs o = {};
   o.x = m->att;
@@ -571,35 +615,60 @@ extern "C" int w4a16_prefill(w4a16_model* m, const int32_t* tokens, int T, const
     const GemvSeg qkv[3] = {{L.wq, hp(L.sq), hp(L.bq), Hq * D}, {L.wk, hp(L.sk), hp(L.bk), Hkv * D},
                             {L.wv, hp(L.sv), hp(L.bv), Hkv * D}};
     if ((rc = gemm_rows(m, w, w.xn, T, H, qkv, 3, nqkv, nullptr, w.qkv, false, s))) return rc;
-    RopeArgs ra = {};
-    ra.q = w.qkv;
-    ra.k = w.qkv + (size_t)Hq * D;
-    ra.v = w.qkv + (size_t)(Hq + Hkv) * D;
-    ra.k_pool = reinterpret_cast<__half*>(L.k_pool);
-    ra.v_pool = reinterpret_cast<__half*>(L.v_pool);
-    if (m->kv8) {  // FP8 pages: quantised rows appended
-      ra.k8 = L.k8;
-      ra.v8 = L.v8;
-      ra.ks = L.k_scale;
-      ra.vs = L.v_scale;
+    if (m->kv4) {
+      Kv4AppendArgs ra = {};
+      ra.q = ra.q_out = w.qkv;
+      ra.k = w.qkv + (size_t)Hq * D;
+      ra.v = w.qkv + (size_t)(Hq + Hkv) * D;
+      ra.k_pool = L.k4;
+      ra.v_pool = L.v4;
+      ra.block_table = w.bt_rep;
+      ra.context_lens = w.lens;
+      ra.err_flag = m->err_flag;
+      ra.stride_q = ra.stride_qo = ra.stride_kv = nqkv;
+      ra.num_pages = c.num_pages;
+      ra.max_blocks = max_blocks;
+      ra.B = T;
+      ra.Hq = Hq;
+      ra.Hkv = Hkv;
+      std::memcpy(ra.inv_freq, m->inv_freq, sizeof(ra.inv_freq));
+      if ((rc = launch_rope_append_int4(ra, s))) return rc;
+    } else {
+      RopeArgs ra = {};
+      ra.q = w.qkv;
+      ra.k = w.qkv + (size_t)Hq * D;
+      ra.v = w.qkv + (size_t)(Hq + Hkv) * D;
+      ra.k_pool = reinterpret_cast<__half*>(L.k_pool);
+      ra.v_pool = reinterpret_cast<__half*>(L.v_pool);
+      if (m->kv8) {  // FP8 pages: quantised rows appended
+        ra.k8 = L.k8;
+        ra.v8 = L.v8;
+        ra.ks = L.k_scale;
+        ra.vs = L.v_scale;
+      }
+      ra.block_table = w.bt_rep;
+      ra.context_lens = w.lens;
+      ra.err_flag = m->err_flag;
+      ra.stride_q = nqkv;
+      ra.stride_kv = nqkv;
+      ra.num_pages = c.num_pages;
+      ra.max_blocks = max_blocks;
+      ra.B = T;
+      ra.Hq = Hq;
+      ra.Hkv = Hkv;
+      std::memcpy(ra.inv_freq, m->inv_freq, sizeof(ra.inv_freq));
+      if ((rc = launch_rope_append(ra, s))) return rc;
     }
-    ra.block_table = w.bt_rep;
-    ra.context_lens = w.lens;
-    ra.err_flag = m->err_flag;
-    ra.stride_q = nqkv;
-    ra.stride_kv = nqkv;
-    ra.num_pages = c.num_pages;
-    ra.max_blocks = max_blocks;
-    ra.B = T;
-    ra.Hq = Hq;
-    ra.Hkv = Hkv;
-    std::memcpy(ra.inv_freq, m->inv_freq, sizeof(ra.inv_freq));
-    if ((rc = launch_rope_append(ra, s))) return rc;
     AttnArgs a = {};
     a.q = w.qkv;
     a.q_stride = nqkv;
-    a.k_pool = ra.k_pool;
-    a.v_pool = ra.v_pool;
+    a.k_pool = reinterpret_cast<__half*>(L.k_pool);
+    a.v_pool = reinterpret_cast<__half*>(L.v_pool);
+    if (m->kv4) {
+      a.kv4 = 1;
+      a.k8 = L.k4;
+      a.v8 = L.v4;
+    }
     if (m->kv8) {
       a.kv8 = 1;
       a.k8 = L.k8;
