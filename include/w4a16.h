@@ -339,6 +339,7 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
  *     splits each sequence's pages evenly over the CTAs that max_context asks
  *     for.  Hq/Hkv may be any of 1..8.  workspace:
  *     paged_gqa_decode_window_workspace_size(.., window = max_context, sinks = 0).
+ *     max_context < 2^24, and B x Hkv x its pages up to 2^30.
  *     A length above max_context sets bit 0 of err_flag; the row attends to its
  *     first max_context tokens, and the fused call appends nothing for it.
  * Every byte of a page past a sequence's length may hold anything.

@@ -85,6 +85,16 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// What a lane copies from starts here, for page 0 and this kv head; pages lie
+// `pitch` bytes apart (FP8: their row scales spitch).
+struct LanePtrs {
+  const unsigned char *k, *v, *s;
+  uint32_t pitch, spitch;
+  static __device__ __forceinline__ const unsigned char* at(const unsigned char* p, int page, uint32_t pitch) {
+    return p + (uint64_t)(uint32_t)page * pitch;
+  }
+};
+
 template <int KIND>
 struct Page;
 
@@ -106,9 +116,13 @@ struct Page<ATW_F16> {
   // each half row are permuted by the row (chunk ^ row % 8), so that neither
   // the K reads (two rows, every other chunk) nor the V reads (four rows, one
   // chunk) of eight lanes meet in a bank.
-  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, int lane) {
-    const unsigned char* k = static_cast<const unsigned char*>(a.k) + slice * 4096 + 16 * lane;
-    const unsigned char* v = static_cast<const unsigned char*>(a.v) + slice * 4096 + 16 * lane;
+  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int lane) {
+    const size_t at = (size_t)kvh * 4096 + 16 * lane;
+    return {static_cast<const unsigned char*>(a.k) + at, static_cast<const unsigned char*>(a.v) + at, nullptr,
+            (uint32_t)a.Hkv * 4096u, 0u};
+  }
+  static __device__ __forceinline__ void fetch(const LanePtrs& lp, int page, uint32_t slot, int lane) {
+    const unsigned char *k = LanePtrs::at(lp.k, page, lp.pitch), *v = LanePtrs::at(lp.v, page, lp.pitch);
     const int row = lane >> 4, c = lane & 15;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -171,9 +185,14 @@ struct Page<ATW_F8> {
   }
   static __device__ __forceinline__ int odim(int mt, int g) { return 16 * g + 2 * mt; }
   // (rows of 128 bytes, their chunks permuted as those of fp16 pages)
-  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, int lane) {
-    const unsigned char* k = static_cast<const unsigned char*>(a.k) + slice * 2048 + 16 * lane;
-    const unsigned char* v = static_cast<const unsigned char*>(a.v) + slice * 2048 + 16 * lane;
+  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int lane) {
+    const size_t at = (size_t)kvh * 2048 + 16 * lane;
+    const float* s = (lane < 4 ? a.ks : a.vs) + (size_t)kvh * ATT_PAGE + 4 * (lane & 3);  // (lanes 0-7)
+    return {static_cast<const unsigned char*>(a.k) + at, static_cast<const unsigned char*>(a.v) + at,
+            reinterpret_cast<const unsigned char*>(s), (uint32_t)a.Hkv * 2048u, (uint32_t)a.Hkv * 64u};
+  }
+  static __device__ __forceinline__ void fetch(const LanePtrs& lp, int page, uint32_t slot, int lane) {
+    const unsigned char *k = LanePtrs::at(lp.k, page, lp.pitch), *v = LanePtrs::at(lp.v, page, lp.pitch);
     const int row = lane >> 3, c = lane & 7;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -181,8 +200,7 @@ struct Page<ATW_F8> {
       copy16(at, k + 512 * i);
       copy16(at + V, v + 512 * i);
     }
-    if (lane < 8)
-      copy16(slot + KS + 16 * lane, (lane < 4 ? a.ks + slice * ATT_PAGE : a.vs + slice * ATT_PAGE) + 4 * (lane & 3));
+    if (lane < 8) copy16(slot + KS + 16 * lane, LanePtrs::at(lp.s, page, lp.spitch));
   }
   static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias&,
                                                 const uint32_t (&qb)[8][2], float (&s)[4]) {
@@ -258,16 +276,20 @@ struct Page<ATW_I4> {
   // K rows as they are (a lane reads the chunks it copied); the 16-byte chunks
   // of a V pair's 128 bytes permuted by the pair, so that the reads of eight
   // lanes (four pairs, two chunks) do not meet in a bank
-  static __device__ __forceinline__ void fetch(const AtwArgs& a, size_t slice, uint32_t slot, int lane) {
-    const uint8_t* k = static_cast<const uint8_t*>(a.k) + slice * KV4_SLICE + 16 * lane;
-    const uint8_t* v = static_cast<const uint8_t*>(a.v) + slice * KV4_SLICE + 16 * lane;
+  static __device__ __forceinline__ LanePtrs lane_ptrs(const AtwArgs& a, int kvh, int lane) {
+    const size_t at = (size_t)kvh * KV4_SLICE + 16 * lane;
+    const unsigned char *k = static_cast<const unsigned char*>(a.k) + at, *v = static_cast<const unsigned char*>(a.v) + at;
+    return {k, v, (lane < 4 ? k : v - 64) + KV4_CODES, (uint32_t)a.Hkv * KV4_SLICE, 0u};  // (scales: lanes 0-7)
+  }
+  static __device__ __forceinline__ void fetch(const LanePtrs& lp, int page, uint32_t slot, int lane) {
+    const unsigned char *k = LanePtrs::at(lp.k, page, lp.pitch), *v = LanePtrs::at(lp.v, page, lp.pitch);
     const int pair = lane >> 3, c = lane & 7;
     const uint32_t kd = slot + 16 * lane, vd = slot + V + 128 * pair + 16 * (c ^ (2 * pair));
     copy16(kd, k);
     copy16(kd + 512, k + 512);
     copy16(vd, v);
     copy16(vd + 512, v + 512);
-    if (lane < 8) copy16(slot + KS + 16 * lane, (lane < 4 ? k : v - 64) + KV4_CODES);
+    if (lane < 8) copy16(slot + KS + 16 * lane, LanePtrs::at(lp.s, page, lp.pitch));
   }
   static __device__ __forceinline__ void scores(const unsigned char* slot, int g, int t4, const Kv4Bias& bias,
                                                 const uint32_t (&qb)[8][2], float (&s)[4]) {
@@ -338,15 +360,13 @@ __device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I
 // (slots), lengths are mixed and a pair rounds up by half a part on average.
 // ---------------------------------------------------------------------------
 struct AtwShare {
-  int b, kvh, part, parts;  // b -1: nothing to do
-  int len, L, w0, S, nsp, wp, n;
-  bool fits;
+  int b, kvh, part, parts;     // b -1: nothing to do
+  int L, w0, S, n, nsp, wp, fits;  // L: the length, up to max_context (fits: it is no longer)
 };
 
 // the visible pages of a sequence of this length
 __device__ __forceinline__ AtwShare atw_visible(const AtwArgs& a, int len) {
   AtwShare r;
-  r.len = len;
   r.fits = len <= a.max_context;
   r.L = max(min(len, a.max_context), 0);
   r.w0 = a.window >= r.L ? 0 : r.L - a.window;  // first token of the window
@@ -358,10 +378,21 @@ __device__ __forceinline__ AtwShare atw_visible(const AtwArgs& a, int len) {
   return r;
 }
 
-__device__ __forceinline__ int atw_parts(int n, int per) { return min(max((n + per - 1) / per, 1), ATW_MAX_PARTITIONS); }
-// (the host refuses batches whose pages, times the kv heads, pass 2^30)
-__device__ __forceinline__ int atw_per(unsigned pages, unsigned fit, int min_pages) {
-  return max((int)((pages + fit - 1) / fit), min_pages);
+// a / b rounded up, 0 <= a <= 2^20: (a - 1/2) / b is 1 / (2 b) away from every
+// whole number, which the quotient's error (2^-22 of it) does not bridge
+__device__ __forceinline__ int atw_div_up(int a, int b) {
+  return a > 0 ? (int)__fdividef((float)a - 0.5f, (float)b) + 1 : 0;
+}
+__device__ __forceinline__ int atw_parts(int n, int per) {
+  return min(max(atw_div_up(n, per), 1), ATW_MAX_PARTITIONS);
+}
+// Pages per part for `pages` in all over `fit` parts: a little more than their
+// quotient at times, never less (the grid has no CTAs for more parts).  The
+// host refuses contexts from 2^24 tokens on, and batches whose pages, times the
+// kv heads, pass 2^30.
+__device__ __forceinline__ int atw_per(unsigned pages, int fit, int min_pages) {
+  const int q = (int)__fdividef((float)pages, (float)fit);
+  return min(max(q + 1 + (q >> 20), min_pages), 1 << 20);
 }
 
 // Up to 32 sequences: one warp's work (every warp's own would be eight times
@@ -480,6 +511,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   __shared__ __align__(16) uint16_t s_new[2][32];  // codes of the new K and V rows (fused)
   __shared__ uint8_t s_news[2][4];
   __shared__ int s_scan[24];
+  __shared__ __align__(16) AtwShare s_share;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -493,31 +525,21 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   if (a.B <= 32) {
     if (warp == 0) {
       const AtwShare r = atw_share_warp(a, PG::MIN_PAGES);
-      if (lane == 0) {
-        s_scan[0] = r.b;
-        s_scan[1] = r.kvh;
-        s_scan[2] = r.part;
-        s_scan[3] = r.parts;
-        s_scan[4] = r.len;
-      }
+      if (lane == 0) s_share = r;
     }
     __syncthreads();
-    sh = atw_visible(a, s_scan[4]);
-    sh.b = s_scan[0];
-    sh.kvh = s_scan[1];
-    sh.part = s_scan[2];
-    sh.parts = s_scan[3];
+    sh = s_share;
   } else {
     sh = atw_share_cta<NW>(a, PG::MIN_PAGES, s_scan);
   }
   if (sh.b < 0) return;
   const int b = sh.b, kvh = sh.kvh, pc = sh.part, active = sh.parts;
   const int L = sh.L, w0 = sh.w0, S = sh.S, n = sh.n, nsp = sh.nsp, wp = sh.wp;
-  const bool fits = sh.fits;
+  const bool fits = sh.fits != 0;
   if (!fits && pc == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
   const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
   uint4 qw = make_uint4(0u, 0u, 0u, 0u);
-  const int chunk = (n + active - 1) / active;
+  const int chunk = atw_div_up(n, active);
   const int v0 = pc * chunk, v1 = min(n, v0 + chunk);
   // The rows that become queries, and (fused, in the CTA of the last page) the
   // new K and V rows 8 and 9: half a warp per row.  They are asked for before
@@ -551,6 +573,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   int ids = table(lane), ids_next = -1;
   unsigned have = 0;  // bit (stage * BATCH + j): that page was copied
   unsigned char* ring = smraw + (size_t)warp * STAGES * BATCH * PG::SLOT;
+  const LanePtrs lp = PG::lane_ptrs(a, kvh, lane);
   // copies step `st`'s pages into its stage (warp-wide; steps come in order)
   auto issue = [&](int st, int stage) {
     const int i = (st * BATCH) & 31;
@@ -561,7 +584,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     for (int j = 0; j < BATCH; ++j) {
       const int id = __shfl_sync(0xffffffffu, ids, i + j);
       if (id >= 0) {
-        PG::fetch(a, (size_t)id * a.Hkv + kvh, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, lane);
+        PG::fetch(lp, id, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, lane);
         have |= 1u << (stage * BATCH + j);
       }
     }
@@ -893,7 +916,8 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
   W4_CHECK_ARG(window >= 0 && sinks >= 0, "%s: window=%d sinks=%d", who, window, sinks);
   W4_CHECK_SHAPE(D == ATT_D, "%s: D=%d, only 128 is built", who, D);
   W4_CHECK_SHAPE(Hq % Hkv == 0 && Hq / Hkv <= 8, "%s: Hq=%d Hkv=%d", who, Hq, Hkv);
-  W4_CHECK_SHAPE((long long)B * Hkv <= (1 << 24) && (long long)B * Hkv * (max_context / ATT_PAGE + 1) <= (1 << 30),
+  W4_CHECK_SHAPE((long long)B * Hkv <= (1 << 24) && max_context < (1 << 24) &&
+                     (long long)B * Hkv * (max_context / ATT_PAGE + 1) <= (1 << 30),
                  "%s: B=%d x Hkv=%d x max_context %d is too large", who, B, Hkv, max_context);
   W4_CHECK_SHAPE((long long)max_context <= (long long)max_blocks * ATT_PAGE, "%s: max_context %d > max_blocks*16", who,
                  max_context);

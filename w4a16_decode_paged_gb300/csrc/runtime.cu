@@ -168,7 +168,7 @@ extern "C" int w4a16_model_create(const w4a16_model_config* cfg, const w4a16_mod
   const size_t o_mlp = off; off += up256((size_t)max_batch * c.inter * 2);
   m->attn_ws_bytes = attention_workspace_bytes(max_batch, c.n_q_heads, c.n_kv_heads, m->P);
   if (m->kv4) {
-    if ((long long)max_batch * c.n_kv_heads * (max_context / 16 + 1) > (1 << 30)) {
+    if (max_context >= (1 << 24) || (long long)max_batch * c.n_kv_heads * (max_context / 16 + 1) > (1 << 30)) {
       delete m;
       return set_error(W4A16_ERR_SHAPE, "model_create: max_context %d is too large for INT4 pools", max_context);
     }
