@@ -391,8 +391,7 @@ __device__ __forceinline__ int atw_parts(int n, int per) {
 // host refuses contexts from 2^24 tokens on, and batches whose pages, times the
 // kv heads, pass 2^30.
 __device__ __forceinline__ int atw_per(unsigned pages, int fit, int min_pages) {
-  const int q = (int)__fdividef((float)pages, (float)fit);
-  return min(max(q + 1 + (q >> 20), min_pages), 1 << 20);
+  return min(max((int)(__fdividef((float)pages, (float)fit) * 1.000001f) + 1, min_pages), 1 << 20);
 }
 
 // Up to 32 sequences: one warp's work (every warp's own would be eight times
