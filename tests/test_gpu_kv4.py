@@ -499,3 +499,53 @@ def test_offsets_past_32_bits(api):
         assert np.array_equal(to_host(x)[0].astype(np.float64), y.transpose(0, 2, 1, 3).reshape(48, Hkv, D)[:40])
     want = ref.attend(to_host(q), lambda p: K[p], lambda p: V[p], np.arange(3)[None], [40], 1 / math.sqrt(D))
     ref.check_attention(to_host(out), want, 40)
+
+
+# ---- the binding on CUDA tensors: the native marshalling and the checked path ------------
+def test_checked_and_native_paths_agree(api):
+    """A stream given by name takes the checked path, none the native one."""
+    r = np.random.default_rng(30)
+    lens = np.array([90, 17], np.int32)
+    bt, pages = _table(r, lens)
+    kp, vp, dbt, dl = dev(ref.random_pool(r, pages, 2), ref.random_pool(r, pages, 2), bt, lens)
+    q, k, v = dev(*(synth.normal_fp16(r, (2, n, D)) for n in (14, 2, 2)))
+    qkv = torch.cat([q, k, v], 1).reshape(2, -1).contiguous()
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    here = torch.cuda.current_stream()
+    calls = (lambda **a: (api.kv_append_rope_int4(q, k, v, kp, vp, dbt, dl, THETA, q_out=torch.empty_like(q), **a), kp, vp),
+             lambda **a: api.kv_read_int4(kp, vp, dbt, dl, 33, starts=dl - 20, **a),
+             lambda **a: (api.paged_gqa_decode_int4(q, kp, vp, dbt, dl, 96, workspace=ws, err_flag=err, **a),),
+             lambda **a: (api.paged_gqa_decode_int4(qkv, kp, vp, dbt, dl, 96, workspace=ws, qkv_theta=THETA, n_q_heads=14,
+                                                    **a), kp, vp),
+             lambda **a: (api.paged_gqa_decode_window(q, kp, vp, dbt, dl, 96, 20, 3, workspace=ws, sm_scale=-0.1, **a),))
+    for call in calls:
+        a = [t.clone() for t in call()]
+        assert all(torch.equal(x, y) for x, y in zip(a, call(stream=here)))
+
+
+def test_refusals_on_cuda_tensors(api):
+    from w4a16_decode_paged_gb300._lib import W4A16Error
+    kp = torch.zeros((4, 2, 1088), dtype=torch.uint8, device="cuda")
+    bt = torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    n = torch.ones(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros((1, 14, D), dtype=torch.float16, device="cuda")
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="q"):
+        api.paged_gqa_decode_int4(q.float(), kp, kp, bt, n, 64, workspace=ws)
+    with pytest.raises(ValueError, match="v_pool"):
+        api.paged_gqa_decode_int4(q, kp, kp[:2], bt, n, 64, workspace=ws)
+    with pytest.raises(ValueError, match="block_table"):
+        api.paged_gqa_decode_int4(q, kp, kp, bt.cpu(), n, 64, workspace=ws)
+    with pytest.raises(ValueError, match="out"):
+        api.paged_gqa_decode_window(q, kp, kp, bt, n, 64, 3, workspace=ws, out=torch.empty((1, 14, D), device="cuda"))
+    with pytest.raises(ValueError, match="window"):
+        api.paged_gqa_decode_window(q, kp, kp, bt, n, 64, -3, workspace=ws)
+    with pytest.raises(W4A16Error, match="max_context"):
+        api.paged_gqa_decode_int4(q, kp, kp, bt, n, 65, workspace=ws)
+    with pytest.raises(W4A16Error, match="Hq=13"):
+        api.paged_gqa_decode_int4(q[:, :13].contiguous(), kp, kp, bt, n, 64, workspace=ws)
+    with pytest.raises(W4A16Error, match="theta"):
+        api.kv_append_rope_int4(q, q[:, :2].contiguous(), q[:, :2].contiguous(), kp, kp.clone(), bt, n, 0.0)
+    with pytest.raises(ValueError, match="T=0"):
+        api.kv_read_int4(kp, kp, bt, n, 0)

@@ -362,13 +362,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 # The calls below are a few microseconds on the GPU at their smallest.  Plain
 # cases (everything on the current device and stream, workspace given) are
-# checked and passed on natively (csrc/torch_args.cpp, `_plain`); whatever that
-# does not take goes through the checks here, which say what is wrong.
-def _plain(entry, lead, *args):
-    """native().entry(*args) for CUDA tensors: its result, or None."""
-    if lead is None or not lead.is_cuda:
-        return None
-    r = getattr(native(), entry)(*args)
+# checked and passed on natively (csrc/torch_args.cpp): a result, an error code,
+# or None for what that does not take.  The rest goes through the checks here,
+# which say what is wrong.
+def _cuda(t):
+    return t is not None and t.is_cuda
+
+
+def _result(r):
     if type(r) is int:
         check(r)
     return r
@@ -432,10 +433,10 @@ def kv_append_rope_int4(q, k, v, k_pool, v_pool, block_table, context_lens, thet
     rotated k row and the v row quantised into their slot.  A row_stride
     (elements, a multiple of 8) makes q, k and v the starts of rows of that
     pitch, e.g. views of a q|k|v buffer."""
-    if stream is None and not row_stride:
-        r = _plain("append", k_pool, q, k, v, k_pool, v_pool, block_table, context_lens, theta, q_out, err_flag)
+    if stream is None and not row_stride and _cuda(k_pool):
+        r = native().append(q, k, v, k_pool, v_pool, block_table, context_lens, theta, q_out, err_flag)
         if r is not None:
-            return r
+            return _result(r)
     pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
     row_stride = int(row_stride)
     if q is None or q.dim() != 3:
@@ -466,10 +467,10 @@ def kv_read_int4(k_pool, v_pool, block_table, context_lens, T, starts=None, k_ou
     sequence b is the token at position starts[b] + i (i without starts) if
     the sequence holds it.  Other rows of a k_out, v_out pair that the caller
     gives are left as they were; of tensors that the call makes, they are zero."""
-    if stream is None:
-        r = _plain("read", k_pool, k_pool, v_pool, block_table, context_lens, T, starts, k_out, v_out, err_flag)
+    if stream is None and _cuda(k_pool):
+        r = native().read(k_pool, v_pool, block_table, context_lens, T, starts, k_out, v_out, err_flag)
         if r is not None:
-            return r
+            return _result(r)
     pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
     T = int(T)
     if T < 1:
@@ -510,11 +511,12 @@ def paged_gqa_decode_int4(q, k_pool, v_pool, block_table, context_lens, max_cont
     128) and the call is the fused RoPE + INT4 append + attention
     (paged_gqa_decode_rope_append_int4).  A workspace the caller gives is
     zeroed once before its first use."""
-    if stream is None and workspace is not None:
-        r = _plain("decode_int4", k_pool, q, k_pool, v_pool, block_table, context_lens, max_context,
-                   _SCALE_128 if sm_scale is None else sm_scale, workspace, out, err_flag, qkv_theta, n_q_heads)
+    if stream is None and workspace is not None and _cuda(k_pool):
+        r = native().decode_int4(q, k_pool, v_pool, block_table, context_lens, max_context,
+                                 _SCALE_128 if sm_scale is None else sm_scale, workspace, out, err_flag, qkv_theta,
+                                 n_q_heads)
         if r is not None:
-            return r
+            return _result(r)
     pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
     max_context = int(max_context)
     fuse = qkv_theta is not None
@@ -558,11 +560,11 @@ def paged_gqa_decode_window(q, k_pool, v_pool, block_table, context_lens, max_co
     [128], FP8 (E4M3) codes of that shape with k_scale / v_scale, or INT4
     [pages][Hkv][KV4_SLICE].  A workspace the caller gives is zeroed once
     before its first use."""
-    if stream is None and workspace is not None:
-        r = _plain("decode_window", k_pool, q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens,
-                   max_context, window, sinks, _SCALE_128 if sm_scale is None else sm_scale, workspace, out, err_flag)
+    if stream is None and workspace is not None and _cuda(k_pool):
+        r = native().decode_window(q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens, max_context, window,
+                                   sinks, _SCALE_128 if sm_scale is None else sm_scale, workspace, out, err_flag)
         if r is not None:
-            return r
+            return _result(r)
     fp8 = k_scale is not None or v_scale is not None
     kind = "fp8" if fp8 else "int4" if k_pool is not None and k_pool.dtype is torch.uint8 else "fp16"
     pages, Hkv, B, blocks, dev = _paging_of(kind, k_pool, v_pool, block_table, context_lens)
