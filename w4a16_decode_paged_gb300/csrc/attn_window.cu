@@ -649,9 +649,8 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 
   const Kv4Bias bias;
   float t0 = -INFINITY, t1 = -INFINITY;  // m0, m1 plus the slack
-  int stage = 0;
   // one step; MASK: some token of its pages is not seen
-  auto attend = [&](auto mask, int v) {
+  auto attend = [&](auto mask, const int stage, int v) {
     constexpr bool MASK = decltype(mask)::value;
     unsigned char* slot = ring + stage * BATCH * PG::SLOT;
     uint32_t live[BATCH];  // bit r: token r of the page is seen
@@ -732,19 +731,24 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
       PG::template output<MASK>(slot + j * PG::SLOT, g, t4, bias, live[j], b0, b1, o);
     }
   };
-  for (int step = 0; step < steps; ++step) {
+  auto one = [&](int step, auto which) {  // the stage is a constant: addresses and masks fold
+    constexpr int stage = decltype(which)::value;
     const int v = wv0 + step * NW * BATCH;  // first visible page of this step
     cp_async_wait<STAGES - 1>();  // this lane's copies,
     __syncwarp();                 // and every other's
     const bool whole = ((have >> (stage * BATCH)) & ((1u << BATCH) - 1u)) == (1u << BATCH) - 1u &&
                        (unsigned)(part_s - v) >= (unsigned)BATCH && (unsigned)(part_w - v) >= (unsigned)BATCH &&
                        (unsigned)(part_l - v) >= (unsigned)BATCH;
-    if (whole) attend(std::false_type{}, v);
-    else attend(std::true_type{}, v);
+    if (whole) attend(std::false_type{}, stage, v);
+    else attend(std::true_type{}, stage, v);
     __syncwarp();  // every lane has read the stage
     if (step + STAGES < steps) issue(step + STAGES, stage);
     cp_async_commit();
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
+  };
+  static_assert(STAGES == 2, "steps alternate between two stages");
+  for (int step = 0; step < steps; step += 2) {
+    one(step, std::integral_constant<int, 0>{});
+    if (step + 1 < steps) one(step + 1, std::integral_constant<int, 1>{});
   }
   cp_async_wait<0>();
   __syncthreads();  // the rings become the merge's buffer
