@@ -101,8 +101,6 @@ struct Page;
 template <>
 struct Page<ATW_F16> {
   static constexpr int NW = 8;      // warps per CTA
-  static constexpr int BATCH = 1;   // pages per step of a warp
-  static constexpr int STAGES = 2;  // steps in flight per warp
   static constexpr int MIN_CTAS = 1;
   static constexpr int MIN_PAGES = 8;
   static constexpr int V = 4096;    // V's offset in a page's slot
@@ -174,8 +172,6 @@ struct Page<ATW_F16> {
 template <>
 struct Page<ATW_F8> {
   static constexpr int NW = 8;
-  static constexpr int BATCH = 1;
-  static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 16;
   static constexpr int V = 2048, KS = 4096, VS = 4160;
@@ -263,8 +259,6 @@ struct Page<ATW_F8> {
 template <>
 struct Page<ATW_I4> {
   static constexpr int NW = 8;
-  static constexpr int BATCH = 2;
-  static constexpr int STAGES = 2;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 32;
   static constexpr int V = 1024, KS = 2048, VS = 2112;
@@ -493,8 +487,9 @@ __device__ __noinline__ AtwShare atw_share_cta(const AtwArgs& a, int min_pages, 
   return r;
 }
 
+constexpr int ATW_STAGES = 2;  // pages in flight per warp (more only make the first pages of all CTAs wait for each other)
 template <int KIND>
-constexpr size_t atw_ring_bytes() { return (size_t)Page<KIND>::NW * Page<KIND>::STAGES * Page<KIND>::BATCH * Page<KIND>::SLOT; }
+constexpr size_t atw_ring_bytes() { return (size_t)Page<KIND>::NW * ATW_STAGES * Page<KIND>::SLOT; }
 template <int KIND>
 constexpr size_t atw_smem() { return std::max(atw_ring_bytes<KIND>(), (size_t)Page<KIND>::NW * 8 * ATW_PITCH * 4); }
 
@@ -502,7 +497,7 @@ template <int KIND, bool FUSE>
 __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     w4pg_attn_window(const __grid_constant__ AtwArgs a) {
   using PG = Page<KIND>;
-  constexpr int NW = PG::NW, BATCH = PG::BATCH, STAGES = PG::STAGES;
+  constexpr int NW = PG::NW, STAGES = ATW_STAGES;
   extern __shared__ __align__(128) unsigned char smraw[];  // the warps' rings, then their merge
   __shared__ __align__(16) __half s_q[8][ATT_D + 8];
   __shared__ float s_ml[NW * 8 * 2];
@@ -552,11 +547,11 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
   auto page_no = [&](int v) { return v < nsp ? v : v - nsp + wp; };
 
-  // this warp takes BATCH consecutive pages of every NW * BATCH
-  const int wv0 = v0 + warp * BATCH;
-  const int steps = wv0 < v1 ? (v1 - wv0 + NW * BATCH - 1) / (NW * BATCH) : 0;
+  // this warp takes every NW-th page
+  const int wv0 = v0 + warp;
+  const int steps = wv0 < v1 ? (v1 - wv0 + NW - 1) / NW : 0;
   auto table = [&](int i) {  // pool page of the warp's i-th page (-1: none, or not in the pool)
-    const int v = wv0 + (i / BATCH) * NW * BATCH + i % BATCH;
+    const int v = wv0 + i * NW;
     if (v >= v1) return -1;
     const int pn = page_no(v);
     const int id = pn < a.max_blocks ? __ldcg(&bt[pn]) : -1;
@@ -566,33 +561,28 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     }
     return id;
   };
-  // 32 page ids at a time, one per lane: `ids` holds those of the steps being
-  // copied (pages 32 c .. of the list), ids_next the 32 after
-  static_assert(32 % BATCH == 0, "a step's ids sit in one group of 32");
+  // 32 page ids at a time, one per lane: `ids` holds those of the pages being
+  // copied (32 k .. of the warp's list), ids_next the 32 after
   int ids = table(lane), ids_next = -1;
-  unsigned have = 0;  // bit (stage * BATCH + j): that page was copied
-  unsigned char* ring = smraw + (size_t)warp * STAGES * BATCH * PG::SLOT;
+  unsigned have = 0;  // bit `stage`: its page was copied
+  unsigned char* ring = smraw + (size_t)warp * STAGES * PG::SLOT;
   const LanePtrs lp = PG::lane_ptrs(a, kvh, lane);
-  // copies step `st`'s pages into its stage (warp-wide; steps come in order)
-  auto issue = [&](int st, int stage) {
-    const int i = (st * BATCH) & 31;
-    if (i == 0 && st > 0) ids = ids_next;
-    if (i == BATCH) ids_next = table(st * BATCH - BATCH + 32 + lane);
-    have &= ~(((1u << BATCH) - 1u) << (stage * BATCH));
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int id = __shfl_sync(0xffffffffu, ids, i + j);
-      if (id >= 0) {
-        PG::fetch(lp, id, smem_u32(ring) + (stage * BATCH + j) * PG::SLOT, lane);
-        have |= 1u << (stage * BATCH + j);
-      }
+  // copies the warp's page i into a stage (warp-wide; pages come in order)
+  auto issue = [&](int i, int stage) {
+    if ((i & 31) == 0 && i > 0) ids = ids_next;
+    if ((i & 31) == 1) ids_next = table(i + 31 + lane);
+    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+    have &= ~(1u << stage);
+    if (id >= 0) {
+      PG::fetch(lp, id, smem_u32(ring) + stage * PG::SLOT, lane);
+      have |= 1u << stage;
     }
   };
   if (FUSE && tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
 #pragma unroll
   for (int st = 0; st < STAGES; ++st) {
     if (st < steps) issue(st, st);
-    cp_async_commit();  // (a group per step, empty behind the last)
+    cp_async_commit();  // (a group per page, empty behind the last)
   }
   // pages some of whose tokens are masked: the last of the sinks, the first of
   // the window, the last of the sequence (-1: none; fused: the new token's)
@@ -649,47 +639,30 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 
   const Kv4Bias bias;
   float t0 = -INFINITY, t1 = -INFINITY;  // m0, m1 plus the slack
-  // one step; MASK: some token of its pages is not seen
+  // one page; MASK: some token of it is not seen
   auto attend = [&](auto mask, const int stage, int v) {
     constexpr bool MASK = decltype(mask)::value;
-    unsigned char* slot = ring + stage * BATCH * PG::SLOT;
-    uint32_t live[BATCH];  // bit r: token r of the page is seen
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      live[j] = 0u;
-      if (MASK && (have >> (stage * BATCH + j)) & 1u) {
-        // t < L, and t >= w0 or t < S
-        const int first = page_no(v + j) * ATT_PAGE;
-        auto below = [&](int t) { return (1u << min(max(t - first, 0), ATT_PAGE)) - 1u; };
-        live[j] = below(L) & (~below(w0) | below(S));
-      }
+    unsigned char* slot = ring + stage * PG::SLOT;
+    uint32_t live = 0u;  // bit r: token r of the page is seen: t < L, and t >= w0 or t < S
+    if (MASK && (have >> stage) & 1u) {
+      const int first = page_no(v) * ATT_PAGE;
+      auto below = [&](int t) { return (1u << min(max(t - first, 0), ATT_PAGE)) - 1u; };
+      live = below(L) & (~below(w0) | below(S));
     }
+    const bool a0 = (live >> g) & 1u, a1 = (live >> (g + 8)) & 1u;  // this lane's tokens (MASK)
     if constexpr (FUSE) {
       if constexpr (MASK) {  // (the new token's page counts as masked)
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j)
-          if (v + j == n - 1 && pos >= 0) PG::patch(slot + j * PG::SLOT, s_new, s_news, pos & 15, lane);
+        if (v == n - 1 && pos >= 0) PG::patch(slot, s_new, s_news, pos & 15, lane);
         __syncwarp();
       }
     }
-    float s[BATCH][4];
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-      PG::scores(slot + j * PG::SLOT, g, t4, bias, qb, s[j]);
-      if (MASK) {
-        if (!((live[j] >> g) & 1u)) s[j][0] = s[j][1] = -INFINITY;
-        if (!((live[j] >> (g + 8)) & 1u)) s[j][2] = s[j][3] = -INFINITY;
-      }
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    PG::scores(slot, g, t4, bias, qb, s);
+    if (MASK) {
+      if (!a0) s[0] = s[1] = -INFINITY;
+      if (!a1) s[2] = s[3] = -INFINITY;
     }
-    float x0 = fmaxf(s[0][0], s[0][2]), x1 = fmaxf(s[0][1], s[0][3]);
-#pragma unroll
-    for (int j = 1; j < BATCH; ++j) {
-      x0 = fmaxf(x0, fmaxf(s[j][0], s[j][2]));
-      x1 = fmaxf(x1, fmaxf(s[j][1], s[j][3]));
-    }
-    x0 *= scale;
-    x1 *= scale;
+    float x0 = fmaxf(s[0], s[2]) * scale, x1 = fmaxf(s[1], s[3]) * scale;
     if (__any_sync(0xffffffffu, x0 > t0 || x1 > t1)) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
@@ -713,42 +686,36 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
         o[mt][3] *= c1;
       }
     }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      float p[4];
-      p[0] = ex2(fmaf(s[j][0], scale, -m0));
-      p[1] = ex2(fmaf(s[j][1], scale, -m1));
-      p[2] = ex2(fmaf(s[j][2], scale, -m0));
-      p[3] = ex2(fmaf(s[j][3], scale, -m1));
-      if (MASK) {  // (-inf under a reference still at -inf is no number)
-        if (!((live[j] >> g) & 1u)) p[0] = p[1] = 0.f;
-        if (!((live[j] >> (g + 8)) & 1u)) p[2] = p[3] = 0.f;
-      }
-      l0 += p[0] + p[2];
-      l1 += p[1] + p[3];
-      PG::template p_scale<MASK>(slot + j * PG::SLOT, g, live[j], p);
-      const uint32_t b0 = movmatrix_trans(pack_h2(p[0], p[1])), b1 = movmatrix_trans(pack_h2(p[2], p[3]));
-      PG::template output<MASK>(slot + j * PG::SLOT, g, t4, bias, live[j], b0, b1, o);
+    float p[4];
+    p[0] = ex2(fmaf(s[0], scale, -m0));
+    p[1] = ex2(fmaf(s[1], scale, -m1));
+    p[2] = ex2(fmaf(s[2], scale, -m0));
+    p[3] = ex2(fmaf(s[3], scale, -m1));
+    if (MASK) {  // (-inf under a reference still at -inf is no number)
+      if (!a0) p[0] = p[1] = 0.f;
+      if (!a1) p[2] = p[3] = 0.f;
     }
+    l0 += p[0] + p[2];
+    l1 += p[1] + p[3];
+    PG::template p_scale<MASK>(slot, g, live, p);
+    const uint32_t b0 = movmatrix_trans(pack_h2(p[0], p[1])), b1 = movmatrix_trans(pack_h2(p[2], p[3]));
+    PG::template output<MASK>(slot, g, t4, bias, live, b0, b1, o);
   };
-  auto one = [&](int step, auto which) {  // the stage is a constant: addresses and masks fold
+  auto one = [&](int i, auto which) {  // the stage is a constant: addresses and masks fold
     constexpr int stage = decltype(which)::value;
-    const int v = wv0 + step * NW * BATCH;  // first visible page of this step
+    const int v = wv0 + i * NW;   // the visible page
     cp_async_wait<STAGES - 1>();  // this lane's copies,
     __syncwarp();                 // and every other's
-    const bool whole = ((have >> (stage * BATCH)) & ((1u << BATCH) - 1u)) == (1u << BATCH) - 1u &&
-                       (unsigned)(part_s - v) >= (unsigned)BATCH && (unsigned)(part_w - v) >= (unsigned)BATCH &&
-                       (unsigned)(part_l - v) >= (unsigned)BATCH;
-    if (whole) attend(std::false_type{}, stage, v);
+    if (((have >> stage) & 1u) && v != part_s && v != part_w && v != part_l) attend(std::false_type{}, stage, v);
     else attend(std::true_type{}, stage, v);
     __syncwarp();  // every lane has read the stage
-    if (step + STAGES < steps) issue(step + STAGES, stage);
+    if (i + STAGES < steps) issue(i + STAGES, stage);
     cp_async_commit();
   };
-  static_assert(STAGES == 2, "steps alternate between two stages");
-  for (int step = 0; step < steps; step += 2) {
-    one(step, std::integral_constant<int, 0>{});
-    if (step + 1 < steps) one(step + 1, std::integral_constant<int, 1>{});
+  static_assert(STAGES == 2, "pages alternate between two stages");
+  for (int i = 0; i < steps; i += 2) {
+    one(i, std::integral_constant<int, 0>{});
+    if (i + 1 < steps) one(i + 1, std::integral_constant<int, 1>{});
   }
   cp_async_wait<0>();
   __syncthreads();  // the rings become the merge's buffer
