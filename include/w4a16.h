@@ -324,8 +324,9 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
  *     row_stride  as for kv_append_rope (elements between the rows of q, k and
  *              v), a multiple of 8, at least Hq * D.
  *     Rows name distinct slots (block_table[b][p / 16], p % 16): rows that name
- *     one slot leave either's bytes there; a row of length 0 is skipped.  A prompt is B = T rows, each with
- *     the sequence's block-table row and the length after its token.
+ *     one slot leave either's bytes there; a row of length 0 is skipped.  A
+ *     prompt is B = T rows, each with the sequence's block-table row and the
+ *     length after its token.
  *   kv_read_int4          rows back as fp16 values (K as cached: rotated).
  *     k_out, v_out  fp16 [B][T][Hkv][D]: row i of sequence b is the token at
  *              position starts[b] + i if that lies in [0, context_lens[b])
@@ -339,7 +340,10 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
  *     splits each sequence's pages evenly over the CTAs that max_context asks
  *     for.  Hq/Hkv may be any of 1..8.  workspace:
  *     paged_gqa_decode_window_workspace_size(.., window = max_context, sinks = 0).
- *     max_context < 2^24, and B x Hkv x its pages up to 2^30.
+ *     It serves every smaller batch, context, window and number of sinks too.
+ *     max_context < 2^24, Hkv up to 2^16, and B x Hkv x its pages up to 2^30.
+ *     In the fused form the page that takes a sequence's new token is none of
+ *     the call's other pages.
  *     A length above max_context sets bit 0 of err_flag; the row attends to its
  *     first max_context tokens, and the fused call appends nothing for it.
  * Every byte of a page past a sequence's length may hold anything.

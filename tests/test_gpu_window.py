@@ -124,6 +124,83 @@ def test_rows_that_see_nothing_give_zeros(api, kind):
     assert np.any(out[0] != 0) and np.all(out[2] == 0)
 
 
+@pytest.mark.parametrize("first", [0, 2, 40])
+def test_tokens_that_score_minus_infinity_weigh_nothing(api, first):
+    """K rows with an infinity whose product is -inf, a page of them and more:
+    pages that come first, pages between, and all but one token."""
+    r = np.random.default_rng(6)
+    G, L = 7, 700
+    bt = synth.block_table(r, np.array([L], np.int32), 50)
+    c = Cache(r, "fp16", 50, 1)
+    q = np.abs(synth.normal_fp16(r, (1, G, D))) + np.float16(0.1)
+    hidden = [0, 1, 2, 3, 4, 5, 6, 7, 20, 43] if first == 0 else [first] if first == 2 else list(range(43))
+    for p in hidden:
+        c.k[bt[0, p], :, :, 5] = -np.inf                           # every token of the page, all heads
+    out = to_host(api.paged_gqa_decode_window(to_dev(q, torch), **c.dev(), block_table=to_dev(bt, torch),
+                                              context_lens=to_dev(np.array([L], np.int32), torch), max_context=L,
+                                              window=L, sinks=0))
+    # the formula without those tokens: they weigh exp(-inf) = 0
+    seen = [t for t in range(L) if t // 16 not in hidden]
+    k = np.concatenate([c.values("k", bt[0, p])[0] for p in range((L + 15) // 16)])[seen]
+    v = np.concatenate([c.values("v", bt[0, p])[0] for p in range((L + 15) // 16)])[seen]
+    s = q[0].astype(np.float64) @ k.T / math.sqrt(D)
+    e = np.exp(s - s.max(1, keepdims=True))
+    p = e / e.sum(1, keepdims=True)
+    ref.check_attention(out, ((p @ v)[None], (p @ np.abs(v))[None], np.abs(v).max()), L, "scores of -inf")
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
+def test_a_call_on_a_given_stream_makes_its_tensors_there(api, kind):
+    """The current stream is busy and its freed memory holds anything; the call on
+    another stream, with no workspace and no output given, is done regardless."""
+    r = np.random.default_rng(7)
+    out, q, c, bt, lens = _run(api, r, kind, 7, 2, [3000, 400], 2500, 4)
+    args = dict(c.dev(), block_table=to_dev(bt, torch), context_lens=to_dev(lens, torch), max_context=3000, window=2500,
+                sinks=4)
+    dq = to_dev(q, torch)
+    torch.full((1 << 22,), 0x7F, dtype=torch.uint8, device="cuda")  # (freed at once)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)
+    got = api.paged_gqa_decode_window(dq, **args, stream=side)
+    side.synchronize()
+    host = torch.empty(got.shape, dtype=got.dtype, pin_memory=True)
+    with torch.cuda.stream(side):
+        host.copy_(got, non_blocking=True)
+    side.synchronize()
+    assert np.array_equal(host.numpy(), out)
+    torch.cuda.synchronize()
+
+
+def test_one_workspace_serves_a_shrinking_batch(api):
+    """38 sequences may be split into more parts than 39."""
+    r = np.random.default_rng(8)
+    n = api.load().paged_gqa_decode_window_workspace_size(39, 28, 4, 2000, 2000, 0, 128)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    lens = np.full(39, 2000, np.int32)
+    bt = np.stack([r.permutation(200)[:125] for _ in lens]).astype(np.int32)   # (pages shared between sequences)
+    for kind in ("fp16", "fp8", "int4"):
+        c = Cache(r, kind, 200, 4)
+        q = synth.normal_fp16(r, (39, 28, D))
+        want = ref.attend(q[:3], lambda p: c.values("k", p), lambda p: c.values("v", p), bt[:3], lens[:3], 1 / math.sqrt(D),
+                          2000, 0)
+        for B in (39, 38, 20, 3):
+            out = api.paged_gqa_decode_window(to_dev(q[:B], torch), **c.dev(), block_table=to_dev(bt[:B], torch),
+                                              context_lens=to_dev(lens[:B], torch), max_context=2000, window=2000,
+                                              sinks=0, workspace=ws)
+            ref.check_attention(to_host(out)[:3], want, 2000, f"{kind} B={B}")
+
+
+def test_the_same_sequence_twice_in_a_batch(api):
+    r = np.random.default_rng(9)
+    _, q, c, bt, lens = _run(api, r, "int4", 7, 2, [1000], 1000, 0)
+    want = ref.attend(q, lambda p: c.values("k", p), lambda p: c.values("v", p), bt, lens, 1 / math.sqrt(D))
+    two = api.paged_gqa_decode_int4(to_dev(np.repeat(q, 2, 0), torch), c.dev()["k_pool"], c.dev()["v_pool"],
+                                    to_dev(np.repeat(bt, 2, 0), torch), to_dev(np.repeat(lens, 2), torch), 1000)
+    assert torch.equal(two[0], two[1])
+    ref.check_attention(to_host(two)[:1], want, 1000, "the same sequence twice")
+
+
 @pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
 def test_a_wide_window_is_plain_attention(api, kind):
     """Window and sinks that cover everything, however they do it: the same bits."""

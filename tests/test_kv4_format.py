@@ -135,6 +135,35 @@ def test_workspace_size_grows_with_what_is_seen(lib):
     assert size(1, 7, 1, 16, 16, 0, 128) <= size(1, 7, 1, 1 << 20, 1 << 20, 0, 128)
 
 
+@pytest.mark.parametrize("form", FORMS)
+def test_attention_refuses_pages_past_32_bit_pitches(lib, form):
+    # (a page of 2^20 fp16 heads is 2^32 bytes: the sizes pass every other check)
+    assert _attn(lib, form, B=1, Hq=1 << 20, Hkv=1 << 20, mc=16, mb=1, window=16) == 3
+    assert b"Hkv" in lib.w4a16_last_error()
+
+
+def test_append_refuses_rows_past_32_bits(lib):
+    assert _append(lib, Hq=(1 << 20) + 1, Hkv=1) == 3
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(28, 4), (7, 1), (8, 8), (6, 2), (64, 8)])
+@pytest.mark.parametrize("mc", [16, 300, 5000, 32768])
+def test_workspace_serves_smaller_calls(lib, Hq, Hkv, mc):
+    """A workspace for a batch serves every smaller one: the size falls with none
+    of the arguments.  The calls check it against their own need, which has to be
+    met for every kind of page."""
+    size = lib.paged_gqa_decode_window_workspace_size
+    sizes = [size(B, Hq, Hkv, mc, mc, 0, 128) for B in (1, 2, 3, 19, 37, 38, 39, 40, 76, 152, 153, 304, 305, 5000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    for B in (1, 38, 39, 146):
+        by_mc = [size(B, Hq, Hkv, n, n, 0, 128) for n in (1, 16, 17, 200, 1000, mc, 40000)[:5]]
+        assert by_mc == sorted(by_mc)
+        by_window = [size(B, Hq, Hkv, mc, w, 4, 128) for w in (0, 1, 100, 1000, 10 ** 6)]
+        assert by_window == sorted(by_window) and by_window[-1] <= max(size(B, Hq, Hkv, mc, mc, 0, 128), 16384)
+        by_sinks = [size(B, Hq, Hkv, mc, 64, n, 128) for n in (0, 1, 100, 10 ** 6)]
+        assert by_sinks == sorted(by_sinks)
+
+
 # ---- the binding's checks ------------------------------------------------------
 @pytest.fixture
 def rec(monkeypatch):

@@ -6,6 +6,7 @@ Nothing here computes any part of the decode path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 
@@ -360,6 +361,9 @@ _SCALE_128 = 1.0 / math.sqrt(128)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+# A call that is given a stream makes its tensors (workspace, outputs) there; they
+# are that stream's, as torch tensors made under torch.cuda.stream are.
+#
 # The calls below are a few microseconds on the GPU at their smallest.  Plain
 # cases (everything on the current device and stream, workspace given) are
 # checked and passed on natively (csrc/torch_args.cpp): a result, an error code,
@@ -397,6 +401,18 @@ def _device_of(t, name):
 
 def _stream_on(stream, dev):
     return _raw_stream(dev) if stream is None and dev >= 0 and _raw_stream is not None else stream_handle(stream)
+
+
+def _made_on(stream, dev):
+    """Where a call makes its tensors: on the stream it was given, whose work
+    alone they are ordered with."""
+    if stream is None or dev < 0:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, dev)
+    if stream.device_index != dev:
+        raise ValueError(f"stream is on device {stream.device_index}, the pools are on device {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _paging_of(kind, k_pool, v_pool, block_table, context_lens):
@@ -480,8 +496,9 @@ def kv_read_int4(k_pool, v_pool, block_table, context_lens, T, starts=None, k_ou
     shape = (B, T, Hkv, 128)
     fresh = k_out is None and v_out is None
     if fresh:
-        k_out = k_pool.new_empty(shape, dtype=torch.float16)
-        v_out = k_pool.new_empty(shape, dtype=torch.float16)
+        with _made_on(stream, dev):
+            k_out = k_pool.new_empty(shape, dtype=torch.float16)
+            v_out = k_pool.new_empty(shape, dtype=torch.float16)
     else:
         _is(k_out, torch.float16, shape, dev, "k_out")
         _is(v_out, torch.float16, shape, dev, "v_out")
@@ -491,16 +508,17 @@ def kv_read_int4(k_pool, v_pool, block_table, context_lens, T, starts=None, k_ou
     return k_out, v_out
 
 
-def _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, like, dev):
-    if workspace is None:
-        nbytes = load().paged_gqa_decode_window_workspace_size(B, Hq, Hkv, max_context, window, sinks, 128)
-        workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=like.device)
-    else:
+def _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, like, dev, stream):
+    if workspace is not None:
         _is(workspace, torch.uint8, workspace.shape, dev, "workspace")
-    if out is None:
-        out = like.new_empty((B, Hq, 128))
-    else:
+    if out is not None:
         _is(out, torch.float16, (B, Hq, 128), dev, "out")
+    with _made_on(stream, dev):
+        if workspace is None:
+            nbytes = load().paged_gqa_decode_window_workspace_size(B, Hq, Hkv, max_context, window, sinks, 128)
+            workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=like.device)
+        if out is None:
+            out = like.new_empty((B, Hq, 128))
     return workspace, out
 
 
@@ -537,7 +555,7 @@ def paged_gqa_decode_int4(q, k_pool, v_pool, block_table, context_lens, max_cont
         if n_q_heads is not None and n_q_heads != Hq:
             raise ValueError(f"q has {Hq} heads, n_q_heads={n_q_heads}")
         _is(q, torch.float16, (B, Hq, 128), dev, "q")
-    workspace, out = _window_buffers(B, Hq, Hkv, max_context, max_context, 0, workspace, out, q, dev)
+    workspace, out = _window_buffers(B, Hq, Hkv, max_context, max_context, 0, workspace, out, q, dev, stream)
     scale = _SCALE_128 if sm_scale is None else float(sm_scale)
     lib, err, sh = load(), _err_flag(err_flag, dev), _stream_on(stream, dev)
     if fuse:
@@ -579,7 +597,7 @@ def paged_gqa_decode_window(q, k_pool, v_pool, block_table, context_lens, max_co
         _arg(q, _H, "q", (B, None, 128))
     Hq = q.shape[1]
     _is(q, torch.float16, (B, Hq, 128), dev, "q")
-    workspace, out = _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, q, dev)
+    workspace, out = _window_buffers(B, Hq, Hkv, max_context, window, sinks, workspace, out, q, dev, stream)
     args = (pages, block_table.data_ptr(), blocks, context_lens.data_ptr(), max_context, window, sinks, B, Hq, Hkv, 128,
             _SCALE_128 if sm_scale is None else float(sm_scale), workspace.data_ptr(), workspace.numel(),
             out.data_ptr(), _err_flag(err_flag, dev), _stream_on(stream, dev))

@@ -23,13 +23,29 @@
 // transposed 8x8 by 8x8 with movmatrix.
 //
 // Softmax: p = exp2(s - m) with a reference m per head that is the running
-// maximum as of the last time a score passed it by more than 2^ATW_SLACK;
+// maximum as of the last time a score passed it by more than ATW_SLACK (log2);
 // only then are the sums rescaled (a warp-wide vote, no shuffles otherwise).
-// p stays <= 2^ATW_SLACK, sums and outputs are fp32, P is rounded to fp16 once.
+// p stays <= 2^ATW_SLACK, sums and outputs are fp32.  P is rounded to fp16 once
+// (relative 2^-11, as large as the output's own rounding): the tensor cores'
+// fp32-accumulating products take fp16.  K and V enter exactly: fp16 as they
+// are, FP8 codes as the fp16 numbers they name with the row scales in fp32, and
+// INT4 values (kv4.cuh) as fp16 numbers.
 //
 // Rows that nothing attends to (an empty window, length 0) give zeros; masked
 // tokens of a visible page take no part whatever their bytes hold: their
 // scores are -inf and their V rows are zeroed.
+//
+// What bounds it (GB300, device time of one call among others): a chain of
+// about 3 us before the first page is there (lengths, block table, page), the
+// pages, and about 3 us to join the parts of a sequence.  fp16 and FP8 pages are
+// waited for (32 sequences, window 1000, fp16: 58 MB in 13.5 us, 4.3 TB/s; batch
+// 8, window 4096, FP8: 70 MB in 16.6 us, 4.2 TB/s); INT4 pages are bound by
+// instructions (4 x 32768 tokens: 71 MB in 20.8 us, 3.4 TB/s; 345 instructions a
+// page all told, 285 of them in the loop, half of those on the logic and integer
+// unit, which masks two codes per operation).  Measured beside two CTAs of eight
+// warps per SM on that case: three CTAs leave 85 registers and spill (29 us and
+// more), 1.5 and 2 times the CTAs pay the chain again (30 and 32 us), three, four
+// or six pages in flight 21.8 us and more.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -43,6 +59,7 @@ namespace w4 {
 
 constexpr int ATW_PITCH = ATT_D + 4;   // floats per head in the warps' merge
 constexpr float ATW_SLACK = 2.0f;
+constexpr float ATW_LOWEST = -3.402823466e38f;  // reference of heads that have met no score: under every finite one
 constexpr float ATW_V8 = 64.0f;        // FP8: factor that keeps p * (V row scale) in fp16's normal range
 
 __device__ __forceinline__ uint4 ldcg16(const void* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
@@ -631,14 +648,16 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 
   // ---- pages --------------------------------------------------------------------
   const float scale = fabsf(a.scale_log2) * atw_s_factor<KIND>();  // (its sign is in the queries)
-  float m0 = -INFINITY, m1 = -INFINITY;  // references of heads 2 t4 and 2 t4 + 1 (log2 domain)
+  // references of heads 2 t4 and 2 t4 + 1 (log2 domain).  Finite from the start:
+  // a score of -inf (an infinity in a K row) under it weighs zero, not NaN
+  float m0 = ATW_LOWEST, m1 = ATW_LOWEST;
   float l0 = 0.f, l1 = 0.f;              // this lane's part of their sums
   float o[8][4];                         // rows: dims odim(mt, g) + {0, 1}, columns: the two heads
 #pragma unroll
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
   const Kv4Bias bias;
-  float t0 = -INFINITY, t1 = -INFINITY;  // m0, m1 plus the slack
+  float t0 = ATW_LOWEST, t1 = ATW_LOWEST;  // m0, m1 plus the slack
   // one page; MASK: some token of it is not seen
   auto attend = [&](auto mask, const int stage, int v) {
     constexpr bool MASK = decltype(mask)::value;
@@ -691,7 +710,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     p[1] = ex2(fmaf(s[1], scale, -m1));
     p[2] = ex2(fmaf(s[2], scale, -m0));
     p[3] = ex2(fmaf(s[3], scale, -m1));
-    if (MASK) {  // (-inf under a reference still at -inf is no number)
+    if (MASK) {  // (-inf times a scale of zero is no number)
       if (!a0) p[0] = p[1] = 0.f;
       if (!a1) p[2] = p[3] = 0.f;
     }
@@ -753,7 +772,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   const int i4 = lane;
   const bool single = active == 1;
   for (int h = warp; h < G; h += NW) {
-    float M = -INFINITY;
+    float M = ATW_LOWEST;
 #pragma unroll
     for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[(w * 8 + h) * 2]);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -761,7 +780,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
       const float mw = s_ml[(w * 8 + h) * 2], lw = s_ml[(w * 8 + h) * 2 + 1];
-      const float f = mw == -INFINITY ? (lw == 0.f ? 0.f : 1.f) : ex2(mw - M);
+      const float f = ex2(mw - M);
       const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + h) * ATW_PITCH + 4 * i4);
       acc.x = fmaf(v.x, f, acc.x);
       acc.y = fmaf(v.y, f, acc.y);
@@ -785,6 +804,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     if (lane == 0)  // releases the warp's partial with the ticket; for the last, acquires the others'
       asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(ticket) : "l"(counter) : "memory");
     ticket = __shfl_sync(0xffffffffu, ticket, 0);
+    __syncwarp();
     if (ticket != (unsigned)(active - 1)) continue;
     if (lane == 0) *counter = 0u;  // ready for the next call
     // one round trip for the first partials and all (max, sum) pairs
@@ -801,14 +821,14 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       e[k] = 32 * k + lane < active ? __ldcg(reinterpret_cast<const float2*>(a.ws_ml) + first + (size_t)(32 * k + lane) * G)
-                                    : make_float2(-INFINITY, 0.f);
+                                    : make_float2(ATW_LOWEST, 0.f);
     float top = fmaxf(e[0].x, e[1].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     float f[2], sum = 0.f;  // weights
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      f[k] = e[k].x == -INFINITY ? (e[k].y == 0.f ? 0.f : 1.f) : ex2(e[k].x - top);
+      f[k] = ex2(e[k].x - top);
       sum = fmaf(e[k].y, f[k], sum);
     }
     sum = warp_sum(sum);
@@ -830,27 +850,54 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   }
 }
 
+// Pages that a sequence can see.
+static long long atw_most_pages(int max_context, int window, int sinks) {
+  const long long all = ((long long)max_context + ATT_PAGE - 1) / ATT_PAGE;
+  const long long seen = ((long long)std::min(sinks, max_context) + ATT_PAGE - 1) / ATT_PAGE +
+                         ((long long)window + ATT_PAGE - 2) / ATT_PAGE + 1;
+  return std::min(all, seen);
+}
+
+template <class F>
+static auto atw_of_kind(int kind, F f) {
+  if (kind == ATW_F16) return f(Page<ATW_F16>{});
+  if (kind == ATW_F8) return f(Page<ATW_F8>{});
+  return f(Page<ATW_I4>{});
+}
+
 // The split's figures (see above) and the CTAs of the grid: no more than either
 // every pair's pages in parts of min_pages, or the shared-out parts and one
 // part of rounding up per pair, can need.
 void atw_plan(AtwArgs& a, int kind, int B, int Hq, int Hkv, int max_context, int window, int sinks) {
   const long long groups = (long long)B * Hkv;
-  const long long all = ((long long)max_context + ATT_PAGE - 1) / ATT_PAGE;
-  const long long seen = ((long long)std::min(sinks, max_context) + ATT_PAGE - 1) / ATT_PAGE +
-                         ((long long)window + ATT_PAGE - 2) / ATT_PAGE + 1;
-  const long long n = std::min(all, seen);
-  const int min_pages = kind == ATW_F16 ? Page<ATW_F16>::MIN_PAGES
-                                        : (kind == ATW_F8 ? Page<ATW_F8>::MIN_PAGES : Page<ATW_I4>::MIN_PAGES);
-  a.slots = ATW_SMS * (kind == ATW_F16 ? Page<ATW_F16>::MIN_CTAS
-                                       : (kind == ATW_F8 ? Page<ATW_F8>::MIN_CTAS : Page<ATW_I4>::MIN_CTAS));
+  const long long n = atw_most_pages(max_context, window, sinks);
+  const int min_pages = atw_of_kind(kind, [](auto p) { return (int)p.MIN_PAGES; });
+  a.slots = ATW_SMS * atw_of_kind(kind, [](auto p) { return (int)p.MIN_CTAS; });
   a.fit = groups <= a.slots ? (int)(a.slots / groups * groups) : a.slots;
   a.fit_mixed = (int)std::max(a.slots - groups / 2, a.slots / 2ll);
   a.ctas = (int)std::min(groups * std::min((n + min_pages - 1) / min_pages, (long long)ATW_MAX_PARTITIONS),
                          std::max(a.fit, a.fit_mixed) + groups);
-  if ((long long)B * Hq * 4 > (long long)ATT_TICKET_BYTES) {  // no ticket for every query head: no splitting
+  if (B * (long long)Hq * 4 > (long long)ATT_TICKET_BYTES) {  // no ticket for every query head: no splitting
     a.fit = a.fit_mixed = 1;
     a.ctas = (int)groups;
   }
+}
+
+// CTAs that no call over up to B sequences, any kind of page and up to this
+// context, window and sinks exceeds where it splits (atw_plan's fit, fit_mixed
+// <= slots): a workspace for a batch serves smaller ones, which may have more
+// parts (Hkv 4: 380 CTAs for 39 sequences, 456 for 38).
+int atw_most_ctas(int B, int Hq, int Hkv, int max_context, int window, int sinks) {
+  const long long tickets = (long long)ATT_TICKET_BYTES / 4 / (Hq / Hkv);  // pairs that split calls can have
+  const long long groups = std::min((long long)B * Hkv, tickets);
+  const long long n = atw_most_pages(max_context, window, sinks);
+  long long most = 0;
+  for (int kind : {ATW_F16, ATW_F8, ATW_I4})
+    most = std::max(most, atw_of_kind(kind, [&](auto p) {
+      return std::min(groups * std::min((n + p.MIN_PAGES - 1) / p.MIN_PAGES, (long long)ATW_MAX_PARTITIONS),
+                      (long long)ATW_SMS * p.MIN_CTAS + groups);
+    }));
+  return (int)most;
 }
 
 template <int KIND, bool FUSE>
@@ -886,6 +933,7 @@ static int atw_call(AtwArgs& a, const uint16_t* q, int q_stride, int num_pages, 
   W4_CHECK_ARG(window >= 0 && sinks >= 0, "%s: window=%d sinks=%d", who, window, sinks);
   W4_CHECK_SHAPE(D == ATT_D, "%s: D=%d, only 128 is built", who, D);
   W4_CHECK_SHAPE(Hq % Hkv == 0 && Hq / Hkv <= 8, "%s: Hq=%d Hkv=%d", who, Hq, Hkv);
+  W4_CHECK_SHAPE(Hkv <= (1 << 16), "%s: Hkv=%d > 65536", who, Hkv);  // (a page of all heads: below 2^32 bytes)
   W4_CHECK_SHAPE((long long)B * Hkv <= (1 << 24) && max_context < (1 << 24) &&
                      (long long)B * Hkv * (max_context / ATT_PAGE + 1) <= (1 << 30),
                  "%s: B=%d x Hkv=%d x max_context %d is too large", who, B, Hkv, max_context);
@@ -933,13 +981,7 @@ extern "C" size_t paged_gqa_decode_window_workspace_size(int B, int Hq, int Hkv,
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_context < 1 || window < 0 || sinks < 0 ||
       (long long)B * Hkv > (1 << 24))
     return 0;
-  int most = 0;  // (whichever kind of page the call is about)
-  for (int kind : {ATW_F16, ATW_F8, ATW_I4}) {
-    AtwArgs a = {};
-    atw_plan(a, kind, B, Hq, Hkv, max_context, window, sinks);
-    if (a.ctas > B * Hkv) most = std::max(most, a.ctas);
-  }
-  return most ? atw_workspace_bytes(most, Hq / Hkv) : ATT_TICKET_BYTES;
+  return atw_workspace_bytes(atw_most_ctas(B, Hq, Hkv, max_context, window, sinks), Hq / Hkv);
 }
 
 extern "C" int paged_gqa_decode_window(const uint16_t* q, int q_stride, const uint16_t* k_pool, const uint16_t* v_pool,

@@ -177,6 +177,7 @@ struct AtwArgs {
 int launch_attn_window(const AtwArgs& a, cudaStream_t s);
 // sets the split and the grid (a.kind, B, Hq, Hkv and the limits given)
 void atw_plan(AtwArgs& a, int kind, int B, int Hq, int Hkv, int max_context, int window, int sinks);
+int atw_most_ctas(int B, int Hq, int Hkv, int max_context, int window, int sinks);
 inline size_t atw_workspace_bytes(int ctas, int G) { return ATT_TICKET_BYTES + (size_t)ctas * G * (128 + 2) * 4; }
 inline void atw_workspace(AtwArgs& a, void* ws, int ctas, int G) {  // tickets first, as for the other workspaces
   char* w = static_cast<char*>(ws);

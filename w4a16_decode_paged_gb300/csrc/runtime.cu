@@ -172,11 +172,8 @@ extern "C" int w4a16_model_create(const w4a16_model_config* cfg, const w4a16_mod
       delete m;
       return set_error(W4A16_ERR_SHAPE, "model_create: max_context %d is too large for INT4 pools", max_context);
     }
-    for (int b = 1; b <= max_batch; ++b) {
-      AtwArgs t = {};
-      atw_plan(t, ATW_I4, b, c.n_q_heads, c.n_kv_heads, max_context, max_context, 0);
-      m->attn_ws_bytes = std::max(m->attn_ws_bytes, atw_workspace_bytes(t.ctas, c.n_q_heads / c.n_kv_heads));
-    }
+    const int ctas = atw_most_ctas(max_batch, c.n_q_heads, c.n_kv_heads, max_context, max_context, 0);
+    m->attn_ws_bytes = std::max(m->attn_ws_bytes, atw_workspace_bytes(ctas, c.n_q_heads / c.n_kv_heads));
   }
   const size_t o_aws = off; off += up256(m->attn_ws_bytes);
   m->lm_ws_bytes = lm_head_workspace_bytes(max_batch, c.vocab);

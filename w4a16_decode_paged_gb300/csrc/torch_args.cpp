@@ -1,7 +1,7 @@
 // torch_args.cpp -- marshalling of torch tensors for the calls whose kernels
 // take a few microseconds: checking eight to fourteen tensors in Python costs
 // more than the kernel behind them (GB300's host cores: 9 to 15 us a call from
-// Python, 4 to 6 us from here).
+// Python, 3 to 4.5 us from here).
 //
 // Each function checks dtype, shape, layout and device of its arguments and
 // calls the C ABI (include/w4a16.h) on the current stream.  It returns the
