@@ -106,48 +106,29 @@ __device__ __forceinline__ void kv4_put(uint8_t* slice, bool is_k, int t, int c,
 // that the lane's half of the row takes them with: the low half rotates to
 // x c - y s, the high half to x c + y s (x its own, y the partner's).
 struct RopeLane {
-  float2 c[4], s[4];
+  float c[8], s[8];
   __device__ __forceinline__ void load(const float* cs, const float* sn, int lane) {
     const int i = 8 * (lane & 7);
     const float sign = (lane & 8) == 0 ? -1.f : 1.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[e] = *reinterpret_cast<const float2*>(cs + i + 2 * e);
-      s[e] = *reinterpret_cast<const float2*>(sn + i + 2 * e);
-      s[e].x *= sign;
-      s[e].y *= sign;
+    for (int e = 0; e < 8; ++e) {
+      c[e] = cs[i + e];
+      s[e] = sign * sn[i + e];
     }
   }
 };
-__device__ __forceinline__ uint64_t bits2(float2 a) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a.x), "f"(a.y));
-  return d;
-}
-__device__ __forceinline__ float2 float2_of(uint64_t d) {
-  float2 a;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(d));
-  return a;
-}
-// two products, two sums: an instruction each
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
-  return float2_of(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
-  return float2_of(d);
-}
 __device__ __forceinline__ void rope_rows(uint4& x, const RopeLane& t) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const uint32_t y = __shfl_xor_sync(0xffffffffu, (&x.x)[w], 8);
-    const float2 own = __half22float2(*reinterpret_cast<const __half2*>(&(&x.x)[w]));
-    const float2 other = __half22float2(*reinterpret_cast<const __half2*>(&y));
-    const float2 r = add2(mul2(own, t.c[w]), mul2(other, t.s[w]));
-    const __half2 h = __floats2half2_rn(r.x, r.y);
+    float r[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float own = __half2float(__ushort_as_half((unsigned short)((&x.x)[w] >> (16 * e))));
+      const float other = __half2float(__ushort_as_half((unsigned short)(y >> (16 * e))));
+      r[e] = __fadd_rn(__fmul_rn(own, t.c[2 * w + e]), __fmul_rn(other, t.s[2 * w + e]));
+    }
+    const __half2 h = __floats2half2_rn(r[0], r[1]);
     (&x.x)[w] = *reinterpret_cast<const uint32_t*>(&h);
   }
 }
