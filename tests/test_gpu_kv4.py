@@ -115,6 +115,35 @@ def test_append_in_place_and_strided_rows_write_the_same_bytes(api):
         assert all(np.array_equal(x, y) for x, y in zip(outs[0], o))
 
 
+def test_rotation_rounds_its_products_and_their_sum(api):
+    """Bit for bit the rotation in single fp32 operations (each rounded once, with
+    the same cosines and sines): what makes every call write the same bytes."""
+    r = np.random.default_rng(12)
+    n, Hq, Hkv = 4000, 28, 4
+    q, k, v = (to_dev(synth.normal_fp16(r, (n, h, D)), torch) for h in (Hq, Hkv, Hkv))
+    bt = torch.arange(n // 16, dtype=torch.int32, device="cuda").expand(n, -1).contiguous()
+    lens = torch.arange(1, n + 1, dtype=torch.int32, device="cuda")
+    kp, vp = (torch.zeros((n // 16, Hkv, 1088), dtype=torch.uint8, device="cuda") for _ in "kv")
+    inv = torch.tensor([THETA ** (-2.0 * i / D) for i in range(D // 2)], dtype=torch.float64).float().cuda()
+    ang = (lens - 1).float()[:, None] * inv
+    c, s = ang.cos()[:, None], ang.sin()[:, None]
+
+    def rotate(x):
+        a, b = x.float().split(D // 2, -1)
+        ac, bs, bc, as_ = a * c, b * s, b * c, a * s
+        return torch.cat([ac - bs, bc + as_], -1).half()
+    out = api.kv_append_rope_int4(q, k, v, kp, vp, bt, lens, THETA, q_out=torch.empty_like(q))
+    assert torch.equal(out, rotate(q))
+    # a small batch's kernel: the same values as the prompt's
+    kp2, vp2 = torch.zeros_like(kp), torch.zeros_like(vp)
+    few = torch.tensor([0, 1, 17, 1999, 2000, 3999], device="cuda")
+    out2 = api.kv_append_rope_int4(q[few], k[few], v[few], kp2, vp2, bt[few], lens[few], THETA,
+                                   q_out=torch.empty_like(q[few]))
+    assert torch.equal(out2, out[few])
+    rows = [api.kv_read_int4(*pools, bt[few], lens[few], 1, starts=lens[few] - 1) for pools in ((kp, vp), (kp2, vp2))]
+    assert torch.equal(rows[0][0], rows[1][0]) and torch.equal(rows[0][1], rows[1][1])
+
+
 def test_append_of_extreme_rows(api):
     """Zeros, the largest and the smallest fp16 numbers, infinities and NaN:
     V is not rotated, so its bytes are the reference's."""

@@ -38,8 +38,8 @@
 // What bounds it (GB300, device time of one call among others): a chain of
 // about 3 us before the first page is there (lengths, block table, page), the
 // pages, and about 3 us to join the parts of a sequence.  fp16 and FP8 pages are
-// waited for (32 sequences, window 1000, fp16: 58 MB in 13.5 us, 4.3 TB/s; batch
-// 8, window 4096, FP8: 70 MB in 16.8 us, 4.2 TB/s); INT4 pages are bound by
+// waited for (32 sequences, window 1000, fp16: 58 MB in 13.4 us, 4.3 TB/s; batch
+// 8, window 4096, FP8: 70 MB in 16.4 us, 4.3 TB/s); INT4 pages are bound by
 // instructions (4 x 32768 tokens: 71 MB in 20.6 us, 3.5 TB/s; 345 instructions a
 // page all told, 285 of them in the loop, half of those on the logic and integer
 // unit, which masks two codes per operation).  Measured beside two CTAs of eight

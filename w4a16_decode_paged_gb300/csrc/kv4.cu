@@ -6,8 +6,9 @@
 // back is 136 bytes in and 512 out per kv head.  A few rows are bound by the
 // chain of latencies (length, table entry, page: 2.5 us a call), a prompt's
 // rows by instructions (the append of 2048 rows issues 0.58 a cycle per
-// scheduler), a whole cache read back by instructions (0.51) and its stores
-// (9 MB in, 33.5 MB out in 9.5 us, 4.5 TB/s).
+// scheduler), a whole cache read back by one burst of stores behind that chain
+// (9 MB in, 33.5 MB out in 9.5 us, 4.5 TB/s; half the instructions, with whole
+// pages stored unchecked, measured the same).
 #include "kernels.h"
 #include "kv4.cuh"
 
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(APPEND_WARPS * 32, 4) w4pg_rope_append_int4(co
 // One row per CTA as long as two per SM hold them (a decode batch: the shortest
 // chain of latencies, 2.5 us); four where a prompt's rows would queue behind each
 // other's chains (2048 rows of 28 + 2 x 4 heads, with the read back of them all:
-// 20.3 us with one row per CTA, 14.6 with two, 13.1 with four).
+// 20.3 us with one row per CTA, 14.6 with two, 13.2 with four).
 int launch_rope_append_int4(const Kv4AppendArgs& a, cudaStream_t s) {
   cudaError_t e;
   if (a.B <= 2 * num_sms()) e = launch_pdl(w4pg_rope_append_int4<1>, dim3(a.B), dim3(APPEND_WARPS * 32), 0, s, a);

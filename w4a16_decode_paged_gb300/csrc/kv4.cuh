@@ -102,6 +102,8 @@ __device__ __forceinline__ void kv4_put(uint8_t* slice, bool is_k, int t, int c,
 // Rotate-half RoPE of rows held eight dims per lane (as above): the partner
 // dims i +- 64 sit eight lanes away.  cs, sn: 64 cosines and sines.  Products
 // and their sum are rounded one by one, so every caller gets the same bits.
+// (Two to an instruction, mul.rn.f32x2 and add.rn.f32x2, came out fused and
+// rounded once; the products alone in pairs saved no time.)
 // This lane's eight cosines and sines of one position, the sines with the sign
 // that the lane's half of the row takes them with: the low half rotates to
 // x c - y s, the high half to x c + y s (x its own, y the partner's).
