@@ -1,0 +1,44 @@
+"""Windowed and INT4 decode attention where single tokens, small weights, small
+values and large scores decide the result, against the 64-bit formula with the
+bound of attn_bound.  GPU only (marked gpu)."""
+import numpy as np
+import pytest
+
+import attn_bound as ab
+from gpu_util import to_dev, to_host
+from test_attn_bound import dominant_tokens, one_hot_pages, sink_queries
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+@pytest.fixture(scope="module")
+def api():
+    from w4a16_decode_paged_gb300 import api as _api
+    from w4a16_decode_paged_gb300 import build
+    build.build()
+    return _api
+
+
+def run(api, x, q, scale, others=()):
+    """Attention of one sequence over x's pages; `others`: lengths of sequences
+    beside it in the batch, over the same pages."""
+    lens = np.array([x.n, *others], np.int32)
+    dev = lambda a: to_dev(a, torch)
+    out = api.paged_gqa_decode_window(dev(np.repeat(q[None], len(lens), 0)), **{k: dev(a) for k, a in x.pools.items()},
+                                      block_table=dev(np.repeat(x.bt, len(lens), 0)), context_lens=dev(lens),
+                                      max_context=16 * x.bt.shape[1], window=x.n, sinks=0, sm_scale=scale)
+    return to_host(out)[0]
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
+@pytest.mark.parametrize("n,above,every", [(600, 17.0, 600), (5000, 14.0, 16), (5000, 16.0, 16), (32768, 18.0, 16),
+                                           (32768, 19.0, 900)])
+def test_small_weights_beside_tokens_without_a_value(api, kind, n, above, every):
+    """The largest weights are tokens whose V is zero (one, or one in every page);
+    the output is the sum of many weights of e^-14 and less of them."""
+    r = np.random.default_rng(int(n + above))
+    x = ab.Rows(r, kind, *dominant_tokens(r, n, 2, above, every))
+    q = sink_queries(r, 14)
+    ab.check(run(api, x, q, 1.0), q, x.K, x.V, 1.0, x.v_scale, f"{kind} {n}")

@@ -22,14 +22,18 @@
 // registers had too little in flight.)  P^T is the scores' accumulator
 // transposed 8x8 by 8x8 with movmatrix.
 //
-// Softmax: p = exp2(s - m) with a reference m per head that is the running
-// maximum as of the last time a score passed it by more than ATW_SLACK (log2);
-// only then are the sums rescaled (a warp-wide vote, no shuffles otherwise).
-// p stays <= 2^ATW_SLACK, sums and outputs are fp32.  P is rounded to fp16 once
-// (relative 2^-11, as large as the output's own rounding): the tensor cores'
-// fp32-accumulating products take fp16.  K and V enter exactly: fp16 as they
-// are, FP8 codes as the fp16 numbers they name with the row scales in fp32, and
-// INT4 values (kv4.cuh) as fp16 numbers.
+// Softmax: p = exp2(s - m) with a reference m per head that lies HEAD (log2)
+// under the running maximum as of the last time a score passed it by more than
+// ATW_SLACK; only then are the sums rescaled (a warp-wide vote, no shuffles
+// otherwise).  Sums and outputs are fp32.  P is rounded to fp16 once: the tensor
+// cores' fp32-accumulating products take fp16.  With HEAD = 13 the largest
+// p is 2^15, fp16's largest power of two; weights down to 2^-27 of the largest
+// are normal numbers (rounded by 2^-11 of themselves, as much as the output)
+// and smaller ones are off by 2^-38 of the largest at most.  (With p <= 1 the
+// many small weights beside a few large ones are lost from 2^-14 down, while
+// their sum keeps them: 32768 tokens, e^-18 below: a quarter of the output.)
+// K and V enter exactly: fp16 as they are, FP8 codes as the fp16 numbers they
+// name with the row scales in fp32, and INT4 values (kv4.cuh) as fp16 numbers.
 //
 // Rows that nothing attends to (an empty window, length 0) give zeros; masked
 // tokens of a visible page take no part whatever their bytes hold: their
@@ -118,6 +122,7 @@ struct Page;
 template <>
 struct Page<ATW_F16> {
   static constexpr int NW = 8;      // warps per CTA
+  static constexpr float HEAD = 13.0f;
   static constexpr int MIN_CTAS = 1;
   static constexpr int MIN_PAGES = 8;
   static constexpr int V = 4096;    // V's offset in a page's slot
@@ -189,6 +194,7 @@ struct Page<ATW_F16> {
 template <>
 struct Page<ATW_F8> {
   static constexpr int NW = 8;
+  static constexpr float HEAD = 0.0f;  // (P carries the row scales)
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 16;
   static constexpr int V = 2048, KS = 4096, VS = 4160;
@@ -276,6 +282,7 @@ struct Page<ATW_F8> {
 template <>
 struct Page<ATW_I4> {
   static constexpr int NW = 8;
+  static constexpr float HEAD = 13.0f;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 32;
   static constexpr int V = 1024, KS = 2048, VS = 2112;
@@ -648,7 +655,8 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 
   // ---- pages --------------------------------------------------------------------
   const float scale = fabsf(a.scale_log2) * atw_s_factor<KIND>();  // (its sign is in the queries)
-  // references of heads 2 t4 and 2 t4 + 1 (log2 domain).  Finite from the start:
+  // references of heads 2 t4 and 2 t4 + 1 (log2 domain, HEAD under the scores that
+  // set them).  Finite from the start:
   // a score of -inf (an infinity in a K row) under it weighs zero, not NaN
   float m0 = ATW_LOWEST, m1 = ATW_LOWEST;
   float l0 = 0.f, l1 = 0.f;              // this lane's part of their sums
@@ -657,7 +665,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   for (int mt = 0; mt < 8; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
 
   const Kv4Bias bias;
-  float t0 = ATW_LOWEST, t1 = ATW_LOWEST;  // m0, m1 plus the slack
+  float t0 = ATW_LOWEST, t1 = ATW_LOWEST;  // scores above these move the references
   // one page; MASK: some token of it is not seen
   auto attend = [&](auto mask, const int stage, int v) {
     constexpr bool MASK = decltype(mask)::value;
@@ -688,13 +696,13 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
       }
-      x0 = fmaxf(m0, x0);
-      x1 = fmaxf(m1, x1);
+      x0 = fmaxf(m0, x0 - PG::HEAD);
+      x1 = fmaxf(m1, x1 - PG::HEAD);
       const float c0 = x0 == m0 ? 1.f : ex2(m0 - x0), c1 = x1 == m1 ? 1.f : ex2(m1 - x1);
       m0 = x0;
       m1 = x1;
-      t0 = m0 + ATW_SLACK;
-      t1 = m1 + ATW_SLACK;
+      t0 = m0 + (PG::HEAD + ATW_SLACK);
+      t1 = m1 + (PG::HEAD + ATW_SLACK);
       l0 *= c0;
       l1 *= c1;
 #pragma unroll
