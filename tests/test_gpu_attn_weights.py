@@ -42,3 +42,45 @@ def test_small_weights_beside_tokens_without_a_value(api, kind, n, above, every)
     x = ab.Rows(r, kind, *dominant_tokens(r, n, 2, above, every))
     q = sink_queries(r, 14)
     ab.check(run(api, x, q, 1.0), q, x.K, x.V, 1.0, x.v_scale, f"{kind} {n}")
+
+
+@pytest.mark.parametrize("size", [1e4, 1.0, 1e-2, 1e-3, 1e-4, 3e-6])
+def test_fp8_values_of_any_size(api, size):
+    """Row scales from 22 down to 7e-9; V with a mean, scores spread by a few units."""
+    r = np.random.default_rng(11)
+    n = 4096
+    K = r.standard_normal((n, 2, D))
+    V = size * (1.0 + 0.5 * r.standard_normal((n, 2, D)))
+    x = ab.Rows(r, "fp8", K, V)
+    q = (3.0 * r.standard_normal((14, D))).astype(np.float16)
+    ab.check(run(api, x, q, D ** -0.5, [100, 37]), q, x.K, x.V, D ** -0.5, x.v_scale, f"V of about {size}")
+
+
+@pytest.mark.parametrize("order", ["falling", "rising", "mixed", "against the weights", "zeros first"])
+def test_fp8_row_scales_that_differ(api, order):
+    """Rows whose sizes lie up to 2^40 apart in one sequence; what counts is their
+    part of the output."""
+    r = np.random.default_rng(12)
+    n, Hkv = 3000, 2
+    K = r.standard_normal((n, Hkv, D)) * 0.5
+    e = np.linspace(8.0, -16.0, n)
+    if order == "rising":
+        e = -8.0 - e
+    if order == "mixed":
+        e = r.uniform(-16.0, 8.0, n)
+    V = (1.0 + 0.5 * r.standard_normal((n, Hkv, D))) * 2.0 ** e[:, None, None]
+    if order == "against the weights":                     # a score of 24 (log2) takes back a size of 2^-24
+        K[:, :, 0] = (8.0 - e[:, None]) * np.log(2.0) * D ** 0.5 / 16
+    if order == "zeros first":
+        V[:2500] = 0.0
+    x = ab.Rows(r, "fp8", K, V)
+    q = r.standard_normal((6, D)).astype(np.float16)
+    if order == "against the weights":
+        q[:, 0] = 16.0
+    ab.check(run(api, x, q, D ** -0.5), q, x.K, x.V, D ** -0.5, x.v_scale, order)
+
+
+def test_fp8_without_any_value(api):
+    r = np.random.default_rng(13)
+    x = ab.Rows(r, "fp8", r.standard_normal((200, 1, D)), np.zeros((200, 1, D)))
+    assert np.all(run(api, x, r.standard_normal((7, D)).astype(np.float16), 0.1) == 0)

@@ -22,18 +22,24 @@
 // registers had too little in flight.)  P^T is the scores' accumulator
 // transposed 8x8 by 8x8 with movmatrix.
 //
-// Softmax: p = exp2(s - m) with a reference m per head that lies HEAD (log2)
+// Softmax: p = exp2(s - m) with a reference m per head that lies ATW_HEAD (log2)
 // under the running maximum as of the last time a score passed it by more than
 // ATW_SLACK; only then are the sums rescaled (a warp-wide vote, no shuffles
 // otherwise).  Sums and outputs are fp32.  P is rounded to fp16 once: the tensor
-// cores' fp32-accumulating products take fp16.  With HEAD = 13 the largest
+// cores' fp32-accumulating products take fp16.  With a head of 13 the largest
 // p is 2^15, fp16's largest power of two; weights down to 2^-27 of the largest
 // are normal numbers (rounded by 2^-11 of themselves, as much as the output)
 // and smaller ones are off by 2^-38 of the largest at most.  (With p <= 1 the
 // many small weights beside a few large ones are lost from 2^-14 down, while
 // their sum keeps them: 32768 tokens, e^-18 below: a quarter of the output.)
-// K and V enter exactly: fp16 as they are, FP8 codes as the fp16 numbers they
-// name with the row scales in fp32, and INT4 values (kv4.cuh) as fp16 numbers.
+// K and V enter exactly: fp16 as they are, INT4 values (kv4.cuh) as fp16 numbers,
+// FP8 codes as the fp16 numbers that they name.  K's row scales multiply the
+// scores; V's go into P before its rounding, where a product p s of a small s
+// would leave fp16's range as small weights do.  So the FP8 outputs have a
+// reference of their own, which follows log2(p s) as m follows log2(p): P is
+// p s 2^(m - mo) <= 2^15 for any row scales, and the warps' outputs go from mo
+// to m where they are merged.  (A fixed factor of 64 lost 4 % of an output of
+// 1e-4.)
 //
 // Rows that nothing attends to (an empty window, length 0) give zeros; masked
 // tokens of a visible page take no part whatever their bytes hold: their
@@ -64,7 +70,8 @@ namespace w4 {
 constexpr int ATW_PITCH = ATT_D + 4;   // floats per head in the warps' merge
 constexpr float ATW_SLACK = 2.0f;
 constexpr float ATW_LOWEST = -3.402823466e38f;  // reference of heads that have met no score: under every finite one
-constexpr float ATW_V8 = 64.0f;        // FP8: factor that keeps p * (V row scale) in fp16's normal range
+constexpr float ATW_HEAD = 13.0f;      // log2: how far references lie under the scores that set them
+constexpr float ATW_MOST = 100.0f;     // log2: bound of FP8's factor on p and row scale (they may be zero)
 
 __device__ __forceinline__ uint4 ldcg16(const void* p) { return __ldcg(reinterpret_cast<const uint4*>(p)); }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -88,6 +95,11 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 __device__ __forceinline__ float ex2(float x) {
   float d;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
+  return d;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float d;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
   return d;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -122,7 +134,6 @@ struct Page;
 template <>
 struct Page<ATW_F16> {
   static constexpr int NW = 8;      // warps per CTA
-  static constexpr float HEAD = 13.0f;
   static constexpr int MIN_CTAS = 1;
   static constexpr int MIN_PAGES = 8;
   static constexpr int V = 4096;    // V's offset in a page's slot
@@ -163,9 +174,6 @@ struct Page<ATW_F16> {
       mma(s, x.z, y.z, x.w, y.w, qb[2 * i + 1][0], qb[2 * i + 1][1]);
     }
   }
-  // factors of P that come before its rounding
-  template <bool MASK>
-  static __device__ __forceinline__ void p_scale(const unsigned char*, int, uint32_t, float (&)[4]) {}
   // O^T += V^T P^T; MASK: bit r of live says that token r is seen, V rows of
   // others count as zero whatever they hold
   template <bool MASK>
@@ -194,7 +202,6 @@ struct Page<ATW_F16> {
 template <>
 struct Page<ATW_F8> {
   static constexpr int NW = 8;
-  static constexpr float HEAD = 0.0f;  // (P carries the row scales)
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 16;
   static constexpr int V = 2048, KS = 4096, VS = 4160;
@@ -243,17 +250,14 @@ struct Page<ATW_F8> {
     s[2] *= f1;
     s[3] *= f1;
   }
-  // V row scales go into P before its rounding
+  // V row scales of tokens g and g + 8 (0: not seen)
   template <bool MASK>
-  static __device__ __forceinline__ void p_scale(const unsigned char* slot, int g, uint32_t live, float (&p)[4]) {
+  static __device__ __forceinline__ void v_scales(const unsigned char* slot, int g, uint32_t live, float& f0, float& f1) {
     const float* vs = reinterpret_cast<const float*>(slot + VS);
-    float f0 = vs[g] * ATW_V8, f1 = vs[g + 8] * ATW_V8;
+    f0 = vs[g];
+    f1 = vs[g + 8];
     if (MASK && !((live >> g) & 1u)) f0 = 0.f;
     if (MASK && !((live >> (g + 8)) & 1u)) f1 = 0.f;
-    p[0] *= f0;
-    p[1] *= f0;
-    p[2] *= f1;
-    p[3] *= f1;
   }
   template <bool MASK>
   static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
@@ -282,7 +286,6 @@ struct Page<ATW_F8> {
 template <>
 struct Page<ATW_I4> {
   static constexpr int NW = 8;
-  static constexpr float HEAD = 13.0f;
   static constexpr int MIN_CTAS = 2;
   static constexpr int MIN_PAGES = 32;
   static constexpr int V = 1024, KS = 2048, VS = 2112;
@@ -325,8 +328,6 @@ struct Page<ATW_I4> {
     }
   }
   template <bool MASK>
-  static __device__ __forceinline__ void p_scale(const unsigned char*, int, uint32_t, float (&)[4]) {}
-  template <bool MASK>
   static __device__ __forceinline__ void output(const unsigned char* slot, int g, int t4, const Kv4Bias& bias, uint32_t live,
                                                 uint32_t b0, uint32_t b1, float (&o)[8][4]) {
     const unsigned char* p = slot + V + 128 * t4 + 16 * (g ^ (2 * t4));
@@ -364,7 +365,7 @@ struct Page<ATW_I4> {
 template <int KIND>
 __device__ __forceinline__ constexpr float atw_s_factor() { return KIND == ATW_I4 ? 64.f : 1.f; }
 template <int KIND>
-__device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I4 ? 64.f : (KIND == ATW_F8 ? 1.f / ATW_V8 : 1.f); }
+__device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I4 ? 64.f : 1.f; }
 
 // ---------------------------------------------------------------------------
 // Which pages a CTA takes.  A (sequence, kv head) pair with n visible pages is
@@ -525,6 +526,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   extern __shared__ __align__(128) unsigned char smraw[];  // the warps' rings, then their merge
   __shared__ __align__(16) __half s_q[8][ATT_D + 8];
   __shared__ float s_ml[NW * 8 * 2];
+  __shared__ float s_mo[KIND == ATW_F8 ? NW * 8 : 1];  // FP8: the references of the warps' outputs
   __shared__ __align__(16) float s_cos[FUSE ? ATT_D / 2 : 4], s_sin[FUSE ? ATT_D / 2 : 4];
   __shared__ __align__(16) uint16_t s_new[2][32];  // codes of the new K and V rows (fused)
   __shared__ uint8_t s_news[2][4];
@@ -655,8 +657,8 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 
   // ---- pages --------------------------------------------------------------------
   const float scale = fabsf(a.scale_log2) * atw_s_factor<KIND>();  // (its sign is in the queries)
-  // references of heads 2 t4 and 2 t4 + 1 (log2 domain, HEAD under the scores that
-  // set them).  Finite from the start:
+  // references of heads 2 t4 and 2 t4 + 1 (log2 domain, ATW_HEAD under the scores
+  // that set them).  Finite from the start:
   // a score of -inf (an infinity in a K row) under it weighs zero, not NaN
   float m0 = ATW_LOWEST, m1 = ATW_LOWEST;
   float l0 = 0.f, l1 = 0.f;              // this lane's part of their sums
@@ -666,6 +668,9 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
 
   const Kv4Bias bias;
   float t0 = ATW_LOWEST, t1 = ATW_LOWEST;  // scores above these move the references
+  // FP8: the outputs' references, the sums log2(p s) that move them, and the
+  // factors 2^(m - mo) of p s
+  float mo0 = ATW_LOWEST, mo1 = ATW_LOWEST, fo0 = 0.f, fo1 = 0.f;
   // one page; MASK: some token of it is not seen
   auto attend = [&](auto mask, const int stage, int v) {
     constexpr bool MASK = decltype(mask)::value;
@@ -690,21 +695,44 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
       if (!a1) s[2] = s[3] = -INFINITY;
     }
     float x0 = fmaxf(s[0], s[2]) * scale, x1 = fmaxf(s[1], s[3]) * scale;
-    if (__any_sync(0xffffffffu, x0 > t0 || x1 > t1)) {
+    bool move = x0 > t0 || x1 > t1;
+    float v0 = 0.f, v1 = 0.f, y0 = 0.f, y1 = 0.f;  // FP8: V's row scales, the largest log2(p s)
+    if constexpr (KIND == ATW_F8) {
+      PG::template v_scales<MASK>(slot, g, live, v0, v1);
+      const float e0 = lg2(fabsf(v0)), e1 = lg2(fabsf(v1));
+      y0 = fmaxf(fmaf(s[0], scale, e0), fmaf(s[2], scale, e1));
+      y1 = fmaxf(fmaf(s[1], scale, e0), fmaf(s[3], scale, e1));
+      move = move || y0 - mo0 > ATW_HEAD + ATW_SLACK || y1 - mo1 > ATW_HEAD + ATW_SLACK;
+    }
+    if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
         x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+        if constexpr (KIND == ATW_F8) {
+          y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, d));
+          y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, d));
+        }
       }
-      x0 = fmaxf(m0, x0 - PG::HEAD);
-      x1 = fmaxf(m1, x1 - PG::HEAD);
-      const float c0 = x0 == m0 ? 1.f : ex2(m0 - x0), c1 = x1 == m1 ? 1.f : ex2(m1 - x1);
+      x0 = fmaxf(m0, x0 - ATW_HEAD);
+      x1 = fmaxf(m1, x1 - ATW_HEAD);
+      float c0 = x0 == m0 ? 1.f : ex2(m0 - x0), c1 = x1 == m1 ? 1.f : ex2(m1 - x1);
       m0 = x0;
       m1 = x1;
-      t0 = m0 + (PG::HEAD + ATW_SLACK);
-      t1 = m1 + (PG::HEAD + ATW_SLACK);
+      t0 = m0 + (ATW_HEAD + ATW_SLACK);
+      t1 = m1 + (ATW_HEAD + ATW_SLACK);
       l0 *= c0;
       l1 *= c1;
+      if constexpr (KIND == ATW_F8) {
+        y0 = fmaxf(mo0, y0 - ATW_HEAD);
+        y1 = fmaxf(mo1, y1 - ATW_HEAD);
+        c0 = y0 == mo0 ? 1.f : ex2(mo0 - y0);
+        c1 = y1 == mo1 ? 1.f : ex2(mo1 - y1);
+        mo0 = y0;
+        mo1 = y1;
+        fo0 = ex2(fminf(m0 - mo0, ATW_MOST));
+        fo1 = ex2(fminf(m1 - mo1, ATW_MOST));
+      }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
         o[mt][0] *= c0;
@@ -724,7 +752,12 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     }
     l0 += p[0] + p[2];
     l1 += p[1] + p[3];
-    PG::template p_scale<MASK>(slot, g, live, p);
+    if constexpr (KIND == ATW_F8) {
+      p[0] *= v0 * fo0;
+      p[1] *= v0 * fo1;
+      p[2] *= v1 * fo0;
+      p[3] *= v1 * fo1;
+    }
     const uint32_t b0 = movmatrix_trans(pack_h2(p[0], p[1])), b1 = movmatrix_trans(pack_h2(p[2], p[3]));
     PG::template output<MASK>(slot, g, t4, bias, live, b0, b1, o);
   };
@@ -767,6 +800,10 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     ml[1] = l0;
     ml[2] = m1;
     ml[3] = l1;
+    if constexpr (KIND == ATW_F8) {
+      s_mo[warp * 8 + 2 * t4] = mo0;
+      s_mo[warp * 8 + 2 * t4 + 1] = mo1;
+    }
   }
   __syncthreads();
   const size_t qh0 = (size_t)b * a.Hq + (size_t)kvh * G;
@@ -789,11 +826,12 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     for (int w = 0; w < NW; ++w) {
       const float mw = s_ml[(w * 8 + h) * 2], lw = s_ml[(w * 8 + h) * 2 + 1];
       const float f = ex2(mw - M);
+      const float fo = KIND == ATW_F8 ? ex2(s_mo[KIND == ATW_F8 ? w * 8 + h : 0] - M) : f;
       const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 8 + h) * ATW_PITCH + 4 * i4);
-      acc.x = fmaf(v.x, f, acc.x);
-      acc.y = fmaf(v.y, f, acc.y);
-      acc.z = fmaf(v.z, f, acc.z);
-      acc.w = fmaf(v.w, f, acc.w);
+      acc.x = fmaf(v.x, fo, acc.x);
+      acc.y = fmaf(v.y, fo, acc.y);
+      acc.z = fmaf(v.z, fo, acc.z);
+      acc.w = fmaf(v.w, fo, acc.w);
       den = fmaf(lw, f, den);
     }
     if (single) {
