@@ -84,3 +84,30 @@ def test_fp8_without_any_value(api):
     r = np.random.default_rng(13)
     x = ab.Rows(r, "fp8", r.standard_normal((200, 1, D)), np.zeros((200, 1, D)))
     assert np.all(run(api, x, r.standard_normal((7, D)).astype(np.float16), 0.1) == 0)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
+@pytest.mark.parametrize("most", [3.0, 300.0, 3000.0, 60000.0])
+def test_scores_of_any_size(api, kind, most):
+    """Keys and queries up to the ends of fp16: scores up to 5e8 (log2), their
+    spacing in fp32 up to 32.  From 300 on one token's score, or three equal ones, are
+    more than 700 above the others, so that the output is its V or their mean: off
+    by the roundings of P and of the output, 2^-11 each.  (3: 8 and more above a
+    thousand others, which count then: the general bound.)"""
+    r = np.random.default_rng(14)
+    n, Hkv, G = 1000, 2, 7
+    K = np.zeros((n, Hkv, D))
+    K[:, :, 0] = most * 0.8 * r.uniform(0.1, 1.0, (n, Hkv))
+    top = [[613], [40, 333, 999]]
+    for h in range(Hkv):
+        K[top[h], h, 0] = most
+    V = r.standard_normal((n, Hkv, D))
+    x = ab.Rows(r, kind, K, V)
+    q = np.zeros((Hkv * G, D), np.float16)
+    q[:, 0] = np.maximum(most, 300.0) * np.linspace(0.5, 1.0, Hkv * G)
+    got = run(api, x, q, D ** -0.5, [10]).astype(np.float64)
+    if most < 300:
+        return ab.check(got, q, x.K, x.V, D ** -0.5, x.v_scale)
+    for h in range(Hkv * G):
+        v = x.V[top[h // G], h // G]
+        assert np.all(np.abs(got[h] - v.mean(0)) <= 2.0 ** -11 * (np.abs(v.mean(0)) + np.abs(v).mean(0)) + 1e-6), h

@@ -102,9 +102,12 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
   return d;
 }
+// to fp16, numbers beyond its range to its largest: a reference that is itself
+// rounded (scores beyond 2^24) may leave P at 2^16
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
+  uint32_t d;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
 }
 
 // ---------------------------------------------------------------------------
@@ -690,18 +693,23 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     }
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     PG::scores(slot, g, t4, bias, qb, s);
+    // (log2 domain; rounded before a reference is taken off, not after it: the
+    // largest of scores beyond 2^24 would come out a multiple of their spacing
+    // above or below its own reference)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = __fmul_rn(s[i], scale);
     if (MASK) {
       if (!a0) s[0] = s[1] = -INFINITY;
       if (!a1) s[2] = s[3] = -INFINITY;
     }
-    float x0 = fmaxf(s[0], s[2]) * scale, x1 = fmaxf(s[1], s[3]) * scale;
+    float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
     bool move = x0 > t0 || x1 > t1;
     float v0 = 0.f, v1 = 0.f, y0 = 0.f, y1 = 0.f;  // FP8: V's row scales, the largest log2(p s)
     if constexpr (KIND == ATW_F8) {
       PG::template v_scales<MASK>(slot, g, live, v0, v1);
       const float e0 = lg2(fabsf(v0)), e1 = lg2(fabsf(v1));
-      y0 = fmaxf(fmaf(s[0], scale, e0), fmaf(s[2], scale, e1));
-      y1 = fmaxf(fmaf(s[1], scale, e0), fmaf(s[3], scale, e1));
+      y0 = fmaxf(s[0] + e0, s[2] + e1);
+      y1 = fmaxf(s[1] + e0, s[3] + e1);
       move = move || y0 - mo0 > ATW_HEAD + ATW_SLACK || y1 - mo1 > ATW_HEAD + ATW_SLACK;
     }
     if (__any_sync(0xffffffffu, move)) {
@@ -742,14 +750,10 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
       }
     }
     float p[4];
-    p[0] = ex2(fmaf(s[0], scale, -m0));
-    p[1] = ex2(fmaf(s[1], scale, -m1));
-    p[2] = ex2(fmaf(s[2], scale, -m0));
-    p[3] = ex2(fmaf(s[3], scale, -m1));
-    if (MASK) {  // (-inf times a scale of zero is no number)
-      if (!a0) p[0] = p[1] = 0.f;
-      if (!a1) p[2] = p[3] = 0.f;
-    }
+    p[0] = ex2(s[0] - m0);
+    p[1] = ex2(s[1] - m1);
+    p[2] = ex2(s[2] - m0);
+    p[3] = ex2(s[3] - m1);
     l0 += p[0] + p[2];
     l1 += p[1] + p[3];
     if constexpr (KIND == ATW_F8) {
