@@ -345,7 +345,8 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
  *     In the fused form the page that takes a sequence's new token is none of
  *     the call's other pages.
  *     A length above max_context sets bit 0 of err_flag; the row attends to its
- *     first max_context tokens, and the fused call appends nothing for it.
+ *     first max_context tokens, and the fused call, which rotates its q for
+ *     position context_lens[b] - 1 all the same, appends nothing for it.
  * Every byte of a page past a sequence's length may hold anything.
  * Pools must be 128-byte aligned.
  * ------------------------------------------------------------------------ */

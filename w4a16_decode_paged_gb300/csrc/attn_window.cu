@@ -383,13 +383,13 @@ __device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I
 // ---------------------------------------------------------------------------
 struct AtwShare {
   int b, kvh, part, parts;     // b -1: nothing to do
-  int L, w0, S, n, nsp, wp, fits;  // L: the length, up to max_context (fits: it is no longer)
+  int len, L, w0, S, n, nsp, wp;  // the length, and up to max_context
 };
 
 // the visible pages of a sequence of this length
 __device__ __forceinline__ AtwShare atw_visible(const AtwArgs& a, int len) {
   AtwShare r;
-  r.fits = len <= a.max_context;
+  r.len = len;
   r.L = max(min(len, a.max_context), 0);
   r.w0 = a.window >= r.L ? 0 : r.L - a.window;  // first token of the window
   r.S = min(a.sinks, r.L);                      // sinks
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   if (sh.b < 0) return;
   const int b = sh.b, kvh = sh.kvh, pc = sh.part, active = sh.parts;
   const int L = sh.L, w0 = sh.w0, S = sh.S, n = sh.n, nsp = sh.nsp, wp = sh.wp;
-  const bool fits = sh.fits != 0;
+  const bool fits = sh.len <= a.max_context;
   if (!fits && pc == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
   const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
   uint4 qw = make_uint4(0u, 0u, 0u, 0u);
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
       have |= 1u << stage;
     }
   };
-  if (FUSE && tid < ATT_D / 2) sincosf(__fmul_rn((float)max(pos, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
+  if (FUSE && tid < ATT_D / 2) sincosf(__fmul_rn((float)max(sh.len - 1, 0), a.inv_freq[tid]), &s_sin[tid], &s_cos[tid]);
 #pragma unroll
   for (int st = 0; st < STAGES; ++st) {
     if (st < steps) issue(st, st);
