@@ -85,3 +85,29 @@ def test_rows_of_every_head_layout(api, Hq, Hkv, cached, T):
     q, out, K, V = p.run(r.integers(0, 512, T))
     rows = sorted({*range(0, T, 1 if T < 50 else 7), *range(max(0, T - 20), T)})
     _check_rows(q, out, K, V, rows)
+
+
+@pytest.mark.parametrize("above", [10.0, 14.0, 16.0])
+def test_rows_with_small_weights_beside_tokens_without_a_value(api, above):
+    """The largest weights of a cached context are tokens whose V is zero, one in
+    every page; the rows' output is the sum of many weights of e^-10 and less of them."""
+    r = np.random.default_rng(int(above))
+    cached, T, Hq, Hkv = 4000, 20, 14, 2
+    d = 63                                                       # dims 63 and 127 turn by 1.2e-6 a position
+    K = r.standard_normal((cached, Hkv, D)) * 0.1
+    K[:, :, d] = r.standard_normal((cached, Hkv)) * 0.5
+    K[::16, :, d] = above
+    V = 200.0 * (1.0 + 0.25 * r.standard_normal((cached, Hkv, D)))
+    V[::16] = 0.0
+
+    def change(case):                                            # q, k, v: their biases
+        w = case["layers"][0]
+        for n in ("sq", "sk", "sv"):
+            w[n] = np.zeros_like(w[n])
+        w["bq"] = (0.3 * r.standard_normal((Hq, D))).astype(np.float16)
+        w["bq"][:, d] = D ** 0.5 * np.linspace(0.8, 1.0, Hq)
+        w["bq"] = w["bq"].reshape(-1)
+        w["bk"], w["bv"] = np.zeros_like(w["bk"]), np.zeros_like(w["bv"])
+    p = Prompt(api, _cfg(Hq, Hkv), K, V, T, 60, change)
+    q, out, K, V = p.run(r.integers(0, 512, T))
+    _check_rows(q, out, K, V, range(T))

@@ -768,7 +768,8 @@ __global__ void __launch_bounds__(PF_WARPS * 32) w4pg_prefill_attn(const __grid_
         attn_page_pair_fp8(sl, tok0, posA, posB, qa, a.scale_log2, g, t4, m_run, l_run, o);
       } else {
         const __half* Ks = reinterpret_cast<const __half*>(sl);
-        attn_page_pair(Ks, Ks + ATT_SSLICE, tok0, posA, posB, qa, a.scale_log2, k_off, v_off, t4, m_run, l_run, o);
+        attn_page_pair<KV == PF_I4 ? 15 : 0>(Ks, Ks + ATT_SSLICE, tok0, posA, posB, qa, a.scale_log2, k_off, v_off, t4,
+                                             m_run, l_run, o);
       }
     }
   }

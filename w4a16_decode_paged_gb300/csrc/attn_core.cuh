@@ -201,7 +201,9 @@ __device__ __forceinline__ void mma_16816_full(float (&d)[4], uint32_t a0, uint3
 // (qa[st][0..3] = a0..a3 of k step st).  Keys at positions past a row's own
 // position (page tokens tok0 + n > pos) are masked.  Per lane: the states of
 // row g (token A) and row 8 + g (token B); o[nb][0..1] row g, o[nb][2..3]
-// row 8 + g.  Warp-wide.
+// row 8 + g.  SHIFT: P and l_run carry the factor 2^SHIFT, with which small P stay
+// normal numbers of fp16 (p <= 1: up to 15).  Warp-wide.
+template <int SHIFT = 0>
 __device__ __forceinline__ void attn_page_pair(const __half* Ks, const __half* Vs, int tok0, int posA, int posB,
                                                const uint32_t (&qa)[8][4], float scale_log2, uint32_t k_off,
                                                uint32_t v_off, int t4, float (&m_run)[2], float (&l_run)[2],
@@ -242,7 +244,10 @@ __device__ __forceinline__ void attn_page_pair(const __half* Ks, const __half* V
     const bool none = m_new == -INFINITY;
     c[r] = none ? 1.f : exp2f(m_run[r] - m_new);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[r][j] = none ? 0.f : exp2f(s[r][j] - m_new);
+    for (int j = 0; j < 4; ++j) {
+      p[r][j] = none ? 0.f : exp2f(s[r][j] - m_new);
+      if (SHIFT > 0) p[r][j] *= (float)(1 << SHIFT);
+    }
     float sum = (p[r][0] + p[r][1]) + (p[r][2] + p[r][3]);
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
