@@ -111,3 +111,51 @@ def test_rows_with_small_weights_beside_tokens_without_a_value(api, above):
     p = Prompt(api, _cfg(Hq, Hkv), K, V, T, 60, change)
     q, out, K, V = p.run(r.integers(0, 512, T))
     _check_rows(q, out, K, V, range(T))
+
+
+@pytest.mark.parametrize("Hq,Hkv,cached,at", [(14, 2, 0, 10), (8, 2, 5, 16), (7, 1, 16, 33), (3, 3, 0, 0)])
+def test_rows_before_a_token_without_numbers(api, Hq, Hkv, cached, at):
+    """A prompt token whose activations are NaN: the rows before it see nothing of it,
+    to the bit; those from it on are NaN."""
+    r = np.random.default_rng(cached + at)
+    K, V = r.standard_normal((2, cached, Hkv, D))
+    T, bad = 40, 500
+
+    def change(case):
+        case["embed"][bad] = np.nan
+    tokens = r.integers(0, bad, T)
+    clean = Prompt(api, _cfg(Hq, Hkv), K, V, T, 70, change).run(tokens)[1]
+    tokens[at] = bad
+    out = Prompt(api, _cfg(Hq, Hkv), K, V, T, 70, change).run(tokens)[1]
+    assert np.all(np.isnan(out[at:]))
+    assert np.all(np.isfinite(out[:at])) and np.array_equal(out[:at], clean[:at])
+
+
+@pytest.mark.parametrize("at", [0, 13, 16, 38, 39])
+def test_a_value_group_without_numbers(api, at):
+    """A token whose V overflows in dims 32 .. 63 of one kv head: NaN there in the
+    rows from it on, and nothing else."""
+    Hq, Hkv, T, bad = 8, 2, 40, 500
+    r = np.random.default_rng(at)
+
+    def change(case):
+        case["embed"][:, :128] = 0                               # (in dims 0 .. 127 this token alone is not zero)
+        case["embed"][bad] = 0
+        case["embed"][bad, 5] = 1
+        w = case["layers"][0]
+        w["sv"][32:64, 0] = 10000.0
+        w["sv"][32:64, 1] = 0.0
+    tokens = r.integers(0, bad, T)
+    tokens[at] = bad
+    q, out, K, V = Prompt(api, _cfg(Hq, Hkv), np.zeros((0, Hkv, D)), np.zeros((0, Hkv, D)), T, 80, change).run(tokens)
+    lost = np.zeros_like(V, bool)
+    lost[at, 0, 32:64] = True
+    assert np.array_equal(np.isnan(V), lost)
+    V = np.where(lost, 0.0, V)
+    for i in range(T):
+        ref_, w = ab.attend(q[i], K[:i + 1], V[:i + 1], D ** -0.5)
+        nan = np.zeros((Hq, D), bool)
+        nan[:Hq // Hkv, 32:64] = i >= at
+        assert np.array_equal(np.isnan(out[i]), nan), i
+        lim = ab.bound(q[i], K[:i + 1], V[:i + 1], D ** -0.5, ref_, w)
+        assert np.all((np.abs(out[i] - ref_) <= lim) | nan), i

@@ -592,11 +592,18 @@ int launch_paged_attention(const AttnArgs& a_in, cudaStream_t s) {
 // FP8 (E4M3) pages: codes and row scales, in the dim orders of the FP8 decode
 // step (attn8_qdim, attn8_odim).  INT4 pages are unpacked to fp16 rows on their
 // way into the ring: each thread loads a page's words two pages ahead and
-// stores their values one page ahead.
+// stores their values one page ahead.  A weight of zero times a NaN is no number,
+// so in the last two pages, which hold tokens that some of the CTA's rows do not
+// see, V values that are no numbers are stored as zeros; the outputs of the rows
+// that do see such a token are written as NaN.  (Products of each row's own, over V
+// masked by its position, cost registers: 7 % on a layer's prompt of 2048.)
 // ---------------------------------------------------------------------------
 constexpr int PF_ROWS = 16;    // query rows per CTA
 constexpr int PF_WARPS = 8;
 constexpr int PF_STAGES = 3;   // page slots of the CTA's ring
+// a page with at most so many tokens from its first one to the CTA's last may have
+// some that a row does not see
+constexpr int PF_PARTLY = ATT_PAGE + PF_ROWS - 2;
 constexpr size_t pf_slot_bytes(bool kv8) { return kv8 ? (size_t)ATT8_SLOT : (size_t)2 * ATT_SSLICE * 2; }
 
 enum { PF_F16 = 0, PF_F8 = 1, PF_I4 = 2 };
@@ -611,7 +618,9 @@ struct PfWords {
     ks = __ldcg(kp + kv4_k_scale(i >> 4, (i & 15) >> 2));
     vs = __ldcg(reinterpret_cast<const unsigned short*>(vp + kv4_v_scale(2 * (i >> 5), (i & 31) >> 3)));
   }
-  // values into the page's fp16 rows; tokens from `tokens` on count as zero in V, whatever they hold
+  static __device__ __forceinline__ bool bad(uint32_t byte) { return byte > KV4_MAX_SCALE; }  // no number
+  // values into the page's fp16 rows; tokens from `tokens` on count as zero in V,
+  // whatever they hold, and in pages seen partly those that are no numbers
   __device__ __forceinline__ void store(__half* kr, __half* vr, int i, int tokens, const Kv4Bias& bias) const {
     uint32_t x[4];
     kv4_unpack(k, kv4_scale_pair(ks * 0x00800080u), bias, x);
@@ -622,13 +631,29 @@ struct PfWords {
                    __byte_perm(x[2], x[3], 0x7632));
     const int t = 2 * (i >> 5);
     const uint32_t s = t >= tokens ? 0u : (t + 1 >= tokens ? vs & 0xFFu : vs);
-    kv4_unpack(v, kv4_scale_pair(((s & 0xFFu) << 7) | ((s & 0xFF00u) << 15)), bias, x);
+    uint32_t two = ((s & 0xFFu) << 7) | ((s & 0xFF00u) << 15);
+    if (tokens <= PF_PARTLY) two &= (bad(s & 0xFFu) ? 0u : 0xFFFFu) | (bad(s >> 8) ? 0u : 0xFFFF0000u);
+    kv4_unpack(v, kv4_scale_pair(two), bias, x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = hmul2_u(x[e], 0x54005400u);
     __half* row = vr + t * ATT_PITCH + 4 * (i & 31);
     *reinterpret_cast<uint2*>(row) = make_uint2(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410));
     *reinterpret_cast<uint2*>(row + ATT_PITCH) =
         make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+  }
+  // bits 4 r + c: a token that row r (0: at posA, 1: at posB) sees has a bad V scale
+  // for dims 32 c ...  vp: the page's V slice; tok0: its first token.  Warp-wide.
+  static __device__ __forceinline__ uint32_t bad_groups(const uint8_t* vp, int tok0, int posA, int posB) {
+    const int lane = threadIdx.x & 31;  // token pair lane / 4, group lane % 4
+    const uint32_t s = __ldcg(reinterpret_cast<const unsigned short*>(vp + kv4_v_scale(2 * (lane >> 2), lane & 3)));
+    uint32_t groups = 0u;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int last = (r ? posB : posA) - tok0, t = 2 * (lane >> 2);
+      const bool hit = (t <= last && bad(s & 0xFFu)) || (t + 1 <= last && bad(s >> 8));
+      groups |= __reduce_or_sync(0xffffffffu, hit ? 1u << (4 * r + (lane & 3)) : 0u);
+    }
+    return groups;
   }
 };
 
@@ -741,8 +766,12 @@ __global__ void __launch_bounds__(PF_WARPS * 32) w4pg_prefill_attn(const __grid_
 #pragma unroll
   for (int nb = 0; nb < 16; ++nb) o[nb][0] = o[nb][1] = o[nb][2] = o[nb][3] = 0.f;
   const uint32_t k_off = attn_k_off(lane), v_off = attn_v_off(lane);
+  uint32_t nans = 0u;  // outputs that become NaN (bad_groups)
   if (KV == PF_I4) {
     issue(0);
+    for (int li = max(npages - 2, 0); li < npages; ++li)
+      if (L - li * ATT_PAGE <= PF_PARTLY && page_id(li) >= 0)
+        nans |= PfWords::bad_groups(a.v8 + ((size_t)page_id(li) * a.Hkv + kvh) * KV4_SLICE, li * ATT_PAGE, posA, posB);
     unpack(0);
     issue(1);
   } else {
@@ -790,9 +819,10 @@ __global__ void __launch_bounds__(PF_WARPS * 32) w4pg_prefill_attn(const __grid_
         }
       } else {
 #pragma unroll
-        for (int nb = 0; nb < 16; ++nb)
-          *reinterpret_cast<__half2*>(outh + 8 * nb + 2 * t4) =
-              __floats2half2_rn(o[nb][2 * r] * inv, o[nb][2 * r + 1] * inv);
+        for (int nb = 0; nb < 16; ++nb) {
+          const float f = KV == PF_I4 && (nans & (1u << (4 * r + (nb >> 2)))) ? __int_as_float(0x7FFFFFFF) : inv;
+          *reinterpret_cast<__half2*>(outh + 8 * nb + 2 * t4) = __floats2half2_rn(o[nb][2 * r] * f, o[nb][2 * r + 1] * f);
+        }
       }
     }
   }

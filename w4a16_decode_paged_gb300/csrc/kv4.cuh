@@ -32,6 +32,7 @@ constexpr int KV4_D = 128;
 constexpr int KV4_PAGE = 16;
 constexpr int KV4_GROUP = 32;                       // dims per scale
 constexpr int KV4_CODES = KV4_PAGE * KV4_D / 2;     // 1024
+constexpr uint32_t KV4_MAX_SCALE = 0xE7;            // largest scale byte of a page but for 0xFF (NaN)
 constexpr int KV4_SLICE = KV4_CODES + KV4_PAGE * KV4_D / KV4_GROUP;  // 1088
 
 // byte offsets in a slice of dims 4i..4i+3 (a halfword) and of group c's scale
