@@ -111,3 +111,33 @@ def test_scores_of_any_size(api, kind, most):
     for h in range(Hkv * G):
         v = x.V[top[h // G], h // G]
         assert np.all(np.abs(got[h] - v.mean(0)) <= 2.0 ** -11 * (np.abs(v.mean(0)) + np.abs(v).mean(0)) + 1e-6), h
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
+@pytest.mark.parametrize("n,Hkv,others", [(32768, 1, ()), (32768, 4, ()), (32761, 4, (32768, 20011, 777)), (9000, 8, ()),
+                                          (100003, 1, ()), (32768, 2, (5,) * 40)])
+def test_every_page_counts_once(api, kind, n, Hkv, others):
+    """Long contexts in up to 64 parts, near-equal weights, and a V that tells which
+    page it came from: one-hot, page p in dim p % 128.  (A lost or doubled page of
+    the 6252 moves its dim by a 49th or more; the bound is a 500th.)"""
+    r = np.random.default_rng(n + Hkv)
+    K, V = one_hot_pages(r, n, Hkv)
+    x = ab.Rows(r, kind, K, V)
+    G = 7 if Hkv <= 4 else 1
+    q = r.standard_normal((G * Hkv, D)).astype(np.float16)
+    ab.check(run(api, x, q, D ** -0.5, [min(m, n) for m in others]), q, x.K, x.V, D ** -0.5, x.v_scale, f"{kind} {n}")
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
+@pytest.mark.parametrize("n,window,sinks", [(32768, 20000, 300), (32768, 4096, 5), (40000, 33, 30000)])
+def test_every_visible_page_counts_once(api, kind, n, window, sinks):
+    r = np.random.default_rng(n + window)
+    K, V = one_hot_pages(r, n, 2)
+    x = ab.Rows(r, kind, K, V)
+    q = r.standard_normal((10, D)).astype(np.float16)
+    dev = lambda a: to_dev(a, torch)
+    out = api.paged_gqa_decode_window(dev(q[None]), **{k: dev(a) for k, a in x.pools.items()}, block_table=dev(x.bt),
+                                      context_lens=dev(np.array([n], np.int32)), max_context=n, window=window, sinks=sinks)
+    t = np.arange(n)
+    seen = (t < sinks) | (t >= n - window)
+    ab.check(to_host(out)[0], q, x.K[seen], x.V[seen], D ** -0.5, None if x.v_scale is None else x.v_scale[seen])
