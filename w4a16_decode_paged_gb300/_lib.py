@@ -11,6 +11,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+import warnings
 
 from . import build as _build
 
@@ -150,27 +151,32 @@ def load() -> ctypes.CDLL:
     return _lib
 
 
-_native = None
+_native = None  # the module; False: not to be had
 _NATIVE_ENTRIES = ("kv_append_rope_int4", "kv_read_int4", "paged_gqa_decode_int4", "paged_gqa_decode_rope_append_int4",
                    "paged_gqa_decode_window", "paged_gqa_decode_window_fp8", "paged_gqa_decode_window_int4")
 
 
 def native():
     """The native argument marshalling (csrc/torch_args.cpp) bound to the
-    library's entries; raises if it has not been built."""
+    library's entries.  None, with a warning the first time, where it was not
+    built or does not load: the binding's own checks do the same work, at 10 us
+    a call."""
     global _native
     if _native is None:
-        lib = load()
-        if not os.path.exists(_build.ARGS_LIB):
-            raise RuntimeError(f"{_build.ARGS_LIB} is missing: build it with "
-                               "`python -c 'import __graft_entry__ as g; g.build()'`")
-        import torch  # noqa: F401  (its libraries have to be in the process first)
-        spec = importlib.util.spec_from_file_location("_w4a16_torch", _build.ARGS_LIB)
-        mod = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(mod)
-        mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_ENTRIES))
+        lib, path = load(), _build.args_lib()
+        try:
+            import torch  # noqa: F401  (its libraries have to be in the process first)
+            if path is None or not os.path.exists(path):
+                raise ImportError(f"{path} is not built: `python -c 'import __graft_entry__ as g; g.build()'`")
+            spec = importlib.util.spec_from_file_location("_w4a16_torch", path)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            mod.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _NATIVE_ENTRIES))
+        except ImportError as e:
+            warnings.warn(f"calls are checked in Python, which is slower: {e}", RuntimeWarning, stacklevel=2)
+            mod = False
         _native = mod
-    return _native
+    return _native or None
 
 
 def check(rc: int) -> None:

@@ -449,8 +449,8 @@ def kv_append_rope_int4(q, k, v, k_pool, v_pool, block_table, context_lens, thet
     rotated k row and the v row quantised into their slot.  A row_stride
     (elements, a multiple of 8) makes q, k and v the starts of rows of that
     pitch, e.g. views of a q|k|v buffer."""
-    if stream is None and not row_stride and _cuda(k_pool):
-        r = native().append(q, k, v, k_pool, v_pool, block_table, context_lens, theta, q_out, err_flag)
+    if stream is None and not row_stride and _cuda(k_pool) and (fast := native()) is not None:
+        r = fast.append(q, k, v, k_pool, v_pool, block_table, context_lens, theta, q_out, err_flag)
         if r is not None:
             return _result(r)
     pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
@@ -483,8 +483,8 @@ def kv_read_int4(k_pool, v_pool, block_table, context_lens, T, starts=None, k_ou
     sequence b is the token at position starts[b] + i (i without starts) if
     the sequence holds it.  Other rows of a k_out, v_out pair that the caller
     gives are left as they were; of tensors that the call makes, they are zero."""
-    if stream is None and _cuda(k_pool):
-        r = native().read(k_pool, v_pool, block_table, context_lens, T, starts, k_out, v_out, err_flag)
+    if stream is None and _cuda(k_pool) and (fast := native()) is not None:
+        r = fast.read(k_pool, v_pool, block_table, context_lens, T, starts, k_out, v_out, err_flag)
         if r is not None:
             return _result(r)
     pages, Hkv, B, blocks, dev = _paging_of("int4", k_pool, v_pool, block_table, context_lens)
@@ -529,8 +529,8 @@ def paged_gqa_decode_int4(q, k_pool, v_pool, block_table, context_lens, max_cont
     128) and the call is the fused RoPE + INT4 append + attention
     (paged_gqa_decode_rope_append_int4).  A workspace the caller gives is
     zeroed once before its first use."""
-    if stream is None and workspace is not None and _cuda(k_pool):
-        r = native().decode_int4(q, k_pool, v_pool, block_table, context_lens, max_context,
+    if stream is None and workspace is not None and _cuda(k_pool) and (fast := native()) is not None:
+        r = fast.decode_int4(q, k_pool, v_pool, block_table, context_lens, max_context,
                                  _SCALE_128 if sm_scale is None else sm_scale, workspace, out, err_flag, qkv_theta,
                                  n_q_heads)
         if r is not None:
@@ -578,8 +578,8 @@ def paged_gqa_decode_window(q, k_pool, v_pool, block_table, context_lens, max_co
     [128], FP8 (E4M3) codes of that shape with k_scale / v_scale, or INT4
     [pages][Hkv][KV4_SLICE].  A workspace the caller gives is zeroed once
     before its first use."""
-    if stream is None and workspace is not None and _cuda(k_pool):
-        r = native().decode_window(q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens, max_context, window,
+    if stream is None and workspace is not None and _cuda(k_pool) and (fast := native()) is not None:
+        r = fast.decode_window(q, k_pool, v_pool, k_scale, v_scale, block_table, context_lens, max_context, window,
                                    sinks, _SCALE_128 if sm_scale is None else sm_scale, workspace, out, err_flag)
         if r is not None:
             return _result(r)

@@ -3,17 +3,20 @@
 Each .cu file under csrc/ is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into one shared
 library with a plain C ABI (include/w4a16.h).  The output goes to
-``w4a16_decode_paged_gb300/_build/``.  Beside it goes _w4a16_torch.so, the
-argument marshalling of the short calls (csrc/torch_args.cpp, g++ against
-torch's headers; it holds no kernel and is given the library's entries by
-address).
+``w4a16_decode_paged_gb300/_build/``.  Beside it goes _w4a16_torch.<python>-
+<torch version>.so, the argument marshalling of the short calls
+(csrc/torch_args.cpp, g++ against torch's headers; it holds no kernel and is
+given the library's entries by address).  The library does not need it: where
+torch or its headers are missing, it is left out.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import functools
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -32,7 +35,24 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 
 
 ARGS_SRC = os.path.join(CSRC, "torch_args.cpp")
-ARGS_LIB = os.path.join(BUILD, "_w4a16_torch.so")
+
+
+@functools.lru_cache(maxsize=None)
+def _torch():
+    """(torch's folder, its version), without importing it; (None, None): no torch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None, None
+    folder = os.path.dirname(spec.origin)
+    with open(os.path.join(folder, "version.py")) as f:
+        return folder, re.search(r"__version__ = '([^']+)'", f.read()).group(1)
+
+
+def args_lib():
+    """The marshalling module's file, named for the interpreter and the torch
+    whose ABI it has; None without torch."""
+    folder, version = _torch()
+    return folder and os.path.join(BUILD, f"_w4a16_torch.{sys.implementation.cache_tag}-{version}.so")
 
 
 def nvcc() -> str:
@@ -95,8 +115,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str
     with cf.ThreadPoolExecutor(max_workers=min(10, len(srcs) + 1)) as ex:
         args = ex.submit(build_args, force) if lib == LIB else None
         objs = list(ex.map(compile_one, srcs))
-        if args is not None:
-            args.result()
     tmp = lib + f".tmp{os.getpid()}"
     rdc = ["-rdc=true"] if "-rdc=true" in flags else []
     cmd = [cc, *ARCH, *rdc, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
@@ -104,29 +122,34 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None, out: str
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
+    if args is not None:
+        args.result()  # (an error of its own comes behind the library)
     return lib
 
 
-def build_args(force: bool = False) -> str:
-    """The native argument marshalling (a CPython module, host code only)."""
+def build_args(force: bool = False):
+    """The native argument marshalling (a CPython module, host code only); None
+    where there is no torch or no headers of it to build against."""
+    out, folder = args_lib(), _torch()[0]
+    inc = [os.path.join(folder, "include", *sub) for sub in ((), ("torch", "csrc", "api", "include"))] if folder else []
+    if not inc or not os.path.isdir(os.path.join(inc[0], "ATen")):
+        sys.stderr.write("torch's headers are not here: calls are checked in Python, _w4a16_torch is not built\n")
+        return None
     deps = [ARGS_SRC, os.path.join(INCLUDE, "w4a16.h")]
-    if not force and os.path.exists(ARGS_LIB) and all(os.path.getmtime(p) <= os.path.getmtime(ARGS_LIB) for p in deps):
-        return ARGS_LIB
+    if not force and os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps):
+        return out
     os.makedirs(BUILD, exist_ok=True)
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
-           os.path.join(cuda, "include")]
-    lib = os.path.join(torch_dir, "lib")
-    tmp = ARGS_LIB + f".tmp{os.getpid()}"
+    inc.append(os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"))
+    lib = os.path.join(folder, "lib")
+    tmp = out + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", ARGS_SRC, "-o", tmp,
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], *[x for p in inc for x in ("-isystem", p)],
            "-L", lib, f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {ARGS_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, ARGS_LIB)
-    return ARGS_LIB
+    os.replace(tmp, out)
+    return out
 
 
 if __name__ == "__main__":
