@@ -306,7 +306,9 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
  *   value = q * s, q in [-7, 7] kept as the nibble q + 8 (element d of a row in
  *   nibble d % 2 of its byte, lowest first); s one byte per 32 elements: the 8
  *   bits below the sign of an fp16 number (s = the number with bits byte << 7).
- *   Every value is an fp16 number exactly.
+ *   A page holds scale bytes up to 0xE7 (15360; appends write up to 10240), with
+ *   |q| s <= 65504, and 0xFF, which makes its 32 elements NaN.  Every value is an
+ *   fp16 number exactly.
  *   K: dims 4i..4i+3 of token t at byte 64 t + 2 i, the scale of dims 32c.. at
  *      1024 + 8 (t % 8) + 2 c + t / 8.
  *   V: dims 4i..4i+3 of token t at byte 128 (t / 2) + 4 i + 2 (t % 2), the scale

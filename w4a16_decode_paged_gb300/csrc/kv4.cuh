@@ -4,8 +4,9 @@
 // dims, two per byte, element d in nibble d % 2, lowest first, offset binary
 // u = q + 8 with q in [-7, 7]) and 64 scale bytes (one per token and 32 dims).
 //   value = q * s,  s = the fp16 number whose bits are byte << 7
-// so a scale has 5 exponent and 3 fraction bits (4 significant bits, all of
-// fp16's range, byte 0 = 0; bytes from 0xF8 on are not finite).  A code has 3
+// so a scale has 5 exponent and 3 fraction bits (4 significant bits, byte 0 = 0).
+// A page holds bytes up to 0xE7 (15360; the quantiser's largest is 10240), as far
+// as the unpacking goes, and 0xFF for a group that is no number.  A code has 3
 // significant bits and a sign: every product is exact in fp16, in fp32 and
 // against a scale that was divided by 64 (multiples of 2^-23).
 // Quantising 32 values: s = the smallest scale with 7 s >= amax, q = x / s
@@ -74,10 +75,11 @@ __device__ __forceinline__ void kv4_quantise(const uint4& x, uint32_t& codes, ui
   byte = kv4_scale_byte(m);
   const bool live = byte != 0u && byte != 0xFFu;
   // q = x / s to nearest even, without a division per value: y = x (1/s) is off
-  // by 2^-21 at most.  x / s is a tie n + 1/2 exactly or 2^-12 or more away from
-  // one (x has 11 bits, (n + 1/2) s has 8), so rounding y to multiples of 2^-14
-  // first (the sum with 768 and back) makes ties exact and moves no other
-  // across.  The sum with 1.5 * 2^23 then leaves q in the low bits.
+  // by 2^-20 at most (two roundings of 2^-24 of |q| <= 7).  x / s is a tie n + 1/2
+  // exactly or 2^-12 or more away from one (x has 11 bits, (n + 1/2) s has 8), so
+  // rounding y to multiples of 2^-14 first (the sum with 768 and back) makes ties
+  // exact and moves no other across.  The sum with 1.5 * 2^23 then leaves q in the
+  // low bits.
   const float inv = live ? __frcp_rn(kv4_scale_value(byte)) : 0.f;
   codes = 0x88888888u - 0x4B400000u * 0x11111111u;  // (q + 8) 16^e, summed modulo 2^32
 #pragma unroll
@@ -142,8 +144,10 @@ __device__ __forceinline__ void rope_rows(uint4& x, const RopeLane& t) {
 // multiply-add takes the bias off and applies the scale:
 //   q s' = (2^(10-b) + u) s' - (2^(10-b) + 8) s',   s' = s / 64
 // exactly, because the bias times a scale still fits fp16's 11 bits at b = 2
-// and 6 (264 and 24).  s / 64 keeps 264 s' in fp16's range for every scale;
-// callers multiply by 64 in fp32.
+// and 6 (264 and 24).  264 s' stays in fp16's range up to s = 15360, the largest
+// that a page may hold (264 / 64 times the next, 16384, does not), and the
+// smallest s', 2^-23, is an fp16 number (2^-17 / 256 were not).  Callers multiply
+// by 64.
 // ---------------------------------------------------------------------------
 struct Kv4Scale {
   uint32_t s, c264, c24;  // packed pairs
@@ -166,9 +170,6 @@ __device__ __forceinline__ Kv4Scale kv4_scale_pair(uint32_t two) {
   r.c24 = hmul2_u(two, 0xB600B600u);   // -24 / 64
   return r;
 }
-// (low, high) bytes at bits 0-7 and 16-23 -> the pair's fp16 bits
-__device__ __forceinline__ uint32_t kv4_bytes_to_half2(uint32_t b) { return b << 7; }
-
 // The exponents, kept in registers: an instruction takes one immediate, which
 // the mask is, and a compiler that may re-create a constant does so at each use.
 struct Kv4Bias {
