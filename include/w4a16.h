@@ -271,8 +271,10 @@ W4A16_API int paged_gqa_decode_rope_append(const uint16_t* qkv, int qkv_stride, 
  * row: scale 0, codes 0).  Per page and kv head: 2 x 2 KiB of codes and
  * 2 x 64 B of scales instead of 2 x 4 KiB.
  *   kv_append_rope_fp8     kv_append_rope into FP8 pools.
- *   paged_gqa_decode_fp8   paged_gqa_decode over FP8 pools (q fp16; scores
- *                          and P V in fp32 on the dequantised values).
+ *   paged_gqa_decode_fp8   paged_gqa_decode over FP8 pools (q fp16; fp32
+ *                          scores and sums; P times V's row scale is rounded
+ *                          to fp16, where products under 2^-14 lose bits that
+ *                          paged_gqa_decode_window_fp8 keeps).
  *   paged_gqa_decode_rope_append_fp8  the fused form (qkv rows as for
  *                          paged_gqa_decode_rope_append).
  * Pools and scales must be 128-byte aligned; the other arguments, the
@@ -333,6 +335,7 @@ W4A16_API int paged_gqa_decode_rope_append_fp8(const uint16_t* qkv, int qkv_stri
  *     k_out, v_out  fp16 [B][T][Hkv][D]: row i of sequence b is the token at
  *              position starts[b] + i if that lies in [0, context_lens[b])
  *     clear    0: other rows are left as they were; 1: they become zero
+ *     B        up to 65535
  *     starts   int32 [B] device, or NULL: 0 for every sequence
  *     err_flag bit 0: a block-table entry outside the pool (its rows count as
  *              the other rows).
@@ -379,8 +382,8 @@ W4A16_API int paged_gqa_decode_rope_append_int4(const uint16_t* qkv, int qkv_str
  *   t >= context_lens[b] - window   (the last `window` tokens, its own included)
  *   or t < sinks                    (the first `sinks` tokens stay visible).
  * window >= 0, sinks >= 0.  Only the pages that hold visible tokens are read
- * (others may be -1 in the block table, or reused); a query that sees nothing
- * gives zeros.  FP8 pools: row scales from 2^-100 to 2^20, or zero.
+ * (others may be -1 in the block table, or reused); a query that sees nothing,
+ * or whose visible scores are all -inf, gives zeros.  FP8 pools: row scales from 2^-100 to 2^20, or zero.
  * Other arguments, the workspace's rules and err_flag as for
  * paged_gqa_decode_int4 (no partition_tokens, any Hq/Hkv in 1..8); workspace of
  * paged_gqa_decode_window_workspace_size() bytes with the same sizes.

@@ -31,7 +31,8 @@
 // are normal numbers (rounded by 2^-11 of themselves, as much as the output)
 // and smaller ones are off by 2^-38 of the largest at most.  (With p <= 1 the
 // many small weights beside a few large ones are lost from 2^-14 down, while
-// their sum keeps them: 32768 tokens, e^-18 below: a quarter of the output.)
+// their sum keeps them: a quarter of the output where 32768 tokens lie e^-18 below
+// a sink without a value, emulated.)
 // K and V enter exactly: fp16 as they are, INT4 values (kv4.cuh) as fp16 numbers,
 // FP8 codes as the fp16 numbers that they name.  K's row scales multiply the
 // scores; V's go into P before its rounding, where a product p s of a small s
@@ -49,13 +50,14 @@
 // about 3 us before the first page is there (lengths, block table, page), the
 // pages, and about 3 us to join the parts of a sequence.  fp16 and FP8 pages are
 // waited for (32 sequences, window 1000, fp16: 58 MB in 13.4 us, 4.3 TB/s; batch
-// 8, window 4096, FP8: 70 MB in 16.4 us, 4.3 TB/s); INT4 pages are bound by
-// instructions (4 x 32768 tokens: 71 MB in 20.6 us, 3.5 TB/s; 345 instructions a
-// page all told, 285 of them in the loop, half of those on the logic and integer
-// unit, which masks two codes per operation).  Measured beside two CTAs of eight
-// warps per SM on that case: three CTAs leave 85 registers and spill (29 us and
-// more), 1.5 and 2 times the CTAs pay the chain again (30 and 32 us), three, four
-// or six pages in flight 21.8 us and more.
+// 8, window 4096, FP8: 70 MB in 16.4 us, 4.3 TB/s).  INT4 pages (4 x 32768 tokens:
+// 71 MB in 20.6 us, 3.5 TB/s) wait for their own instructions: 346 a page all
+// told, 9 us of issue slots of the 20.6; 0.53 of a cycle's slot is used, no pipe
+// is full, and a warp's next instruction most often waits for its last at 16
+// warps per SM.  Measured beside two CTAs of eight warps per SM on that case:
+// three CTAs leave 85 registers and spill (29 us and more), 1.5 and 2 times the
+// CTAs pay the chain again (30 and 32 us), three, four or six pages in flight 21.8
+// us and more.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -857,7 +859,8 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     __syncwarp();
     if (ticket != (unsigned)(active - 1)) continue;
     if (lane == 0) *counter = 0u;  // ready for the next call
-    // one round trip for the first partials and all (max, sum) pairs
+    // one round trip for the first partials and all (max, sum) pairs.  FLIGHT: as
+    // many partials as go into the registers that the page loop has (32 spill)
     constexpr int FLIGHT = 20;
     const size_t first = (size_t)(blockIdx.x - pc) * G + h;  // the parts are consecutive CTAs
     const float4* src = reinterpret_cast<const float4*>(a.ws_o) + first * (ATT_D / 4) + i4;
@@ -885,7 +888,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
     }
     sum = warp_sum(sum);
     acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0;;) {  // (the rest FLIGHT at a time: 64 parts of 32768 tokens, 4 heads 16.3 -> 13.5 us; 32 spill)
+    for (int j0 = 0;;) {  // (the rest FLIGHT at a time: 64 parts of 32768 tokens, 4 heads 16.3 -> 13.5 us)
 #pragma unroll
       for (int j = 0; j < FLIGHT; ++j) {
         if (j0 + j >= active) break;

@@ -152,7 +152,9 @@ int launch_rope_append_int4(const Kv4AppendArgs& a, cudaStream_t s);
 // Decode attention with tokens as MMA rows (attn_window.cu): INT4 pages, and
 // a sliding window with sinks over any kind of page.
 enum { ATW_F16 = 0, ATW_F8 = 1, ATW_I4 = 2 };
-constexpr int ATW_SMS = 152;             // SMs the split over a long context is sized for
+// SMs the split over a long context is sized for: a GB300's, so that a workspace's
+// size can be asked for where there is no GPU, and is the calls' own
+constexpr int ATW_SMS = 152;
 constexpr int ATW_MAX_PARTITIONS = 64;
 struct AtwArgs {
   const __half* q;          // [B][Hq][D] pitch q_stride (fused: q | k_new | v_new rows)

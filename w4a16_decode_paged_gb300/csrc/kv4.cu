@@ -5,8 +5,9 @@
 // Hq of them out again and 2 Hkv x 68 bytes of codes and scales; a token read
 // back is 136 bytes in and 512 out per kv head.  A few rows are bound by the
 // chain of latencies (length, table entry, page: 2.5 us a call), a prompt's
-// rows by instructions (the append of 2048 rows issues 0.58 a cycle per
-// scheduler), a whole cache read back by one burst of stores behind that chain
+// rows by that chain and their instructions one after the other (2048 rows are
+// 512 CTAs, resident at once and in step: loads, sines, rotation; 0.58 of the
+// issue slots used), a whole cache read back by one burst of stores behind that chain
 // (9 MB in, 33.5 MB out in 9.5 us, 4.5 TB/s; half the instructions, with whole
 // pages stored unchecked, measured the same).
 #include "kernels.h"

@@ -383,7 +383,8 @@ static int run_layer(w4a16_model* m, int l, __half* x, const int32_t* bt, int ma
   if ((rc = project(m, g, false, s, &tag))) return rc;
 
   // RoPE of q and the new k, the KV append and the paged attention are one
-  // kernel: it prefetches this partition's pages while the q|k|v GEMV runs.
+  // kernel.  Over fp16 and FP8 pages it fetches its partition's first pages while
+  // the q|k|v GEMV runs; over INT4 pages it starts with everything behind it.
   if (m->kv4) {
     AtwArgs a = {};
     a.kind = ATW_I4;
