@@ -141,3 +141,20 @@ def test_every_visible_page_counts_once(api, kind, n, window, sinks):
     t = np.arange(n)
     seen = (t < sinks) | (t >= n - window)
     ab.check(to_host(out)[0], q, x.K[seen], x.V[seen], D ** -0.5, None if x.v_scale is None else x.v_scale[seen])
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
+@pytest.mark.parametrize("n,Hkv,batch", [(6000, 8, 40), (20001, 4, 100)])
+def test_more_pages_than_a_warp_lists_at_once(api, kind, n, Hkv, batch):
+    """Batches with more (sequence, kv head) pairs than CTAs fit at once: a pair is one
+    CTA's, and a warp's list of page ids (32 at a time) is filled again."""
+    r = np.random.default_rng(n)
+    x = ab.Rows(r, kind, *one_hot_pages(r, n, Hkv))
+    q = r.standard_normal((2 * Hkv, D)).astype(np.float16)
+    dev = lambda a: to_dev(a, torch)
+    lens = np.full(batch, n, np.int32)
+    out = api.paged_gqa_decode_window(dev(np.repeat(q[None], batch, 0)), **{k: dev(a) for k, a in x.pools.items()},
+                                      block_table=dev(np.repeat(x.bt, batch, 0)), context_lens=dev(lens), max_context=n,
+                                      window=n, sinks=0)
+    for b in (0, batch // 2, batch - 1):
+        ab.check(to_host(out)[b], q, x.K, x.V, D ** -0.5, x.v_scale, f"{kind} {b}")

@@ -32,7 +32,10 @@
 // and smaller ones are off by 2^-38 of the largest at most.  (With p <= 1 the
 // many small weights beside a few large ones are lost from 2^-14 down, while
 // their sum keeps them: a quarter of the output where 32768 tokens lie e^-18 below
-// a sink without a value, emulated.)
+// a sink without a value, emulated.)  P's rest in a second product would bring the
+// error from 1.1 to 1.3 times that of 32-bit sums down to theirs, at 7 % of the time
+// over INT4 pages, 4 % over FP8 and 1 % over fp16 ones: not kept, as the output's
+// own rounding is as large.
 // K and V enter exactly: fp16 as they are, INT4 values (kv4.cuh) as fp16 numbers,
 // FP8 codes as the fp16 numbers that they name.  K's row scales multiply the
 // scores; V's go into P before its rounding, where a product p s of a small s
@@ -50,7 +53,7 @@
 // about 3 us before the first page is there (lengths, block table, page), the
 // pages, and about 3 us to join the parts of a sequence.  fp16 and FP8 pages are
 // waited for (32 sequences, window 1000, fp16: 58 MB in 13.4 us, 4.3 TB/s; batch
-// 8, window 4096, FP8: 70 MB in 16.4 us, 4.3 TB/s).  INT4 pages (4 x 32768 tokens:
+// 8, window 4096, FP8: 70 MB in 16.6 us, 4.2 TB/s).  INT4 pages (4 x 32768 tokens:
 // 71 MB in 20.6 us, 3.5 TB/s) wait for their own instructions: 346 a page all
 // told, 9 us of issue slots of the 20.6; 0.53 of a cycle's slot is used, no pipe
 // is full, and a warp's next instruction most often waits for its last at 16
@@ -385,12 +388,14 @@ __device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I
 // ---------------------------------------------------------------------------
 struct AtwShare {
   int b, kvh, part, parts;     // b -1: nothing to do
-  int len, L, w0, S, n, nsp, wp;  // the length, and up to max_context
+  int L, w0, S, n, nsp, wp;    // L: the length, up to max_context
+  int fits, len;               // the length itself, and whether it is no longer
 };
 
 // the visible pages of a sequence of this length
 __device__ __forceinline__ AtwShare atw_visible(const AtwArgs& a, int len) {
   AtwShare r;
+  r.fits = len <= a.max_context;
   r.len = len;
   r.L = max(min(len, a.max_context), 0);
   r.w0 = a.window >= r.L ? 0 : r.L - a.window;  // first token of the window
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(Page<KIND>::NW * 32, Page<KIND>::MIN_CTAS)
   if (sh.b < 0) return;
   const int b = sh.b, kvh = sh.kvh, pc = sh.part, active = sh.parts;
   const int L = sh.L, w0 = sh.w0, S = sh.S, n = sh.n, nsp = sh.nsp, wp = sh.wp;
-  const bool fits = sh.len <= a.max_context;
+  const bool fits = sh.fits != 0;
   if (!fits && pc == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, 1);
   const __half* qrow = a.q + (size_t)b * a.q_stride + (size_t)kvh * G * ATT_D;
   uint4 qw = make_uint4(0u, 0u, 0u, 0u);
