@@ -383,7 +383,8 @@ W4A16_API int paged_gqa_decode_rope_append_int4(const uint16_t* qkv, int qkv_str
  *   or t < sinks                    (the first `sinks` tokens stay visible).
  * window >= 0, sinks >= 0.  Only the pages that hold visible tokens are read
  * (others may be -1 in the block table, or reused); a query that sees nothing,
- * or whose visible scores are all -inf, gives zeros.  FP8 pools: row scales from 2^-100 to 2^20, or zero.
+ * or whose visible scores are all -inf, gives zeros.  FP8 pools: V's row scales
+ * from 2^-100 to 2^20, or zero.
  * Other arguments, the workspace's rules and err_flag as for
  * paged_gqa_decode_int4 (no partition_tokens, any Hq/Hkv in 1..8); workspace of
  * paged_gqa_decode_window_workspace_size() bytes with the same sizes.

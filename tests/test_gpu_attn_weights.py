@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 import attn_bound as ab
+import kv4_ref as ref
 from gpu_util import to_dev, to_host
 from test_attn_bound import dominant_tokens, one_hot_pages, sink_queries
 
@@ -158,3 +159,27 @@ def test_more_pages_than_a_warp_lists_at_once(api, kind, n, Hkv, batch):
                                       window=n, sinks=0)
     for b in (0, batch // 2, batch - 1):
         ab.check(to_host(out)[b], q, x.K, x.V, D ** -0.5, x.v_scale, f"{kind} {b}")
+
+
+@pytest.mark.parametrize("kind", ["fp16", "fp8", "int4"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_a_visible_token_without_numbers(api, kind, which):
+    """NaN in K makes its kv head's outputs NaN, NaN in V the dims it is in (INT4: the
+    32 of its scale); the other outputs are the formula's."""
+    r = np.random.default_rng(15)
+    n, Hkv, t, h, d = 1500, 3, 777, 1, 40
+    x = ab.Rows(r, kind, *r.standard_normal((2, n, Hkv, D)))
+    page, slot = x.bt[0, t // 16], t % 16
+    pool = x.pools[which + "_pool"]
+    if kind == "int4":
+        pool[page, h, (ref.k_scale if which == "k" else ref.v_scale)(slot, d // 32)] = 0xFF
+    else:
+        pool[page, h, slot, d] = np.nan if kind == "fp16" else 0x7F
+    q = r.standard_normal((2 * Hkv, D)).astype(np.float16)
+    got = run(api, x, q, D ** -0.5, [40, 2])
+    nan = np.zeros((Hkv, 2, D), bool)
+    nan[h, :, slice(None) if which == "k" else slice(32, 64) if kind == "int4" else d] = True
+    nan = nan.reshape(2 * Hkv, D)
+    assert np.array_equal(np.isnan(got), nan)
+    out, w = ab.attend(q, x.K, x.V, D ** -0.5)
+    assert np.all((np.abs(got - out) <= ab.bound(q, x.K, x.V, D ** -0.5, out, w, x.v_scale)) | nan)

@@ -43,7 +43,7 @@
 // reference of their own, which follows log2(p s) as m follows log2(p): P is
 // p s 2^(m - mo) <= 2^15 for any row scales, and the warps' outputs go from mo
 // to m where they are merged.  (A fixed factor of 64 lost 4 % of an output of
-// 1e-4.)
+// 4e-6.)
 //
 // Rows that nothing attends to (an empty window, length 0) give zeros; masked
 // tokens of a visible page take no part whatever their bytes hold: their
@@ -389,7 +389,7 @@ __device__ __forceinline__ constexpr float atw_o_factor() { return KIND == ATW_I
 struct AtwShare {
   int b, kvh, part, parts;     // b -1: nothing to do
   int L, w0, S, n, nsp, wp;    // L: the length, up to max_context
-  int fits, len;               // the length itself, and whether it is no longer
+  int fits, len;               // whether the length is no longer than that; the length
 };
 
 // the visible pages of a sequence of this length
