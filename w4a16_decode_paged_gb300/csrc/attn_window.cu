@@ -33,7 +33,7 @@
 // many small weights beside a few large ones are lost from 2^-14 down, while
 // their sum keeps them: a quarter of the output where 32768 tokens lie e^-18 below
 // a sink without a value, emulated.)  P's rest in a second product would bring the
-// error from 1.1 to 1.3 times that of 32-bit sums down to theirs, at 7 % of the time
+// error from up to 1.35 times that of 32-bit sums down to theirs, at 7 % of the time
 // over INT4 pages, 4 % over FP8 and 1 % over fp16 ones: not kept, as the output's
 // own rounding is as large.
 // K and V enter exactly: fp16 as they are, INT4 values (kv4.cuh) as fp16 numbers,
