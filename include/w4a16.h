@@ -139,6 +139,73 @@ W4A16_API int w4a16_gemm_silu_mul(const uint16_t* x, int M, int K, const uint32_
                                   size_t workspace_bytes, w4a16_stream_t stream);
 W4A16_API size_t w4a16_gemm_workspace_size(int M, int K, int N, int silu);
 
+/* ------------------------------------------------------------------------
+ * MXFP4 matrices: 4-bit floating point with one power of two per 32 elements
+ * (the OCP microscaling format), 4.25 bits an element like INT4 with group 64.
+ *   value = c * 2^(b - 127), c an E2M1 code (sign bit, then 0, 0.5, 1, 1.5, 2,
+ *   3, 4, 6) and b an E8M0 byte per 32 consecutive elements of a row (255: NaN).
+ *   codes   uint32 [rows][K/8], nibble k % 8 of word k / 8, the lowest first
+ *           (the order of the packed INT4 weight).
+ *   scales  uint8, tiles of 128 rows x 128 elements, 512 bytes each,
+ *           [rows / 128 rounded up][K / 128]: row r and block j of a tile (32
+ *           elements) at byte 16 (r % 32) + 4 (r / 32) + j.  Bytes of rows past
+ *           the last are not used; mxfp4_scales_size() is the whole size.
+ * K % 128 == 0, K <= W4A16_MXFP4_MAX_K, rows <= W4A16_MXFP4_MAX_ROWS.
+ *
+ *   mxfp4_quantize    fp16 rows x [M][K] to codes and scales.  Per 32 elements:
+ *     a = max |x|, e = max(floor(log2 a) - 2, -23), b = e + 127, c = x 2^-e
+ *     rounded to nearest, ties to even, 6 at most.  An infinity or a NaN makes
+ *     its 32 elements NaN (b = 255, codes 0).  Scale bytes of rows past M in the
+ *     last tile are left as they were.  Every value is an fp16 number exactly
+ *     (b in 104..140).
+ *   mxfp4_dequantize  the values, each rounded to fp16 once (beyond: infinite).
+ *     Any scale byte.
+ *   w4a16_gemm_mxfp4  y = x . W^T (+ bias) (+ residual): x fp16 [M][K], W MXFP4
+ *     [N][K], y fp16 [M][N], bias fp16 [N] or NULL, residual fp16 [M][N] or
+ *     NULL (may be y).  Scale bytes of W: 104..140 as written by
+ *     mxfp4_quantize, or 255; smaller ones count as zero (0..102) or as
+ *     2^-24 (103), 141..254 are not served.
+ *   w4a16_gemm_silu_mul_mxfp4  y = silu(x . G^T) * (x . U^T), G and U as W.
+ *     Both sums stay fp32 into SiLU: silu(g) = g / (1 + exp(-g)), and its
+ *     product with u is rounded once.
+ *   w4a4_gemm_mxfp4   y = X . W^T (+ bias) (+ residual), both MXFP4, any scale
+ *     byte but 0: the block-scaled product of the tensor cores.
+ * Sums are fp32, y is rounded once.  y must not overlap x or the weights.
+ * Unlike the INT4 projections above, no call here reads weights before the
+ * call ahead of it on the stream is done: W may come straight out of
+ * mxfp4_quantize.
+ *
+ * workspace: NULL, or device memory of any size, zeroed once before its first
+ * use (every call leaves its counters, the first 8 KiB, zero), for products
+ * that split K across CTAs: with the *_workspace_size() bytes of a call's
+ * sizes it may split as it likes, with less, or none, it splits less or not
+ * at all.  One workspace serves calls of different shapes, and the other
+ * split-K GEMMs, in turn; calls that overlap on the GPU need one each.
+ * err_flag: int32 device word or NULL: bit 1 is set if a bounded wait inside
+ * a kernel gave up (its output is then not valid).
+ * ------------------------------------------------------------------------ */
+#define W4A16_MXFP4_MAX_K 131072
+#define W4A16_MXFP4_MAX_ROWS 1048576
+W4A16_API size_t mxfp4_scales_size(int rows, int K);
+W4A16_API int mxfp4_quantize(const uint16_t* x, int M, int K, uint32_t* codes, uint8_t* scales,
+                             w4a16_stream_t stream);
+W4A16_API int mxfp4_dequantize(const uint32_t* codes, const uint8_t* scales, int M, int K, uint16_t* y,
+                               w4a16_stream_t stream);
+W4A16_API int w4a16_gemm_mxfp4(const uint16_t* x, int M, int K, const uint32_t* codes, const uint8_t* scales,
+                               int N, const uint16_t* bias, const uint16_t* residual, uint16_t* y,
+                               void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                               w4a16_stream_t stream);
+W4A16_API int w4a16_gemm_silu_mul_mxfp4(const uint16_t* x, int M, int K, const uint32_t* codes_gate,
+                                        const uint8_t* scales_gate, const uint32_t* codes_up,
+                                        const uint8_t* scales_up, int N, uint16_t* y, void* workspace,
+                                        size_t workspace_bytes, int32_t* err_flag, w4a16_stream_t stream);
+W4A16_API int w4a4_gemm_mxfp4(const uint32_t* x_codes, const uint8_t* x_scales, int M, int K,
+                              const uint32_t* codes, const uint8_t* scales, int N, const uint16_t* bias,
+                              const uint16_t* residual, uint16_t* y, void* workspace, size_t workspace_bytes,
+                              int32_t* err_flag, w4a16_stream_t stream);
+W4A16_API size_t w4a16_gemm_mxfp4_workspace_size(int M, int K, int N, int silu);
+W4A16_API size_t w4a4_gemm_mxfp4_workspace_size(int M, int K, int N);
+
 /* Test hook for the failure path of the persistent decode kernel
  * (W4A16_PATH_PERSISTENT below).  Its grid-barrier waits are bounded
  * (default 2 s of the GPU's global timer); a wait that runs out sets bit 1

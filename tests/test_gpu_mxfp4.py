@@ -1,0 +1,375 @@
+"""MXFP4 matrices on the GPU: quantising and reading back bit for bit, the products
+against the 64-bit formula at every kind of tile edge, scales, NaN, streams, graphs
+and workspaces."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import mxfp4_ref as ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def api():
+    from w4a16_decode_paged_gb300 import api as a
+    return a
+
+
+def dev(a):
+    a = np.ascontiguousarray(a)
+    return torch.from_numpy(a.view(np.int32) if a.dtype == np.uint32 else a).cuda()
+
+
+def host(t):
+    return t.cpu().numpy()
+
+
+def matrix(code, byte):
+    """An MXFP4 matrix on the GPU; bytes of rows past the last are NaN scales."""
+    return dev(ref.pack(code)), dev(ref.tiles(byte, fill=255))
+
+
+def random_matrix(rng, n, k):
+    code, byte = ref.quantise(ref.weights(rng, n, k))
+    return matrix(code, byte), ref.values(code, byte)
+
+
+def activations(rng, m, k):
+    x = rng.standard_normal((m, k)) * np.where(rng.random(k) < 1 / 64, 8.0, 1.0)
+    return x.astype(np.float16)
+
+
+# --------------------------------------------------------------------------- quantising
+@pytest.mark.parametrize("m,k", [(1, 128), (1, 3584), (3, 256), (31, 896), (33, 384), (127, 640), (129, 2432), (300, 1152),
+                                 (1025, 128)])
+def test_quantise_and_read_back(api, m, k):
+    rng = np.random.default_rng(m * 7 + k)
+    x = activations(rng, m, k)
+    x *= np.exp2(rng.integers(-24, 12, (m, k // 32))).repeat(32, 1).astype(np.float16)   # blocks of every size
+    x[rng.random((m, k)) < 0.05] = 0
+    c, s = api.mxfp4_quantize(dev(x))
+    code, byte = ref.quantise(x)
+    assert np.array_equal(ref.unpack(host(c)), code)
+    assert np.array_equal(ref.untiled(host(s), m), byte)
+    y = host(api.mxfp4_dequantize(c, s)).astype(np.float64)
+    assert np.array_equal(y, ref.values(code, byte), equal_nan=True)
+
+
+def test_quantise_every_fp16_number(api):
+    """Each of the 65536 bit patterns as a block's largest, beside its halves."""
+    bits = np.arange(65536, dtype=np.uint16).view(np.float16)
+    x = np.zeros((65536, 128), np.float16)
+    with np.errstate(all="ignore"):
+        for j, f in enumerate((1, .5, .7, -.35, .2, -.125, .0625, .9)):
+            x[:, j] = (bits.astype(np.float32) * f).astype(np.float16)
+            x[:, 40 + j] = bits if j == 0 else 0
+            x[:, 71 - j] = bits if j < 2 else 0
+    c, s = api.mxfp4_quantize(dev(x))
+    code, byte = ref.quantise(x)
+    assert np.array_equal(ref.unpack(host(c)), code) and np.array_equal(ref.untiled(host(s), 65536), byte)
+    y, want = host(api.mxfp4_dequantize(c, s)).astype(np.float64), ref.values(code, byte)
+    assert np.array_equal(y, want, equal_nan=True) and np.isnan(want).any()
+
+
+def test_quantise_leaves_the_rest_alone(api):
+    m, k = 37, 256
+    s = torch.full((1, 2, 512), 77, dtype=torch.uint8, device="cuda")
+    x = activations(np.random.default_rng(1), m, k)
+    api.mxfp4_quantize(dev(x), scales=s)
+    t = host(s)
+    rows = ref.untiled(t, 128)
+    assert (rows[m:] == 77).all() and np.array_equal(rows[:m], ref.quantise(x)[1])
+
+
+def test_read_back_of_any_scale_byte(api):
+    """Every byte with every code, rounded to fp16 once."""
+    byte = np.arange(256).repeat(4).reshape(256, 4).astype(np.uint8)
+    code = np.tile(np.arange(16, dtype=np.uint8), (256, 8))
+    y = host(api.mxfp4_dequantize(*matrix(code, byte)))
+    with np.errstate(over="ignore"):
+        want = ref.values(code, byte).astype(np.float16)
+    assert np.array_equal(y[1:], want[1:], equal_nan=True) and not y[0].any()
+
+
+# --------------------------------------------------------------------------- products
+SHAPES = [(1, 1, 128), (1, 512, 3584), (1, 513, 128), (2, 33, 256), (3, 127, 384), (4, 128, 896), (5, 129, 512), (6, 16, 1152),
+          (7, 2432, 896), (8, 640, 2432), (9, 255, 640), (15, 31, 768), (16, 17, 1408), (17, 300, 256), (31, 1, 128),
+          (32, 512, 1152), (33, 257, 384), (48, 96, 640), (63, 130, 256), (64, 64, 1024), (65, 200, 128), (96, 384, 896),
+          (127, 129, 512), (128, 256, 384), (129, 127, 640), (191, 500, 256), (192, 128, 128), (193, 65, 1280),
+          (255, 385, 384), (256, 256, 256), (257, 641, 128), (300, 1000, 384), (513, 130, 256), (1000, 7, 128)]
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_a16(api, m, n, k):
+    rng = np.random.default_rng(m + 1000 * n + k)
+    x, (w, wv) = activations(rng, m, k), random_matrix(rng, n, k)
+    bias = (0.1 * rng.standard_normal(n)).astype(np.float16)
+    res = rng.standard_normal((m, n)).astype(np.float16)
+    xd = dev(x)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    y = api.w4a16_gemm_mxfp4(xd, *w, workspace=ws)
+    ref.check_product(host(y), x.astype(np.float64), wv, what="plain")
+    y = api.w4a16_gemm_mxfp4(xd, *w, bias=dev(bias), residual=dev(res), workspace=ws)
+    ref.check_product(host(y), x.astype(np.float64), wv, bias.astype(np.float64), res.astype(np.float64), "bias, residual")
+    # no room to split; the residual's own memory as the output
+    y = dev(res)
+    api.w4a16_gemm_mxfp4(xd, *w, residual=y, out=y, workspace=ws[:0])
+    ref.check_product(host(y), x.astype(np.float64), wv, None, res.astype(np.float64), "in place, no workspace")
+    assert not ws[:8192].any()
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_silu(api, m, n, k):
+    rng = np.random.default_rng(m + 1000 * n + k + 1)
+    x, (g, gv), (u, uv) = activations(rng, m, k), random_matrix(rng, n, k), random_matrix(rng, n, k)
+    y = api.w4a16_gemm_silu_mul_mxfp4(dev(x), *g, *u)
+    ref.check_silu(host(y), x.astype(np.float64), gv, uv)
+    y = api.w4a16_gemm_silu_mul_mxfp4(dev(x), *g, *u, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    ref.check_silu(host(y), x.astype(np.float64), gv, uv, "no workspace")
+
+
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_a4(api, m, n, k):
+    rng = np.random.default_rng(m + 1000 * n + k + 2)
+    code, byte = ref.quantise(activations(rng, m, k))
+    x, xv = matrix(code, byte), ref.values(code, byte)
+    w, wv = random_matrix(rng, n, k)
+    bias = (0.1 * rng.standard_normal(n)).astype(np.float16)
+    res = rng.standard_normal((m, n)).astype(np.float16)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    ref.check_product(host(api.w4a4_gemm_mxfp4(*x, *w, workspace=ws)), xv, wv, what="plain")
+    y = dev(res)
+    api.w4a4_gemm_mxfp4(*x, *w, bias=dev(bias), residual=y, out=y, workspace=ws)
+    ref.check_product(host(y), xv, wv, bias.astype(np.float64), res.astype(np.float64), "bias, residual in place")
+    y = api.w4a4_gemm_mxfp4(*x, *w, workspace=ws[:256])
+    ref.check_product(host(y), xv, wv, what="no workspace")
+    assert not ws[:8192].any()
+
+
+@pytest.mark.parametrize("m", [1, 4, 5, 8, 16, 32, 64, 128, 130])
+@pytest.mark.parametrize("call", ["a16", "silu", "a4"])
+def test_each_weight_meets_its_own_x(api, call, m):
+    """x picks one element of each row of W (a one-hot x): codes and scales all
+    different along K and N, results exact."""
+    n, k = 272, 1280
+    rng = np.random.default_rng(m)
+    code = rng.integers(0, 16, (n, k)).astype(np.uint8)
+    byte = rng.integers(117, 130, (n, k // 32)).astype(np.uint8)
+    w, wv = matrix(code, byte), ref.values(code, byte)
+    at = rng.integers(0, k, m)
+    x = np.zeros((m, k), np.float16)
+    x[np.arange(m), at] = 1
+    if call == "a4":
+        c, b = ref.quantise(x)
+        got = host(api.w4a4_gemm_mxfp4(*matrix(c, b), *w))
+    elif call == "a16":
+        got = host(api.w4a16_gemm_mxfp4(dev(x), *w))
+    else:
+        one = matrix(np.full((n, k), 2, np.uint8), np.full((n, k // 32), 127, np.uint8))    # G = 1: silu(1) * u
+        got = host(api.w4a16_gemm_silu_mul_mxfp4(dev(x), *one, *w)).astype(np.float64)
+        s = 1 / (1 + np.exp(-1.0))
+        assert (np.abs(got - s * wv[:, at].T) <= ref.half_step(s * wv[:, at].T) * (1 + 2.0 ** -10)).all()
+        return
+    assert np.array_equal(got.astype(np.float64), wv[:, at].T)
+
+
+@pytest.mark.parametrize("m", [1, 7, 32, 130])
+def test_scales_at_both_ends(api, m):
+    """Weights from 2^-24 to 49152 beside one another: fp16's whole range."""
+    rng = np.random.default_rng(3)
+    n, k = 96, 256
+    code = rng.integers(0, 16, (n, k)).astype(np.uint8)
+    byte = rng.choice([104, 105, 113, 127, 139, 140], (n, k // 32)).astype(np.uint8)
+    wv = ref.values(code, byte)
+    x = (rng.standard_normal((m, k)) * 2.0 ** -14).astype(np.float16)
+    ref.check_product(host(api.w4a16_gemm_mxfp4(dev(x), *matrix(code, byte))), x.astype(np.float64), wv)
+    small = np.full((n, k // 32), 104, np.uint8)                      # all small: nothing is lost beside larger ones
+    x = (rng.standard_normal((m, k)) * 1000).astype(np.float16)
+    ref.check_product(host(api.w4a16_gemm_mxfp4(dev(x), *matrix(code, small))), x.astype(np.float64), ref.values(code, small))
+    zero = rng.integers(0, 103, (n, k // 32)).astype(np.uint8)        # bytes that stand for zero
+    assert not host(api.w4a16_gemm_mxfp4(dev(x), *matrix(code, zero))).any()
+
+
+@pytest.mark.parametrize("m", [1, 33, 200])
+def test_a4_takes_any_scale(api, m):
+    rng = np.random.default_rng(5)
+    n, k = 130, 384
+    cx, cw = rng.integers(0, 16, (m, k)).astype(np.uint8), rng.integers(0, 16, (n, k)).astype(np.uint8)
+    # bytes far apart whose products are of ordinary size: each block's two bytes add up to about 254
+    bx = np.tile(rng.integers(30, 225, k // 32), (m, 1)) + rng.integers(-2, 3, (m, k // 32))
+    bw = 254 - np.tile(bx[:1], (n, 1)) + rng.integers(-2, 3, (n, k // 32))
+    bx, bw = bx.astype(np.uint8), bw.astype(np.uint8)
+    y = host(api.w4a4_gemm_mxfp4(*matrix(cx, bx), *matrix(cw, bw)))
+    ref.check_product(y, ref.values(cx, bx), ref.values(cw, bw))
+
+
+@pytest.mark.parametrize("m", [1, 5, 33, 200])
+@pytest.mark.parametrize("call", ["a16", "silu", "a4"])
+def test_nan_stays_in_its_row(api, call, m):
+    rng = np.random.default_rng(9)
+    n, k = 150, 512
+    x = activations(rng, m, k)
+    code, byte = ref.quantise(ref.weights(rng, n, k))
+    code[code & 7 == 0] = 1                                          # no zero weight: inf * 0 would be NaN as well
+    byte[17, 3] = 255
+    x[m // 2, 100] = np.nan if m % 2 else np.inf
+    w = matrix(code, byte)
+    if call == "a4":
+        y = api.w4a4_gemm_mxfp4(*api.mxfp4_quantize(dev(x)), *w)
+    elif call == "a16":
+        y = api.w4a16_gemm_mxfp4(dev(x), *w)
+    else:
+        y = api.w4a16_gemm_silu_mul_mxfp4(dev(x), *w, *w)
+    fine = np.isfinite(host(y))
+    want = np.ones((m, n), bool)
+    want[m // 2], want[:, 17] = False, False
+    if call == "silu" and m % 2 == 0:                                # silu(-inf) * -inf: 0 * inf, or inf: not finite either
+        assert not fine[~want].any()
+    assert np.array_equal(fine, want)
+    assert np.isnan(host(y)[:, 17]).all()
+
+
+# --------------------------------------------------------------------------- use
+def _mlp(api, x, w, ws):
+    """A decode MLP's projections in one run: quantised weights straight from the quantiser."""
+    y = api.w4a16_gemm_silu_mul_mxfp4(x, *w["g"], *w["u"], workspace=ws)
+    return api.w4a16_gemm_mxfp4(y, *w["d"], residual=x, workspace=ws)
+
+
+@pytest.mark.parametrize("m", [1, 8, 40, 256])
+def test_a_run_of_them_equals_its_parts(api, m):
+    """Weights quantised on the GPU, read back, and used at once, the MLP in 16 and
+    in 4 bits; captured and replayed with new inputs, it gives the same bits."""
+    rng = np.random.default_rng(m)
+    h, i = 512, 1152
+    w = {p: ref.weights(rng, *s) for p, s in (("g", (i, h)), ("u", (i, h)), ("d", (h, i)))}
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+    x = activations(rng, m, h)
+    q, dw = {}, {p: dev(a) for p, a in w.items()}
+    for p in w:
+        q[p] = api.mxfp4_quantize(dw[p])
+    xd = dev(x)
+    q["d2"] = api.mxfp4_quantize(dw["d"])
+    first = api.w4a16_gemm_mxfp4(dev(np.ones((m, i), np.float16)), *q["d2"], workspace=ws)   # right behind the quantiser
+    vals = {p: host(api.mxfp4_dequantize(*q[p])).astype(np.float64) for p in w}
+    for p in w:
+        assert np.array_equal(vals[p], ref.values(*ref.quantise(w[p])))
+    ref.check_product(host(first), np.ones((m, i)), vals["d"])
+    y = api.w4a16_gemm_silu_mul_mxfp4(xd, *q["g"], *q["u"], workspace=ws)
+    ref.check_silu(host(y), x.astype(np.float64), vals["g"], vals["u"])
+    z = api.w4a16_gemm_mxfp4(y, *q["d"], residual=xd, workspace=ws)
+    ref.check_product(host(z), host(y).astype(np.float64), vals["d"], None, x.astype(np.float64))
+    y4 = api.mxfp4_quantize(y)
+    z4 = api.w4a4_gemm_mxfp4(*y4, *q["d"], residual=xd, workspace=ws)
+    ref.check_product(host(z4), host(api.mxfp4_dequantize(*y4)).astype(np.float64), vals["d"], None, x.astype(np.float64))
+
+    def run():
+        y = api.w4a16_gemm_silu_mul_mxfp4(xd, *q["g"], *q["u"], workspace=ws)
+        return api.w4a16_gemm_mxfp4(y, *q["d"], residual=xd, workspace=ws), api.w4a4_gemm_mxfp4(
+            *api.mxfp4_quantize(y), *q["d"], residual=xd, workspace=ws)
+    assert torch.equal(run()[0], z) and torch.equal(run()[1], z4)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    x2 = dev(activations(rng, m, h))
+    for new in (xd.clone(), x2, xd.clone()):
+        xd.copy_(new)
+        graph.replay()
+        got = [t.clone() for t in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, run()))
+
+
+@pytest.mark.parametrize("m", [1, 16, 100])
+def test_on_another_stream(api, m):
+    """A call given a stream works there, and so do the tensors it makes."""
+    rng = np.random.default_rng(m)
+    n, k = 300, 896
+    x = activations(rng, m, k)
+    w, wv = random_matrix(rng, n, k)
+    xd, s = dev(x), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = api.w4a16_gemm_mxfp4(xd, *w, stream=s)
+    q = api.mxfp4_quantize(xd, stream=s)
+    y4 = api.w4a4_gemm_mxfp4(*q, *w, stream=s)
+    xr = api.mxfp4_dequantize(*q, stream=s)
+    ys = api.w4a16_gemm_silu_mul_mxfp4(xd, *w, *w, stream=s)
+    s.synchronize()
+    ref.check_product(host(y), x.astype(np.float64), wv)
+    ref.check_product(host(y4), host(xr).astype(np.float64), wv)
+    ref.check_silu(host(ys), x.astype(np.float64), wv, wv)
+
+
+def test_two_calls_at_once_with_a_workspace_each(api):
+    rng = np.random.default_rng(0)
+    n, k = 384, 2432
+    w, wv = random_matrix(rng, n, k)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [api.mxfp4_workspace(24, k, n) for _ in streams]
+    xs = [activations(rng, 24, k) for _ in streams]
+    xd = [dev(x) for x in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        ys = [api.w4a16_gemm_mxfp4(xd[i], *w, workspace=spaces[i], stream=streams[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    for x, y in zip(xs, ys):
+        ref.check_product(host(y), x.astype(np.float64), wv)
+
+
+def test_rows_past_the_last_are_left_alone(api):
+    rng = np.random.default_rng(4)
+    n, k = 131, 256
+    w, _ = random_matrix(rng, n, k)
+    for m in (1, 3, 6, 33, 129):
+        buf = torch.full((m * n + 4096,), 7.0, dtype=torch.float16, device="cuda")
+        y = buf[:m * n].view(m, n)
+        x = dev(activations(rng, m, k))
+        api.w4a16_gemm_mxfp4(x, *w, out=y)
+        assert (buf[m * n:] == 7).all()
+        api.w4a16_gemm_silu_mul_mxfp4(x, *w, *w, out=y)
+        assert (buf[m * n:] == 7).all()
+        api.w4a4_gemm_mxfp4(*api.mxfp4_quantize(x), *w, out=y)
+        assert (buf[m * n:] == 7).all()
+
+
+def test_same_bits_each_time(api):
+    """Split sums are joined in one order."""
+    rng = np.random.default_rng(8)
+    for m, n, k in ((1, 512, 3584), (7, 256, 3584), (32, 384, 3584), (100, 256, 3584)):
+        x, (w, _) = dev(activations(rng, m, k)), random_matrix(rng, n, k)
+        ws = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")
+        q = api.mxfp4_quantize(x)
+        y, y4 = api.w4a16_gemm_mxfp4(x, *w, workspace=ws), api.w4a4_gemm_mxfp4(*q, *w, workspace=ws)
+        for _ in range(20):
+            assert torch.equal(api.w4a16_gemm_mxfp4(x, *w, workspace=ws), y)
+            assert torch.equal(api.w4a4_gemm_mxfp4(*q, *w, workspace=ws), y4)
+
+
+@pytest.mark.parametrize("call,m,n,k", [("a16", 1, 3584, 18944), ("a16", 32, 3584, 18944), ("silu", 1, 18944, 3584),
+                                        ("silu", 32, 18944, 3584), ("a16", 2048, 3584, 3584), ("a4", 512, 18944, 3584),
+                                        ("a4", 700, 3584, 18944)])
+def test_full_size(api, call, m, n, k):
+    """The projections of the model shape the benchmark runs, against 64 bits on the GPU."""
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")
+    x = (rnd(m, k) * torch.where(torch.rand(k, generator=gen, device="cuda") < 1 / 64, 8.0, 1.0)).half()
+    ws = [(rnd(n, k) / k ** 0.5).half() for _ in range(2 if call == "silu" else 1)]
+    q = [api.mxfp4_quantize(w) for w in ws]
+    wv = [api.mxfp4_dequantize(*p).double() for p in q]
+    if call == "silu":
+        y = api.w4a16_gemm_silu_mul_mxfp4(x, *q[0], *q[1])
+        g, u = x.double() @ wv[0].T, x.double() @ wv[1].T
+        want = g * torch.sigmoid(g) * u
+    else:
+        xq = api.mxfp4_quantize(x)
+        xv = api.mxfp4_dequantize(*xq) if call == "a4" else x
+        y = api.w4a4_gemm_mxfp4(*xq, *q[0]) if call == "a4" else api.w4a16_gemm_mxfp4(x, *q[0])
+        want = xv.double() @ wv[0].T
+    rms = float(((y.double() - want) ** 2).mean().sqrt() / (want ** 2).mean().sqrt())
+    assert rms <= 2.0 ** -10 / 12 ** 0.5 * 1.02, rms
+    assert float(((y.double() - want).abs() / (want.abs() + float((want ** 2).mean().sqrt()))).max()) <= 2.0 ** -10

@@ -57,6 +57,14 @@ SIGNATURES = {
     "w4a16_gemm": (I32, [P, I32, I32, P, P, I32, P, P, P, P, SZ, P]),
     "w4a16_gemm_silu_mul": (I32, [P, I32, I32, P, P, P, P, I32, P, P, SZ, P]),
     "w4a16_gemm_workspace_size": (SZ, [I32, I32, I32, I32]),
+    "mxfp4_scales_size": (SZ, [I32, I32]),
+    "mxfp4_quantize": (I32, [P, I32, I32, P, P, P]),
+    "mxfp4_dequantize": (I32, [P, P, I32, I32, P, P]),
+    "w4a16_gemm_mxfp4": (I32, [P, I32, I32, P, P, I32, P, P, P, P, SZ, P, P]),
+    "w4a16_gemm_silu_mul_mxfp4": (I32, [P, I32, I32, P, P, P, P, I32, P, P, SZ, P, P]),
+    "w4a4_gemm_mxfp4": (I32, [P, P, I32, I32, P, P, I32, P, P, P, P, SZ, P, P]),
+    "w4a16_gemm_mxfp4_workspace_size": (SZ, [I32, I32, I32, I32]),
+    "w4a4_gemm_mxfp4_workspace_size": (SZ, [I32, I32, I32]),
     "w4a16_debug_set_wait_limit_ns": (ctypes.c_ulonglong, [ctypes.c_ulonglong]),
     "lm_head_logits_batched": (I32, [P, I32, I32, P, I32, P, P]),
     "argmax_rows": (I32, [P, I32, I32, P, P, P]),

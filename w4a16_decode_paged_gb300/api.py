@@ -17,6 +17,8 @@ from ._lib import LayerWeights, ModelConfig, ModelWeights, check, load, native
 __all__ = ["w4a16_gemv", "w4a16_gemm", "w4a16_gemm_silu_mul", "lm_head_logits_batched", "argmax_rows", "w4a16_gemv_rmsnorm", "w4a16_gemv_silu_mul", "rmsnorm", "kv_append_rope",
            "paged_gqa_decode", "paged_gqa_decode_rope_append", "paged_gqa_decode_workspace_size", "paged_gqa_decode_default_partition",
            "kv_append_rope_int4", "kv_read_int4", "paged_gqa_decode_int4", "paged_gqa_decode_window", "KV4_SLICE",
+           "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_tile_scales", "mxfp4_untile_scales", "w4a16_gemm_mxfp4",
+           "w4a16_gemm_silu_mul_mxfp4", "w4a4_gemm_mxfp4", "mxfp4_workspace",
            "workspace_clear", "embedding_gather", "lm_head_argmax", "Model", "stream_handle"]
 
 
@@ -413,6 +415,173 @@ def _made_on(stream, dev):
     if stream.device_index != dev:
         raise ValueError(f"stream is on device {stream.device_index}, the pools are on device {dev}")
     return torch.cuda.stream(stream)
+
+
+MXFP4_MAX_K, MXFP4_MAX_ROWS = 131072, 1048576
+
+
+def _mx_k(K, name):
+    if K < 128 or K % 128 or K > MXFP4_MAX_K:
+        raise ValueError(f"{name}: K={K}, expected a multiple of 128 up to {MXFP4_MAX_K}")
+
+
+def _mx_rows(n, name):
+    if not 1 <= n <= MXFP4_MAX_ROWS:
+        raise ValueError(f"{name}: {n} rows, expected 1 to {MXFP4_MAX_ROWS}")
+
+
+def _mx_matrix(codes, scales, name, dev=None, K=None):
+    """(rows, K, device) of an MXFP4 matrix: codes [rows][K/8], scales
+    [rows/128 rounded up][K/128][512]."""
+    cname, sname = name + "codes", name + "scales"
+    if codes is None or codes.dim() != 2 or codes.dtype not in _W:
+        _arg(codes, _W, cname, (None, None))
+    dev = _device_of(codes, cname) if dev is None else dev
+    rows, words = codes.shape
+    _mx_rows(rows, cname)
+    if K is None:
+        K = words * 8
+        _mx_k(K, cname)
+    _is(codes, codes.dtype, (rows, K // 8), dev, cname)
+    _is(scales, torch.uint8, (-(-rows // 128), K // 128, 512), dev, sname)
+    return rows, K, dev
+
+
+def _mx_x(x):
+    """(M, K, device) of fp16 activations x [M][K]."""
+    if x is None or x.dim() != 2:
+        _arg(x, _H, "x", (None, None))
+    dev = _device_of(x, "x")
+    M, K = x.shape
+    _is(x, torch.float16, (M, K), dev, "x")
+    _mx_rows(M, "x")
+    _mx_k(K, "x")
+    return M, K, dev
+
+
+def mxfp4_tile_scales(scales):
+    """Scale bytes [N][K/32], one row after another, in the tiles that the
+    calls here take: uint8 [N/128 rounded up][K/128][512] (a layout done once,
+    e.g. for the scales of a checkpoint; rows past N hold 127)."""
+    if scales.dtype != torch.uint8 or scales.dim() != 2 or scales.shape[1] % 4 or not scales.numel():
+        raise ValueError(f"scales: {scales.dtype} {tuple(scales.shape)}, expected uint8 (N, K/32), K a multiple of 128")
+    n, kt = scales.shape[0], scales.shape[1] // 4
+    t = -(-n // 128)
+    full = scales.new_full((t * 128, kt * 4), 127)
+    full[:n] = scales
+    return full.view(t, 4, 32, kt, 4).permute(0, 3, 2, 1, 4).reshape(t, kt, 512)
+
+
+def mxfp4_untile_scales(tiles, rows):
+    """Scale bytes [rows][K/32] of scale tiles (the reverse of mxfp4_tile_scales)."""
+    if tiles.dtype != torch.uint8 or tiles.dim() != 3 or tiles.shape[2] != 512 or not 1 <= rows <= 128 * tiles.shape[0]:
+        raise ValueError(f"tiles: {tiles.dtype} {tuple(tiles.shape)}, rows={rows}: expected uint8 (rows/128 rounded "
+                         f"up, K/128, 512)")
+    t, kt, _ = tiles.shape
+    return tiles.reshape(t, kt, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(t * 128, kt * 4)[:rows].contiguous()
+
+
+def mxfp4_quantize(x, codes=None, scales=None, stream=None):
+    """(codes, scales) of fp16 rows x [M][K]: int32 [M][K/8] and scale tiles
+    uint8 [M/128 rounded up][K/128][512] (bytes of rows past M are left as they
+    were in tiles that the caller gives, and are not used by any call)."""
+    M, K, dev = _mx_x(x)
+    if codes is not None and codes.dtype not in _W:
+        _arg(codes, _W, "codes")
+    if codes is not None:
+        _is(codes, codes.dtype, (M, K // 8), dev, "codes")
+    if scales is not None:
+        _is(scales, torch.uint8, (-(-M // 128), K // 128, 512), dev, "scales")
+    with _made_on(stream, dev):
+        if codes is None:
+            codes = x.new_empty((M, K // 8), dtype=torch.int32)
+        if scales is None:
+            scales = x.new_empty((-(-M // 128), K // 128, 512), dtype=torch.uint8)
+    check(load().mxfp4_quantize(x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(), _stream_on(stream, dev)))
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, out=None, stream=None):
+    """fp16 values [M][K] of an MXFP4 matrix."""
+    M, K, dev = _mx_matrix(codes, scales, "")
+    if out is not None:
+        _is(out, torch.float16, (M, K), dev, "out")
+    else:
+        with _made_on(stream, dev):
+            out = codes.new_empty((M, K), dtype=torch.float16)
+    check(load().mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, out.data_ptr(), _stream_on(stream, dev)))
+    return out
+
+
+def mxfp4_workspace(M, K, N, kind="a16", device="cuda"):
+    """A zeroed workspace for w4a16_gemm_mxfp4 (kind "a16"),
+    w4a16_gemm_silu_mul_mxfp4 ("silu") or w4a4_gemm_mxfp4 ("a4") of these sizes;
+    one serves every call that does not overlap another on the GPU."""
+    if kind not in ("a16", "silu", "a4"):
+        raise ValueError(f"kind={kind!r}, expected 'a16', 'silu' or 'a4'")
+    lib = load()
+    n = lib.w4a4_gemm_mxfp4_workspace_size(M, K, N) if kind == "a4" else \
+        lib.w4a16_gemm_mxfp4_workspace_size(M, K, N, int(kind == "silu"))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def _mx_buffers(M, K, N, kind, out, workspace, err_flag, bias, residual, like, dev, stream):
+    if bias is not None:
+        _is(bias, torch.float16, (N,), dev, "bias")
+    if residual is not None:
+        _is(residual, torch.float16, (M, N), dev, "residual")
+    if out is not None:
+        _is(out, torch.float16, (M, N), dev, "out")
+    if workspace is not None:
+        _is(workspace, torch.uint8, workspace.shape, dev, "workspace")
+    err = _err_flag(err_flag, dev)
+    with _made_on(stream, dev):
+        if out is None:
+            out = like.new_empty((M, N), dtype=torch.float16)
+        if workspace is None:
+            workspace = mxfp4_workspace(M, K, N, kind, like.device)
+    return out, workspace, err
+
+
+def w4a16_gemm_mxfp4(x, codes, scales, bias=None, residual=None, out=None, workspace=None, err_flag=None, stream=None):
+    """y = x . W^T (+ bias) (+ residual): x fp16 [M][K], W MXFP4 (codes int32
+    [N][K/8], scale tiles), from one token to a prompt's rows.  A workspace the
+    caller gives is zeroed once before its first use (mxfp4_workspace); without
+    one, each call makes its own.  residual may be out."""
+    M, K, dev = _mx_x(x)
+    N = _mx_matrix(codes, scales, "", dev, K)[0]
+    out, workspace, err = _mx_buffers(M, K, N, "a16", out, workspace, err_flag, bias, residual, x, dev, stream)
+    check(load().w4a16_gemm_mxfp4(x.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(), N, _p(bias), _p(residual),
+                                  out.data_ptr(), workspace.data_ptr(), workspace.numel(), err,
+                                  _stream_on(stream, dev)))
+    return out
+
+
+def w4a16_gemm_silu_mul_mxfp4(x, codes_gate, scales_gate, codes_up, scales_up, out=None, workspace=None, err_flag=None,
+                              stream=None):
+    """y = silu(x . G^T) * (x . U^T): the gated MLP's front half over MXFP4 weights."""
+    M, K, dev = _mx_x(x)
+    N = _mx_matrix(codes_gate, scales_gate, "gate ", dev, K)[0]
+    if _mx_matrix(codes_up, scales_up, "up ", dev, K)[0] != N:
+        raise ValueError(f"up codes: {codes_up.shape[0]} rows, gate codes {N}")
+    out, workspace, err = _mx_buffers(M, K, N, "silu", out, workspace, err_flag, None, None, x, dev, stream)
+    check(load().w4a16_gemm_silu_mul_mxfp4(x.data_ptr(), M, K, codes_gate.data_ptr(), scales_gate.data_ptr(),
+                                           codes_up.data_ptr(), scales_up.data_ptr(), N, out.data_ptr(),
+                                           workspace.data_ptr(), workspace.numel(), err, _stream_on(stream, dev)))
+    return out
+
+
+def w4a4_gemm_mxfp4(x_codes, x_scales, codes, scales, bias=None, residual=None, out=None, workspace=None,
+                    err_flag=None, stream=None):
+    """y = X . W^T (+ bias) (+ residual), both MXFP4 matrices (X from
+    mxfp4_quantize): the block-scaled 4-bit product of the tensor cores."""
+    M, K, dev = _mx_matrix(x_codes, x_scales, "x_")
+    N = _mx_matrix(codes, scales, "", dev, K)[0]
+    out, workspace, err = _mx_buffers(M, K, N, "a4", out, workspace, err_flag, bias, residual, x_codes, dev, stream)
+    check(load().w4a4_gemm_mxfp4(x_codes.data_ptr(), x_scales.data_ptr(), M, K, codes.data_ptr(), scales.data_ptr(), N,
+                                 _p(bias), _p(residual), out.data_ptr(), workspace.data_ptr(), workspace.numel(), err,
+                                 _stream_on(stream, dev)))
+    return out
 
 
 def _paging_of(kind, k_pool, v_pool, block_table, context_lens):

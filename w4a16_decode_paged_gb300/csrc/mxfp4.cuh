@@ -1,0 +1,77 @@
+// mxfp4.cuh -- the MXFP4 matrix format, shared by its kernels.
+//
+// value = c * 2^(b - 127): c an E2M1 code (sign, then 0, 0.5, 1, 1.5, 2, 3, 4,
+// 6), b one byte per 32 consecutive elements of a row (255: NaN).  Codes:
+// uint32 [rows][K/8], the lowest nibble first.  Scale bytes: tiles of 128 rows
+// x 128 elements, 512 bytes each, [rows/128 rounded up][K/128]; row r, block j
+// of a tile at byte 16 (r % 32) + 4 (r / 32) + j.  That is the order in which
+// the tensor core takes its scales (32 lanes of four 32-bit columns), so that
+// they go there by plain copies; a thread that wants one row's scales reads
+// the 4 bytes of 128 elements at once.
+#pragma once
+
+#include "common.cuh"
+
+namespace w4 {
+
+constexpr int MX_TILE = 512;          // bytes of a scale tile (128 rows x 4 blocks)
+constexpr int MX_MIN_BYTE = 104;      // least scale written: 2^-23, whose half is the last fp16 bit
+__host__ __device__ inline size_t mx_tiles(int rows, int K) { return (size_t)((rows + 127) / 128) * (K / 128); }
+
+// byte offset of the four scales of row r, elements 128 kt .. 128 kt + 127
+__host__ __device__ __forceinline__ size_t mx_scale_at(int r, int kt, int ktiles) {
+  return ((size_t)(r >> 7) * ktiles + kt) * MX_TILE + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
+
+// the eight values of a code word as fp16 pairs (0 1) (2 3) (4 5) (6 7)
+__device__ __forceinline__ uint4 mx_values(uint32_t w) {
+  uint4 v;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+      : "r"(w));
+  return v;
+}
+
+// 2^(byte - 127) in fp32 (byte 0: zero); inf * 0 + inf makes the 255 a NaN
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  const float f = __uint_as_float(byte << 23);
+  return fmaf(f, 0.f, f);
+}
+
+// the same rounded to fp16, in both halves: exact for bytes 103..142, zero below
+__device__ __forceinline__ uint32_t mx_scale_h2(uint32_t byte) {
+  const __half2 h = __float2half2_rn(mx_scale(byte));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// One product (mxfp4_gemm): y[m][n] = sum_k x[m][k] w[n][k] (+ bias[n])
+// (+ residual[m][n]), or silu(x g^T) * (x u^T) with two weight matrices.
+struct MxWeights {
+  const uint32_t* codes;   // [N][K/8]
+  const uint8_t* scales;   // tiles
+};
+struct MxArgs {
+  const __half* x;         // [M][K], or
+  MxWeights xq;            // x in MXFP4 (x null)
+  MxWeights w[2];          // w, or gate and up
+  const __half* bias;      // [N] or null
+  const __half* residual;  // [M][N] or null
+  __half* y;               // [M][N]
+  int M, N, K;
+  void* workspace;
+  size_t workspace_bytes;
+  int32_t* err_flag;
+};
+
+}  // namespace w4
