@@ -73,5 +73,7 @@ struct MxArgs {
   size_t workspace_bytes;
   int32_t* err_flag;
 };
+bool mxfp4_matvec_serves(int M, int K);
+int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s);
 
 }  // namespace w4

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(256) w4pg_mxfp4_tile(const MxArgs a) {
 }
 
 static int launch_mxfp4(const MxArgs& a, bool silu, cudaStream_t s) {
+  if (a.x && mxfp4_matvec_serves(a.M, a.K)) return launch_mxfp4_matvec(a, silu, s);
   const dim3 grid((a.N + MXS_N - 1) / MXS_N, (a.M + MXS_M - 1) / MXS_M);
   const cudaError_t e = silu ? launch_pdl(w4pg_mxfp4_tile<true>, grid, dim3(256), 0, s, a)
                              : launch_pdl(w4pg_mxfp4_tile<false>, grid, dim3(256), 0, s, a);
