@@ -163,8 +163,8 @@ W4A16_API size_t w4a16_gemm_workspace_size(int M, int K, int N, int silu);
  *   w4a16_gemm_mxfp4  y = x . W^T (+ bias) (+ residual): x fp16 [M][K], W MXFP4
  *     [N][K], y fp16 [M][N], bias fp16 [N] or NULL, residual fp16 [M][N] or
  *     NULL (may be y).  Scale bytes of W: 104..140 as written by
- *     mxfp4_quantize, or 255; smaller ones count as zero (0..102) or as
- *     2^-24 (103), 141..254 are not served.
+ *     mxfp4_quantize, or 255; blocks with smaller ones (values up to 6 * 2^-24)
+ *     may count as zero, 141..254 are not served.
  *   w4a16_gemm_silu_mul_mxfp4  y = silu(x . G^T) * (x . U^T), G and U as W.
  *     Both sums stay fp32 into SiLU: silu(g) = g / (1 + exp(-g)), and its
  *     product with u is rounded once.

@@ -188,8 +188,12 @@ def test_scales_at_both_ends(api, m):
     small = np.full((n, k // 32), 104, np.uint8)                      # all small: nothing is lost beside larger ones
     x = (rng.standard_normal((m, k)) * 1000).astype(np.float16)
     ref.check_product(host(api.w4a16_gemm_mxfp4(dev(x), *matrix(code, small))), x.astype(np.float64), ref.values(code, small))
-    zero = rng.integers(0, 103, (n, k // 32)).astype(np.uint8)        # bytes that stand for zero
-    assert not host(api.w4a16_gemm_mxfp4(dev(x), *matrix(code, zero))).any()
+    tiny = rng.integers(0, 104, (n, k // 32)).astype(np.uint8)        # such blocks count as themselves or as zero
+    y = host(api.w4a16_gemm_mxfp4(dev(x), *matrix(code, tiny))).astype(np.float64)
+    most = np.abs(x.astype(np.float64)) @ np.abs(ref.values(code, tiny)).T
+    assert (np.abs(y) <= most * (1 + 2.0 ** -10) + 2.0 ** -24).all()
+    y = host(api.w4a16_gemm_mxfp4(dev(x), *matrix(code & 8, tiny)))   # zero codes under any of them: zero
+    assert not y.any()
 
 
 @pytest.mark.parametrize("m", [1, 33, 200])

@@ -14,8 +14,8 @@
 //
 // Split: one persistent CTA of 16 warps per SM; clusters of C CTAs split K (the
 // sums meet through distributed shared memory); a cluster's 16-row groups times
-// its CTA's scale tiles along K are one stream of units that the 16 warps share
-// out evenly, each keeping MV_D units of loads in flight across group borders.
+// its CTA's scale tiles along K are one stream of units that its warps share
+// out evenly, each keeping D units of loads in flight across group borders.
 // A warp parks its sum of a group, or of a piece of one, in shared memory; at the
 // end the pieces are added in the order of K, whatever the timing.
 #include <algorithm>
@@ -29,240 +29,271 @@ constexpr int MV_WARPS = 16;
 constexpr int MV_THREADS = 32 * MV_WARPS;
 constexpr int MV_ROWS = 16;
 constexpr int MV_GROUPS = 32;    // groups of a cluster between two joins
-constexpr int MV_SMEM = 220 * 1024;
+template <int MS>
+constexpr int MV_D = MS == 1 ? 4 : 3;
 
+template <bool FIRST>  // FIRST: d = a b, else d += a b
 __device__ __forceinline__ void mv_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if (FIRST)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 bytes global -> shared through L1 (x: the next groups read it again)
+__device__ __forceinline__ void cp_async16_ca(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int q) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; }
 
-// a float at the same shared-memory offset in CTA `rank` of the cluster (between
-// two cluster barriers: not to be moved)
-__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+// store a float at the same shared-memory offset in CTA `rank` of the cluster
+__device__ __forceinline__ void st_cluster(float* p, int rank, float v) {
   uint32_t remote;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// two scale bytes as fp32 (255: NaN)
+__device__ __forceinline__ float2 mv_scales(uint16_t bytes) {
+  uint32_t v;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(v) : "h"(bytes));
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
-// a scale beside fp16 activations: bytes that fp16 cannot hold count as zero
-__device__ __forceinline__ float mv_scale(uint32_t byte) { return byte < 103 ? 0.f : mx_scale(byte); }
-
-// shared memory: x of this CTA's K in the MMA's order, this CTA's sums of the
-// groups, the pieces of them
-template <int NW, int MS>
+// shared memory: the rings, zeros, this cluster's sums of the groups, this CTA's
+// pieces of them
+template <int MS>
 struct MvShape {
   static constexpr int MT = 2 * MS;                      // rows of x
-  static constexpr int PIECE = NW * MT * MV_ROWS;        // floats
-  static constexpr int D = NW == 2 ? 3 : 6;              // units in flight per warp
-  static size_t smem(int ktiles, int groups) {
-    const int n = std::min(groups, MV_GROUPS);
-    return (size_t)ktiles * 16 * MT * 16 + (size_t)(n + n + MV_WARPS) * PIECE * 4;
+  static constexpr int PIECE = MT * MV_ROWS;             // floats
+  static constexpr int D = MV_D<MS>;                     // units in flight per warp
+  static constexpr int XAT = 1088;                       // a unit: 16 rows x (64 bytes of codes, 4 of scales), x
+  static constexpr int UNIT = XAT + MT * 256;
+  static constexpr int RING = MV_WARPS * D * UNIT;
+  static constexpr int ZEROS = 4 * MT * 64;              // bytes
+  static size_t smem(int groups) {                       // groups: of a round
+    return (size_t)RING + ZEROS + (size_t)(groups + 16 + groups + MV_WARPS) * PIECE * 4;
   }
 };
 
-// NW weight matrices (2: gate and up); MS MMAs per 16 k, 2 rows of x each
+// NW weight matrices (2: gate and up, their groups in turn); MS MMAs per 16 k, 2
+// rows of x each.  64 registers, so that the next kernel's CTA fits beside this one.
 template <int NW, int MS>
-__global__ void __launch_bounds__(MV_THREADS, 1)
-    w4pg_mxfp4_matvec(const __grid_constant__ MxArgs a, int csize, int groups, int gcap) {
-  using SH = MvShape<NW, MS>;
+__global__ void __launch_bounds__(MV_THREADS, 2)
+    w4pg_mxfp4_matvec(const __grid_constant__ MxArgs a, int clog, int groups, int gcap) {
+  using SH = MvShape<MS>;
   constexpr int MT = SH::MT, PIECE = SH::PIECE, D = SH::D;
+  W4_TRACE_SCOPE(0);
+  if (clog > 0) cluster_arrive();
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ int ubegin[MV_WARPS + 1];
+  __shared__ int first[MV_GROUPS], last[MV_GROUPS];  // the warps that have a group's pieces
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int rank = blockIdx.x % csize, cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
+  const int csize = 1 << clog, rank = blockIdx.x & (csize - 1), cluster = blockIdx.x >> clog, clusters = gridDim.x >> clog;
   const int K = a.K, KT = K / 128;
-  const int c0 = KT * rank / csize, kc = KT * (rank + 1) / csize - c0;  // this CTA's scale tiles along K
-  uint4* xs = reinterpret_cast<uint4*>(smem);
-  float* sums = reinterpret_cast<float*>(smem + (size_t)((KT + csize - 1) / csize) * 16 * MT * 16);
-  float* pieces = sums + gcap * PIECE;
+  const int c0 = KT * rank >> clog, kc = (KT * (rank + 1) >> clog) - c0;  // this CTA's scale tiles along K
+  unsigned char* ring = smem + warp * D * SH::UNIT;
+  uint4* zeros = reinterpret_cast<uint4*>(smem + SH::RING);
+  float* sums = reinterpret_cast<float*>(smem + SH::RING + SH::ZEROS);
+  float* pieces = sums + (gcap + 16) * PIECE;
 
-  const int ngroups = (groups - cluster + clusters - 1) / clusters;  // of this cluster: cluster, cluster + clusters, ..
-  const uint4* wp[NW][2];
-  const uint8_t* sp[NW];
+  // the cluster's groups: cluster, cluster + clusters, .., of each matrix in turn
+  const int ngroups = NW * ((groups - cluster + clusters - 1) / clusters);
+  const uint4 *wp0, *wp1;
+  const uint8_t* sp;
   // lane's rows g and g + 8 of a group: its 16 rows are four times four, 32 apart,
   // so that their scales are 64 contiguous bytes of a tile; rows past the last
   // read the last one
-  auto point = [&](int i) {
-    const int group = cluster + i * clusters, row0 = (group >> 3) * 128 + (group & 7) * 4;
-    const int r0 = min(row0 + (g & 3) + 32 * (g >> 2), a.N - 1), r1 = min(row0 + (g & 3) + 32 * (g >> 2) + 64, a.N - 1);
-    const size_t at = ((size_t)(group >> 3) * KT + c0) * MX_TILE + (group & 7) * 64 + (g & 3) * 16 + (g >> 2) * 4 + 2 * (t & 1);
-#pragma unroll
-    for (int j = 0; j < NW; ++j) {
-      wp[j][0] = reinterpret_cast<const uint4*>(a.w[j].codes + (size_t)r0 * (K / 8)) + 4 * c0 + t;
-      wp[j][1] = reinterpret_cast<const uint4*>(a.w[j].codes + (size_t)r1 * (K / 8)) + 4 * c0 + t;
-      sp[j] = a.w[j].scales + at;
-    }
+  auto point = [&](int i, int kt) {
+    const int group = cluster + i / NW * clusters, row0 = (group >> 3) * 128 + (group & 7) * 4 + (g & 3) + 32 * (g >> 2);
+    const MxWeights& w = a.w[NW == 2 ? i & 1 : 0];
+    const int at = 4 * (c0 + kt) + t;
+    wp0 = reinterpret_cast<const uint4*>(w.codes + (size_t)min(row0, a.N - 1) * (K / 8)) + at;
+    wp1 = reinterpret_cast<const uint4*>(w.codes + (size_t)min(row0 + 64, a.N - 1) * (K / 8)) + at;
+    sp = w.scales + ((size_t)(group >> 3) * KT + c0 + kt) * MX_TILE + (group & 7) * 64 + (lane & 3) * 16;
   };
 
-  uint4 wv[D][NW][2];
-  uint16_t sv[D][NW][2];
-  float acc[NW][MS][2];
-  const bool mine = t == (g & 3);
-  const uint4* xl = xs + (g >> 2) * 4 + t;
-  const int rounds = (groups + clusters * gcap - 1) / (clusters * gcap);  // as many for every cluster
+  const int soff = 1024 + (g & 3) * 16 + (g >> 2) * 4 + 2 * (t & 1);
+  // column g of the MMA's B: block g % 4 of x's row g / 4 (+ 2 s), read by lane t = g % 4; zeros elsewhere
+  const unsigned char* xl[MS];
+  int xstep[MS];
+#pragma unroll
+  for (int s = 0; s < MS; ++s) {
+    const bool live = t == (g & 3) && 2 * s + (g >> 2) < a.M;
+    xl[s] = live ? ring + SH::XAT + ((2 * s + (g >> 2)) * 4 + t) * 16 : smem + SH::RING;
+    xstep[s] = live ? SH::UNIT : 0;
+  }
+  for (int i = tid; i < SH::ZEROS / 16; i += MV_THREADS) zeros[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  // copies of x: 16 bytes (8 k) of row m, block b, quarter q at [q][m][b]
+  const int xc = lane & 15, xm = lane >> 4;
+  const int xto = SH::XAT + (((xc & 3) * MT + xm) * 4 + (xc >> 2)) * 16;
+  const __half* xp = a.x + (size_t)min(xm, a.M - 1) * K + c0 * 128 + xc * 8;
+  const int most = NW * ((groups + clusters - 1) / clusters), rounds = (most + gcap - 1) / gcap;  // alike in every cluster
   for (int round = 0; round < rounds; ++round) {
     const int g0 = round * gcap, ng = min(gcap, max(0, ngroups - g0)), units = ng * kc;
-    const int u0 = units * warp / MV_WARPS, u1 = units * (warp + 1) / MV_WARPS;
-    if (tid <= MV_WARPS) ubegin[tid] = units * tid / MV_WARPS;
+    const int nw = min(MV_WARPS, max(1, units));  // warps with work: unit u is warp (nw (u + 1) - 1) / units's
+    const int u0 = units * min(warp, nw) / nw, u1 = units * min(warp + 1, nw) / nw;
     int li = u0 / kc, lk = u0 - li * kc, lu = u0;  // next unit to load: group, tile
-    if (lu < u1) point(g0 + li);
+    if (lu < u1) point(g0 + li, lk);
     auto load = [&](int d) {
+      // (a group is committed for every unit, also past the last, so that the
+      // wait below counts units)
+      if (lu < u1) {
+        unsigned char* r = ring + d * SH::UNIT;
+        cp_async16(r + lane * 16, wp0);
+        cp_async16(r + 512 + lane * 16, wp1);
+        if (lane < 4) cp_async16(r + 1024 + lane * 16, sp);
 #pragma unroll
-      for (int j = 0; j < NW; ++j) {
-        wv[d][j][0] = ldg_stream(wp[j][0] + 4 * lk);
-        wv[d][j][1] = ldg_stream(wp[j][1] + 4 * lk);
-        const uint8_t* s = sp[j] + (size_t)lk * MX_TILE;
-        sv[d][j][0] = *reinterpret_cast<const uint16_t*>(s);
-        sv[d][j][1] = *reinterpret_cast<const uint16_t*>(s + 8);
+        for (int s = 0; s < MS; ++s)
+          if (2 * s + xm < a.M) cp_async16_ca(r + xto + s * 128, xp + (size_t)(2 * s) * K + lk * 128);
+        wp0 += 4;
+        wp1 += 4;
+        sp += MX_TILE;
       }
+      cp_async_commit();
       ++lu;
       if (++lk == kc) {
         lk = 0;
         ++li;
-        if (lu < u1) point(g0 + li);
+        if (lu < u1) point(g0 + li, 0);
       }
     };
     if (round == 0) {
       // the weights may come from the call just before: into L2 ahead of the wait, read behind it
       if (t == 0) {
 #pragma unroll
-        for (int d = 0; d < D; ++d)
+        for (int d = 0; d < 2 * D; d += 2)  // (128 bytes: two tiles)
           if (lu + d < u1 && lk + d < kc) {
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-              prefetch_l2(wp[j][0] + 4 * (lk + d));
-              prefetch_l2(wp[j][1] + 4 * (lk + d));
-            }
+            prefetch_l2(wp0 + 4 * d);
+            prefetch_l2(wp1 + 4 * d);
           }
       }
       pdl_wait_then_trigger();
+      W4_TRACE_WAITED();
     }
 #pragma unroll
-    for (int d = 0; d < D; ++d)
-      if (lu < u1) load(d);
-    if (round == 0) {
-      // 16 bytes (8 k) of x[m], block t, quarter q of tile kt at [kt][q][m][t]
-      for (int i = tid; i < kc * 16 * MT; i += MV_THREADS) {
-        const int m = i % MT, c = i / MT;
-        if (m < a.M)
-          cp_async16(&xs[(((c >> 4) * 4 + (c & 3)) * MT + m) * 4 + ((c >> 2) & 3)], a.x + (size_t)m * K + (c0 * 16 + c) * 8);
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-    }
-    __syncthreads();
+    for (int d = 0; d < D; ++d) load(d);
+    W4_TRACE_MARK(0);
 
-    int ci = u0 / kc, ck = u0 - ci * kc;  // the unit to add up
+    int ci = u0 / kc, ck = u0 - ci * kc, d = 0;  // the unit to add up
+    bool fresh = ck == 0;                          // from its group's first tile
+    float acc[MS][2];
 #pragma unroll
-    for (int j = 0; j < NW; ++j)
-#pragma unroll
-      for (int s = 0; s < MS; ++s) acc[j][s][0] = acc[j][s][1] = 0.f;
+    for (int s = 0; s < MS; ++s) acc[s][0] = acc[s][1] = 0.f;
+#pragma unroll 1
     for (int u = u0; u < u1;) {
+      float c[MS][4];
+      cp_async_wait<D - 1>();
+      __syncwarp();
+      const unsigned char* r = ring + d * SH::UNIT;
+      const uint4 w0 = *reinterpret_cast<const uint4*>(r + lane * 16);
+      const uint4 w1 = *reinterpret_cast<const uint4*>(r + 512 + lane * 16);
+      const float2 s0 = mv_scales(*reinterpret_cast<const uint16_t*>(r + soff));
+      const float2 s1 = mv_scales(*reinterpret_cast<const uint16_t*>(r + soff + 8));
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (u < u1) {
-          float c[NW][MS][4] = {};
+      for (int q = 0; q < 4; ++q) {
+        const uint4 v0 = mx_values(word_of(w0, q)), v1 = mx_values(word_of(w1, q));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint4 xv[MS];
-#pragma unroll
-            for (int s = 0; s < MS; ++s) {
-              xv[s] = make_uint4(0, 0, 0, 0);
-              if (mine && 2 * s + (g >> 2) < a.M) xv[s] = xl[((ck * 4 + q) * MT + 2 * s) * 4];
-            }
-#pragma unroll
-            for (int j = 0; j < NW; ++j) {
-              const uint4 v0 = mx_values(word_of(wv[d][j][0], q)), v1 = mx_values(word_of(wv[d][j][1], q));
-#pragma unroll
-              for (int s = 0; s < MS; ++s) {
-                mv_mma(c[j][s], v0.x, v1.x, v0.y, v1.y, xv[s].x, xv[s].y);
-                mv_mma(c[j][s], v0.z, v1.z, v0.w, v1.w, xv[s].z, xv[s].w);
-              }
-            }
-          }
-          // columns 2 t, 2 t + 1 of this lane: blocks 2 (t & 1) and the next of row m = t / 2
-#pragma unroll
-          for (int j = 0; j < NW; ++j) {
-            const float a0 = mv_scale(sv[d][j][0] & 255u), a1 = mv_scale(sv[d][j][0] >> 8);
-            const float b0 = mv_scale(sv[d][j][1] & 255u), b1 = mv_scale(sv[d][j][1] >> 8);
-#pragma unroll
-            for (int s = 0; s < MS; ++s) {
-              acc[j][s][0] = fmaf(a1, c[j][s][1], fmaf(a0, c[j][s][0], acc[j][s][0]));
-              acc[j][s][1] = fmaf(b1, c[j][s][3], fmaf(b0, c[j][s][2], acc[j][s][1]));
-            }
-          }
-          if (lu < u1) load(d);
-          ++u;
-          if (++ck == kc || u == u1) {
-            // a group's, or a piece's, end: piece (warp, group) is number group + warp
-            float* p = pieces + (ci + warp) * PIECE;
-#pragma unroll
-            for (int j = 0; j < NW; ++j)
-#pragma unroll
-              for (int s = 0; s < MS; ++s)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float v = acc[j][s][h] + __shfl_xor_sync(0xffffffffu, acc[j][s][h], 1);
-                  if (!(t & 1)) p[(j * MT + 2 * s + (t >> 1)) * MV_ROWS + g + 8 * h] = v;
-                  acc[j][s][h] = 0.f;
-                }
-            ck = 0;
-            ++ci;
-          }
+        for (int s = 0; s < MS; ++s) {
+          const uint4 xv = *reinterpret_cast<const uint4*>(xl[s] + d * xstep[s] + q * MT * 64);
+          if (q == 0) mv_mma<true>(c[s], v0.x, v1.x, v0.y, v1.y, xv.x, xv.y);
+          else mv_mma<false>(c[s], v0.x, v1.x, v0.y, v1.y, xv.x, xv.y);
+          mv_mma<false>(c[s], v0.z, v1.z, v0.w, v1.w, xv.z, xv.w);
         }
       }
-    }
-    __syncthreads();
-    // this CTA's sums, each group's pieces in the order of K
-    for (int i = tid; i < ng * PIECE; i += MV_THREADS) {
-      const int grp = i / PIECE, e = i % PIECE, ua = grp * kc, ub = ua + kc;
-      float v = 0.f;
+      // columns 2 t, 2 t + 1 of this lane: blocks 2 (t & 1) and the next of row m = t / 2
 #pragma unroll
-      for (int w = 0; w < MV_WARPS; ++w)
-        if (max(ubegin[w], ua) < min(ubegin[w + 1], ub)) v += pieces[(grp + w) * PIECE + e];
-      sums[i] = v;
+      for (int s = 0; s < MS; ++s) {
+        acc[s][0] = fmaf(s0.y, c[s][1], fmaf(s0.x, c[s][0], acc[s][0]));
+        acc[s][1] = fmaf(s1.y, c[s][3], fmaf(s1.x, c[s][2], acc[s][1]));
+      }
+      __syncwarp();  // (the scales are read by other lanes than copied them)
+      load(d);
+      d = d + 1 == D ? 0 : d + 1;
+      ++u;
+      if (++ck == kc || u == u1) {
+        // a group's, or a piece's, end: piece (warp, group) is number group + warp
+        float* p = pieces + (ci + warp) * PIECE;
+        if (lane == 0) {
+          if (fresh) first[ci] = warp;
+          if (ck == kc) last[ci] = warp;
+        }
+        fresh = true;
+#pragma unroll
+        for (int s = 0; s < MS; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float v = acc[s][h] + __shfl_xor_sync(0xffffffffu, acc[s][h], 1);
+            if (!(t & 1)) p[(2 * s + (t >> 1)) * MV_ROWS + g + 8 * h] = v;
+            acc[s][h] = 0.f;
+          }
+        ck = 0;
+        ++ci;
+      }
+    }
+    // this thread's first output, and what is added to it, asked for ahead of the join
+    struct Out {
+      bool live;
+      size_t at;
+      float add;
+    };
+    auto place_of = [&](int i) {
+      const int e = i % PIECE, m = e / MV_ROWS, r = e % MV_ROWS, pair = (i / PIECE << clog) + rank;
+      const int group = cluster + (g0 / NW + pair) * clusters;
+      const int n = (group >> 3) * 128 + (group & 7) * 4 + (r & 3) + 32 * (r >> 2);
+      Out o = {pair * NW < ng && m < a.M && n < a.N, (size_t)m * a.N + n, 0.f};
+      if (o.live && a.bias) o.add = __half2float(a.bias[n]);
+      if (o.live && a.residual) o.add += __half2float(a.residual[o.at]);
+      return o;
+    };
+    Out o = place_of(tid);
+    __syncthreads();
+    W4_TRACE_MARK(1);
+    // this CTA's sums, each group's pieces in the order of K
+    if (csize > 1) cluster_wait();  // every CTA of the cluster has started, and read its sums of the round before
+    for (int i = tid; i < ng * PIECE; i += MV_THREADS) {
+      const int grp = i / PIECE, e = i % PIECE;
+      float v = 0.f;
+      for (int w = first[grp]; w <= last[grp]; ++w) v += pieces[(grp + w) * PIECE + e];
+      // to the CTA of the cluster that joins this group (they take them in turn, gate and up together)
+      const int pair = grp / NW, owner = pair & (csize - 1), place = (pair - owner + rank) * NW + grp % NW;
+      if (csize == 1) sums[place * PIECE + e] = v;
+      else st_cluster(sums + place * PIECE + e, owner, v);
     }
     if (csize > 1) cluster_sync();
     else __syncthreads();
-    // the cluster's: its CTAs take the groups in turn
-    for (int i = tid; i < ng * MT * MV_ROWS; i += MV_THREADS) {
-      const int grp = i / (MT * MV_ROWS), e = i % (MT * MV_ROWS), m = e / MV_ROWS, r = e % MV_ROWS;
-      if (grp % csize != rank || m >= a.M) continue;
-      const int group = cluster + (g0 + grp) * clusters;
-      const int n = (group >> 3) * 128 + (group & 7) * 4 + (r & 3) + 32 * (r >> 2);
-      if (n >= a.N) continue;
-      const float* p = sums + grp * PIECE + e;
+    W4_TRACE_MARK(2);
+    for (int i = tid;;) {
+      if (!o.live) break;
+      const float* p = sums + (i / PIECE << clog) * NW * PIECE + i % PIECE;
       float v = 0.f, w = 0.f;
-      if (csize == 1) {
-        v = p[0];
-        if (NW == 2) w = p[MT * MV_ROWS];
-      } else {
-        for (int c = 0; c < csize; ++c) {
-          v += ld_cluster(p, c);
-          if (NW == 2) w += ld_cluster(p + MT * MV_ROWS, c);
-        }
+      for (int c = 0; c < csize; ++c) {
+        v += p[c * NW * PIECE];
+        if (NW == 2) w += p[c * NW * PIECE + PIECE];
       }
       if (NW == 2) v = v / (1.f + expf(-v)) * w;
-      if (a.bias) v += __half2float(a.bias[n]);
-      if (a.residual) v += __half2float(a.residual[(size_t)m * a.N + n]);
-      a.y[(size_t)m * a.N + n] = __float2half_rn(v);
+      a.y[o.at] = __float2half_rn(v + o.add);
+      o = place_of(i += MV_THREADS);
     }
-    // the sums are read, the pieces' and the sums' places are free
-    if (csize > 1) cluster_sync();
-    else if (round + 1 < rounds) __syncthreads();
+    if (round + 1 < rounds) {
+      if (csize > 1) cluster_arrive();
+      __syncthreads();
+    }
   }
 }
 
 // How a call is split: clusters of csize CTAs over K, `clusters` of them.
 struct MvPlan {
-  int groups, csize, clusters, gcap;
+  int groups, clog, clusters, gcap;
   size_t smem;
 };
 
@@ -292,14 +323,14 @@ constexpr double MV_JOIN = 16;
 
 template <int NW, int MS>
 static MvPlan mv_plan(int N, int K) {
-  using SH = MvShape<NW, MS>;
+  using SH = MvShape<MS>;
   static PerDeviceOnce once;
   static int room[64][4];  // clusters of 1, 2, 4, 8 CTAs that the device holds at once
   const int dev = device_index() & 63;
   once_per_device(once, [&] {
-    cudaFuncSetAttribute(w4pg_mxfp4_matvec<NW, MS>, cudaFuncAttributeMaxDynamicSharedMemorySize, MV_SMEM);
+    cudaFuncSetAttribute(w4pg_mxfp4_matvec<NW, MS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SH::smem(MV_GROUPS));
     room[dev][0] = num_sms();
-    for (int l = 1; l < 4; ++l) room[dev][l] = mv_max_clusters<NW, MS>(1 << l, MV_SMEM);
+    for (int l = 1; l < 4; ++l) room[dev][l] = mv_max_clusters<NW, MS>(1 << l, SH::smem(MV_GROUPS));
   });
   const int groups = N / 128 * 8 + std::min(8, (N % 128 + 3) / 4);  // (those of the last tile that have rows)
   const int ktiles = K / 128;
@@ -308,14 +339,12 @@ static MvPlan mv_plan(int N, int K) {
   for (int l = 0; l < 4; ++l) {
     const int c = 1 << l;
     if (c > ktiles && l > 0) break;
-    const int clusters = std::min(groups, room[dev][l]);
-    const int n = (groups + clusters - 1) / clusters, kc = (ktiles + c - 1) / c, gcap = std::min(n, MV_GROUPS);
-    const size_t smem = SH::smem(kc, gcap);
-    if (smem > MV_SMEM) continue;
-    const double v = (double)n * kc + (l ? MV_JOIN : 0);
-    if (best.csize == 0 || v < cost) {
+    const int clusters = std::min(groups, std::min(room[dev][l], num_sms() / c));
+    const int n = NW * ((groups + clusters - 1) / clusters), kc = (ktiles + c - 1) / c, gcap = std::min(n, MV_GROUPS);
+        const double v = (double)n * kc + (l ? MV_JOIN : 0);
+    if (best.groups == 0 || v < cost) {
       cost = v;
-      best = {groups, c, clusters, gcap, smem};
+      best = {groups, l, clusters, gcap, SH::smem(gcap)};
     }
   }
   return best;
@@ -325,7 +354,7 @@ template <int NW, int MS>
 static int mv_launch(const MxArgs& a, cudaStream_t s) {
   const MvPlan p = mv_plan<NW, MS>(a.N, a.K);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.clusters * p.csize);
+  cfg.gridDim = dim3(p.clusters << p.clog);
   cfg.blockDim = dim3(MV_THREADS);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = s;
@@ -333,11 +362,11 @@ static int mv_launch(const MxArgs& a, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.csize;
+  attr[1].val.clusterDim.x = 1 << p.clog;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = p.csize > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, w4pg_mxfp4_matvec<NW, MS>, a, p.csize, p.groups, p.gcap);
+  cfg.numAttrs = p.clog > 0 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, w4pg_mxfp4_matvec<NW, MS>, a, p.clog, p.groups, p.gcap);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "mxfp4 product launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }
