@@ -46,10 +46,6 @@ __device__ __forceinline__ void mv_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// 16 bytes global -> shared through L1 (x: the next groups read it again)
-__device__ __forceinline__ void cp_async16_ca(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int q) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; }
 
@@ -61,6 +57,24 @@ __device__ __forceinline__ void st_cluster(float* p, int rank, float v) {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cpa16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// through L1: x, which the next groups read again
+__device__ __forceinline__ void cpa16_ca(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 
 // two scale bytes as fp32 (255: NaN)
 __device__ __forceinline__ float2 mv_scales(uint16_t bytes) {
@@ -100,7 +114,7 @@ __global__ void __launch_bounds__(MV_THREADS, 2)
   const int csize = 1 << clog, rank = blockIdx.x & (csize - 1), cluster = blockIdx.x >> clog, clusters = gridDim.x >> clog;
   const int K = a.K, KT = K / 128;
   const int c0 = KT * rank >> clog, kc = (KT * (rank + 1) >> clog) - c0;  // this CTA's scale tiles along K
-  unsigned char* ring = smem + warp * D * SH::UNIT;
+  const uint32_t ring = smem_u32(smem) + warp * D * SH::UNIT;
   uint4* zeros = reinterpret_cast<uint4*>(smem + SH::RING);
   float* sums = reinterpret_cast<float*>(smem + SH::RING + SH::ZEROS);
   float* pieces = sums + (gcap + 16) * PIECE;
@@ -121,58 +135,64 @@ __global__ void __launch_bounds__(MV_THREADS, 2)
     sp = w.scales + ((size_t)(group >> 3) * KT + c0 + kt) * MX_TILE + (group & 7) * 64 + (lane & 3) * 16;
   };
 
-  const int soff = 1024 + (g & 3) * 16 + (g >> 2) * 4 + 2 * (t & 1);
-  // column g of the MMA's B: block g % 4 of x's row g / 4 (+ 2 s), read by lane t = g % 4; zeros elsewhere
-  const unsigned char* xl[MS];
-  int xstep[MS];
+  // this lane's places in a unit: its codes, the two rows' scales, x.  Column g of
+  // the MMA's B is block g % 4 of x's row g / 4 (+ 2 s), read by lane t = g % 4; zeros elsewhere
+  const uint32_t rl = ring + lane * 16, rs = ring + 1024 + (g & 3) * 16 + (g >> 2) * 4 + 2 * (t & 1);
+  uint32_t rx[MS], xstep[MS];
 #pragma unroll
   for (int s = 0; s < MS; ++s) {
     const bool live = t == (g & 3) && 2 * s + (g >> 2) < a.M;
-    xl[s] = live ? ring + SH::XAT + ((2 * s + (g >> 2)) * 4 + t) * 16 : smem + SH::RING;
+    rx[s] = live ? ring + SH::XAT + ((2 * s + (g >> 2)) * 4 + t) * 16 : smem_u32(zeros);
     xstep[s] = live ? SH::UNIT : 0;
   }
   for (int i = tid; i < SH::ZEROS / 16; i += MV_THREADS) zeros[i] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   // copies of x: 16 bytes (8 k) of row m, block b, quarter q at [q][m][b]
   const int xc = lane & 15, xm = lane >> 4;
-  const int xto = SH::XAT + (((xc & 3) * MT + xm) * 4 + (xc >> 2)) * 16;
-  const __half* xp = a.x + (size_t)min(xm, a.M - 1) * K + c0 * 128 + xc * 8;
+  const uint32_t xto = ring + SH::XAT + (((xc & 3) * MT + xm) * 4 + (xc >> 2)) * 16;
+  const __half* const x0 = a.x + (size_t)min(xm, a.M - 1) * K + c0 * 128 + xc * 8;
+  const size_t xrows = (size_t)2 * K;  // from one set's rows to the next one's
+  bool xlive[MS];
+#pragma unroll
+  for (int s = 0; s < MS; ++s) xlive[s] = 2 * s + xm < a.M;
   const int most = NW * ((groups + clusters - 1) / clusters), rounds = (most + gcap - 1) / gcap;  // alike in every cluster
   for (int round = 0; round < rounds; ++round) {
     const int g0 = round * gcap, ng = min(gcap, max(0, ngroups - g0)), units = ng * kc;
     const int nw = min(MV_WARPS, max(1, units));  // warps with work: unit u is warp (nw (u + 1) - 1) / units's
     const int u0 = units * min(warp, nw) / nw, u1 = units * min(warp + 1, nw) / nw;
-    int li = u0 / kc, lk = u0 - li * kc, lu = u0;  // next unit to load: group, tile
-    if (lu < u1) point(g0 + li, lk);
+    // next unit to load: its group, the units until the group's or this warp's end, those behind
+    int li = u0 / kc, left = min(kc - (u0 - li * kc), u1 - u0), rest = u1 - u0 - left;
+    const __half* xp = x0 + (u0 - li * kc) * 128;
+    if (left > 0) point(g0 + li, u0 - li * kc);
     auto load = [&](int d) {
       // (a group is committed for every unit, also past the last, so that the
       // wait below counts units)
-      if (lu < u1) {
-        unsigned char* r = ring + d * SH::UNIT;
-        cp_async16(r + lane * 16, wp0);
-        cp_async16(r + 512 + lane * 16, wp1);
-        if (lane < 4) cp_async16(r + 1024 + lane * 16, sp);
+      if (left > 0) {
+        cpa16(rl + d * SH::UNIT, wp0);
+        cpa16(rl + d * SH::UNIT + 512, wp1);
+        if (lane < 4) cpa16(rl + d * SH::UNIT + 1024, sp);
 #pragma unroll
         for (int s = 0; s < MS; ++s)
-          if (2 * s + xm < a.M) cp_async16_ca(r + xto + s * 128, xp + (size_t)(2 * s) * K + lk * 128);
+          if (xlive[s]) cpa16_ca(xto + d * SH::UNIT + s * 128, xp + s * xrows);
         wp0 += 4;
         wp1 += 4;
         sp += MX_TILE;
+        xp += 128;
+        if (--left == 0 && rest > 0) {
+          left = min(kc, rest);
+          rest -= left;
+          xp = x0;
+          point(g0 + ++li, 0);
+        }
       }
       cp_async_commit();
-      ++lu;
-      if (++lk == kc) {
-        lk = 0;
-        ++li;
-        if (lu < u1) point(g0 + li, 0);
-      }
     };
     if (round == 0) {
       // the weights may come from the call just before: into L2 ahead of the wait, read behind it
       if (t == 0) {
 #pragma unroll
         for (int d = 0; d < 2 * D; d += 2)  // (128 bytes: two tiles)
-          if (lu + d < u1 && lk + d < kc) {
+          if (d < left) {
             prefetch_l2(wp0 + 4 * d);
             prefetch_l2(wp1 + 4 * d);
           }
@@ -184,60 +204,61 @@ __global__ void __launch_bounds__(MV_THREADS, 2)
     for (int d = 0; d < D; ++d) load(d);
     W4_TRACE_MARK(0);
 
-    int ci = u0 / kc, ck = u0 - ci * kc, d = 0;  // the unit to add up
-    bool fresh = ck == 0;                          // from its group's first tile
+    int ci = u0 / kc, togo = u1 - u0;                  // the unit to add up: its group
+    int ck = kc - (u0 - ci * kc);                      // units until the group's end
+    bool fresh = ck == kc;                             // from its group's first tile
     float acc[MS][2];
 #pragma unroll
     for (int s = 0; s < MS; ++s) acc[s][0] = acc[s][1] = 0.f;
 #pragma unroll 1
-    for (int u = u0; u < u1;) {
-      float c[MS][4];
-      cp_async_wait<D - 1>();
-      __syncwarp();
-      const unsigned char* r = ring + d * SH::UNIT;
-      const uint4 w0 = *reinterpret_cast<const uint4*>(r + lane * 16);
-      const uint4 w1 = *reinterpret_cast<const uint4*>(r + 512 + lane * 16);
-      const float2 s0 = mv_scales(*reinterpret_cast<const uint16_t*>(r + soff));
-      const float2 s1 = mv_scales(*reinterpret_cast<const uint16_t*>(r + soff + 8));
+    while (togo > 0) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 v0 = mx_values(word_of(w0, q)), v1 = mx_values(word_of(w1, q));
+      for (int d = 0; d < D; ++d) {
+        float c[MS][4];
+        cp_async_wait<D - 1>();
+        __syncwarp();
+        const uint4 w0 = lds128(rl + d * SH::UNIT), w1 = lds128(rl + d * SH::UNIT + 512);
+        const float2 s0 = mv_scales(lds16(rs + d * SH::UNIT)), s1 = mv_scales(lds16(rs + d * SH::UNIT + 8));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 v0 = mx_values(word_of(w0, q)), v1 = mx_values(word_of(w1, q));
+#pragma unroll
+          for (int s = 0; s < MS; ++s) {
+            const uint4 xv = lds128(rx[s] + d * xstep[s] + q * MT * 64);
+            if (q == 0) mv_mma<true>(c[s], v0.x, v1.x, v0.y, v1.y, xv.x, xv.y);
+            else mv_mma<false>(c[s], v0.x, v1.x, v0.y, v1.y, xv.x, xv.y);
+            mv_mma<false>(c[s], v0.z, v1.z, v0.w, v1.w, xv.z, xv.w);
+          }
+        }
+        // columns 2 t, 2 t + 1 of this lane: blocks 2 (t & 1) and the next of row m = t / 2
 #pragma unroll
         for (int s = 0; s < MS; ++s) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(xl[s] + d * xstep[s] + q * MT * 64);
-          if (q == 0) mv_mma<true>(c[s], v0.x, v1.x, v0.y, v1.y, xv.x, xv.y);
-          else mv_mma<false>(c[s], v0.x, v1.x, v0.y, v1.y, xv.x, xv.y);
-          mv_mma<false>(c[s], v0.z, v1.z, v0.w, v1.w, xv.z, xv.w);
+          acc[s][0] = fmaf(s0.y, c[s][1], fmaf(s0.x, c[s][0], acc[s][0]));
+          acc[s][1] = fmaf(s1.y, c[s][3], fmaf(s1.x, c[s][2], acc[s][1]));
         }
-      }
-      // columns 2 t, 2 t + 1 of this lane: blocks 2 (t & 1) and the next of row m = t / 2
-#pragma unroll
-      for (int s = 0; s < MS; ++s) {
-        acc[s][0] = fmaf(s0.y, c[s][1], fmaf(s0.x, c[s][0], acc[s][0]));
-        acc[s][1] = fmaf(s1.y, c[s][3], fmaf(s1.x, c[s][2], acc[s][1]));
-      }
-      __syncwarp();  // (the scales are read by other lanes than copied them)
-      load(d);
-      d = d + 1 == D ? 0 : d + 1;
-      ++u;
-      if (++ck == kc || u == u1) {
-        // a group's, or a piece's, end: piece (warp, group) is number group + warp
-        float* p = pieces + (ci + warp) * PIECE;
-        if (lane == 0) {
-          if (fresh) first[ci] = warp;
-          if (ck == kc) last[ci] = warp;
-        }
-        fresh = true;
-#pragma unroll
-        for (int s = 0; s < MS; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float v = acc[s][h] + __shfl_xor_sync(0xffffffffu, acc[s][h], 1);
-            if (!(t & 1)) p[(2 * s + (t >> 1)) * MV_ROWS + g + 8 * h] = v;
-            acc[s][h] = 0.f;
+        __syncwarp();  // (the scales are read by other lanes than copied them)
+        load(d);
+        --togo;
+        if (--ck == 0 || togo == 0) {
+          // a group's, or a piece's, end: piece (warp, group) is number group + warp
+          float* p = pieces + (ci + warp) * PIECE;
+          if (lane == 0) {
+            if (fresh) first[ci] = warp;
+            if (ck == 0) last[ci] = warp;
           }
-        ck = 0;
-        ++ci;
+          fresh = true;
+#pragma unroll
+          for (int s = 0; s < MS; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float v = acc[s][h] + __shfl_xor_sync(0xffffffffu, acc[s][h], 1);
+              if (!(t & 1)) p[(2 * s + (t >> 1)) * MV_ROWS + g + 8 * h] = v;
+              acc[s][h] = 0.f;
+            }
+          ck = kc;
+          ++ci;
+          if (togo == 0) break;
+        }
       }
     }
     // this thread's first output, and what is added to it, asked for ahead of the join
