@@ -75,5 +75,7 @@ struct MxArgs {
 };
 bool mxfp4_matvec_serves(int M, int K);
 int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s);
+int launch_mxfp4_a16(const MxArgs& a, bool silu, cudaStream_t s);
+size_t mxfp4_a16_workspace(int M, int N, int K, bool silu);
 
 }  // namespace w4

@@ -1,0 +1,386 @@
+// mxfp4_a16.cu -- products of many fp16 rows (a decode batch, a prompt) with MXFP4
+// weights on the 5th-generation tensor cores.
+//
+// y[m][n] = sum_k x[m][k] w[n][k], w = c 2^(b - 127) an fp16 number exactly, so the
+// MMA's operands are x as it is and the weights expanded: the expander warps
+// convert codes (hardware E2M1 to fp16 pairs), apply the block's scale with one
+// packed multiplication, and store the tile in tensor memory, from which the MMA
+// takes its A operand (weights as rows: D[n][m], 128 lanes x NC columns, fp32).
+// The whole of K is summed in tensor memory; nothing is read out before the end.
+//
+// A CTA's tile is 2 x 128 weight rows (two neighbouring tiles, or gate and up) x
+// NC rows of x, so that a stage (128 k) of x, its largest operand, serves 256
+// weight rows: at NC = 128 49 KB for 1024 cycles of MMAs.  NC = 32 and 64 are for
+// decode batches and short prompts, where the weights' bytes decide.
+//
+// Roles (18 warps), meeting only at mbarriers: a producer lane copies codes,
+// scales and x into a ring; 16 expander warps (lane quadrant, tile, half of the
+// stage's k) fill one of NAB tensor-memory A buffers; one warp issues the MMAs;
+// the expander warps run the epilogue.  Tiles are dealt by mt_deal: the last
+// round's are split along K, their fp32 parts meet in the workspace, and the
+// last part to arrive adds them in order.
+#include "mxfp4_tc.cuh"
+
+namespace w4 {
+
+constexpr int MA_K = 128;                    // k of a stage: one scale tile's width
+constexpr int MA_EXP = 16;                   // expander warps
+constexpr int MA_THREADS = 64 + 32 * MA_EXP;
+constexpr uint32_t MA_W = 128 * MA_K / 2;    // bytes of a tile's codes per stage
+
+template <int NC>
+struct MaShape {
+  static constexpr uint32_t XHALF = NC * 128;                         // 64 k of x, 128-byte rows
+  static constexpr uint32_t WAT = 2 * XHALF, SAT = WAT + 2 * MA_W;    // a slot: x, codes, scales
+  static constexpr uint32_t SLOT = SAT + 2 * MX_TILE;
+  static constexpr int S = 204800 / SLOT;
+  static constexpr size_t SMEM = S * SLOT + 1024;
+  static constexpr int NAB = (512 - 2 * NC) / 128 > 3 ? 3 : (512 - 2 * NC) / 128;
+  static constexpr int TA = 2 * NC;                                   // tensor memory: sums, then A buffers
+  static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(NC >> 3) << 17) | ((128u >> 4) << 24);
+  static_assert(SLOT % 1024 == 0 && NAB >= 2 && S >= 4, "swizzled tiles start on 1024-byte boundaries");
+};
+
+struct MaArgs {
+  MxArgs a;
+  int silu, mtiles, ntiles, whole, split, items;   // ntiles: of 128 weight rows; items as mt_deal
+  float* parts;
+  unsigned int* tickets;
+  CUtensorMap tm_w[2], tm_x;
+};
+
+template <int NC>
+__global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_constant__ MaArgs p) {
+  using SH = MaShape<NC>;
+  constexpr int S = SH::S, NAB = SH::NAB;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const unsigned char* ringp = smem_raw + (ring - smem_u32(smem_raw));
+  __shared__ __align__(8) uint64_t full[S], empty[S], afull[NAB], aempty[NAB], dfull, dempty, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_last;
+  __shared__ volatile int s_fail;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int K = p.a.K, stages = K / MA_K, KT = K / 128;
+
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], MA_EXP + 1);
+    }
+    for (int i = 0; i < NAB; ++i) {
+      mbar_init(&afull[i], MA_EXP);
+      mbar_init(&aempty[i], 1);
+    }
+    mbar_init(&dfull, 1);
+    mbar_init(&dempty, MA_EXP);
+    mbar_init(&drain, 1);
+    s_fail = 0;
+    fence_mbar_init();
+  }
+  mt_fence_before();
+  __syncthreads();
+  mt_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // item -> its m tile, first 128-row weight tile (and the second's distance), part, k range
+  auto item = [&](int i, int* mt, int* nt, int* part, int* k0, int* k1) {
+    int tile;
+    mt_item(i, p.whole, p.split, stages, &tile, part, k0, k1);
+    *mt = tile % p.mtiles;
+    *nt = tile / p.mtiles * (p.silu ? 1 : 2);
+    return tile;
+  };
+
+  if (warp == 0) {
+    // ---- producer ----
+    if (lane == 0) {
+      int mt, nt, part, k0, k1;
+      if (blockIdx.x < p.items) {
+        // weights may come from the call just before: into L2 ahead of the wait, read behind it
+        item(blockIdx.x, &mt, &nt, &part, &k0, &k1);
+        for (int k = k0; k < min(k1, k0 + S); ++k)
+          for (int g = 0; g < 2; ++g) mt_prefetch_2d(&p.tm_w[p.silu ? g : 0], k * (MA_K / 8), (p.silu ? nt : nt + g) * 128);
+      }
+      pdl_wait_then_trigger();
+      uint32_t s = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+        item(i, &mt, &nt, &part, &k0, &k1);
+        for (int k = k0; k < k1; ++k, ++s) {
+          const int slot = s % S;
+          if (s >= S && !(ok = mt_wait(&empty[slot], (s / S - 1) & 1, &s_fail))) break;
+          const uint32_t sl = ring + slot * SH::SLOT;
+          mbar_arrive_expect_tx(&full[slot], SH::SLOT);
+          for (int g = 0; g < 2; ++g) {
+            const int t = p.silu ? nt : nt + g;  // (past the last tile: zeros, under the last tile's scales)
+            mt_load_2d(sl + SH::WAT + g * MA_W, &p.tm_w[p.silu ? g : 0], k * (MA_K / 8), t * 128, &full[slot]);
+            mt_load(sl + SH::SAT + g * MX_TILE, p.a.w[p.silu ? g : 0].scales + ((size_t)min(t, p.ntiles - 1) * KT + k) * MX_TILE,
+                    MX_TILE, &full[slot]);
+          }
+          for (int h = 0; h < 2; ++h) mt_load_2d(sl + h * SH::XHALF, &p.tm_x, k * MA_K + h * 64, mt * NC, &full[slot]);
+        }
+      }
+      // shared memory is given back only when the copies into it are done
+      for (uint32_t i = s > S ? s - S : 0; i < s && s_fail; ++i) (void)mt_wait(&full[i % S], (i / S) & 1, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA issue ----
+    pdl_wait_then_trigger();
+    uint32_t s = 0, n = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, ++n) {
+      int mt, nt, part, k0, k1;
+      item(i, &mt, &nt, &part, &k0, &k1);
+      if (n > 0) ok = __all_sync(0xffffffffu, mt_wait(&dempty, (n - 1) & 1, &s_fail));
+      for (int k = k0; k < k1 && ok; ++k, ++s) {
+        const int slot = s % S, ab = s % NAB;
+        ok = mt_wait(&full[slot], (s / S) & 1, &s_fail) && mt_wait(&afull[ab], (s / NAB) & 1, &s_fail);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        mt_fence_after();
+        if (lane == 0) {
+          const uint64_t b0 = mt_desc(ring + slot * SH::SLOT), b1 = mt_desc(ring + slot * SH::SLOT + SH::XHALF);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int kk = 0; kk < MA_K / 16; ++kk) {
+              const uint64_t b = (kk < 4 ? b0 : b1) + (uint64_t)((kk & 3) * 2);
+              const uint32_t at = tmem + SH::TA + (uint32_t)((ab * 2 + g) * 64 + kk * 8);
+              asm volatile(
+                  "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem + (uint32_t)(g * NC)),
+                  "r"(at), "l"(b), "r"(SH::IDESC), "r"(k > k0 || kk > 0 ? 1u : 0u)
+                  : "memory");
+            }
+          mt_commit(&empty[slot]);
+          mt_commit(&aempty[ab]);
+          if (k == k1 - 1) mt_commit(&dfull);
+        }
+        __syncwarp();
+      }
+    }
+    // tensor memory is freed only when every MMA issued is done, whatever happened elsewhere
+    if (s > 0) {
+      if (lane == 0) mt_commit(&drain);
+      __syncwarp();
+      (void)mt_wait(&drain, 0, nullptr);
+    }
+  } else {
+    // ---- expanders and epilogue ----
+    pdl_wait_then_trigger();
+    const int e = warp - 2, quad = warp & 3, g = (e >> 2) & 1, h = e >> 3;
+    const int row = 32 * quad + lane;  // of the tile; the tensor-memory lane
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    uint32_t s = 0, n = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, ++n) {
+      int mt, nt, part, k0, k1;
+      const int tile = item(i, &mt, &nt, &part, &k0, &k1);
+      for (int k = k0; k < k1; ++k, ++s) {
+        const int slot = s % S, ab = s % NAB;
+        ok = mt_wait(&full[slot], (s / S) & 1, &s_fail);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        // 32 bytes of this row (chunks swizzled: c at c ^ (row / 2) % 4), the two scales
+        const unsigned char* w = ringp + slot * SH::SLOT + SH::WAT + g * MA_W + row * 64;
+        const int sw = (row >> 1) & 3;
+        const uint4 c0 = *reinterpret_cast<const uint4*>(w + (((2 * h) ^ sw) << 4));
+        const uint4 c1 = *reinterpret_cast<const uint4*>(w + (((2 * h + 1) ^ sw) << 4));
+        const uint16_t sc = *reinterpret_cast<const uint16_t*>(ringp + slot * SH::SLOT + SH::SAT + g * MX_TILE + lane * 16 +
+                                                               quad * 4 + 2 * h);
+        const uint32_t s0 = mx_scale_h2(sc & 255u), s1 = mx_scale_h2((uint32_t)sc >> 8);
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4& c = j < 4 ? c0 : c1;
+          const uint4 f = mx_values((j & 3) == 0 ? c.x : (j & 3) == 1 ? c.y : (j & 3) == 2 ? c.z : c.w);
+          const uint32_t sj = j < 4 ? s0 : s1;
+          v[4 * j] = hmul2_u32(f.x, sj);
+          v[4 * j + 1] = hmul2_u32(f.y, sj);
+          v[4 * j + 2] = hmul2_u32(f.z, sj);
+          v[4 * j + 3] = hmul2_u32(f.w, sj);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        if (s >= NAB) ok = mt_wait(&aempty[ab], (s / NAB - 1) & 1, &s_fail);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        mt_fence_after();
+        const uint32_t ta = lanes + SH::TA + (uint32_t)((ab * 2 + g) * 64 + h * 32);
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+            "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta),
+            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+            "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+            "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+            "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+            : "memory");
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        mt_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&afull[ab]);
+      }
+      if (!ok) break;
+      // epilogue: warp e has columns [e / 4 * NC / 4, ..) of both tiles' rows of its quadrant
+      ok = __all_sync(0xffffffffu, mt_wait(&dfull, n & 1, &s_fail));
+      if (!ok) break;
+      mt_fence_after();
+      constexpr int CW = NC / 4;
+      const int col0 = (e >> 2) * CW, M = p.a.M, N = p.a.N;
+      uint32_t acc[2][CW];
+#pragma unroll
+      for (int gg = 0; gg < 2; ++gg)
+#pragma unroll
+        for (int c = 0; c < CW; c += 8)
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                       : "=r"(acc[gg][c]), "=r"(acc[gg][c + 1]), "=r"(acc[gg][c + 2]), "=r"(acc[gg][c + 3]),
+                         "=r"(acc[gg][c + 4]), "=r"(acc[gg][c + 5]), "=r"(acc[gg][c + 6]), "=r"(acc[gg][c + 7])
+                       : "r"(lanes + (uint32_t)(gg * NC + col0 + c)));
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      mt_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&dempty);
+      const int m0 = mt * NC + col0;
+      bool finish = true;
+      if (i >= p.whole && p.split > 1) {
+        const int t = tile - p.whole;
+        float* mine = p.parts + ((size_t)t * p.split + part) * (2 * NC * 128);
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg)
+#pragma unroll
+          for (int c = 0; c < CW; ++c)
+            if (m0 + c < M) mine[(gg * NC + col0 + c) * 128 + row] = __uint_as_float(acc[gg][c]);
+        __threadfence();
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * MA_EXP) : "memory");
+        if (e == 0 && lane == 0) s_last = atomicAdd(&p.tickets[t], 1u) == (unsigned int)(p.split - 1);
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * MA_EXP) : "memory");
+        finish = s_last;
+        if (finish) {
+          __threadfence();
+          if (e == 0 && lane == 0) p.tickets[t] = 0u;
+          const float* all = p.parts + (size_t)t * p.split * (2 * NC * 128);
+#pragma unroll
+          for (int gg = 0; gg < 2; ++gg)
+#pragma unroll
+            for (int c = 0; c < CW; ++c) acc[gg][c] = 0u;  // (0.f: its own part is among them)
+          for (int q = 0; q < p.split; ++q)
+#pragma unroll
+            for (int gg = 0; gg < 2; ++gg)
+#pragma unroll
+              for (int c = 0; c < CW; ++c)
+                if (m0 + c < M)
+                  acc[gg][c] = __float_as_uint(
+                      __uint_as_float(acc[gg][c]) +
+                      __ldcg(&all[(size_t)q * (2 * NC * 128) + (gg * NC + col0 + c) * 128 + row]));
+        }
+      }
+      if (!finish) continue;
+#pragma unroll
+      for (int gg = 0; gg < 2; ++gg) {
+        if (p.silu && gg) break;
+        const int nn = (nt + gg) * 128 + row;
+        if (nn >= N) break;
+        const float bias = p.a.bias ? __half2float(p.a.bias[nn]) : 0.f;
+#pragma unroll
+        for (int c = 0; c < CW; ++c) {
+          if (m0 + c >= M) break;
+          float v = __uint_as_float(acc[gg][c]);
+          if (p.silu) v = v / (1.f + expf(-v)) * __uint_as_float(acc[1][c]);
+          const size_t at = (size_t)(m0 + c) * N + nn;
+          v += bias;
+          if (p.a.residual) v += __half2float(p.a.residual[at]);
+          p.a.y[at] = __float2half_rn(v);
+        }
+      }
+    }
+  }
+  mt_fence_before();
+  __syncthreads();
+  if (s_fail && tid == 0 && p.a.err_flag) atomicOr(p.a.err_flag, 2);
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem_slot) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+bool mt_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
+            uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw) {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {inner, rows}, strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_inner, box_rows}, es[2] = {1, 1};
+  return enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int ma_cols(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+static int ma_tiles(int M, int N, bool silu) {
+  const int nc = ma_cols(M), nt = (N + 127) / 128;
+  return (M + nc - 1) / nc * (silu ? nt : (nt + 1) / 2);
+}
+constexpr int MA_SPLIT = 16;
+
+// the deal for these sizes with room for `bytes` of workspace
+static MtDeal ma_deal(int M, int N, int K, bool silu, size_t bytes, int slots) {
+  const size_t part = (size_t)2 * 128 * ma_cols(M) * 4;
+  for (int most = MA_SPLIT; most > 1; --most) {
+    const MtDeal d = mt_deal(ma_tiles(M, N, silu), K / MA_K, slots, most);
+    const int over = d.items == d.whole ? 0 : (d.items - d.whole) / d.split;
+    if (over <= (int)(TC_TICKET_BYTES / 4) && (over == 0 || TC_TICKET_BYTES + (size_t)over * d.split * part <= bytes)) return d;
+  }
+  return mt_deal(ma_tiles(M, N, silu), K / MA_K, slots, 1);
+}
+
+size_t mxfp4_a16_workspace(int M, int N, int K, bool silu) {
+  // for the split of a GB300's 152 SMs, so that it can be asked for where there is no GPU
+  const MtDeal d = ma_deal(M, N, K, silu, ~(size_t)0, ATW_SMS);
+  return TC_TICKET_BYTES + (size_t)(d.items - d.whole) * 2 * 128 * ma_cols(M) * 4;
+}
+
+template <int NC>
+static int ma_launch(MaArgs& p, int slots, cudaStream_t s) {
+  using SH = MaShape<NC>;
+  static PerDeviceOnce once;
+  once_per_device(once, [] {
+    cudaFuncSetAttribute(w4pg_mxfp4_a16<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SH::SMEM);
+  });
+  const MxArgs& a = p.a;
+  bool ok = mt_map(&p.tm_x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.x, a.K, a.M, (uint64_t)a.K * 2, 64, NC,
+                   CU_TENSOR_MAP_SWIZZLE_128B);
+  for (int g = 0; g < (p.silu ? 2 : 1); ++g)
+    ok = ok && mt_map(&p.tm_w[g], CU_TENSOR_MAP_DATA_TYPE_UINT32, a.w[g].codes, a.K / 8, a.N, (uint64_t)a.K / 2, MA_K / 8, 128,
+                      CU_TENSOR_MAP_SWIZZLE_64B);
+  if (!ok) return set_error(W4A16_ERR_CUDA, "mxfp4 product: no tensor maps for the operands");
+  const cudaError_t e = launch_pdl(w4pg_mxfp4_a16<NC>, dim3(std::min(p.items, slots)), dim3(MA_THREADS), SH::SMEM, s, p);
+  if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "mxfp4 product launch: %s", cudaGetErrorString(e));
+  return W4A16_OK;
+}
+
+int launch_mxfp4_a16(const MxArgs& a, bool silu, cudaStream_t s) {
+  MaArgs p = {};
+  const int nc = ma_cols(a.M), slots = num_sms();
+  const MtDeal d = ma_deal(a.M, a.N, a.K, silu, a.workspace ? a.workspace_bytes : 0, slots);
+  p.a = a;
+  p.silu = silu;
+  p.mtiles = (a.M + nc - 1) / nc;
+  p.ntiles = (a.N + 127) / 128;
+  p.whole = d.whole;
+  p.split = d.split;
+  p.items = d.items;
+  p.tickets = static_cast<unsigned int*>(a.workspace);
+  if (d.split > 1) p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + TC_TICKET_BYTES);
+  return nc == 32 ? ma_launch<32>(p, slots, s) : nc == 64 ? ma_launch<64>(p, slots, s) : ma_launch<128>(p, slots, s);
+}
+
+}  // namespace w4

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(256) w4pg_mxfp4_tile(const MxArgs a) {
 
 static int launch_mxfp4(const MxArgs& a, bool silu, cudaStream_t s) {
   if (a.x && mxfp4_matvec_serves(a.M, a.K)) return launch_mxfp4_matvec(a, silu, s);
+  if (a.x) return launch_mxfp4_a16(a, silu, s);
   const dim3 grid((a.N + MXS_N - 1) / MXS_N, (a.M + MXS_M - 1) / MXS_M);
   const cudaError_t e = silu ? launch_pdl(w4pg_mxfp4_tile<true>, grid, dim3(256), 0, s, a)
                              : launch_pdl(w4pg_mxfp4_tile<false>, grid, dim3(256), 0, s, a);
@@ -131,7 +132,10 @@ static int mx_product_checks(const char* what, const MxArgs& a) {
   return W4A16_OK;
 }
 
-extern "C" size_t w4a16_gemm_mxfp4_workspace_size(int M, int K, int N, int silu) { return 256; }
+extern "C" size_t w4a16_gemm_mxfp4_workspace_size(int M, int K, int N, int silu) {
+  if (M < 1 || K < 128 || N < 1) return 0;
+  return mxfp4_matvec_serves(M, K) ? 256 : mxfp4_a16_workspace(M, N, K, silu != 0);
+}
 extern "C" size_t w4a4_gemm_mxfp4_workspace_size(int M, int K, int N) { return 256; }
 
 extern "C" int w4a16_gemm_mxfp4(const uint16_t* x, int M, int K, const uint32_t* codes, const uint8_t* scales, int N,

@@ -341,6 +341,9 @@ static int mv_max_clusters(int csize, size_t smem) {
 // The busiest CTA's units decide, with some MV_JOIN units' time for a join
 // through the cluster.
 constexpr double MV_JOIN = 16;
+// From so many units per warp two CTAs share an SM instead of leaving room for the
+// next kernel's: b1 gate|up (28) 15.8 us against 16.4, down (14) 10.7 against 9.0.
+constexpr int MV_TWO = 20;
 
 template <int NW, int MS>
 static MvPlan mv_plan(int N, int K) {
@@ -350,19 +353,20 @@ static MvPlan mv_plan(int N, int K) {
   const int dev = device_index() & 63;
   once_per_device(once, [&] {
     cudaFuncSetAttribute(w4pg_mxfp4_matvec<NW, MS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SH::smem(MV_GROUPS));
-    room[dev][0] = num_sms();
+    room[dev][0] = 2 * num_sms();
     for (int l = 1; l < 4; ++l) room[dev][l] = mv_max_clusters<NW, MS>(1 << l, SH::smem(MV_GROUPS));
   });
   const int groups = N / 128 * 8 + std::min(8, (N % 128 + 3) / 4);  // (those of the last tile that have rows)
-  const int ktiles = K / 128;
+  const int ktiles = K / 128, sms = num_sms();
+  const int per = (long long)NW * groups * ktiles >= (long long)MV_TWO * MV_WARPS * sms ? 2 : 1;
   MvPlan best = {};
   double cost = 0;
   for (int l = 0; l < 4; ++l) {
     const int c = 1 << l;
-    if (c > ktiles && l > 0) break;
-    const int clusters = std::min(groups, std::min(room[dev][l], num_sms() / c));
+    if (c > ktiles) break;
+    const int clusters = std::min(groups, std::min(room[dev][l], per * sms / c));
     const int n = NW * ((groups + clusters - 1) / clusters), kc = (ktiles + c - 1) / c, gcap = std::min(n, MV_GROUPS);
-        const double v = (double)n * kc + (l ? MV_JOIN : 0);
+    const double v = (double)n * kc + (l ? MV_JOIN : 0);
     if (best.groups == 0 || v < cost) {
       cost = v;
       best = {groups, l, clusters, gcap, SH::smem(gcap)};

@@ -1,0 +1,103 @@
+// mxfp4_tc.cuh -- what the MXFP4 tensor-core products share: bounded barrier
+// waits, bulk-tensor copies and their maps, tcgen05 descriptors, and how a
+// product's output tiles are dealt to CTAs.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "mxfp4.cuh"
+#include "kernels.h"
+
+namespace w4 {
+
+constexpr unsigned long long MT_TIMEOUT_NS = 2000000000ull;
+
+__device__ __forceinline__ unsigned long long mt_now() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+// Bounded wait; gives up as well once another role of the CTA has (*fail).
+// fail null: only its own bound counts (drains).
+__device__ __forceinline__ bool mt_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = mt_now();
+  while (true) {
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (fail && *fail) return false;
+    if (mt_now() - t0 > MT_TIMEOUT_NS) {
+      if (fail) *fail = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void mt_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mt_prefetch_2d(const CUtensorMap* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+// `bytes` (a multiple of 16) in one piece
+__device__ __forceinline__ void mt_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mt_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mt_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void mt_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory matrix descriptor of a K-major tile with 128-byte rows in the
+// 128-byte swizzle (8-row atoms of 1024 bytes); 32 bytes of a row further on is
+// two more in its address field.
+__device__ __forceinline__ uint64_t mt_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// 2-D map over rows of `inner` elements, `row_bytes` apart; boxes of box_inner x
+// box_rows (what lies outside reads as zeros)
+bool mt_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t rows, uint64_t row_bytes,
+            uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle sw);
+
+// How T output tiles of `stages` steps along K are dealt to `slots` CTAs: whole
+// rounds of tiles as they are, and what is left over split along K, so that the
+// last round is as full as the others.
+struct MtDeal {
+  int whole;      // tiles that are not split: items 0 .. whole - 1
+  int split;      // parts of each other tile
+  int items;
+};
+inline MtDeal mt_deal(int tiles, int stages, int slots, int most_split) {
+  MtDeal d = {tiles, 1, tiles};
+  const int over = tiles % slots;
+  if (over == 0 || most_split < 2) return d;
+  const int split = std::min(std::min(slots / over, stages / 2), most_split);
+  if (split < 2) return d;
+  d.whole = tiles - over;
+  d.split = split;
+  d.items = d.whole + over * split;
+  return d;
+}
+__device__ __host__ __forceinline__ void mt_item(int i, int whole, int split, int stages, int* tile, int* part, int* k0,
+                                                  int* k1) {
+  *tile = i < whole ? i : whole + (i - whole) / split;
+  *part = i < whole ? 0 : (i - whole) % split;
+  *k0 = i < whole ? 0 : (int)((long long)stages * *part / split);
+  *k1 = i < whole ? stages : (int)((long long)stages * (*part + 1) / split);
+}
+
+}  // namespace w4
