@@ -76,6 +76,8 @@ struct MxArgs {
 bool mxfp4_matvec_serves(int M, int K);
 int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s);
 int launch_mxfp4_a16(const MxArgs& a, bool silu, cudaStream_t s);
+int launch_mxfp4_a4(const MxArgs& a, cudaStream_t s);
+size_t mxfp4_a4_workspace(int M, int N, int K);
 size_t mxfp4_a16_workspace(int M, int N, int K, bool silu);
 
 }  // namespace w4
