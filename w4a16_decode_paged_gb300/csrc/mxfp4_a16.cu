@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
   __shared__ uint32_t tmem_slot;
   __shared__ int s_last;
   __shared__ volatile int s_fail;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int K = p.a.K, stages = K / MA_K, KT = K / 128;
 
   if (warp == 0) {
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
 
   if (warp == 0) {
     // ---- producer ----
-    if (lane == 0) {
+    if (mt_elect()) {
       int mt, nt, part, k0, k1;
       if (blockIdx.x < p.items) {
         // weights may come from the call just before: into L2 ahead of the wait, read behind it
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
         ok = mt_wait(&full[slot], (s / S) & 1, &s_fail) && mt_wait(&afull[ab], (s / NAB) & 1, &s_fail);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         mt_fence_after();
-        if (lane == 0) {
+        if (mt_elect()) {
           const uint64_t b0 = mt_desc(ring + slot * SH::SLOT), b1 = mt_desc(ring + slot * SH::SLOT + SH::XHALF);
 #pragma unroll
           for (int g = 0; g < 2; ++g)
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
     }
     // tensor memory is freed only when every MMA issued is done, whatever happened elsewhere
     if (s > 0) {
-      if (lane == 0) mt_commit(&drain);
+      if (mt_elect()) mt_commit(&drain);
       __syncwarp();
       (void)mt_wait(&drain, 0, nullptr);
     }

@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
   __shared__ uint32_t tmem_slot;
   __shared__ int s_last;
   __shared__ volatile int s_fail;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int K = p.a.K, KT = K / 128, stages = (K + MB_K - 1) / MB_K;
 
   if (warp == 0) {
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
 
   if (warp == 0) {
     // ---- producer ----
-    if (lane == 0) {
+    if (mt_elect()) {
       int mt, nt, part, k0, k1;
       if (blockIdx.x < p.items) {
         // weights may come from the call just before: into L2 ahead of the wait, read behind it
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
         ok = __all_sync(0xffffffffu, mt_wait(&full[slot], (s / S) & 1, &s_fail));
         if (!ok) break;
         mt_fence_after();
-        if (lane == 0) {
+        if (mt_elect()) {
           const uint32_t sl = ring + slot * SH::SLOT, ts = tmem + SH::TS;
           const int halves = 2 * k + 2 <= KT ? 2 : 1;
           // columns: weights tile g, half j at 8 g + 4 j; x half j, tile g at 16 + 8 j + 4 g
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
     }
     // tensor memory is freed only when every MMA issued is done, whatever happened elsewhere
     if (s > 0) {
-      if (lane == 0) mt_commit(&drain);
+      if (mt_elect()) mt_commit(&drain);
       __syncwarp();
       (void)mt_wait(&drain, 0, nullptr);
     }

@@ -21,6 +21,15 @@ __device__ __forceinline__ unsigned long long mt_now() {
   return t;
 }
 
+// One lane of a converged warp.  (Chosen by elect.sync, and with the warp's number
+// taken from one lane, the compiler knows what follows to be uniform: MMAs behind
+// `lane == 0` took 80 to 190 cycles each to issue, whatever their size.)
+__device__ __forceinline__ bool mt_elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Bounded wait; gives up as well once another role of the CTA has (*fail).
 // fail null: only its own bound counts (drains).
 __device__ __forceinline__ bool mt_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
