@@ -14,11 +14,12 @@
 // decode batches and short prompts, where the weights' bytes decide.
 //
 // Roles (18 warps), meeting only at mbarriers: a producer lane copies codes,
-// scales and x into a ring; 16 expander warps (lane quadrant, tile, half of the
-// stage's k) fill one of NAB tensor-memory A buffers; one warp issues the MMAs;
-// the expander warps run the epilogue.  Tiles are dealt by mt_deal: the last
-// round's are split along K, their fp32 parts meet in the workspace, and the
-// last part to arrive adds them in order.
+// scales and x into a ring; two sets of 8 expander warps (lane quadrant, tile) take
+// the stages in turn and fill one of NAB tensor-memory A buffers each, so that one
+// set's waits lie under the other's work; one warp issues the MMAs; the expander
+// warps run the epilogue, turning 8 columns at a time through shared memory, so
+// that stores (and the residual's loads) are 16 bytes of a row of y.  Tiles are
+// dealt by mt_deal.
 #include "mxfp4_tc.cuh"
 
 namespace w4 {
@@ -34,7 +35,7 @@ struct MaShape {
   static constexpr uint32_t WAT = 2 * XHALF, SAT = WAT + 2 * MA_W;    // a slot: x, codes, scales
   static constexpr uint32_t SLOT = SAT + 2 * MX_TILE;
   static constexpr int S = 204800 / SLOT;
-  static constexpr size_t SMEM = S * SLOT + 1024;
+  static constexpr size_t SMEM = S * SLOT + MA_EXP * 1024 + 1024;     // + a warp's 8 columns x 32 rows, fp32
   static constexpr int NAB = (512 - 2 * NC) / 128 > 3 ? 3 : (512 - 2 * NC) / 128;
   static constexpr int TA = 2 * NC;                                   // tensor memory: sums, then A buffers
   static constexpr uint32_t IDESC = (1u << 4) | ((uint32_t)(NC >> 3) << 17) | ((128u >> 4) << 24);
@@ -45,7 +46,6 @@ struct MaArgs {
   MxArgs a;
   int silu, mtiles, ntiles, whole, split, items;   // ntiles: of 128 weight rows; items as mt_deal
   float* parts;
-  unsigned int* tickets;
   CUtensorMap tm_w[2], tm_x;
 };
 
@@ -58,7 +58,6 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
   const unsigned char* ringp = smem_raw + (ring - smem_u32(smem_raw));
   __shared__ __align__(8) uint64_t full[S], empty[S], afull[NAB], aempty[NAB], dfull, dempty, drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_last;
   __shared__ volatile int s_fail;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int K = p.a.K, stages = K / MA_K, KT = K / 128;
@@ -70,10 +69,10 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
   if (tid == 32) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], MA_EXP + 1);
+      mbar_init(&empty[i], MA_EXP / 2 + 1);
     }
     for (int i = 0; i < NAB; ++i) {
-      mbar_init(&afull[i], MA_EXP);
+      mbar_init(&afull[i], MA_EXP / 2);
       mbar_init(&aempty[i], 1);
     }
     mbar_init(&dfull, 1);
@@ -173,51 +172,60 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
   } else {
     // ---- expanders and epilogue ----
     pdl_wait_then_trigger();
-    const int e = warp - 2, quad = warp & 3, g = (e >> 2) & 1, h = e >> 3;
+    const int e = warp - 2, quad = warp & 3, g = (e >> 2) & 1, set = e >> 3;
     const int row = 32 * quad + lane;  // of the tile; the tensor-memory lane
+    const int sw = (row >> 1) & 3;     // 16-byte chunk c of a row's codes is at c ^ sw
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+    float* turn = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * SH::SLOT) + e * 256;
+    const int M = p.a.M, N = p.a.N;
+    const bool wide = N % 8 == 0;      // rows of y (and of the residual) start on 16 bytes
     uint32_t s = 0, n = 0;
     bool ok = true;
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, ++n) {
       int mt, nt, part, k0, k1;
       const int tile = item(i, &mt, &nt, &part, &k0, &k1);
       for (int k = k0; k < k1; ++k, ++s) {
+        if ((s & 1) != set) continue;
         const int slot = s % S, ab = s % NAB;
-        ok = mt_wait(&full[slot], (s / S) & 1, &s_fail);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        // 32 bytes of this row (chunks swizzled: c at c ^ (row / 2) % 4), the two scales
+        ok = __all_sync(0xffffffffu, mt_wait(&full[slot], (s / S) & 1, &s_fail));
+        if (!ok) break;
         const unsigned char* w = ringp + slot * SH::SLOT + SH::WAT + g * MA_W + row * 64;
-        const int sw = (row >> 1) & 3;
-        const uint4 c0 = *reinterpret_cast<const uint4*>(w + (((2 * h) ^ sw) << 4));
-        const uint4 c1 = *reinterpret_cast<const uint4*>(w + (((2 * h + 1) ^ sw) << 4));
-        const uint16_t sc = *reinterpret_cast<const uint16_t*>(ringp + slot * SH::SLOT + SH::SAT + g * MX_TILE + lane * 16 +
-                                                               quad * 4 + 2 * h);
-        const uint32_t s0 = mx_scale_h2(sc & 255u), s1 = mx_scale_h2((uint32_t)sc >> 8);
-        uint32_t v[32];
+        uint4 c[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4& c = j < 4 ? c0 : c1;
-          const uint4 f = mx_values((j & 3) == 0 ? c.x : (j & 3) == 1 ? c.y : (j & 3) == 2 ? c.z : c.w);
-          const uint32_t sj = j < 4 ? s0 : s1;
-          v[4 * j] = hmul2_u32(f.x, sj);
-          v[4 * j + 1] = hmul2_u32(f.y, sj);
-          v[4 * j + 2] = hmul2_u32(f.z, sj);
-          v[4 * j + 3] = hmul2_u32(f.w, sj);
-        }
+        for (int q = 0; q < 4; ++q) c[q] = *reinterpret_cast<const uint4*>(w + ((q ^ sw) << 4));
+        const uint32_t sc = *reinterpret_cast<const uint32_t*>(ringp + slot * SH::SLOT + SH::SAT + g * MX_TILE + lane * 16 + quad * 4);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
-        if (s >= NAB) ok = mt_wait(&aempty[ab], (s / NAB - 1) & 1, &s_fail);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        mt_fence_after();
-        const uint32_t ta = lanes + SH::TA + (uint32_t)((ab * 2 + g) * 64 + h * 32);
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-            "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta),
-            "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-            "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-            "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-            "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-            : "memory");
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t s0 = mx_scale_h2((sc >> (16 * h)) & 255u), s1 = mx_scale_h2((sc >> (16 * h + 8)) & 255u);
+          uint32_t v[32];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint4& cc = c[2 * h + (j >> 2)];
+            const uint4 f = mx_values((j & 3) == 0 ? cc.x : (j & 3) == 1 ? cc.y : (j & 3) == 2 ? cc.z : cc.w);
+            const uint32_t sj = j < 4 ? s0 : s1;
+            v[4 * j] = hmul2_u32(f.x, sj);
+            v[4 * j + 1] = hmul2_u32(f.y, sj);
+            v[4 * j + 2] = hmul2_u32(f.z, sj);
+            v[4 * j + 3] = hmul2_u32(f.w, sj);
+          }
+          if (h == 0) {
+            if (s >= NAB) ok = __all_sync(0xffffffffu, mt_wait(&aempty[ab], (s / NAB - 1) & 1, &s_fail));
+            if (!ok) break;
+            mt_fence_after();
+          }
+          const uint32_t ta = lanes + SH::TA + (uint32_t)((ab * 2 + g) * 64 + h * 32);
+          asm volatile(
+              "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+              "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta),
+              "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+              "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+              "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+              "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+              : "memory");
+        }
+        if (!ok) break;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         mt_fence_before();
         __syncwarp();
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
       if (!ok) break;
       mt_fence_after();
       constexpr int CW = NC / 4;
-      const int col0 = (e >> 2) * CW, M = p.a.M, N = p.a.N;
+      const int col0 = (e >> 2) * CW, m0 = mt * NC + col0;
       uint32_t acc[2][CW];
 #pragma unroll
       for (int gg = 0; gg < 2; ++gg)
@@ -243,56 +251,51 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
       mt_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&dempty);
-      const int m0 = mt * NC + col0;
-      bool finish = true;
       if (i >= p.whole && p.split > 1) {
-        const int t = tile - p.whole;
-        float* mine = p.parts + ((size_t)t * p.split + part) * (2 * NC * 128);
+        float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NC * 256);
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg)
 #pragma unroll
           for (int c = 0; c < CW; ++c)
-            if (m0 + c < M) mine[(gg * NC + col0 + c) * 128 + row] = __uint_as_float(acc[gg][c]);
-        __threadfence();
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * MA_EXP) : "memory");
-        if (e == 0 && lane == 0) s_last = atomicAdd(&p.tickets[t], 1u) == (unsigned int)(p.split - 1);
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * MA_EXP) : "memory");
-        finish = s_last;
-        if (finish) {
-          __threadfence();
-          if (e == 0 && lane == 0) p.tickets[t] = 0u;
-          const float* all = p.parts + (size_t)t * p.split * (2 * NC * 128);
-#pragma unroll
-          for (int gg = 0; gg < 2; ++gg)
-#pragma unroll
-            for (int c = 0; c < CW; ++c) acc[gg][c] = 0u;  // (0.f: its own part is among them)
-          for (int q = 0; q < p.split; ++q)
-#pragma unroll
-            for (int gg = 0; gg < 2; ++gg)
-#pragma unroll
-              for (int c = 0; c < CW; ++c)
-                if (m0 + c < M)
-                  acc[gg][c] = __float_as_uint(
-                      __uint_as_float(acc[gg][c]) +
-                      __ldcg(&all[(size_t)q * (2 * NC * 128) + (gg * NC + col0 + c) * 128 + row]));
-        }
+            if (m0 + c < M) mine[(col0 + c) * 256 + gg * 128 + row] = __uint_as_float(acc[gg][c]);
+        continue;
       }
-      if (!finish) continue;
 #pragma unroll
       for (int gg = 0; gg < 2; ++gg) {
         if (p.silu && gg) break;
-        const int nn = (nt + gg) * 128 + row;
-        if (nn >= N) break;
-        const float bias = p.a.bias ? __half2float(p.a.bias[nn]) : 0.f;
+        const int n0 = (nt + gg) * 128 + 32 * quad;
+        if (n0 >= N) break;
+        const float bias = p.a.bias && n0 + lane < N ? __half2float(p.a.bias[n0 + lane]) : 0.f;
 #pragma unroll
-        for (int c = 0; c < CW; ++c) {
-          if (m0 + c >= M) break;
-          float v = __uint_as_float(acc[gg][c]);
-          if (p.silu) v = v / (1.f + expf(-v)) * __uint_as_float(acc[1][c]);
-          const size_t at = (size_t)(m0 + c) * N + nn;
-          v += bias;
-          if (p.a.residual) v += __half2float(p.a.residual[at]);
-          p.a.y[at] = __float2half_rn(v);
+        for (int c0 = 0; c0 < CW; c0 += 8) {
+          if (m0 + c0 >= M) break;
+          float v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            v[c] = __uint_as_float(acc[gg][c0 + c]);
+            if (p.silu) v[c] = v[c] / (1.f + expf(-v[c])) * __uint_as_float(acc[1][c0 + c]);
+            v[c] += bias;
+          }
+          if (wide) {
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) turn[c * 32 + lane] = v[c];
+            __syncwarp();
+            // lane: row m0 + c0 + lane / 4, 8 weight rows
+            const int m = m0 + c0 + (lane >> 2), nn = n0 + (lane & 3) * 8;
+            if (m < M && nn < N) {
+              const float4 lo = *reinterpret_cast<const float4*>(turn + lane * 8), hi = *reinterpret_cast<const float4*>(turn + lane * 8 + 4);
+              mx_store8(p.a, (size_t)m * N + nn, lo, hi);
+            }
+          } else if (n0 + lane < N) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              if (m0 + c0 + c >= M) break;
+              const size_t at = (size_t)(m0 + c0 + c) * N + n0 + lane;
+              if (p.a.residual) v[c] += __half2float(p.a.residual[at]);
+              p.a.y[at] = __float2half_rn(v[c]);
+            }
+          }
         }
       }
     }
@@ -333,19 +336,16 @@ constexpr int MA_SPLIT = 16;
 
 // the deal for these sizes with room for `bytes` of workspace
 static MtDeal ma_deal(int M, int N, int K, bool silu, size_t bytes, int slots) {
-  const size_t part = (size_t)2 * 128 * ma_cols(M) * 4;
   for (int most = MA_SPLIT; most > 1; --most) {
     const MtDeal d = mt_deal(ma_tiles(M, N, silu), K / MA_K, slots, most);
-    const int over = d.items == d.whole ? 0 : (d.items - d.whole) / d.split;
-    if (over <= (int)(TC_TICKET_BYTES / 4) && (over == 0 || TC_TICKET_BYTES + (size_t)over * d.split * part <= bytes)) return d;
+    if (mt_workspace(d, ma_cols(M), 256) <= bytes) return d;
   }
   return mt_deal(ma_tiles(M, N, silu), K / MA_K, slots, 1);
 }
 
 size_t mxfp4_a16_workspace(int M, int N, int K, bool silu) {
   // for the split of a GB300's 152 SMs, so that it can be asked for where there is no GPU
-  const MtDeal d = ma_deal(M, N, K, silu, ~(size_t)0, ATW_SMS);
-  return TC_TICKET_BYTES + (size_t)(d.items - d.whole) * 2 * 128 * ma_cols(M) * 4;
+  return mt_workspace(ma_deal(M, N, K, silu, ~(size_t)0, ATW_SMS), ma_cols(M), 256);
 }
 
 template <int NC>
@@ -378,9 +378,11 @@ int launch_mxfp4_a16(const MxArgs& a, bool silu, cudaStream_t s) {
   p.whole = d.whole;
   p.split = d.split;
   p.items = d.items;
-  p.tickets = static_cast<unsigned int*>(a.workspace);
   if (d.split > 1) p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + TC_TICKET_BYTES);
-  return nc == 32 ? ma_launch<32>(p, slots, s) : nc == 64 ? ma_launch<64>(p, slots, s) : ma_launch<128>(p, slots, s);
+  const int rc = nc == 32 ? ma_launch<32>(p, slots, s) : nc == 64 ? ma_launch<64>(p, slots, s) : ma_launch<128>(p, slots, s);
+  if (rc || d.split < 2) return rc;
+  return launch_mxfp4_join({a, p.parts, d.whole, (d.items - d.whole) / d.split, d.split, nc, 256, p.mtiles, silu ? 128 : 256, silu},
+                           s);
 }
 
 }  // namespace w4

@@ -4,10 +4,50 @@
 // fp16 at the end (SiLU's two sums are not rounded before it).
 #include <algorithm>
 
-#include "mxfp4.cuh"
-#include "kernels.h"
+#include "mxfp4_tc.cuh"
 
 namespace w4 {
+
+// The sums of tiles that were split along K: a thread adds the parts of four
+// neighbouring outputs, in order.
+__global__ void __launch_bounds__(256) w4pg_mxfp4_join(const __grid_constant__ MtJoin j) {
+  pdl_wait_then_trigger();
+  const int width = (j.silu ? 128 : j.tn) / 4;     // threads along a row
+  const int i = blockIdx.x * 256 + threadIdx.x, c = i % width * 4, row = i / width % j.tm, t = i / width / j.tm;
+  if (t >= j.tiles) return;
+  const int tile = j.first + t, m = tile % j.mtiles * j.tm + row, n = tile / j.mtiles * j.tstep + c;
+  if (m >= j.a.M || n >= j.a.N) return;
+  const size_t part = (size_t)j.tm * j.tn;
+  const float* p = j.parts + (size_t)t * j.split * part + (size_t)row * j.tn + c;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v;
+#pragma unroll 8
+  for (int q = 0; q < j.split; ++q) {
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(p + q * part));
+    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    if (j.silu) {
+      const float4 z = __ldcg(reinterpret_cast<const float4*>(p + q * part + 128));
+      u.x += z.x, u.y += z.y, u.z += z.z, u.w += z.w;
+    }
+  }
+  float o[4] = {v.x, v.y, v.z, v.w};
+  const float up[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (n + k >= j.a.N) break;
+    const size_t at = (size_t)m * j.a.N + n + k;
+    if (j.silu) o[k] = o[k] / (1.f + expf(-o[k])) * up[k];
+    if (j.a.bias) o[k] += __half2float(j.a.bias[n + k]);
+    if (j.a.residual) o[k] += __half2float(j.a.residual[at]);
+    j.a.y[at] = __float2half_rn(o[k]);
+  }
+}
+
+int launch_mxfp4_join(const MtJoin& j, cudaStream_t s) {
+  const long long threads = (long long)j.tiles * j.tm * (j.silu ? 128 : j.tn) / 4;
+  const cudaError_t e = launch_pdl(w4pg_mxfp4_join, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, j);
+  if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "mxfp4 join launch: %s", cudaGetErrorString(e));
+  return W4A16_OK;
+}
 
 static int launch_mxfp4(const MxArgs& a, bool silu, cudaStream_t s) {
   if (a.x == nullptr) return launch_mxfp4_a4(a, s);

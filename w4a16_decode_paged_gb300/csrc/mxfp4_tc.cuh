@@ -84,7 +84,8 @@ bool mt_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_t i
 
 // How T output tiles of `stages` steps along K are dealt to `slots` CTAs: whole
 // rounds of tiles as they are, and what is left over split along K, so that the
-// last round is as full as the others.
+// last round is as full as the others.  The parts' fp32 sums go to the workspace
+// and a second kernel adds them in order (launch_mxfp4_join).
 struct MtDeal {
   int whole;      // tiles that are not split: items 0 .. whole - 1
   int split;      // parts of each other tile
@@ -101,6 +102,20 @@ inline MtDeal mt_deal(int tiles, int stages, int slots, int most_split) {
   d.items = d.whole + over * split;
   return d;
 }
+// Parts in the workspace lie behind the block that the other split-K calls keep
+// their tickets in; a part is [rows of x][weight rows] of its tile, fp32.
+inline size_t mt_workspace(const MtDeal& d, int tm, int tn) {
+  return d.split > 1 ? TC_TICKET_BYTES + (size_t)(d.items - d.whole) * tm * tn * 4 : 0;
+}
+struct MtJoin {
+  MxArgs a;
+  const float* parts;
+  int first, tiles, split;   // the split tiles: numbers first .. first + tiles - 1, in `split` parts each
+  int tm, tn, mtiles;        // tile t covers rows tm (t % mtiles) .., weight rows tstep (t / mtiles) ..
+  int tstep, silu;           // silu: a part's columns are 128 gate, 128 up
+};
+int launch_mxfp4_join(const MtJoin& j, cudaStream_t s);
+
 __device__ __host__ __forceinline__ void mt_item(int i, int whole, int split, int stages, int* tile, int* part, int* k0,
                                                   int* k1) {
   *tile = i < whole ? i : whole + (i - whole) / split;
