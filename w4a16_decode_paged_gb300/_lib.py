@@ -161,7 +161,9 @@ def load() -> ctypes.CDLL:
 
 _native = None  # the module; False: not to be had
 _NATIVE_ENTRIES = ("kv_append_rope_int4", "kv_read_int4", "paged_gqa_decode_int4", "paged_gqa_decode_rope_append_int4",
-                   "paged_gqa_decode_window", "paged_gqa_decode_window_fp8", "paged_gqa_decode_window_int4")
+                   "paged_gqa_decode_window", "paged_gqa_decode_window_fp8", "paged_gqa_decode_window_int4",
+                   "mxfp4_quantize", "mxfp4_dequantize", "w4a16_gemm_mxfp4", "w4a16_gemm_silu_mul_mxfp4",
+                   "w4a4_gemm_mxfp4")
 
 
 def native():

@@ -485,6 +485,10 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
     """(codes, scales) of fp16 rows x [M][K]: int32 [M][K/8] and scale tiles
     uint8 [M/128 rounded up][K/128][512] (bytes of rows past M are left as they
     were in tiles that the caller gives, and are not used by any call)."""
+    if stream is None and _cuda(x) and (fast := native()) is not None:
+        r = fast.mx_quantize(x, codes, scales)
+        if r is not None:
+            return _result(r)
     M, K, dev = _mx_x(x)
     if codes is not None and codes.dtype not in _W:
         _arg(codes, _W, "codes")
@@ -503,6 +507,10 @@ def mxfp4_quantize(x, codes=None, scales=None, stream=None):
 
 def mxfp4_dequantize(codes, scales, out=None, stream=None):
     """fp16 values [M][K] of an MXFP4 matrix."""
+    if stream is None and _cuda(codes) and (fast := native()) is not None:
+        r = fast.mx_dequantize(codes, scales, out)
+        if r is not None:
+            return _result(r)
     M, K, dev = _mx_matrix(codes, scales, "")
     if out is not None:
         _is(out, torch.float16, (M, K), dev, "out")
@@ -548,6 +556,10 @@ def w4a16_gemm_mxfp4(x, codes, scales, bias=None, residual=None, out=None, works
     [N][K/8], scale tiles), from one token to a prompt's rows.  A workspace the
     caller gives is zeroed once before its first use (mxfp4_workspace); without
     one, each call makes its own.  residual may be out."""
+    if stream is None and workspace is not None and _cuda(x) and (fast := native()) is not None:
+        r = fast.mx_gemm16(x, codes, scales, bias, residual, out, workspace, err_flag)
+        if r is not None:
+            return _result(r)
     M, K, dev = _mx_x(x)
     N = _mx_matrix(codes, scales, "", dev, K)[0]
     out, workspace, err = _mx_buffers(M, K, N, "a16", out, workspace, err_flag, bias, residual, x, dev, stream)
@@ -560,6 +572,10 @@ def w4a16_gemm_mxfp4(x, codes, scales, bias=None, residual=None, out=None, works
 def w4a16_gemm_silu_mul_mxfp4(x, codes_gate, scales_gate, codes_up, scales_up, out=None, workspace=None, err_flag=None,
                               stream=None):
     """y = silu(x . G^T) * (x . U^T): the gated MLP's front half over MXFP4 weights."""
+    if stream is None and workspace is not None and _cuda(x) and (fast := native()) is not None:
+        r = fast.mx_silu(x, codes_gate, scales_gate, codes_up, scales_up, out, workspace, err_flag)
+        if r is not None:
+            return _result(r)
     M, K, dev = _mx_x(x)
     N = _mx_matrix(codes_gate, scales_gate, "gate ", dev, K)[0]
     if _mx_matrix(codes_up, scales_up, "up ", dev, K)[0] != N:
@@ -575,6 +591,10 @@ def w4a4_gemm_mxfp4(x_codes, x_scales, codes, scales, bias=None, residual=None, 
                     err_flag=None, stream=None):
     """y = X . W^T (+ bias) (+ residual), both MXFP4 matrices (X from
     mxfp4_quantize): the block-scaled 4-bit product of the tensor cores."""
+    if stream is None and workspace is not None and _cuda(x_codes) and (fast := native()) is not None:
+        r = fast.mx_gemm4(x_codes, x_scales, codes, scales, bias, residual, out, workspace, err_flag)
+        if r is not None:
+            return _result(r)
     M, K, dev = _mx_matrix(x_codes, x_scales, "x_")
     N = _mx_matrix(codes, scales, "", dev, K)[0]
     out, workspace, err = _mx_buffers(M, K, N, "a4", out, workspace, err_flag, bias, residual, x_codes, dev, stream)

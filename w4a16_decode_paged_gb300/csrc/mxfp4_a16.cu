@@ -196,36 +196,34 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
         const uint32_t sc = *reinterpret_cast<const uint32_t*>(ringp + slot * SH::SLOT + SH::SAT + g * MX_TILE + lane * 16 + quad * 4);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
+        uint32_t v[64];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t s0 = mx_scale_h2((sc >> (16 * h)) & 255u), s1 = mx_scale_h2((sc >> (16 * h + 8)) & 255u);
-          uint32_t v[32];
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t sb = mx_scale_h2((sc >> (8 * b)) & 255u), cw[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4& cc = c[2 * h + (j >> 2)];
-            const uint4 f = mx_values((j & 3) == 0 ? cc.x : (j & 3) == 1 ? cc.y : (j & 3) == 2 ? cc.z : cc.w);
-            const uint32_t sj = j < 4 ? s0 : s1;
-            v[4 * j] = hmul2_u32(f.x, sj);
-            v[4 * j + 1] = hmul2_u32(f.y, sj);
-            v[4 * j + 2] = hmul2_u32(f.z, sj);
-            v[4 * j + 3] = hmul2_u32(f.w, sj);
+          for (int j = 0; j < 4; ++j) {
+            const uint4 f = mx_values(cw[j]);
+            v[16 * b + 4 * j] = hmul2_u32(f.x, sb);
+            v[16 * b + 4 * j + 1] = hmul2_u32(f.y, sb);
+            v[16 * b + 4 * j + 2] = hmul2_u32(f.z, sb);
+            v[16 * b + 4 * j + 3] = hmul2_u32(f.w, sb);
           }
-          if (h == 0) {
-            if (s >= NAB) ok = __all_sync(0xffffffffu, mt_wait(&aempty[ab], (s / NAB - 1) & 1, &s_fail));
-            if (!ok) break;
-            mt_fence_after();
-          }
-          const uint32_t ta = lanes + SH::TA + (uint32_t)((ab * 2 + g) * 64 + h * 32);
+        }
+        if (s >= NAB) ok = __all_sync(0xffffffffu, mt_wait(&aempty[ab], (s / NAB - 1) & 1, &s_fail));
+        if (!ok) break;
+        mt_fence_after();
+        const uint32_t ta = lanes + SH::TA + (uint32_t)((ab * 2 + g) * 64);
+#pragma unroll
+        for (int h = 0; h < 64; h += 32)
           asm volatile(
               "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-              "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta),
-              "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-              "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-              "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-              "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+              "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(ta + h),
+              "r"(v[h]), "r"(v[h + 1]), "r"(v[h + 2]), "r"(v[h + 3]), "r"(v[h + 4]), "r"(v[h + 5]), "r"(v[h + 6]),
+              "r"(v[h + 7]), "r"(v[h + 8]), "r"(v[h + 9]), "r"(v[h + 10]), "r"(v[h + 11]), "r"(v[h + 12]), "r"(v[h + 13]),
+              "r"(v[h + 14]), "r"(v[h + 15]), "r"(v[h + 16]), "r"(v[h + 17]), "r"(v[h + 18]), "r"(v[h + 19]), "r"(v[h + 20]),
+              "r"(v[h + 21]), "r"(v[h + 22]), "r"(v[h + 23]), "r"(v[h + 24]), "r"(v[h + 25]), "r"(v[h + 26]), "r"(v[h + 27]),
+              "r"(v[h + 28]), "r"(v[h + 29]), "r"(v[h + 30]), "r"(v[h + 31])
               : "memory");
-        }
-        if (!ok) break;
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         mt_fence_before();
         __syncwarp();

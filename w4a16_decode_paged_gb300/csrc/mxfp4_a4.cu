@@ -26,6 +26,8 @@ constexpr int MB_EPI = 8;                     // epilogue warps
 constexpr int MB_THREADS = 64 + 32 * MB_EPI;
 constexpr uint32_t MB_X = 128 * MB_K / 2;     // bytes of 128 rows of x per stage
 constexpr int MB_SPLIT = 16;
+constexpr int MB_PITCH = 36;                  // floats from row to row of a warp's 32 x 32 outputs, without bank conflicts
+constexpr int MB_TURN = 32 * MB_PITCH * 4;
 
 template <int NA, int NC>
 struct MbShape {
@@ -33,8 +35,8 @@ struct MbShape {
   static constexpr uint32_t W = NC * MB_K / 2;
   static constexpr uint32_t WAT = NA * MB_X, SAT = WAT + W;           // a slot: x, weights, scales of x, of the weights
   static constexpr uint32_t SLOT = (SAT + (NA + NB) * 2 * MX_TILE + 1023) / 1024 * 1024;
-  static constexpr int S = 225 * 1024 / SLOT;
-  static constexpr size_t SMEM = S * SLOT + 1024;
+  static constexpr int S = (225 * 1024 - MB_EPI * MB_TURN) / SLOT;
+  static constexpr size_t SMEM = S * SLOT + MB_EPI * MB_TURN + 1024;
   static constexpr uint32_t TS = NA * NC;                             // tensor memory: sums, scales of x, of the weights
   static constexpr uint32_t IDESC =
       (1u << 7) | (1u << 10) | ((uint32_t)(NC >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
     constexpr int CW = NC / 2;  // columns of a warp, of each 128 rows
     const int col0 = (e >> 2) * CW, M = p.a.M, N = p.a.N;
     const bool wide = N % 8 == 0;  // rows of y (and of the residual) start on 16 bytes
+    float* turn = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * SH::SLOT + e * MB_TURN);
     uint32_t n = 0;
     for (int i = blockIdx.x; i < p.items; i += gridDim.x, ++n) {
       int mt, nt, part, k0, k1;
@@ -240,21 +243,32 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
             if (lane == 0) mbar_arrive(&dempty[g]);
           }
           const int nn = nt * NC + col0 + c0;
-          if (parts) {
-            float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NA * 128 * NC) + (size_t)r * NC + col0 + c0;
-            if (m < M) {
+          if (parts || wide) {
+            // turned in shared memory: 4 lanes have 32 columns of a row, 8 rows a store
+            __syncwarp();
 #pragma unroll
-              for (int c = 0; c < 32; c += 4)
-                *reinterpret_cast<float4*>(mine + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-            }
-          } else if (m < M && wide) {
+            for (int c = 0; c < 32; c += 4)
+              *reinterpret_cast<float4*>(turn + lane * MB_PITCH + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+            __syncwarp();
+            const int q = (lane & 3) * 8, n8 = nn + q;
+            float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
+            if (p.a.bias && !parts && n8 < N) mx_add8(b0, b1, p.a.bias + n8);
 #pragma unroll
-            for (int c = 0; c < 32; c += 8) {
-              if (nn + c >= N) break;
-              float4 lo = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-              float4 hi = make_float4(v[c + 4], v[c + 5], v[c + 6], v[c + 7]);
-              if (p.a.bias) mx_add8(lo, hi, p.a.bias + nn + c);
-              mx_store8(p.a, (size_t)m * N + nn + c, lo, hi);
+            for (int h = 0; h < 32; h += 8) {
+              const int rr = h + (lane >> 2), mm = m - lane + rr;
+              float4 lo = *reinterpret_cast<const float4*>(turn + rr * MB_PITCH + q);
+              float4 hi = *reinterpret_cast<const float4*>(turn + rr * MB_PITCH + q + 4);
+              if (mm >= M || n8 >= N) continue;
+              if (parts) {
+                float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NA * 128 * NC) +
+                              (size_t)(r - lane + rr) * NC + col0 + c0 + q;
+                *reinterpret_cast<float4*>(mine) = lo;
+                *reinterpret_cast<float4*>(mine + 4) = hi;
+              } else {
+                lo.x += b0.x, lo.y += b0.y, lo.z += b0.z, lo.w += b0.w;
+                hi.x += b1.x, hi.y += b1.y, hi.z += b1.z, hi.w += b1.w;
+                mx_store8(p.a, (size_t)mm * N + n8, lo, hi);
+              }
             }
           } else if (m < M) {
 #pragma unroll

@@ -33,6 +33,11 @@ decltype(&::paged_gqa_decode_rope_append_int4) f_step = nullptr;
 decltype(&::paged_gqa_decode_window) f_win16 = nullptr;
 decltype(&::paged_gqa_decode_window_fp8) f_win8 = nullptr;
 decltype(&::paged_gqa_decode_window_int4) f_win4 = nullptr;
+decltype(&::mxfp4_quantize) f_mxq = nullptr;
+decltype(&::mxfp4_dequantize) f_mxd = nullptr;
+decltype(&::w4a16_gemm_mxfp4) f_mx16 = nullptr;
+decltype(&::w4a16_gemm_silu_mul_mxfp4) f_mxsilu = nullptr;
+decltype(&::w4a4_gemm_mxfp4) f_mx4 = nullptr;
 
 constexpr int64_t D = 128;
 
@@ -295,14 +300,160 @@ PyObject* decode_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (addresses of the seven entries, in the order of the declarations above)
+// An MXFP4 matrix: codes [rows][K/8] (int32), scale tiles [rows/128 rounded up][K/128][512].
+struct Mx {
+  const uint32_t* codes;
+  const uint8_t* scales;
+  int rows, K, dev;
+};
+int64_t tiles(int64_t rows) { return (rows + 127) / 128; }
+Mx mx(PyObject* co, PyObject* so, int64_t K = -1) {
+  const at::Tensor& c = tensor(co);
+  if (!c.is_cuda() || c.dim() != 2) throw NotPlain();
+  Mx m;
+  m.dev = c.get_device();
+  if (m.dev != c10::cuda::current_device()) throw NotPlain();
+  const int64_t rows = c.size(0), k = c.size(1) * 8;
+  if (rows < 1 || k < 128 || k % 128 != 0 || (K >= 0 && k != K)) throw NotPlain();
+  m.rows = narrow(rows);
+  m.K = narrow(k);
+  m.codes = static_cast<const uint32_t*>(checked(c, at::kInt, m.dev, {rows, k / 8}));
+  m.scales = static_cast<const uint8_t*>(checked(so, at::kByte, m.dev, {tiles(rows), k / 128, 512}));
+  return m;
+}
+// activations fp16 [M][K]
+struct Rows {
+  uint16_t* x;
+  int M, K, dev;
+};
+Rows rows_of(PyObject* o) {
+  const at::Tensor& t = tensor(o);
+  if (!t.is_cuda() || t.dim() != 2) throw NotPlain();
+  Rows r;
+  r.dev = t.get_device();
+  if (r.dev != c10::cuda::current_device()) throw NotPlain();
+  if (t.size(0) < 1 || t.size(1) < 128 || t.size(1) % 128 != 0) throw NotPlain();
+  r.M = narrow(t.size(0));
+  r.K = narrow(t.size(1));
+  r.x = half(checked(t, at::kHalf, r.dev, {r.M, r.K}));
+  return r;
+}
+at::Tensor made(PyObject* like, at::ScalarType type, c10::IntArrayRef shape) {
+  return at::empty(shape, tensor(like).options().dtype(type).requires_grad(false));
+}
+uint16_t* optional_half(PyObject* o, int dev, std::initializer_list<int64_t> shape) {
+  return o == Py_None ? nullptr : half(checked(o, at::kHalf, dev, shape));
+}
+// what the products share: output (given or made), workspace, error word
+struct Product {
+  at::Tensor out;
+  uint16_t* y;
+  void* ws;
+  size_t wb;
+  int32_t* err;
+  w4a16_stream_t s;
+};
+Product product(PyObject* like, int M, int N, int dev, PyObject* out, PyObject* ws, PyObject* err) {
+  Product p;
+  const at::Tensor& w = tensor(ws);
+  p.ws = checked(w, at::kByte, dev, {-1});
+  p.wb = (size_t)w.numel();
+  p.err = err_flag(err, dev);
+  p.out = out == Py_None ? made(like, at::kHalf, {M, N}) : tensor(out);
+  p.y = half(checked(p.out, at::kHalf, dev, {M, N}));
+  p.s = stream_of(dev);
+  return p;
+}
+PyObject* finished(int rc, const Product& p, PyObject* out) { return out == Py_None ? result(rc, p.out) : result(rc, out); }
+
+// (x, codes or None, scales or None)
+PyObject* mx_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 3) throw NotPlain();
+    const Rows r = rows_of(a[0]);
+    const at::Tensor c = a[1] == Py_None ? made(a[0], at::kInt, {r.M, r.K / 8}) : tensor(a[1]);
+    const at::Tensor t = a[2] == Py_None ? made(a[0], at::kByte, {tiles(r.M), r.K / 128, 512}) : tensor(a[2]);
+    void* cp = checked(c, at::kInt, r.dev, {r.M, r.K / 8});
+    void* sp = checked(t, at::kByte, r.dev, {tiles(r.M), r.K / 128, 512});
+    const w4a16_stream_t s = stream_of(r.dev);
+    const int rc = unlocked([&] { return f_mxq(r.x, r.M, r.K, static_cast<uint32_t*>(cp), byte(sp), s); });
+    if (rc) return PyLong_FromLong(rc);
+    PyObject* co = a[1] == Py_None ? THPVariable_Wrap(c) : (Py_INCREF(a[1]), a[1]);
+    PyObject* so = a[2] == Py_None ? THPVariable_Wrap(t) : (Py_INCREF(a[2]), a[2]);
+    PyObject* pair = co && so ? PyTuple_Pack(2, co, so) : nullptr;
+    Py_XDECREF(co);
+    Py_XDECREF(so);
+    return pair;
+  });
+}
+
+// (codes, scales, out or None)
+PyObject* mx_dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 3) throw NotPlain();
+    const Mx m = mx(a[0], a[1]);
+    const at::Tensor out = a[2] == Py_None ? made(a[0], at::kHalf, {m.rows, m.K}) : tensor(a[2]);
+    void* op = checked(out, at::kHalf, m.dev, {m.rows, m.K});
+    const w4a16_stream_t s = stream_of(m.dev);
+    const int rc = unlocked([&] { return f_mxd(m.codes, m.scales, m.rows, m.K, half(op), s); });
+    return a[2] == Py_None ? result(rc, out) : result(rc, a[2]);
+  });
+}
+
+// (x, codes, scales, bias or None, residual or None, out or None, workspace, err_flag or None)
+PyObject* mx_gemm16(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 8) throw NotPlain();
+    const Rows r = rows_of(a[0]);
+    const Mx w = mx(a[1], a[2], r.K);
+    const uint16_t *bias = optional_half(a[3], r.dev, {w.rows}), *res = optional_half(a[4], r.dev, {r.M, w.rows});
+    const Product p = product(a[0], r.M, w.rows, r.dev, a[5], a[6], a[7]);
+    const int rc = unlocked([&] {
+      return f_mx16(r.x, r.M, r.K, w.codes, w.scales, w.rows, bias, res, p.y, p.ws, p.wb, p.err, p.s);
+    });
+    return finished(rc, p, a[5]);
+  });
+}
+
+// (x, codes_gate, scales_gate, codes_up, scales_up, out or None, workspace, err_flag or None)
+PyObject* mx_silu(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 8) throw NotPlain();
+    const Rows r = rows_of(a[0]);
+    const Mx g = mx(a[1], a[2], r.K), u = mx(a[3], a[4], r.K);
+    if (g.rows != u.rows) throw NotPlain();
+    const Product p = product(a[0], r.M, g.rows, r.dev, a[5], a[6], a[7]);
+    const int rc = unlocked([&] {
+      return f_mxsilu(r.x, r.M, r.K, g.codes, g.scales, u.codes, u.scales, g.rows, p.y, p.ws, p.wb, p.err, p.s);
+    });
+    return finished(rc, p, a[5]);
+  });
+}
+
+// (x_codes, x_scales, codes, scales, bias or None, residual or None, out or None, workspace, err_flag or None)
+PyObject* mx_gemm4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    if (n != 9) throw NotPlain();
+    const Mx x = mx(a[0], a[1]), w = mx(a[2], a[3], x.K);
+    if (w.dev != x.dev) throw NotPlain();
+    const uint16_t *bias = optional_half(a[4], x.dev, {w.rows}), *res = optional_half(a[5], x.dev, {x.rows, w.rows});
+    const Product p = product(a[0], x.rows, w.rows, x.dev, a[6], a[7], a[8]);
+    const int rc = unlocked([&] {
+      return f_mx4(x.codes, x.scales, x.rows, x.K, w.codes, w.scales, w.rows, bias, res, p.y, p.ws, p.wb, p.err, p.s);
+    });
+    return finished(rc, p, a[6]);
+  });
+}
+
+// (addresses of the entries, in the order of the declarations above)
+constexpr int ENTRIES = 12;
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* p[7];
-  if (n != 7) {
-    PyErr_SetString(PyExc_ValueError, "bind: seven addresses expected");
+  void* p[ENTRIES];
+  if (n != ENTRIES) {
+    PyErr_SetString(PyExc_ValueError, "bind: twelve addresses expected");
     return nullptr;
   }
-  for (int i = 0; i < 7; ++i) {
+  for (int i = 0; i < ENTRIES; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (!p[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: null address");
@@ -316,11 +467,17 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   f_win16 = reinterpret_cast<decltype(f_win16)>(p[4]);
   f_win8 = reinterpret_cast<decltype(f_win8)>(p[5]);
   f_win4 = reinterpret_cast<decltype(f_win4)>(p[6]);
+  f_mxq = reinterpret_cast<decltype(f_mxq)>(p[7]);
+  f_mxd = reinterpret_cast<decltype(f_mxd)>(p[8]);
+  f_mx16 = reinterpret_cast<decltype(f_mx16)>(p[9]);
+  f_mxsilu = reinterpret_cast<decltype(f_mxsilu)>(p[10]);
+  f_mx4 = reinterpret_cast<decltype(f_mx4)>(p[11]);
   Py_RETURN_NONE;
 }
 
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(append), ENTRY(read), ENTRY(decode_int4), ENTRY(decode_window), ENTRY(bind),
+PyMethodDef methods[] = {ENTRY(append), ENTRY(read), ENTRY(decode_int4), ENTRY(decode_window), ENTRY(mx_quantize), ENTRY(mx_dequantize),
+                         ENTRY(mx_gemm16), ENTRY(mx_silu), ENTRY(mx_gemm4), ENTRY(bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_w4a16_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
