@@ -88,7 +88,7 @@ __device__ __forceinline__ void mx_store8(const MxArgs& a, size_t at, float4 lo,
                         __floats2half2_rn(hi.z, hi.w)};
   *reinterpret_cast<uint4*>(a.y + at) = *reinterpret_cast<const uint4*>(h);
 }
-bool mxfp4_matvec_serves(int M, int K);
+bool mxfp4_matvec_serves(int M, int N, int K, bool silu);
 int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s);
 int launch_mxfp4_a16(const MxArgs& a, bool silu, cudaStream_t s);
 int launch_mxfp4_a4(const MxArgs& a, cudaStream_t s);

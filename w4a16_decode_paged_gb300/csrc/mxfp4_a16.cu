@@ -98,6 +98,9 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
   if (warp == 0) {
     // ---- producer ----
     if (mt_elect()) {
+      mt_prefetch_map(&p.tm_w[0]);
+      if (p.silu) mt_prefetch_map(&p.tm_w[1]);
+      mt_prefetch_map(&p.tm_x);
       int mt, nt, part, k0, k1;
       if (blockIdx.x < p.items) {
         // weights may come from the call just before: into L2 ahead of the wait, read behind it
@@ -332,13 +335,24 @@ static int ma_tiles(int M, int N, bool silu) {
 }
 constexpr int MA_SPLIT = 16;
 
-// the deal for these sizes with room for `bytes` of workspace
+// The deal for these sizes with room for `bytes` of workspace: the split along K,
+// or none, whose busiest CTA has least to do, in cycles as measured (a stage 980,
+// 1150, 1580 for 32, 64, 128 rows; a tile's epilogue 2000 to 8000; the join 5000).
 static MtDeal ma_deal(int M, int N, int K, bool silu, size_t bytes, int slots) {
-  for (int most = MA_SPLIT; most > 1; --most) {
-    const MtDeal d = mt_deal(ma_tiles(M, N, silu), K / MA_K, slots, most);
-    if (mt_workspace(d, ma_cols(M), 256) <= bytes) return d;
+  const int nc = ma_cols(M), tiles = ma_tiles(M, N, silu), stages = K / MA_K;
+  const double stage = nc == 32 ? 980 : nc == 64 ? 1150 : 1580, tail = 62.0 * nc;
+  MtDeal best = mt_deal(tiles, stages, slots, 1);
+  double cost = (double)((tiles + slots - 1) / slots) * (stages * stage + tail);
+  for (int most = 2; most <= MA_SPLIT; ++most) {
+    const MtDeal d = mt_deal(tiles, stages, slots, most);
+    if (d.split != most || mt_workspace(d, nc, 256) > bytes) continue;
+    const double v = (double)(d.whole / slots) * (stages * stage + tail) + (stages + most - 1) / most * stage + tail + 5000;
+    if (v < cost) {
+      cost = v;
+      best = d;
+    }
   }
-  return mt_deal(ma_tiles(M, N, silu), K / MA_K, slots, 1);
+  return best;
 }
 
 size_t mxfp4_a16_workspace(int M, int N, int K, bool silu) {

@@ -101,6 +101,8 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
   if (warp == 0) {
     // ---- producer ----
     if (mt_elect()) {
+      mt_prefetch_map(&p.tm_w);
+      mt_prefetch_map(&p.tm_x);
       int mt, nt, part, k0, k1;
       if (blockIdx.x < p.items) {
         // weights may come from the call just before: into L2 ahead of the wait, read behind it
@@ -224,18 +226,21 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
       if (!__all_sync(0xffffffffu, mt_wait(&dfull, n & 1, &s_fail))) break;
       mt_fence_after();
       const bool parts = i >= p.whole && p.split > 1;
-#pragma unroll 1
+      float v[32];
+      auto fetch = [&](int g, int c0) {  // 32 columns of this lane, on their way
+#pragma unroll
+        for (int c = 0; c < 32; c += 8)
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                       : "=f"(v[c]), "=f"(v[c + 1]), "=f"(v[c + 2]), "=f"(v[c + 3]), "=f"(v[c + 4]), "=f"(v[c + 5]),
+                         "=f"(v[c + 6]), "=f"(v[c + 7])
+                       : "r"(lanes + (uint32_t)(g * NC + col0 + c0)  + c));
+      };
+      fetch(0, 0);
+#pragma unroll
       for (int g = 0; g < NA; ++g) {
         const int r = g * 128 + 32 * quad + lane, m = mt * NA * 128 + r;
 #pragma unroll
         for (int c0 = 0; c0 < CW; c0 += 32) {
-          float v[32];
-#pragma unroll
-          for (int c = 0; c < 32; c += 8)
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                         : "=f"(v[c]), "=f"(v[c + 1]), "=f"(v[c + 2]), "=f"(v[c + 3]), "=f"(v[c + 4]), "=f"(v[c + 5]),
-                           "=f"(v[c + 6]), "=f"(v[c + 7])
-                         : "r"(lanes + (uint32_t)(g * NC + col0 + c0 + c)));
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           if (c0 + 32 == CW) {
             mt_fence_before();
@@ -250,6 +255,8 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
             for (int c = 0; c < 32; c += 4)
               *reinterpret_cast<float4*>(turn + lane * MB_PITCH + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
             __syncwarp();
+            if (c0 + 32 < CW) fetch(g, c0 + 32);
+            else if (g + 1 < NA) fetch(g + 1, 0);
             const int q = (lane & 3) * 8, n8 = nn + q;
             float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
             if (p.a.bias && !parts && n8 < N) mx_add8(b0, b1, p.a.bias + n8);
@@ -270,15 +277,18 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
                 mx_store8(p.a, (size_t)mm * N + n8, lo, hi);
               }
             }
-          } else if (m < M) {
+          } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) {
-              if (nn + c >= N) break;
+              if (m >= M || nn + c >= N) break;
               const size_t at = (size_t)m * N + nn + c;
               if (p.a.bias) v[c] += __half2float(p.a.bias[nn + c]);
               if (p.a.residual) v[c] += __half2float(p.a.residual[at]);
               p.a.y[at] = __float2half_rn(v[c]);
             }
+            __syncwarp();
+            if (c0 + 32 < CW) fetch(g, c0 + 32);
+            else if (g + 1 < NA) fetch(g + 1, 0);
           }
         }
       }

@@ -30,7 +30,7 @@ constexpr int MV_THREADS = 32 * MV_WARPS;
 constexpr int MV_ROWS = 16;
 constexpr int MV_GROUPS = 32;    // groups of a cluster between two joins
 template <int MS>
-constexpr int MV_D = MS == 1 ? 4 : 3;
+constexpr int MV_D = MS == 1 ? 4 : 3;  // units in flight per warp
 
 template <bool FIRST>  // FIRST: d = a b, else d += a b
 __device__ __forceinline__ void mv_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -89,7 +89,7 @@ template <int MS>
 struct MvShape {
   static constexpr int MT = 2 * MS;                      // rows of x
   static constexpr int PIECE = MT * MV_ROWS;             // floats
-  static constexpr int D = MV_D<MS>;                     // units in flight per warp
+  static constexpr int D = MV_D<MS>;
   static constexpr int XAT = 1088;                       // a unit: 16 rows x (64 bytes of codes, 4 of scales), x
   static constexpr int UNIT = XAT + MT * 256;
   static constexpr int RING = MV_WARPS * D * UNIT;
@@ -100,9 +100,10 @@ struct MvShape {
 };
 
 // NW weight matrices (2: gate and up, their groups in turn); MS MMAs per 16 k, 2
-// rows of x each.  64 registers, so that the next kernel's CTA fits beside this one.
+// rows of x each.  Up to 4 rows 64 registers, so that the next kernel's CTA fits
+// beside this one.
 template <int NW, int MS>
-__global__ void __launch_bounds__(MV_THREADS, 2)
+__global__ void __launch_bounds__(MV_THREADS, MS <= 2 ? 2 : 1)
     w4pg_mxfp4_matvec(const __grid_constant__ MxArgs a, int clog, int groups, int gcap) {
   using SH = MvShape<MS>;
   constexpr int MT = SH::MT, PIECE = SH::PIECE, D = SH::D;
@@ -358,7 +359,7 @@ static MvPlan mv_plan(int N, int K) {
   });
   const int groups = N / 128 * 8 + std::min(8, (N % 128 + 3) / 4);  // (those of the last tile that have rows)
   const int ktiles = K / 128, sms = num_sms();
-  const int per = (long long)NW * groups * ktiles >= (long long)MV_TWO * MV_WARPS * sms ? 2 : 1;
+  const int per = MS <= 2 && (long long)NW * groups * ktiles >= (long long)MV_TWO * MV_WARPS * sms ? 2 : 1;
   MvPlan best = {};
   double cost = 0;
   for (int l = 0; l < 4; ++l) {
@@ -396,11 +397,16 @@ static int mv_launch(const MxArgs& a, cudaStream_t s) {
   return W4A16_OK;
 }
 
-bool mxfp4_matvec_serves(int M, int) { return M <= 4; }
+// Up to 4 rows always.  5 to 8 take twice the MMAs a unit and still beat the tensor
+// cores while start and join decide, up to MV_SMALL scale tiles in all.
+constexpr long long MV_SMALL = 4096;
+bool mxfp4_matvec_serves(int M, int N, int K, bool silu) {
+  return M <= 4 || (M <= 8 && (long long)(N + 127) / 128 * (K / 128) * (silu ? 2 : 1) <= MV_SMALL);
+}
 
 int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s) {
-  if (silu) return a.M <= 2 ? mv_launch<2, 1>(a, s) : mv_launch<2, 2>(a, s);
-  return a.M <= 2 ? mv_launch<1, 1>(a, s) : mv_launch<1, 2>(a, s);
+  if (silu) return a.M <= 2 ? mv_launch<2, 1>(a, s) : a.M <= 4 ? mv_launch<2, 2>(a, s) : mv_launch<2, 4>(a, s);
+  return a.M <= 2 ? mv_launch<1, 1>(a, s) : a.M <= 4 ? mv_launch<1, 2>(a, s) : mv_launch<1, 4>(a, s);
 }
 
 }  // namespace w4

@@ -58,6 +58,9 @@ __device__ __forceinline__ void mt_prefetch_2d(const CUtensorMap* map, int c0, i
                "r"(c0), "r"(c1)
                : "memory");
 }
+__device__ __forceinline__ void mt_prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 // `bytes` (a multiple of 16) in one piece
 __device__ __forceinline__ void mt_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
