@@ -73,20 +73,17 @@ struct MxArgs {
   size_t workspace_bytes;
   int32_t* err_flag;
 };
-// eight neighbouring fp16 numbers added to eight sums
-__device__ __forceinline__ void mx_add8(float4& lo, float4& hi, const __half* p) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
+// eight fp16 numbers added to eight sums
+__device__ __forceinline__ void mx_add8(float4& lo, float4& hi, const uint4& r) {
   const float2 r0 = __half22float2(*reinterpret_cast<const __half2*>(&r.x)), r1 = __half22float2(*reinterpret_cast<const __half2*>(&r.y));
   const float2 r2 = __half22float2(*reinterpret_cast<const __half2*>(&r.z)), r3 = __half22float2(*reinterpret_cast<const __half2*>(&r.w));
   lo.x += r0.x, lo.y += r0.y, lo.z += r1.x, lo.w += r1.y;
   hi.x += r2.x, hi.y += r2.y, hi.z += r3.x, hi.w += r3.y;
 }
-// eight neighbouring outputs, plus the residual, in one 16-byte store (at % 8 == 0)
-__device__ __forceinline__ void mx_store8(const MxArgs& a, size_t at, float4 lo, float4 hi) {
-  if (a.residual) mx_add8(lo, hi, a.residual + at);
+__device__ __forceinline__ uint4 mx_round8(const float4& lo, const float4& hi) {
   const __half2 h[4] = {__floats2half2_rn(lo.x, lo.y), __floats2half2_rn(lo.z, lo.w), __floats2half2_rn(hi.x, hi.y),
                         __floats2half2_rn(hi.z, hi.w)};
-  *reinterpret_cast<uint4*>(a.y + at) = *reinterpret_cast<const uint4*>(h);
+  return *reinterpret_cast<const uint4*>(h);
 }
 bool mxfp4_matvec_serves(int M, int N, int K, bool silu);
 int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s);

@@ -49,6 +49,12 @@ struct MaArgs {
   CUtensorMap tm_w[2], tm_x;
 };
 
+__device__ __forceinline__ void mx_tmem_ld8(float (&v)[8], uint32_t taddr) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "r"(taddr));
+}
+
 template <int NC>
 __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_constant__ MaArgs p) {
   using SH = MaShape<NC>;
@@ -237,65 +243,58 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
       ok = __all_sync(0xffffffffu, mt_wait(&dfull, n & 1, &s_fail));
       if (!ok) break;
       mt_fence_after();
-      constexpr int CW = NC / 4;
-      const int col0 = (e >> 2) * CW, m0 = mt * NC + col0;
-      uint32_t acc[2][CW];
-#pragma unroll
-      for (int gg = 0; gg < 2; ++gg)
-#pragma unroll
-        for (int c = 0; c < CW; c += 8)
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                       : "=r"(acc[gg][c]), "=r"(acc[gg][c + 1]), "=r"(acc[gg][c + 2]), "=r"(acc[gg][c + 3]),
-                         "=r"(acc[gg][c + 4]), "=r"(acc[gg][c + 5]), "=r"(acc[gg][c + 6]), "=r"(acc[gg][c + 7])
-                       : "r"(lanes + (uint32_t)(gg * NC + col0 + c)));
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-      mt_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&dempty);
-      if (i >= p.whole && p.split > 1) {
-        float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NC * 256);
-#pragma unroll
-        for (int gg = 0; gg < 2; ++gg)
-#pragma unroll
-          for (int c = 0; c < CW; ++c)
-            if (m0 + c < M) mine[(col0 + c) * 256 + gg * 128 + row] = __uint_as_float(acc[gg][c]);
-        continue;
-      }
-#pragma unroll
-      for (int gg = 0; gg < 2; ++gg) {
-        if (p.silu && gg) break;
-        const int n0 = (nt + gg) * 128 + 32 * quad;
-        if (n0 >= N) break;
+      constexpr int CW = NC / 4, PC = CW / 8;
+      const int col0 = (e >> 2) * CW;
+      const bool parts = i >= p.whole && p.split > 1;
+      float* mine = parts ? p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NC * 256) : nullptr;
+      const int rounds = p.silu && !parts ? PC : 2 * PC;  // silu takes both tiles' columns at once
+#pragma unroll 1
+      for (int pc = 0; pc < rounds; ++pc) {
+        const int gg = pc >= PC ? 1 : 0, c0 = col0 + (pc - gg * PC) * 8, m0 = mt * NC + c0;
+        const int n0 = (nt + gg) * 128 + 32 * quad;      // the quadrant's first weight row
+        float v[8], u[8];
+        mx_tmem_ld8(v, lanes + (uint32_t)(gg * NC + c0));
+        if (p.silu && !parts) mx_tmem_ld8(u, lanes + (uint32_t)(NC + c0));
+        // this lane's share of the turned outputs: row m, 8 weight rows from nn
+        const int m = m0 + (lane >> 2), nn = n0 + (lane & 3) * 8;
+        const bool inside = m < M && nn < N && !parts;
+        const size_t at = (size_t)m * N + nn;
+        uint4 add = make_uint4(0, 0, 0, 0);
+        if (wide && inside && p.a.residual) add = *reinterpret_cast<const uint4*>(p.a.residual + at);
         const float bias = p.a.bias && n0 + lane < N ? __half2float(p.a.bias[n0 + lane]) : 0.f;
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        if (pc == rounds - 1) {
+          mt_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&dempty);
+        }
+        if (parts) {
 #pragma unroll
-        for (int c0 = 0; c0 < CW; c0 += 8) {
-          if (m0 + c0 >= M) break;
-          float v[8];
+          for (int c = 0; c < 8; ++c)
+            if (m0 + c < M) mine[(c0 + c) * 256 + gg * 128 + row] = v[c];
+          continue;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (p.silu) v[c] = v[c] / (1.f + expf(-v[c])) * u[c];
+          v[c] += bias;
+        }
+        if (wide) {
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) turn[c * 32 + lane] = v[c];
+          __syncwarp();
+          float4 lo = *reinterpret_cast<const float4*>(turn + lane * 8), hi = *reinterpret_cast<const float4*>(turn + lane * 8 + 4);
+          if (p.a.residual) mx_add8(lo, hi, add);
+          const uint4 o = mx_round8(lo, hi);
+          if (inside) *reinterpret_cast<uint4*>(p.a.y + at) = o;
+        } else if (n0 + lane < N) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            v[c] = __uint_as_float(acc[gg][c0 + c]);
-            if (p.silu) v[c] = v[c] / (1.f + expf(-v[c])) * __uint_as_float(acc[1][c0 + c]);
-            v[c] += bias;
-          }
-          if (wide) {
-            __syncwarp();
-#pragma unroll
-            for (int c = 0; c < 8; ++c) turn[c * 32 + lane] = v[c];
-            __syncwarp();
-            // lane: row m0 + c0 + lane / 4, 8 weight rows
-            const int m = m0 + c0 + (lane >> 2), nn = n0 + (lane & 3) * 8;
-            if (m < M && nn < N) {
-              const float4 lo = *reinterpret_cast<const float4*>(turn + lane * 8), hi = *reinterpret_cast<const float4*>(turn + lane * 8 + 4);
-              mx_store8(p.a, (size_t)m * N + nn, lo, hi);
-            }
-          } else if (n0 + lane < N) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              if (m0 + c0 + c >= M) break;
-              const size_t at = (size_t)(m0 + c0 + c) * N + n0 + lane;
-              if (p.a.residual) v[c] += __half2float(p.a.residual[at]);
-              p.a.y[at] = __float2half_rn(v[c]);
-            }
+            if (m0 + c >= M) break;
+            const size_t at = (size_t)(m0 + c) * N + n0 + lane;
+            if (p.a.residual) v[c] += __half2float(p.a.residual[at]);
+            p.a.y[at] = __float2half_rn(v[c]);
           }
         }
       }

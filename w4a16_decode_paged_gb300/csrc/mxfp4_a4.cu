@@ -226,69 +226,84 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
       if (!__all_sync(0xffffffffu, mt_wait(&dfull, n & 1, &s_fail))) break;
       mt_fence_after();
       const bool parts = i >= p.whole && p.split > 1;
-      float v[32];
-      auto fetch = [&](int g, int c0) {  // 32 columns of this lane, on their way
+      constexpr int PC = CW / 32;
+#pragma unroll 1
+      for (int pc = 0; pc < NA * PC; ++pc) {
+        const int g = NA == 2 && pc >= PC ? 1 : 0, c0 = (pc - g * PC) * 32;
+        const int r = g * 128 + 32 * quad, m = mt * NA * 128 + r, nn = nt * NC + col0 + c0;  // first row, first column
+        float v[32];
 #pragma unroll
         for (int c = 0; c < 32; c += 8)
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                        : "=f"(v[c]), "=f"(v[c + 1]), "=f"(v[c + 2]), "=f"(v[c + 3]), "=f"(v[c + 4]), "=f"(v[c + 5]),
                          "=f"(v[c + 6]), "=f"(v[c + 7])
-                       : "r"(lanes + (uint32_t)(g * NC + col0 + c0)  + c));
-      };
-      fetch(0, 0);
+                       : "r"(lanes + (uint32_t)(g * NC + col0 + c0 + c)));
+        // This lane's share of the turned outputs: 8 columns from n8 of rows m + lane / 4
+        // + 8 h.  What is added to them is asked for ahead; nothing branches between the
+        // loads and the stores, whose latencies are all a tile's epilogue is (4 rows at a
+        // time behind branches: 0.65 us a piece).
+        const int q = (lane & 3) * 8, n8 = nn + q, r8 = lane >> 2;
+        const bool inside = n8 < N && !parts;
+        const size_t at = (size_t)(m + r8) * N + n8;
+        uint4 add[4], bias = make_uint4(0, 0, 0, 0);
+        if (wide && inside) {
+          if (p.a.bias) bias = *reinterpret_cast<const uint4*>(p.a.bias + n8);
+          if (p.a.residual) {
 #pragma unroll
-      for (int g = 0; g < NA; ++g) {
-        const int r = g * 128 + 32 * quad + lane, m = mt * NA * 128 + r;
-#pragma unroll
-        for (int c0 = 0; c0 < CW; c0 += 32) {
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          if (c0 + 32 == CW) {
-            mt_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&dempty[g]);
+            for (int h = 0; h < 4; ++h)
+              if (m + r8 + 8 * h < M) add[h] = *reinterpret_cast<const uint4*>(p.a.residual + at + (size_t)(8 * h) * N);
           }
-          const int nn = nt * NC + col0 + c0;
-          if (parts || wide) {
-            // turned in shared memory: 4 lanes have 32 columns of a row, 8 rows a store
-            __syncwarp();
+        }
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        if (c0 + 32 == CW) {
+          mt_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&dempty[g]);
+        }
+        // turned in shared memory: 4 lanes have 32 columns of a row, 8 rows a store
+        __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              *reinterpret_cast<float4*>(turn + lane * MB_PITCH + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
-            __syncwarp();
-            if (c0 + 32 < CW) fetch(g, c0 + 32);
-            else if (g + 1 < NA) fetch(g + 1, 0);
-            const int q = (lane & 3) * 8, n8 = nn + q;
-            float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
-            if (p.a.bias && !parts && n8 < N) mx_add8(b0, b1, p.a.bias + n8);
+        for (int c = 0; c < 32; c += 4)
+          *reinterpret_cast<float4*>(turn + lane * MB_PITCH + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        __syncwarp();
+        if (parts || wide) {
+          float4 lo[4], hi[4];
 #pragma unroll
-            for (int h = 0; h < 32; h += 8) {
-              const int rr = h + (lane >> 2), mm = m - lane + rr;
-              float4 lo = *reinterpret_cast<const float4*>(turn + rr * MB_PITCH + q);
-              float4 hi = *reinterpret_cast<const float4*>(turn + rr * MB_PITCH + q + 4);
-              if (mm >= M || n8 >= N) continue;
-              if (parts) {
-                float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NA * 128 * NC) +
-                              (size_t)(r - lane + rr) * NC + col0 + c0 + q;
-                *reinterpret_cast<float4*>(mine) = lo;
-                *reinterpret_cast<float4*>(mine + 4) = hi;
-              } else {
-                lo.x += b0.x, lo.y += b0.y, lo.z += b0.z, lo.w += b0.w;
-                hi.x += b1.x, hi.y += b1.y, hi.z += b1.z, hi.w += b1.w;
-                mx_store8(p.a, (size_t)mm * N + n8, lo, hi);
+          for (int h = 0; h < 4; ++h) {
+            lo[h] = *reinterpret_cast<const float4*>(turn + (r8 + 8 * h) * MB_PITCH + q);
+            hi[h] = *reinterpret_cast<const float4*>(turn + (r8 + 8 * h) * MB_PITCH + q + 4);
+          }
+          if (parts) {
+            float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NA * 128 * NC) + (size_t)(r + r8) * NC + col0 + c0 + q;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+              if (m + r8 + 8 * h < M) {
+                *reinterpret_cast<float4*>(mine + 8 * h * NC) = lo[h];
+                *reinterpret_cast<float4*>(mine + 8 * h * NC + 4) = hi[h];
               }
-            }
           } else {
+            if (p.a.bias) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (m >= M || nn + c >= N) break;
-              const size_t at = (size_t)m * N + nn + c;
-              if (p.a.bias) v[c] += __half2float(p.a.bias[nn + c]);
-              if (p.a.residual) v[c] += __half2float(p.a.residual[at]);
-              p.a.y[at] = __float2half_rn(v[c]);
+              for (int h = 0; h < 4; ++h) mx_add8(lo[h], hi[h], bias);
             }
-            __syncwarp();
-            if (c0 + 32 < CW) fetch(g, c0 + 32);
-            else if (g + 1 < NA) fetch(g + 1, 0);
+            if (p.a.residual) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) mx_add8(lo[h], hi[h], add[h]);
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const uint4 o = mx_round8(lo[h], hi[h]);
+              if (inside && m + r8 + 8 * h < M) *reinterpret_cast<uint4*>(p.a.y + at + (size_t)(8 * h) * N) = o;
+            }
+          }
+        } else if (nn + lane < N) {
+          const float bias = p.a.bias ? __half2float(p.a.bias[nn + lane]) : 0.f;
+#pragma unroll 4
+          for (int rr = 0; rr < 32 && m + rr < M; ++rr) {
+            const size_t at = (size_t)(m + rr) * N + nn + lane;
+            float f = turn[rr * MB_PITCH + lane] + bias;
+            if (p.a.residual) f += __half2float(p.a.residual[at]);
+            p.a.y[at] = __float2half_rn(f);
           }
         }
       }

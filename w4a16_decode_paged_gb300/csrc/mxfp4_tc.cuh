@@ -13,13 +13,7 @@
 
 namespace w4 {
 
-constexpr unsigned long long MT_TIMEOUT_NS = 2000000000ull;
-
-__device__ __forceinline__ unsigned long long mt_now() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
+constexpr long long MT_TIMEOUT_CYCLES = 4000000000ll;  // 2 s at the highest clock
 
 // One lane of a converged warp.  (Chosen by elect.sync, and with the warp's number
 // taken from one lane, the compiler knows what follows to be uniform: MMAs behind
@@ -34,12 +28,12 @@ __device__ __forceinline__ bool mt_elect() {
 // fail null: only its own bound counts (drains).
 __device__ __forceinline__ bool mt_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
   if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = mt_now();
+  const long long t0 = clock64();
   while (true) {
     for (int i = 0; i < 32; ++i)
       if (mbar_try_wait(bar, parity)) return true;
     if (fail && *fail) return false;
-    if (mt_now() - t0 > MT_TIMEOUT_NS) {
+    if (clock64() - t0 > MT_TIMEOUT_CYCLES) {
       if (fail) *fail = 1;
       return false;
     }
