@@ -8,43 +8,93 @@
 
 namespace w4 {
 
-// The sums of tiles that were split along K: a thread adds the parts of four
-// neighbouring outputs, in order.
+// The sums of tiles that were split along K: a thread adds, in order, the parts of
+// four neighbouring outputs in each of R rows; R times MJ_LOADS / R parts are asked
+// for at once, so that few parts (a prompt's tiles) and many (a decode batch's) both
+// keep eight loads in flight.
+constexpr int MJ_LOADS = 8;
+
+template <bool SILU, int R>
 __global__ void __launch_bounds__(256) w4pg_mxfp4_join(const __grid_constant__ MtJoin j) {
+  constexpr int AHEAD = MJ_LOADS / R;
   pdl_wait_then_trigger();
-  const int width = (j.silu ? 128 : j.tn) / 4;     // threads along a row
-  const int i = blockIdx.x * 256 + threadIdx.x, c = i % width * 4, row = i / width % j.tm, t = i / width / j.tm;
-  if (t >= j.tiles) return;
-  const int tile = j.first + t, m = tile % j.mtiles * j.tm + row, n = tile / j.mtiles * j.tstep + c;
-  if (m >= j.a.M || n >= j.a.N) return;
-  const size_t part = (size_t)j.tm * j.tn;
-  const float* p = j.parts + (size_t)t * j.split * part + (size_t)row * j.tn + c;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f), u = v;
-#pragma unroll 8
-  for (int q = 0; q < j.split; ++q) {
-    const float4 w = __ldcg(reinterpret_cast<const float4*>(p + q * part));
-    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-    if (j.silu) {
-      const float4 z = __ldcg(reinterpret_cast<const float4*>(p + q * part + 128));
-      u.x += z.x, u.y += z.y, u.z += z.z, u.w += z.w;
-    }
-  }
-  float o[4] = {v.x, v.y, v.z, v.w};
-  const float up[4] = {u.x, u.y, u.z, u.w};
+  const int width = (SILU ? 128 : j.tn) / 4;       // threads along a row
+  const int i = blockIdx.x * 256 + threadIdx.x, row0 = i / width, c = (i - row0 * width) * 4, rstep = j.tm / R;
+  const int tile = j.first + blockIdx.y, nt = tile / j.mtiles, n = nt * j.tstep + c;
+  const int N = j.a.N, m0 = (tile - nt * j.mtiles) * j.tm + row0;
+  if (row0 >= rstep || n >= N) return;
+  const size_t part = (size_t)j.tm * j.tn / 4;
+  const float4* p = reinterpret_cast<const float4*>(j.parts) + (size_t)blockIdx.y * j.split * part + (row0 * j.tn + c) / 4;
+  const bool wide = N % 4 == 0;                    // four outputs lie on 8 bytes
+  uint2 res[R];
+  if (wide && j.a.residual) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (n + k >= j.a.N) break;
-    const size_t at = (size_t)m * j.a.N + n + k;
-    if (j.silu) o[k] = o[k] / (1.f + expf(-o[k])) * up[k];
-    if (j.a.bias) o[k] += __half2float(j.a.bias[n + k]);
-    if (j.a.residual) o[k] += __half2float(j.a.residual[at]);
-    j.a.y[at] = __float2half_rn(o[k]);
+    for (int r = 0; r < R; ++r)
+      if (m0 + r * rstep < j.a.M) res[r] = *reinterpret_cast<const uint2*>(j.a.residual + (size_t)(m0 + r * rstep) * N + n);
+  }
+  auto sums = [&](float (&v)[R][4], const float4* p) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r][0] = v[r][1] = v[r][2] = v[r][3] = 0.f;
+    for (int q = 0; q < j.split; q += AHEAD) {
+      float4 a[R][AHEAD];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+          if (q + k < j.split && m0 + r * rstep < j.a.M) a[r][k] = __ldcg(p + (q + k) * part + (size_t)r * rstep * j.tn / 4);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+          if (q + k < j.split) v[r][0] += a[r][k].x, v[r][1] += a[r][k].y, v[r][2] += a[r][k].z, v[r][3] += a[r][k].w;
+    }
+  };
+  float v[R][4];
+  sums(v, p);
+  if (SILU) {
+    float u[R][4];
+    sums(u, p + 32);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[r][k] = v[r][k] / (1.f + expf(-v[r][k])) * u[r][k];
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int m = m0 + r * rstep;
+    if (m >= j.a.M) break;
+    const size_t at = (size_t)m * N + n;
+    if (wide && j.a.residual) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&res[r].x)), b = __half22float2(*reinterpret_cast<const __half2*>(&res[r].y));
+      v[r][0] += a.x, v[r][1] += a.y, v[r][2] += b.x, v[r][3] += b.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (n + k >= N) break;
+      if (j.a.bias) v[r][k] += __half2float(j.a.bias[n + k]);
+      if (!wide) {
+        if (j.a.residual) v[r][k] += __half2float(j.a.residual[at + k]);
+        j.a.y[at + k] = __float2half_rn(v[r][k]);
+      }
+    }
+    if (wide) {
+      const __half2 h[2] = {__floats2half2_rn(v[r][0], v[r][1]), __floats2half2_rn(v[r][2], v[r][3])};
+      *reinterpret_cast<uint2*>(j.a.y + at) = *reinterpret_cast<const uint2*>(h);
+    }
   }
 }
 
+template <bool SILU, int R>
+static cudaError_t mj_launch(const MtJoin& j, cudaStream_t s) {
+  const dim3 grid((unsigned)((j.tm / R * (SILU ? 128 : j.tn) / 4 + 255) / 256), (unsigned)j.tiles);
+  return launch_pdl(w4pg_mxfp4_join<SILU, R>, grid, dim3(256), 0, s, j);
+}
+
 int launch_mxfp4_join(const MtJoin& j, cudaStream_t s) {
-  const long long threads = (long long)j.tiles * j.tm * (j.silu ? 128 : j.tn) / 4;
-  const cudaError_t e = launch_pdl(w4pg_mxfp4_join, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, s, j);
+  // four parts and fewer: several rows a thread
+  cudaError_t e;
+  if (j.silu) e = j.split > 4 ? mj_launch<true, 1>(j, s) : j.split > 2 ? mj_launch<true, 2>(j, s) : mj_launch<true, 4>(j, s);
+  else e = j.split > 4 ? mj_launch<false, 1>(j, s) : j.split > 2 ? mj_launch<false, 2>(j, s) : mj_launch<false, 4>(j, s);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "mxfp4 join launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }
