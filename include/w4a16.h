@@ -175,12 +175,12 @@ W4A16_API size_t w4a16_gemm_workspace_size(int M, int K, int N, int silu);
  * call ahead of it on the stream is done: W may come straight out of
  * mxfp4_quantize.
  *
- * workspace: NULL, or device memory of any size, zeroed once before its first
- * use (every call leaves its counters, the first 8 KiB, zero), for products
- * that split K across CTAs: with the *_workspace_size() bytes of a call's
- * sizes it may split as it likes, with less, or none, it splits less or not
- * at all.  One workspace serves calls of different shapes, and the other
- * split-K GEMMs, in turn; calls that overlap on the GPU need one each.
+ * workspace: NULL, or device memory of any size and contents, for products that
+ * split K across CTAs (their partial sums): with the *_workspace_size() bytes of a
+ * call's sizes it may split as it likes, with less, or none, it splits less or
+ * not at all.  Its first 8 KiB are left as they are, so that the split-K GEMMs
+ * above, which keep their counters there, can have the same workspace in turn;
+ * calls that overlap on the GPU need one each.
  * err_flag: int32 device word or NULL: bit 1 is set if a bounded wait inside
  * a kernel gave up (its output is then not valid).
  * ------------------------------------------------------------------------ */

@@ -377,3 +377,168 @@ def test_full_size(api, call, m, n, k):
     rms = float(((y.double() - want) ** 2).mean().sqrt() / (want ** 2).mean().sqrt())
     assert rms <= 2.0 ** -10 / 12 ** 0.5 * 1.02, rms
     assert float(((y.double() - want).abs() / (want.abs() + float((want ** 2).mean().sqrt()))).max()) <= 2.0 ** -10
+
+
+def test_workspace_of_any_contents(api):
+    """Parts are written before they are read, and the block that the other split-K
+    GEMMs keep their counters in is left alone: they share a workspace in turn."""
+    rng = np.random.default_rng(2)
+    m, n, k = 40, 512, 3584
+    x, (w, wv) = activations(rng, m, k), random_matrix(rng, n, k)
+    xd = dev(x)
+    q = api.mxfp4_quantize(xd)
+    assert api.mxfp4_workspace(m, k, n).numel() > 8192 and api.mxfp4_workspace(m, k, n, "a4").numel() > 8192
+    for call, xv in (("a16", x.astype(np.float64)), ("a4", host(api.mxfp4_dequantize(*q)).astype(np.float64))):
+        ws = torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda")
+        y = api.w4a16_gemm_mxfp4(xd, *w, workspace=ws) if call == "a16" else api.w4a4_gemm_mxfp4(*q, *w, workspace=ws)
+        ref.check_product(host(y), xv, wv)
+        assert (ws[:8192] == 255).all() and not (ws[8192:65536] == 255).all()
+    ws = torch.zeros(8 << 20, dtype=torch.uint8, device="cuda")
+    qw = torch.randint(-2 ** 31, 2 ** 31 - 1, (n, k // 8), device="cuda", dtype=torch.int32)
+    sc = torch.full((n, k // 128), 0.01, dtype=torch.float16, device="cuda")
+    want = api.w4a16_gemm(xd[:32], qw, sc)
+    for _ in range(3):
+        ref.check_product(host(api.w4a16_gemm_mxfp4(xd, *w, workspace=ws)), x.astype(np.float64), wv)
+        assert torch.equal(api.w4a16_gemm(xd[:32].contiguous(), qw, sc, workspace=ws), want)
+
+
+@pytest.mark.parametrize("m", [1, 6, 40])
+def test_the_checked_path_is_the_native_one(api, m):
+    """With a stream given the binding checks in Python, without one natively."""
+    rng = np.random.default_rng(m)
+    n, k = 150, 640
+    x, (w, _), (u, _) = dev(activations(rng, m, k)), random_matrix(rng, n, k), random_matrix(rng, n, k)
+    bias, res = dev(rng.standard_normal(n).astype(np.float16)), dev(rng.standard_normal((m, n)).astype(np.float16))
+    ws, here = api.mxfp4_workspace(m, k, n), torch.cuda.current_stream()
+    a, b = api.mxfp4_quantize(x), api.mxfp4_quantize(x, stream=here)
+    assert torch.equal(a[0], b[0]) and torch.equal(api.mxfp4_dequantize(*a), api.mxfp4_dequantize(*b, stream=here))
+    for args in (dict(), dict(bias=bias), dict(residual=res), dict(bias=bias, residual=res)):
+        out = torch.empty((m, n), dtype=torch.float16, device="cuda")
+        y = api.w4a16_gemm_mxfp4(x, *w, workspace=ws, **args)
+        assert torch.equal(y, api.w4a16_gemm_mxfp4(x, *w, workspace=ws, stream=here, **args))
+        assert api.w4a16_gemm_mxfp4(x, *w, workspace=ws, out=out, **args) is out and torch.equal(out, y)
+        y = api.w4a4_gemm_mxfp4(*a, *w, workspace=ws, **args)
+        assert torch.equal(y, api.w4a4_gemm_mxfp4(*a, *w, workspace=ws, stream=here, **args))
+    y = api.w4a16_gemm_silu_mul_mxfp4(x, *w, *u, workspace=ws)
+    assert torch.equal(y, api.w4a16_gemm_silu_mul_mxfp4(x, *w, *u, workspace=ws, stream=here))
+    wu = (w[0].view(torch.uint32), w[1])
+    assert torch.equal(api.w4a16_gemm_mxfp4(x, *wu, workspace=ws), api.w4a16_gemm_mxfp4(x, *w, workspace=ws))
+    with pytest.raises(ValueError, match="codes"):
+        api.w4a16_gemm_mxfp4(x, w[0][:, :-16].contiguous(), w[1], workspace=ws)
+    with pytest.raises(ValueError, match="workspace"):
+        api.w4a16_gemm_mxfp4(x, *w, workspace=ws.view(torch.int8))
+
+
+def _close(y, xv, wv, k):
+    """y against xv . wv^T in 64 bits on the GPU: the bounds of mxfp4_ref.check_product."""
+    s, a = xv @ wv.T, xv.abs() @ wv.abs().T
+    err = ref.sum_error(a, k)
+    over = (y.double() - s).abs() - err - ((s.abs() + err) * 2.0 ** -11).clamp(min=2.0 ** -25)
+    assert bool(torch.isfinite(y).all()) and float(over.max()) <= 0
+
+
+@pytest.mark.parametrize("m", [1, 3, 4, 7, 20, 200])
+def test_the_longest_k(api, m):
+    rng = np.random.default_rng(m)
+    n, k = 24, 131072
+    x, (w, wv) = activations(rng, m, k), random_matrix(rng, n, k)
+    xd, wv = dev(x), dev(wv)
+    _close(api.w4a16_gemm_mxfp4(xd, *w), xd.double(), wv, k)
+    q = api.mxfp4_quantize(xd)
+    _close(api.w4a4_gemm_mxfp4(*q, *w), api.mxfp4_dequantize(*q).double(), wv, k)
+
+
+def test_more_rows_than_a_grid_is_wide(api):
+    rng = np.random.default_rng(6)
+    m, n, k = 70001, 24, 128
+    x, (w, wv), (u, uv) = activations(rng, m, k), random_matrix(rng, n, k), random_matrix(rng, n, k)
+    xd, wv, uv = dev(x), dev(wv), dev(uv)
+    q = api.mxfp4_quantize(xd)
+    code, byte = ref.quantise(x[-500:])
+    assert np.array_equal(host(api.mxfp4_dequantize(*q))[-500:].astype(np.float64), ref.values(code, byte))
+    _close(api.w4a16_gemm_mxfp4(xd, *w), xd.double(), wv, k)
+    _close(api.w4a4_gemm_mxfp4(*q, *w), api.mxfp4_dequantize(*q).double(), wv, k)
+    y = api.w4a16_gemm_silu_mul_mxfp4(xd, *w, *u)
+    ref.check_silu(host(y)[-500:], x[-500:].astype(np.float64), host(wv), host(uv))
+    y = api.w4a16_gemm_mxfp4(api.mxfp4_dequantize(*w), *q)                # as many weight rows
+    _close(y, wv, api.mxfp4_dequantize(*q).double(), k)
+    for rows in (1, 6):
+        y = api.w4a16_gemm_mxfp4(api.mxfp4_dequantize(*w)[:rows].contiguous(), *q)
+        _close(y, wv[:rows], api.mxfp4_dequantize(*q).double(), k)
+
+
+@pytest.mark.parametrize("call", ["a16", "a4"])
+def test_outputs_past_32_bits(api, call):
+    """More than 2^31 outputs: the last rows are what they would be alone."""
+    rng = np.random.default_rng(7)
+    m, n, k = 66000, 33000, 128
+    x, (w, wv) = activations(rng, m, k), random_matrix(rng, n, k)
+    xd = dev(x)
+    q = api.mxfp4_quantize(xd)
+    xv = (xd if call == "a16" else api.mxfp4_dequantize(*q)).double()
+    y = api.w4a16_gemm_mxfp4(xd, *w) if call == "a16" else api.w4a4_gemm_mxfp4(*q, *w)
+    assert y.numel() > 2 ** 31
+    for rows in (slice(0, 40), slice(32000, 32100), slice(65070, 65090), slice(m - 40, m)):
+        _close(y[rows], xv[rows], dev(wv), k)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_sizes(api, seed):
+    """Sizes over the whole range, with and without room to split, odd rows of y."""
+    rng = np.random.default_rng(100 + seed)
+    for _ in range(6):
+        log = lambda lo, hi: int(round(np.exp(rng.uniform(np.log(lo), np.log(hi)))))
+        m, n, k = log(1, 1500), log(1, 4000), 128 * log(1, 40)
+        if rng.random() < 0.5:
+            n = -(-n // 8) * 8
+        x, (w, wv) = activations(rng, m, k), random_matrix(rng, n, k)
+        xd, wv = dev(x), dev(wv)
+        ws = torch.zeros(int(rng.choice([256, 1 << 20, 64 << 20])), dtype=torch.uint8, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        _close(api.w4a16_gemm_mxfp4(xd, *w, workspace=ws, err_flag=err), xd.double(), wv, k)
+        q = api.mxfp4_quantize(xd)
+        _close(api.w4a4_gemm_mxfp4(*q, *w, workspace=ws, err_flag=err), api.mxfp4_dequantize(*q).double(), wv, k)
+        res = dev(rng.standard_normal((m, n)).astype(np.float16))
+        one = torch.cat([xd.double(), torch.ones((m, 1), device="cuda", dtype=torch.double)], 1)
+        bias = dev(rng.standard_normal(n).astype(np.float16))
+        y = api.w4a16_gemm_mxfp4(xd, *w, bias=bias, residual=res, workspace=ws, err_flag=err)
+        s = one @ torch.cat([wv, bias.double()[:, None]], 1).T + res.double()
+        a = xd.double().abs() @ wv.abs().T + bias.double().abs() + res.double().abs()
+        e = ref.sum_error(a, k)
+        assert bool(((y.double() - s).abs() <= e + ((s.abs() + e) * 2.0 ** -11).clamp(min=2.0 ** -25)).all())
+        g = api.w4a16_gemm_silu_mul_mxfp4(xd, *w, *w, workspace=ws, err_flag=err)
+        t = xd.double() @ wv.T
+        e = ref.sum_error(xd.double().abs() @ wv.abs().T, k)
+        want = t * torch.sigmoid(t) * t
+        e = 1.1 * e * (t.abs() + e) + (t * torch.sigmoid(t)).abs() * e + 2.0 ** -21 * want.abs()
+        assert bool(((g.double() - want).abs() <= e + ((want.abs() + e) * 2.0 ** -11).clamp(min=2.0 ** -25)).all())
+        assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("m", [1, 5, 12, 150])
+def test_graphs_of_two_users(api, m):
+    """Two graphs with a workspace each, replayed at once on two streams; one that has
+    the workspace of a call that ran before it."""
+    rng = np.random.default_rng(m)
+    n, k = 256, 2432
+    w, wv = random_matrix(rng, n, k)
+    users = []
+    for _ in range(2):
+        x = dev(activations(rng, m, k))
+        ws = api.mxfp4_workspace(m, k, n)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            api.w4a16_gemm_mxfp4(x, *w, workspace=ws)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = api.w4a16_gemm_mxfp4(x, *w, workspace=ws)
+        users.append((x, s, g, y))
+    for _ in range(30):
+        for x, s, g, y in users:
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for x, s, g, y in users:
+        ref.check_product(host(y), host(x).astype(np.float64), wv)

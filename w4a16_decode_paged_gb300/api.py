@@ -522,15 +522,20 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
 
 
 def mxfp4_workspace(M, K, N, kind="a16", device="cuda"):
-    """A zeroed workspace for w4a16_gemm_mxfp4 (kind "a16"),
-    w4a16_gemm_silu_mul_mxfp4 ("silu") or w4a4_gemm_mxfp4 ("a4") of these sizes;
-    one serves every call that does not overlap another on the GPU."""
+    """A workspace for w4a16_gemm_mxfp4 (kind "a16"), w4a16_gemm_silu_mul_mxfp4
+    ("silu") or w4a4_gemm_mxfp4 ("a4") of these sizes; one serves every call that
+    does not overlap another on the GPU.  It is zeroed, so that the other split-K
+    calls may have it as well; these calls take any contents."""
+    return torch.zeros(_mx_workspace_bytes(M, K, N, kind), dtype=torch.uint8, device=device)
+
+
+def _mx_workspace_bytes(M, K, N, kind):
     if kind not in ("a16", "silu", "a4"):
         raise ValueError(f"kind={kind!r}, expected 'a16', 'silu' or 'a4'")
     lib = load()
     n = lib.w4a4_gemm_mxfp4_workspace_size(M, K, N) if kind == "a4" else \
         lib.w4a16_gemm_mxfp4_workspace_size(M, K, N, int(kind == "silu"))
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+    return max(n, 256)
 
 
 def _mx_buffers(M, K, N, kind, out, workspace, err_flag, bias, residual, like, dev, stream):
@@ -547,15 +552,14 @@ def _mx_buffers(M, K, N, kind, out, workspace, err_flag, bias, residual, like, d
         if out is None:
             out = like.new_empty((M, N), dtype=torch.float16)
         if workspace is None:
-            workspace = mxfp4_workspace(M, K, N, kind, like.device)
+            workspace = like.new_empty(_mx_workspace_bytes(M, K, N, kind), dtype=torch.uint8)
     return out, workspace, err
 
 
 def w4a16_gemm_mxfp4(x, codes, scales, bias=None, residual=None, out=None, workspace=None, err_flag=None, stream=None):
     """y = x . W^T (+ bias) (+ residual): x fp16 [M][K], W MXFP4 (codes int32
-    [N][K/8], scale tiles), from one token to a prompt's rows.  A workspace the
-    caller gives is zeroed once before its first use (mxfp4_workspace); without
-    one, each call makes its own.  residual may be out."""
+    [N][K/8], scale tiles), from one token to a prompt's rows.  Without a
+    workspace (mxfp4_workspace) each call makes its own.  residual may be out."""
     if stream is None and workspace is not None and _cuda(x) and (fast := native()) is not None:
         r = fast.mx_gemm16(x, codes, scales, bias, residual, out, workspace, err_flag)
         if r is not None:

@@ -135,7 +135,7 @@ static int mx_product_checks(const char* what, const MxArgs& a) {
 
 extern "C" size_t w4a16_gemm_mxfp4_workspace_size(int M, int K, int N, int silu) {
   if (M < 1 || K < 128 || N < 1) return 0;
-  return mxfp4_matvec_serves(M, N, K, silu != 0) ? 256 : mxfp4_a16_workspace(M, N, K, silu != 0);
+  return mxfp4_matvec_serves(M, N, K, silu != 0) ? 0 : mxfp4_a16_workspace(M, N, K, silu != 0);
 }
 extern "C" size_t w4a4_gemm_mxfp4_workspace_size(int M, int K, int N) {
   return M < 1 || K < 128 || N < 1 ? 0 : mxfp4_a4_workspace(M, N, K);
