@@ -1,10 +1,10 @@
-// mxfp4_matvec.cu -- products of a few fp16 rows (decode steps of up to 4
-// sequences) with MXFP4 weights.
+// mxfp4_matvec.cu -- products of a few fp16 rows (decode steps of one or two
+// sequences, of up to 8 where the weights are small) with MXFP4 weights.
 //
 // y[m][n] = sum_k x[m][k] c[n][k] 2^(b[n][k/32] - 127).  At these M the weights'
-// bytes are all the time there is (4.25 bits a weight), so the kernel is a stream
-// of 16-byte loads with as little work per code as possible.  A lane's 16 bytes
-// are one scale block; the hardware conversion makes fp16 pairs of its codes, and
+// bytes are all the time there is (4.25 bits a weight), so the kernel is a stream of
+// 16-byte copies with as little work per code as possible.  A lane's 16 bytes are
+// one scale block; the hardware conversion makes fp16 pairs of its codes, and
 // m16n8k16 MMAs (16 weight rows) take them as they are: the order of k within an
 // MMA is free as long as x's fragments follow it.  The MMA's 8 columns are 2 rows
 // of x times 4 scale blocks: column 4 m + j holds x[m] in block j and zeros in
@@ -12,12 +12,20 @@
 // and the scales enter as 4 fp32 FMAs per 128 k (32 packed multiplications of
 // the codes otherwise).  Codes and products are exact, sums fp32.
 //
-// Split: one persistent CTA of 16 warps per SM; clusters of C CTAs split K (the
-// sums meet through distributed shared memory); a cluster's 16-row groups times
-// its CTA's scale tiles along K are one stream of units that its warps share
-// out evenly, each keeping D units of loads in flight across group borders.
-// A warp parks its sum of a group, or of a piece of one, in shared memory; at the
-// end the pieces are added in the order of K, whatever the timing.
+// Split: one persistent CTA of 16 warps per SM (two for long streams, MV_TWO);
+// clusters of C CTAs split K (the sums meet through distributed shared memory); a
+// cluster's 16-row groups times its CTA's scale tiles along K are one stream of
+// units that its warps share out evenly, each keeping D units of copies in flight
+// across group borders, x among them (staged once a CTA ahead of everything, it
+// cost 2 us of a call).  A warp parks its sum of a group, or of a piece of one, in
+// shared memory; at the end the pieces are added in the order of K, whatever the
+// timing.
+//
+// What bounds it: a call of next to no bytes takes 2.4 us (one row, 512 x 3584:
+// launch, one chain of copies, the join); in the stream 138 instructions a unit of
+// 1088 bytes at 0.53 of the issue slots, 16 warps, no pipe full: 152064 x 3584 5.6
+// TB/s, one row of 18944 x 3584 twice 15.8 us, of 3584 x 18944 8.8 us.  Two chains
+// of MMAs a unit lost 5 %; copies straight to registers 15 %.
 #include <algorithm>
 
 #include "mxfp4.cuh"
@@ -30,7 +38,7 @@ constexpr int MV_THREADS = 32 * MV_WARPS;
 constexpr int MV_ROWS = 16;
 constexpr int MV_GROUPS = 32;    // groups of a cluster between two joins
 template <int MS>
-constexpr int MV_D = MS == 1 ? 4 : 3;  // units in flight per warp
+constexpr int MV_D = MS <= 2 ? 4 : 3;  // units in flight per warp
 
 template <bool FIRST>  // FIRST: d = a b, else d += a b
 __device__ __forceinline__ void mv_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -100,10 +108,10 @@ struct MvShape {
 };
 
 // NW weight matrices (2: gate and up, their groups in turn); MS MMAs per 16 k, 2
-// rows of x each.  Up to 4 rows 64 registers, so that the next kernel's CTA fits
+// rows of x each.  Up to 2 rows 64 registers, so that the next kernel's CTA fits
 // beside this one.
 template <int NW, int MS>
-__global__ void __launch_bounds__(MV_THREADS, MS <= 2 ? 2 : 1)
+__global__ void __launch_bounds__(MV_THREADS, MS == 1 ? 2 : 1)
     w4pg_mxfp4_matvec(const __grid_constant__ MxArgs a, int clog, int groups, int gcap) {
   using SH = MvShape<MS>;
   constexpr int MT = SH::MT, PIECE = SH::PIECE, D = SH::D;
@@ -359,7 +367,7 @@ static MvPlan mv_plan(int N, int K) {
   });
   const int groups = N / 128 * 8 + std::min(8, (N % 128 + 3) / 4);  // (those of the last tile that have rows)
   const int ktiles = K / 128, sms = num_sms();
-  const int per = MS <= 2 && (long long)NW * groups * ktiles >= (long long)MV_TWO * MV_WARPS * sms ? 2 : 1;
+  const int per = MS == 1 && (long long)NW * groups * ktiles >= (long long)MV_TWO * MV_WARPS * sms ? 2 : 1;
   MvPlan best = {};
   double cost = 0;
   for (int l = 0; l < 4; ++l) {
@@ -397,11 +405,15 @@ static int mv_launch(const MxArgs& a, cudaStream_t s) {
   return W4A16_OK;
 }
 
-// Up to 4 rows always.  5 to 8 take twice the MMAs a unit and still beat the tensor
-// cores while start and join decide, up to MV_SMALL scale tiles in all.
-constexpr long long MV_SMALL = 4096;
+// Up to 2 rows always (gate|up 17.6 us against 19.7 on the tensor cores).  3 and 4
+// take twice the MMAs a unit, 5 to 8 four times, and win while the tensor-core
+// kernel's start and join decide: up to so many scale tiles of weights.  4 rows,
+// 3584 x 3584 (784 tiles): 4.9 us against 8.3, 18944 x 3584 twice (8288): 25 against
+// 19.7; 8 rows, 784 tiles: 7.5 against 8.4, 1568 tiles: 11.5 against 10.9.
+constexpr long long MV_TILES4 = 4096, MV_TILES8 = 1200;
 bool mxfp4_matvec_serves(int M, int N, int K, bool silu) {
-  return M <= 4 || (M <= 8 && (long long)(N + 127) / 128 * (K / 128) * (silu ? 2 : 1) <= MV_SMALL);
+  const long long tiles = (long long)((N + 127) / 128) * (K / 128) * (silu ? 2 : 1);
+  return M <= 2 || (M <= 8 && tiles <= (M <= 4 ? MV_TILES4 : MV_TILES8));
 }
 
 int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s) {
