@@ -319,9 +319,17 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
 // host
 // ---------------------------------------------------------------------------
 // A call's tile shape and deal: of the shapes built, and with and without the
-// split along K, the one whose busiest CTA has least to do, in cycles as measured:
-// a stage's MMAs 4 NA (45 + NC / 2), a tile's epilogue some 4 per column and 2000,
-// the join 5000.
+// split along K, the one whose busiest CTA has least to do, in cycles as measured
+// with every SM at work: a stage (shared memory's reads and writes bound it: NA MMAs
+// of 4 + NC / 32 KB read per 64 k, 4 NA + NC / 32 KB copied in), what a tile's
+// epilogue keeps the next one's MMAs from, and the join.
+struct MbTile {
+  int na, nc;
+  double stage, tail;
+};
+constexpr MbTile MB_TILES[] = {
+    {2, 192, 1160, 5900}, {1, 256, 800, 4200}, {2, 128, 1030, 4200}, {1, 192, 670, 3000}, {1, 128, 570, 2200}};
+constexpr double MB_JOIN = 5000;
 struct MbPlan {
   int na, nc, mtiles;
   MtDeal d;
@@ -330,22 +338,20 @@ static MbPlan mb_plan(int M, int N, int K, size_t bytes, int slots) {
   const int stages = (K + MB_K - 1) / MB_K;
   MbPlan best = {};
   double cost = 0;
-  for (const auto& shape : {std::pair<int, int>{2, 192}, {2, 128}, {1, 192}, {1, 128}}) {
-    const int na = shape.first, nc = shape.second;
-    if (na == 2 && M <= 128) continue;
-    const int mtiles = (M + 128 * na - 1) / (128 * na), tiles = mtiles * ((N + nc - 1) / nc);
-    const double stage = 4.0 * na * (45 + nc / 2), tail = 4.0 * na * nc + 2000;
+  for (const MbTile& t : MB_TILES) {
+    if (t.na == 2 && M <= 128) continue;
+    const int mtiles = (M + 128 * t.na - 1) / (128 * t.na), tiles = mtiles * ((N + t.nc - 1) / t.nc);
     for (int most = 1; most <= MB_SPLIT; ++most) {
       const MtDeal d = mt_deal(tiles, stages, slots, most);
-      if (most > 1 && (d.split != most || mt_workspace(d, 128 * na, nc) > bytes)) continue;
+      if (most > 1 && (d.split != most || mt_workspace(d, 128 * t.na, t.nc) > bytes)) continue;
       double v;
       if (d.split > 1)
-        v = d.whole / slots * (stages * stage + tail) + (stages + d.split - 1) / d.split * stage + tail + 5000;
+        v = d.whole / slots * (stages * t.stage + t.tail) + (stages + d.split - 1) / d.split * t.stage + t.tail + MB_JOIN;
       else
-        v = (tiles + slots - 1) / slots * (stages * stage + tail);
+        v = (tiles + slots - 1) / slots * (stages * t.stage + t.tail);
       if (best.na == 0 || v < cost) {
         cost = v;
-        best = {na, nc, mtiles, d};
+        best = {t.na, t.nc, mtiles, d};
       }
     }
   }
@@ -388,8 +394,10 @@ int launch_mxfp4_a4(const MxArgs& a, cudaStream_t s) {
   p.split = d.split;
   p.items = d.items;
   if (d.split > 1) p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + TC_TICKET_BYTES);
-  const int rc = b.na == 2 ? (b.nc == 192 ? mb_launch<2, 192>(p, slots, s) : mb_launch<2, 128>(p, slots, s))
-                           : (b.nc == 192 ? mb_launch<1, 192>(p, slots, s) : mb_launch<1, 128>(p, slots, s));
+  const int rc = b.na == 2      ? (b.nc == 192 ? mb_launch<2, 192>(p, slots, s) : mb_launch<2, 128>(p, slots, s))
+                 : b.nc == 256 ? mb_launch<1, 256>(p, slots, s)
+                 : b.nc == 192 ? mb_launch<1, 192>(p, slots, s)
+                               : mb_launch<1, 128>(p, slots, s);
   if (rc || d.split < 2) return rc;
   return launch_mxfp4_join({a, p.parts, d.whole, (d.items - d.whole) / d.split, d.split, 128 * b.na, b.nc, b.mtiles, b.nc, 0}, s);
 }
