@@ -8,15 +8,22 @@
 // them: 32 lanes of four 32-bit columns, repeated for the four lane quadrants.
 //
 // A CTA's tile is NA x 128 rows of x (lanes of D) x NC weight rows (its columns), so
-// that a thread of the epilogue has neighbouring outputs of one row.  A stage is
-// 256 k: 128-byte rows of codes and two scale tiles per 128 rows; at 2 x 192 60 KB
-// for 768 cycles of MMAs.  NC = 192 starts in the middle of a scale tile every
-// other time, which is two columns further on in tensor memory.
+// that a thread of the epilogue has neighbouring outputs of one row.  Where tensor
+// memory holds the tile's sums twice (DB = 2), its epilogue lies under the next
+// tile's MMAs.  A stage is 256 k: 128-byte rows of codes, two scale tiles per 128
+// rows.  NC = 192 starts in the middle of a scale tile every other time, which is two
+// columns further on in tensor memory (scales have to start on an even column, so
+// that NC is a multiple of 64).
+//
+// What bounds it is shared memory: per 64 k an MMA reads 4 KB of x and NC / 32 KB of
+// weights, and as much is copied in (NA MMAs share the weights); at 128 bytes a
+// clock that gives every stage time measured, 0.61 us at 2 x 192, 0.42 at 1 x 256.
+// (256 x 192 by pairs of CTAs, each with half of the weight rows, took 0.38 us a
+// stage, 0.30 two single ones: not kept.)
 //
 // Roles: a producer lane, one warp that issues the scales' copies and the MMAs
 // (these run in the order issued, so one set of scale columns serves; leaving the
-// copies out gained 2 %), 8 epilogue warps.  The next tile's MMAs on the first 128
-// rows begin as soon as these are read out.  Tiles are dealt by mt_deal.
+// copies out gained 2 %), 8 epilogue warps.  Tiles are dealt by mt_deal.
 #include "mxfp4_tc.cuh"
 
 namespace w4 {
@@ -26,10 +33,9 @@ constexpr int MB_EPI = 8;                     // epilogue warps
 constexpr int MB_THREADS = 64 + 32 * MB_EPI;
 constexpr uint32_t MB_X = 128 * MB_K / 2;     // bytes of 128 rows of x per stage
 constexpr int MB_SPLIT = 16;
-constexpr int MB_PITCH = 36;                  // floats from row to row of a warp's 32 x 32 outputs, without bank conflicts
-constexpr int MB_TURN = 32 * MB_PITCH * 4;
+constexpr int MB_TURN = 32 * 32 * 4;          // a warp's 32 x 32 outputs, fp32: four columns c of row r at c ^ r % 8
 
-template <int NA, int NC>
+template <int NA, int NC, int DB>
 struct MbShape {
   static constexpr int NB = NC == 128 ? 1 : 2;                        // weight scale tiles that NC rows can touch
   static constexpr uint32_t W = NC * MB_K / 2;
@@ -37,10 +43,10 @@ struct MbShape {
   static constexpr uint32_t SLOT = (SAT + (NA + NB) * 2 * MX_TILE + 1023) / 1024 * 1024;
   static constexpr int S = (225 * 1024 - MB_EPI * MB_TURN) / SLOT;
   static constexpr size_t SMEM = S * SLOT + MB_EPI * MB_TURN + 1024;
-  static constexpr uint32_t TS = NA * NC;                             // tensor memory: sums, scales of x, of the weights
+  static constexpr uint32_t TS = DB * NA * NC;                        // tensor memory: sums, scales of x, of the weights
   static constexpr uint32_t IDESC =
       (1u << 7) | (1u << 10) | ((uint32_t)(NC >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
-  static_assert(NC % 64 == 0 && TS + 8 * (NA + NB) <= 512 && S >= 3, "tensor memory, ring");
+  static_assert(NC % 64 == 0 && NC <= 256 && TS + 8 * (NA + NB) <= 512 && S >= 3, "tensor memory, ring");
 };
 
 struct MbArgs {
@@ -58,13 +64,13 @@ __device__ __forceinline__ void mb_copy_scales(uint32_t taddr, uint32_t saddr) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(mb_scale_desc(saddr)) : "memory");
 }
 
-template <int NA, int NC>
+template <int NA, int NC, int DB>
 __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_constant__ MbArgs p) {
-  using SH = MbShape<NA, NC>;
+  using SH = MbShape<NA, NC, DB>;
   constexpr int S = SH::S, NB = SH::NB;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  __shared__ __align__(8) uint64_t full[S], empty[S], dfull, dempty[NA], drain;
+  __shared__ __align__(8) uint64_t full[S], empty[S], dfull[DB], dempty[DB][NA], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int s_fail;
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -79,8 +85,10 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(&dfull, 1);
-    for (int g = 0; g < NA; ++g) mbar_init(&dempty[g], MB_EPI);
+    for (int b = 0; b < DB; ++b) {
+      mbar_init(&dfull[b], 1);
+      for (int g = 0; g < NA; ++g) mbar_init(&dempty[b][g], MB_EPI);
+    }
     mbar_init(&drain, 1);
     s_fail = 0;
     fence_mbar_init();
@@ -148,6 +156,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
       int mt, nt, part, k0, k1;
       item(i, &mt, &nt, &part, &k0, &k1);
       const uint32_t woff = (uint32_t)(nt * NC % 128) / 32;  // the first weight row's scale column in its tile
+      const int buf = DB == 2 ? n & 1 : 0;
       for (int k = k0; k < k1; ++k, ++s) {
         const int slot = s % S;
         ok = __all_sync(0xffffffffu, mt_wait(&full[slot], (s / S) & 1, &s_fail));
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
             asm volatile(
                 "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
                 "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-                    tmem + (uint32_t)(g * NC)),
+                    tmem + (uint32_t)((buf * NA + g) * NC)),
                 "l"(ad), "l"(bd), "r"(id), "r"(ts + 8 * g + 4 * j), "r"(ts + 8 * NA + 4 * NB * j + woff),
                 "r"(k > k0 || j > 0 || kk > 0 ? 1u : 0u)
                 : "memory");
@@ -180,9 +189,9 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
         const bool both = 2 * k + 2 <= KT;
 #pragma unroll
         for (int g = 0; g < NA; ++g) {
-          // the tile before has left these columns of tensor memory
-          if (k == k0 && n > 0) {
-            ok = __all_sync(0xffffffffu, mt_wait(&dempty[g], (n - 1) & 1, &s_fail));
+          // an earlier tile has left these columns of tensor memory
+          if (k == k0 && n >= DB) {
+            ok = __all_sync(0xffffffffu, mt_wait(&dempty[buf][g], (n / DB - 1) & 1, &s_fail));
             if (!ok) break;
             mt_fence_after();
           }
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
         }
         if (mt_elect()) {
           mt_commit(&empty[slot]);
-          if (k == k1 - 1) mt_commit(&dfull);
+          if (k == k1 - 1) mt_commit(&dfull[buf]);
         }
         __syncwarp();
         if (!ok) { ++s; break; }
@@ -215,29 +224,30 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
     pdl_wait_then_trigger();
     const int e = warp - 2, quad = warp & 3;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    constexpr int CW = NC / 2;  // columns of a warp, of each 128 rows
-    const int col0 = (e >> 2) * CW, M = p.a.M, N = p.a.N;
+    const int M = p.a.M, N = p.a.N;
     const bool wide = N % 8 == 0;  // rows of y (and of the residual) start on 16 bytes
-    float* turn = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * SH::SLOT + e * MB_TURN);
+    float4* turn = reinterpret_cast<float4*>(smem_raw + (ring - smem_u32(smem_raw)) + S * SH::SLOT + e * MB_TURN);
     uint32_t n = 0;
     for (int i = blockIdx.x; i < p.items; i += gridDim.x, ++n) {
       int mt, nt, part, k0, k1;
       const int tile = item(i, &mt, &nt, &part, &k0, &k1);
-      if (!__all_sync(0xffffffffu, mt_wait(&dfull, n & 1, &s_fail))) break;
+      const int buf = DB == 2 ? n & 1 : 0;
+      if (!__all_sync(0xffffffffu, mt_wait(&dfull[buf], (n / DB) & 1, &s_fail))) break;
       mt_fence_after();
       const bool parts = i >= p.whole && p.split > 1;
-      constexpr int PC = CW / 32;
+      // pieces of 32 rows x 32 columns, the two halves of the warps in turn
+      constexpr int PC = NC / 32;
 #pragma unroll 1
-      for (int pc = 0; pc < NA * PC; ++pc) {
+      for (int pc = e >> 2; pc < NA * PC; pc += 2) {
         const int g = NA == 2 && pc >= PC ? 1 : 0, c0 = (pc - g * PC) * 32;
-        const int r = g * 128 + 32 * quad, m = mt * NA * 128 + r, nn = nt * NC + col0 + c0;  // first row, first column
+        const int r = g * 128 + 32 * quad, m = mt * NA * 128 + r, nn = nt * NC + c0;  // first row, first column
         float v[32];
 #pragma unroll
         for (int c = 0; c < 32; c += 8)
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                        : "=f"(v[c]), "=f"(v[c + 1]), "=f"(v[c + 2]), "=f"(v[c + 3]), "=f"(v[c + 4]), "=f"(v[c + 5]),
                          "=f"(v[c + 6]), "=f"(v[c + 7])
-                       : "r"(lanes + (uint32_t)(g * NC + col0 + c0 + c)));
+                       : "r"(lanes + (uint32_t)((buf * NA + g) * NC + c0 + c)));
         // This lane's share of the turned outputs: 8 columns from n8 of rows m + lane / 4
         // + 8 h.  What is added to them is asked for ahead; nothing branches between the
         // loads and the stores, whose latencies are all a tile's epilogue is (4 rows at a
@@ -255,26 +265,26 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
           }
         }
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        if (c0 + 32 == CW) {
+        if (pc + 2 >= (g + 1) * PC) {  // this warp's last piece of these 128 rows
           mt_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&dempty[g]);
+          if (lane == 0) mbar_arrive(&dempty[buf][g]);
         }
         // turned in shared memory: 4 lanes have 32 columns of a row, 8 rows a store
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 32; c += 4)
-          *reinterpret_cast<float4*>(turn + lane * MB_PITCH + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        for (int c = 0; c < 8; ++c)
+          turn[lane * 8 + (c ^ (lane & 7))] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
         __syncwarp();
         if (parts || wide) {
           float4 lo[4], hi[4];
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
-            lo[h] = *reinterpret_cast<const float4*>(turn + (r8 + 8 * h) * MB_PITCH + q);
-            hi[h] = *reinterpret_cast<const float4*>(turn + (r8 + 8 * h) * MB_PITCH + q + 4);
+            lo[h] = turn[(r8 + 8 * h) * 8 + ((q / 4) ^ r8)];
+            hi[h] = turn[(r8 + 8 * h) * 8 + ((q / 4 + 1) ^ r8)];
           }
           if (parts) {
-            float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NA * 128 * NC) + (size_t)(r + r8) * NC + col0 + c0 + q;
+            float* mine = p.parts + ((size_t)(tile - p.whole) * p.split + part) * (NA * 128 * NC) + (size_t)(r + r8) * NC + c0 + q;
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               if (m + r8 + 8 * h < M) {
@@ -301,7 +311,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
 #pragma unroll 4
           for (int rr = 0; rr < 32 && m + rr < M; ++rr) {
             const size_t at = (size_t)(m + rr) * N + nn + lane;
-            float f = turn[rr * MB_PITCH + lane] + bias;
+            float f = reinterpret_cast<const float*>(turn)[rr * 32 + (((lane >> 2) ^ (rr & 7)) << 2) + (lane & 3)] + bias;
             if (p.a.residual) f += __half2float(p.a.residual[at]);
             p.a.y[at] = __float2half_rn(f);
           }
@@ -324,11 +334,11 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
 // of 4 + NC / 32 KB read per 64 k, 4 NA + NC / 32 KB copied in), what a tile's
 // epilogue keeps the next one's MMAs from, and the join.
 struct MbTile {
-  int na, nc;
+  int na, nc, db;
   double stage, tail;
 };
 constexpr MbTile MB_TILES[] = {
-    {2, 192, 1160, 5900}, {1, 256, 800, 4200}, {2, 128, 1030, 4200}, {1, 192, 670, 3000}, {1, 128, 570, 2200}};
+    {2, 192, 1, 1160, 5900}, {1, 256, 1, 800, 4200}, {1, 192, 2, 730, 3500}, {1, 128, 2, 570, 2500}};
 constexpr double MB_JOIN = 5000;
 struct MbPlan {
   int na, nc, mtiles;
@@ -344,11 +354,12 @@ static MbPlan mb_plan(int M, int N, int K, size_t bytes, int slots) {
     for (int most = 1; most <= MB_SPLIT; ++most) {
       const MtDeal d = mt_deal(tiles, stages, slots, most);
       if (most > 1 && (d.split != most || mt_workspace(d, 128 * t.na, t.nc) > bytes)) continue;
+      // two sets of sums: the epilogue costs time of its own only behind the last tile
+      const double tile = t.db == 2 ? std::max(stages * t.stage, t.tail) : stages * t.stage + t.tail;
+      const double last = t.db == 2 ? t.tail : 0;
       double v;
-      if (d.split > 1)
-        v = d.whole / slots * (stages * t.stage + t.tail) + (stages + d.split - 1) / d.split * t.stage + t.tail + MB_JOIN;
-      else
-        v = (tiles + slots - 1) / slots * (stages * t.stage + t.tail);
+      if (d.split > 1) v = d.whole / slots * tile + (stages + d.split - 1) / d.split * t.stage + t.tail + MB_JOIN;
+      else v = (tiles + slots - 1) / slots * tile + last;
       if (best.na == 0 || v < cost) {
         cost = v;
         best = {t.na, t.nc, mtiles, d};
@@ -364,12 +375,12 @@ size_t mxfp4_a4_workspace(int M, int N, int K) {
   return mt_workspace(b.d, 128 * b.na, b.nc);
 }
 
-template <int NA, int NC>
+template <int NA, int NC, int DB>
 static int mb_launch(MbArgs& p, int slots, cudaStream_t s) {
-  using SH = MbShape<NA, NC>;
+  using SH = MbShape<NA, NC, DB>;
   static PerDeviceOnce once;
   once_per_device(once, [] {
-    cudaFuncSetAttribute(w4pg_mxfp4_a4<NA, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SH::SMEM);
+    cudaFuncSetAttribute(w4pg_mxfp4_a4<NA, NC, DB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SH::SMEM);
   });
   const MxArgs& a = p.a;
   const bool ok = mt_map(&p.tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.xq.codes, a.K / 2, a.M, (uint64_t)a.K / 2, MB_K / 2, 128,
@@ -377,7 +388,7 @@ static int mb_launch(MbArgs& p, int slots, cudaStream_t s) {
                   mt_map(&p.tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w[0].codes, a.K / 2, a.N, (uint64_t)a.K / 2, MB_K / 2, NC,
                          CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return set_error(W4A16_ERR_CUDA, "mxfp4 product: no tensor maps for the operands");
-  const cudaError_t e = launch_pdl(w4pg_mxfp4_a4<NA, NC>, dim3(std::min(p.items, slots)), dim3(MB_THREADS), SH::SMEM, s, p);
+  const cudaError_t e = launch_pdl(w4pg_mxfp4_a4<NA, NC, DB>, dim3(std::min(p.items, slots)), dim3(MB_THREADS), SH::SMEM, s, p);
   if (e != cudaSuccess) return set_error(W4A16_ERR_CUDA, "mxfp4 product launch: %s", cudaGetErrorString(e));
   return W4A16_OK;
 }
@@ -394,10 +405,10 @@ int launch_mxfp4_a4(const MxArgs& a, cudaStream_t s) {
   p.split = d.split;
   p.items = d.items;
   if (d.split > 1) p.parts = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + TC_TICKET_BYTES);
-  const int rc = b.na == 2      ? (b.nc == 192 ? mb_launch<2, 192>(p, slots, s) : mb_launch<2, 128>(p, slots, s))
-                 : b.nc == 256 ? mb_launch<1, 256>(p, slots, s)
-                 : b.nc == 192 ? mb_launch<1, 192>(p, slots, s)
-                               : mb_launch<1, 128>(p, slots, s);
+  const int rc = b.na == 2     ? mb_launch<2, 192, 1>(p, slots, s)
+                 : b.nc == 256 ? mb_launch<1, 256, 1>(p, slots, s)
+                 : b.nc == 192 ? mb_launch<1, 192, 2>(p, slots, s)
+                               : mb_launch<1, 128, 2>(p, slots, s);
   if (rc || d.split < 2) return rc;
   return launch_mxfp4_join({a, p.parts, d.whole, (d.items - d.whole) / d.split, d.split, 128 * b.na, b.nc, b.mtiles, b.nc, 0}, s);
 }
