@@ -17,13 +17,13 @@
 //
 // What bounds it is shared memory: per 64 k an MMA reads 4 KB of x and NC / 32 KB of
 // weights, and as much is copied in (NA MMAs share the weights); at 128 bytes a
-// clock that gives every stage time measured, 0.61 us at 2 x 192, 0.42 at 1 x 256.
+// clock that gives the stage times measured (a fit, no counter shows it), 0.61 us at
+// 2 x 192, 0.42 at 1 x 256, 0.38 at 1 x 192.
 // (256 x 192 by pairs of CTAs, each with half of the weight rows, took 0.38 us a
 // stage, 0.30 two single ones: not kept.)
 //
 // Roles: a producer lane, one warp that issues the scales' copies and the MMAs
-// (these run in the order issued, so one set of scale columns serves; leaving the
-// copies out gained 2 %), 8 epilogue warps.  Tiles are dealt by mt_deal.
+// (these run in the order issued, so one set of scale columns serves), 8 epilogue warps.  Tiles are dealt by mt_deal.
 #include "mxfp4_tc.cuh"
 
 namespace w4 {

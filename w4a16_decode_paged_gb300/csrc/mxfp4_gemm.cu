@@ -11,7 +11,9 @@ namespace w4 {
 // The sums of tiles that were split along K: a thread adds, in order, the parts of
 // four neighbouring outputs in each of R rows; R times MJ_LOADS / R parts are asked
 // for at once, so that few parts (a prompt's tiles) and many (a decode batch's) both
-// keep eight loads in flight.
+// keep eight loads in flight.  (One row a thread, only its own
+// parts in flight: 2048 rows, 3584 x 3584
+// 53.9 us, so 50.9; 32 rows, 512 x 3584 9.1 us, so 6.6.)
 constexpr int MJ_LOADS = 8;
 
 template <bool SILU, int R>

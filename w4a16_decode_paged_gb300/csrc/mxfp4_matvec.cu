@@ -25,7 +25,7 @@
 // launch, one chain of copies, the join); in the stream 138 instructions a unit of
 // 1088 bytes at 0.53 of the issue slots, 16 warps, no pipe full: 152064 x 3584 5.6
 // TB/s, one row of 18944 x 3584 twice 15.8 us, of 3584 x 18944 8.8 us.  Two chains
-// of MMAs a unit lost 5 %; copies straight to registers 15 %.
+// of MMAs a unit lost 5 %.
 #include <algorithm>
 
 #include "mxfp4.cuh"
