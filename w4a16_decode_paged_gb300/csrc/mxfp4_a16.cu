@@ -141,8 +141,9 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
           for (int h = 0; h < 2; ++h) mt_load_2d(sl + h * SH::XHALF, &p.tm_x, k * MA_K + h * 64, mt * NC, &full[slot]);
         }
       }
-      // shared memory is given back only when the copies into it are done
-      for (uint32_t i = s > S ? s - S : 0; i < s && s_fail; ++i) (void)mt_wait(&full[i % S], (i / S) & 1, nullptr);
+      // shared memory is given back only when the copies into it are done, also where
+      // another role gives up behind this one's end (the last S: the others were waited for)
+      for (uint32_t i = s > S ? s - S : 0; i < s; ++i) (void)mt_wait(&full[i % S], (i / S) & 1, nullptr);
     }
     __syncwarp();
   } else if (warp == 1) {

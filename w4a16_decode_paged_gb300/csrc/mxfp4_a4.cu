@@ -143,8 +143,9 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
                     p.a.w[0].scales + ((size_t)min(nt * NC / 128 + g, p.ntiles - 1) * KT + 2 * k) * MX_TILE, sb, &full[slot]);
         }
       }
-      // shared memory is given back only when the copies into it are done
-      for (uint32_t i = s > S ? s - S : 0; i < s && s_fail; ++i) (void)mt_wait(&full[i % S], (i / S) & 1, nullptr);
+      // shared memory is given back only when the copies into it are done, also where
+      // another role gives up behind this one's end (the last S: the others were waited for)
+      for (uint32_t i = s > S ? s - S : 0; i < s; ++i) (void)mt_wait(&full[i % S], (i / S) & 1, nullptr);
     }
     __syncwarp();
   } else if (warp == 1) {
