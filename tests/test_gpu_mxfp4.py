@@ -467,6 +467,24 @@ def test_more_rows_than_a_grid_is_wide(api):
         _close(y, wv[:rows], api.mxfp4_dequantize(*q).double(), k)
 
 
+@pytest.mark.parametrize("k", [128, 256, 384, 640])
+@pytest.mark.parametrize("m,n", [(20, 130001), (50, 130000), (200, 70001)])
+def test_many_tiles_a_cta(api, m, n, k):
+    """Tiles of one to five steps along K, several to a CTA, so that each begins under the one
+    before: whole and split along K, and with SiLU."""
+    rng = np.random.default_rng(m + n + k)
+    gen = torch.Generator("cuda").manual_seed(m + n + k)
+    xd = dev(activations(rng, m, k))
+    w = [api.mxfp4_quantize((0.3 * torch.randn(n, k, generator=gen, device="cuda")).half()) for _ in range(2)]
+    wv = [api.mxfp4_dequantize(*m_).double() for m_ in w]
+    for ws in (torch.empty(256, dtype=torch.uint8, device="cuda"), api.mxfp4_workspace(m, k, n)):
+        y = torch.full((m, n), float("nan"), dtype=torch.float16, device="cuda")
+        _close(api.w4a16_gemm_mxfp4(xd, *w[0], out=y, workspace=ws), xd.double(), wv[0], k)
+    y = api.w4a16_gemm_silu_mul_mxfp4(xd, *w[0], *w[1], workspace=api.mxfp4_workspace(m, k, n, "silu"))
+    for r in (slice(0, 300), slice(n // 2, n // 2 + 300), slice(n - 300, n)):
+        ref.check_silu(host(y[:, r]), host(xd).astype(np.float64), host(wv[0][r]), host(wv[1][r]))
+
+
 @pytest.mark.parametrize("call", ["a16", "a4"])
 def test_outputs_past_32_bits(api, call):
     """More than 2^31 outputs: the last rows are what they would be alone."""

@@ -25,8 +25,11 @@
 // 0.42 without the conversions, which is the DRAM's rate; of 64 rows 0.61, 0.54 without
 // the conversions and 0.48 without the stores as well; of 128 rows 0.80 to 0.83, 0.74
 // without both, where a bf16 product of that size takes 0.65 at the rate of a large one.
-// 32 rows, 18944 x 3584 twice, with SiLU 18.9 us; 2048 rows, 3584 x 3584 50.3 us, 18944
-// x 3584 203 us (1370 TFLOP/s).  A stage handed over by halves 0.67 (32 rows) and 0.83
+// 32 rows, 18944 x 3584 twice, with SiLU 18.9 us; 2048 rows, 3584 x 3584 49.5 us, 18944
+// x 3584 198 us (1405 TFLOP/s).  A tile's first two stages under the one before's last
+// MMAs and ahead of its epilogue: 203.9 us to 198.1 there, 47.8 to 42.0 at 4096 rows, 8960
+// x 256; where a CTA has one tile only it costs up to 2 % (300 rows, 3584 x 3584 16.7 us to
+// 17.0).  A stage handed over by halves 0.67 (32 rows) and 0.83
 // us; direct 2-byte stores 5.4 us an epilogue, turned 4.3.
 #include "mxfp4_tc.cuh"
 
@@ -194,15 +197,20 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
     const int row = 32 * quad + lane;  // of the tile; the tensor-memory lane
     const int sw = (row >> 1) & 3;     // 16-byte chunk c of a row's codes is at c ^ sw
     const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-    float* turn = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * SH::SLOT) + e * 256;
-    const int M = p.a.M, N = p.a.N;
-    const bool wide = N % 8 == 0;      // rows of y (and of the residual) start on 16 bytes
     uint32_t s = 0, n = 0;
+    int early = 0;                     // stages of this item done under the one before
     bool ok = true;
     for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x, ++n) {
-      int mt, nt, part, k0, k1;
-      const int tile = item(i, &mt, &nt, &part, &k0, &k1);
-      for (int k = k0; k < k1; ++k, ++s) {
+      int mt, nt, part, k0, k1, ahead = 0;
+      // Behind the item's stages the next one's first two, one of each set: they
+      // lie under the item's last MMAs, and the next one's first need not wait.  (Their
+      // buffers are left by MMAs of this item: none of them waits for the epilogue below.)
+      if (i + (int)gridDim.x < p.items) {
+        item(i + gridDim.x, &mt, &nt, &part, &k0, &k1);
+        ahead = min(k1 - k0, 2);
+      }
+      int tile = item(i, &mt, &nt, &part, &k0, &k1);
+      for (int left = k1 - k0 - early + ahead; left > 0; --left, ++s) {
         if ((s & 1) != set) continue;
         const int slot = s % S, ab = s % NAB;
         ok = __all_sync(0xffffffffu, mt_wait(&full[slot], (s / S) & 1, &s_fail));
@@ -248,10 +256,18 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
         if (lane == 0) mbar_arrive(&afull[ab]);
       }
       if (!ok) break;
+      early = ahead;
+      // Where the item lies is found again below 128 columns, as registers are short above
+      // (18944 x 3584 twice of 32 rows 18.9 us, 19.4 without; of 128 columns, 2048 rows of
+      // 18944 x 3584, 206 us with it and 199 without).
+      if (NC < 128) tile = item(i, &mt, &nt, &part, &k0, &k1);
       // epilogue: warp e has columns [e / 4 * NC / 4, ..) of both tiles' rows of its quadrant
       ok = __all_sync(0xffffffffu, mt_wait(&dfull, n & 1, &s_fail));
       if (!ok) break;
       mt_fence_after();
+      float* turn = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S * SH::SLOT) + e * 256;
+      const int M = p.a.M, N = p.a.N;
+      const bool wide = N % 8 == 0;      // rows of y (and of the residual) start on 16 bytes
       constexpr int CW = NC / 4, PC = CW / 8;
       const int col0 = (e >> 2) * CW;
       const bool parts = i >= p.whole && p.split > 1;
