@@ -15,9 +15,10 @@
 // columns further on in tensor memory (scales have to start on an even column, so
 // that NC is a multiple of 64).
 //
-// What bounds it is shared memory: per 64 k an MMA reads 4 KB of x and NC / 32 KB of
+// What bounds it, as far as a model tells, is shared memory: per 64 k an MMA reads 4 KB of x and NC / 32 KB of
 // weights, and as much is copied in (NA MMAs share the weights); at 128 bytes a
-// clock that gives the stage times measured (a fit, no counter shows it), 0.61 us at
+// clock that gives the stage times measured (a fit: the L1 data bank
+// counters are far from full, and may not count operands), 0.61 us at
 // 2 x 192, 0.42 at 1 x 256, 0.38 at 1 x 192.
 // (256 x 192 by pairs of CTAs, each with half of the weight rows, took 0.38 us a
 // stage, 0.30 two single ones: not kept.)
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
 // ---------------------------------------------------------------------------
 // A call's tile shape and deal: of the shapes built, and with and without the
 // split along K, the one whose busiest CTA has least to do, in cycles as measured
-// with every SM at work: a stage (shared memory's reads and writes bound it: NA MMAs
+// with every SM at work: a stage (in proportion to shared memory's traffic: NA MMAs
 // of 4 + NC / 32 KB read per 64 k, 4 NA + NC / 32 KB copied in), what a tile's
 // epilogue keeps the next one's MMAs from, and the join.
 struct MbTile {
