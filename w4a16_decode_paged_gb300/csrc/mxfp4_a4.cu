@@ -15,16 +15,17 @@
 // columns further on in tensor memory (scales have to start on an even column, so
 // that NC is a multiple of 64).
 //
-// What bounds it, as far as a model tells, is shared memory: per 64 k an MMA reads 4 KB of x and NC / 32 KB of
-// weights, and as much is copied in (NA MMAs share the weights); at 128 bytes a
-// clock that gives the stage times measured (a fit: the L1 data bank
-// counters are far from full, and may not count operands), 0.61 us at
-// 2 x 192, 0.42 at 1 x 256, 0.38 at 1 x 192.
-// (256 x 192 by pairs of CTAs, each with half of the weight rows, took 0.38 us a
-// stage, 0.30 two single ones: not kept.)
+// What bounds it, as far as a model tells, is shared memory: per 64 k an MMA reads 4 KB
+// of x and NC / 32 KB of weights, and as much is copied in (NA MMAs share the weights).
+// At 128 bytes a clock that is 4 to 12 % below the stages measured, 0.61 us at 2 x 192,
+// 0.42 at 1 x 256, 0.38 at 1 x 192.  It is a fit: the L1 data bank
+// counters are far from full, and may not count what the MMAs read.  (256 x 192 by pairs
+// of CTAs, each with half of the weight rows, took 0.38 us a stage, 0.30 two single
+// ones: not kept.)
 //
 // Roles: a producer lane, one warp that issues the scales' copies and the MMAs
-// (these run in the order issued, so one set of scale columns serves), 8 epilogue warps.  Tiles are dealt by mt_deal.
+// (these run in the order issued, so one set of scale columns serves), 8 epilogue
+// warps.  Tiles are dealt by mt_deal.
 #include "mxfp4_tc.cuh"
 
 namespace w4 {
