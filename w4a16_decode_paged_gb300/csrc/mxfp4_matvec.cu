@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(MV_THREADS, MS == 1 ? 2 : 1)
       if (csize == 1) sums[place * PIECE + e] = v;
       else st_cluster(sums + place * PIECE + e, owner, v);
     }
+    __syncwarp();  // the cluster's barriers are for whole warps
     if (csize > 1) cluster_sync();
     else __syncthreads();
     W4_TRACE_MARK(2);
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(MV_THREADS, MS == 1 ? 2 : 1)
       o = place_of(i += MV_THREADS);
     }
     if (round + 1 < rounds) {
+      __syncwarp();  // lanes leave the loop above at different turns
       if (csize > 1) cluster_arrive();
       __syncthreads();
     }
