@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
             v[16 * b + 4 * j + 3] = hmul2_u32(f.w, sb);
           }
         }
-        if (s >= NAB) ok = __all_sync(0xffffffffu, mt_wait(&aempty[ab], (s / NAB - 1) & 1, &s_fail));
+        ok = __all_sync(0xffffffffu, s < NAB || mt_wait(&aempty[ab], (s / NAB - 1) & 1, &s_fail));
         if (!ok) break;
         mt_fence_after();
         const uint32_t ta = lanes + SH::TA + (uint32_t)((ab * 2 + g) * 64);
@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
         const int gg = pc >= PC ? 1 : 0, c0 = col0 + (pc - gg * PC) * 8, m0 = mt * NC + c0;
         const int n0 = (nt + gg) * 128 + 32 * quad;      // the quadrant's first weight row
         float v[8], u[8];
+        __syncwarp();  // tensor memory is read, and waited for, by whole warps
         mx_tmem_ld8(v, lanes + (uint32_t)(gg * NC + c0));
         if (p.silu && !parts) mx_tmem_ld8(u, lanes + (uint32_t)(NC + c0));
         // this lane's share of the turned outputs: row m, 8 weight rows from nn
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
         uint4 add = make_uint4(0, 0, 0, 0);
         if (wide && inside && p.a.residual) add = *reinterpret_cast<const uint4*>(p.a.residual + at);
         const float bias = p.a.bias && n0 + lane < N ? __half2float(p.a.bias[n0 + lane]) : 0.f;
+        __syncwarp();
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
         if (pc == rounds - 1) {
           mt_fence_before();
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
   mt_fence_before();
   __syncthreads();
   if (s_fail && tid == 0 && p.a.err_flag) atomicOr(p.a.err_flag, 2);
+  __syncwarp();
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem_slot) : "memory");
 }
 

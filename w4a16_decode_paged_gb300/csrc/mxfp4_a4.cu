@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
         const int g = NA == 2 && pc >= PC ? 1 : 0, c0 = (pc - g * PC) * 32;
         const int r = g * 128 + 32 * quad, m = mt * NA * 128 + r, nn = nt * NC + c0;  // first row, first column
         float v[32];
+        __syncwarp();  // tensor memory is read, and waited for, by whole warps
 #pragma unroll
         for (int c = 0; c < 32; c += 8)
           asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
               if (m + r8 + 8 * h < M) add[h] = *reinterpret_cast<const uint4*>(p.a.residual + at + (size_t)(8 * h) * N);
           }
         }
+        __syncwarp();
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
         if (pc + 2 >= (g + 1) * PC) {  // this warp's last piece of these 128 rows
           mt_fence_before();
@@ -325,6 +327,7 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
   mt_fence_before();
   __syncthreads();
   if (s_fail && tid == 0 && p.a.err_flag) atomicOr(p.a.err_flag, 2);
+  __syncwarp();
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem_slot) : "memory");
 }
 
