@@ -374,7 +374,7 @@ static MvPlan mv_plan(int N, int K) {
   double cost = 0;
   for (int l = 0; l < 4; ++l) {
     const int c = 1 << l;
-    if (c > ktiles) break;
+    if (c > ktiles || c > per * sms) break;  // (no device: one SM is assumed, and the launch fails)
     const int clusters = std::min(groups, std::min(room[dev][l], per * sms / c));
     const int n = NW * ((groups + clusters - 1) / clusters), kc = (ktiles + c - 1) / c, gcap = std::min(n, MV_GROUPS);
     const double v = (double)n * kc + (l ? MV_JOIN : 0);
