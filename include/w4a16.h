@@ -206,6 +206,18 @@ W4A16_API int w4a4_gemm_mxfp4(const uint32_t* x_codes, const uint8_t* x_scales, 
 W4A16_API size_t w4a16_gemm_mxfp4_workspace_size(int M, int K, int N, int silu);
 W4A16_API size_t w4a4_gemm_mxfp4_workspace_size(int M, int K, int N);
 
+/* Test hook: how an MXFP4 product of these sizes with so much workspace runs, so
+ * that a test can name the form it covers.  kind: 0 w4a16_gemm_mxfp4, 1
+ * w4a16_gemm_silu_mul_mxfp4, 2 w4a4_gemm_mxfp4; sms: of the tensor-core kernels'
+ * device, 0 for the current one (the stream kernel's plan is always that one's).
+ *   plan[0] 1, tensor cores: [1], [2] rows of x and weight rows of a tile, [3]
+ *     tiles that are whole, [4] tiles that are split along K, [5] parts of each,
+ *     [6] CTAs
+ *   plan[0] 0, the stream kernel of a few rows: [1] CTAs of a cluster, [2]
+ *     clusters, [3] groups of 16 weight rows of the busiest cluster, [4] its rounds */
+W4A16_API int w4a16_debug_mxfp4_plan(int kind, int M, int K, int N, size_t workspace_bytes, int sms,
+                                     int32_t plan[7]);
+
 /* Test hook for the failure path of the persistent decode kernel
  * (W4A16_PATH_PERSISTENT below).  Its grid-barrier waits are bounded
  * (default 2 s of the GPU's global timer); a wait that runs out sets bit 1

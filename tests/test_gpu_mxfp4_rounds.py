@@ -39,7 +39,8 @@ def hold(y, want, err):
 
 # (more than two rows of larger weights go to the tensor cores)
 @pytest.mark.parametrize("n,k,m", [(n, k, m) for n, k, most in ((262144, 128, 4), (262139, 256, 4), (77840, 5120, 2),
-                                                               (46000, 8704, 2)) for m in range(1, most + 1)])
+                                                               (46000, 8704, 2)) for m in range(1, most + 1)] +
+                         [(80000, 128, 5), (80000, 128, 8), (151936, 8192, 1)])
 def test_rounds(api, n, k, m):
     gen = torch.Generator("cuda").manual_seed(n + m)
     x = torch.randn((m, k), generator=gen, device="cuda").half()

@@ -65,6 +65,7 @@ SIGNATURES = {
     "w4a4_gemm_mxfp4": (I32, [P, P, I32, I32, P, P, I32, P, P, P, P, SZ, P, P]),
     "w4a16_gemm_mxfp4_workspace_size": (SZ, [I32, I32, I32, I32]),
     "w4a4_gemm_mxfp4_workspace_size": (SZ, [I32, I32, I32]),
+    "w4a16_debug_mxfp4_plan": (I32, [I32, I32, I32, I32, SZ, I32, P]),
     "w4a16_debug_set_wait_limit_ns": (ctypes.c_ulonglong, [ctypes.c_ulonglong]),
     "lm_head_logits_batched": (I32, [P, I32, I32, P, I32, P, P]),
     "argmax_rows": (I32, [P, I32, I32, P, P, P]),

@@ -381,6 +381,11 @@ size_t mxfp4_a4_workspace(int M, int N, int K) {
   return mt_workspace(b.d, 128 * b.na, b.nc);
 }
 
+void mxfp4_a4_plan(int M, int N, int K, size_t bytes, int slots, int32_t* plan) {
+  const MbPlan b = mb_plan(M, N, K, bytes, slots);
+  mt_tell(b.d, 128 * b.na, b.nc, slots, plan);
+}
+
 template <int NA, int NC, int DB>
 static int mb_launch(MbArgs& p, int slots, cudaStream_t s) {
   using SH = MbShape<NA, NC, DB>;

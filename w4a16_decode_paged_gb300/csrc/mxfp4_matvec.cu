@@ -418,6 +418,18 @@ bool mxfp4_matvec_serves(int M, int N, int K, bool silu) {
   return M <= 2 || (M <= 8 && tiles <= (M <= 4 ? MV_TILES4 : MV_TILES8));
 }
 
+void mxfp4_matvec_plan(int M, int N, int K, bool silu, int32_t* plan) {
+  const MvPlan p = silu ? (M <= 2 ? mv_plan<2, 1>(N, K) : M <= 4 ? mv_plan<2, 2>(N, K) : mv_plan<2, 4>(N, K))
+                        : (M <= 2 ? mv_plan<1, 1>(N, K) : M <= 4 ? mv_plan<1, 2>(N, K) : mv_plan<1, 4>(N, K));
+  const int most = (silu ? 2 : 1) * ((p.groups + p.clusters - 1) / p.clusters);
+  plan[0] = 0;
+  plan[1] = 1 << p.clog;
+  plan[2] = p.clusters;
+  plan[3] = most;
+  plan[4] = (most + p.gcap - 1) / p.gcap;
+  plan[5] = plan[6] = 0;
+}
+
 int launch_mxfp4_matvec(const MxArgs& a, bool silu, cudaStream_t s) {
   if (silu) return a.M <= 2 ? mv_launch<2, 1>(a, s) : a.M <= 4 ? mv_launch<2, 2>(a, s) : mv_launch<2, 4>(a, s);
   return a.M <= 2 ? mv_launch<1, 1>(a, s) : a.M <= 4 ? mv_launch<1, 2>(a, s) : mv_launch<1, 4>(a, s);

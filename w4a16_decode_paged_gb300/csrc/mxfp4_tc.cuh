@@ -100,6 +100,15 @@ inline MtDeal mt_deal(int tiles, int stages, int slots, int most_split) {
   d.items = d.whole + over * split;
   return d;
 }
+inline void mt_tell(const MtDeal& d, int tm, int tn, int slots, int32_t* plan) {
+  plan[0] = 1;
+  plan[1] = tm;
+  plan[2] = tn;
+  plan[3] = d.whole;
+  plan[4] = d.split > 1 ? (d.items - d.whole) / d.split : 0;
+  plan[5] = d.split;
+  plan[6] = std::min(d.items, slots);
+}
 // Parts in the workspace lie behind the block that the other split-K calls keep
 // their tickets in; a part is [rows of x][weight rows] of its tile, fp32.
 inline size_t mt_workspace(const MtDeal& d, int tm, int tn) {
