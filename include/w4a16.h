@@ -162,14 +162,15 @@ W4A16_API size_t w4a16_gemm_workspace_size(int M, int K, int N, int silu);
  *     Any scale byte.
  *   w4a16_gemm_mxfp4  y = x . W^T (+ bias) (+ residual): x fp16 [M][K], W MXFP4
  *     [N][K], y fp16 [M][N], bias fp16 [N] or NULL, residual fp16 [M][N] or
- *     NULL (may be y).  Scale bytes of W: 104..140 as written by
- *     mxfp4_quantize, or 255; blocks with smaller ones (values up to 6 * 2^-24)
- *     may count as zero, 141..254 are not served.
+ *     NULL (may be y).  Scale bytes of W: 104..140, as mxfp4_quantize writes
+ *     them, under which every value is an fp16 number; a block with a smaller
+ *     one (values up to 6 * 2^-24) counts as zero and one with a larger one as
+ *     NaN, for any M alike.
  *   w4a16_gemm_silu_mul_mxfp4  y = silu(x . G^T) * (x . U^T), G and U as W.
  *     Both sums stay fp32 into SiLU: silu(g) = g / (1 + exp(-g)), and its
  *     product with u is rounded once.
  *   w4a4_gemm_mxfp4   y = X . W^T (+ bias) (+ residual), both MXFP4, any scale
- *     byte but 0: the block-scaled product of the tensor cores.
+ *     byte: the block-scaled product of the tensor cores.
  * Sums are fp32, y is rounded once.  y must not overlap x or the weights.
  * Unlike the INT4 projections above, no call here reads weights before the
  * call ahead of it on the stream is done: W may come straight out of

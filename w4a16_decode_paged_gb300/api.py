@@ -558,7 +558,9 @@ def _mx_buffers(M, K, N, kind, out, workspace, err_flag, bias, residual, like, d
 
 def w4a16_gemm_mxfp4(x, codes, scales, bias=None, residual=None, out=None, workspace=None, err_flag=None, stream=None):
     """y = x . W^T (+ bias) (+ residual): x fp16 [M][K], W MXFP4 (codes int32
-    [N][K/8], scale tiles), from one token to a prompt's rows.  Without a
+    [N][K/8], scale tiles of bytes 104..140 as mxfp4_quantize writes them; blocks
+    with smaller ones count as zero, with larger ones as NaN), from one token to a
+    prompt's rows.  Without a
     workspace (mxfp4_workspace) each call makes its own.  residual may be out; out must
     not overlap x or the weights."""
     if stream is None and workspace is not None and _cuda(x) and (fast := native()) is not None:

@@ -43,10 +43,17 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
   return fmaf(f, 0.f, f);
 }
 
-// the same rounded to fp16, in both halves: exact for bytes 103..142, zero below
-__device__ __forceinline__ uint32_t mx_scale_h2(uint32_t byte) {
-  const __half2 h = __float2half2_rn(mx_scale(byte));
-  return *reinterpret_cast<const uint32_t*>(&h);
+// What a weight's scale bytes stand for in the products with fp16 rows, two at a
+// time (in bits 0..7 and 16..23), as a pair of bf16 numbers: 2^(byte - 127) for the
+// bytes under which every value is an fp16 number (104..140, as the quantiser
+// writes), zero below, NaN above.  One meaning for every kernel: what an operand in
+// fp16 cannot hold does not depend on how many rows of x there are.
+__device__ __forceinline__ uint32_t mx_weight_scales(uint32_t bytes) {
+  const uint32_t e = bytes << 7;  // (255 is an infinity here)
+  uint32_t least, above;
+  asm("set.ge.u32.bf16x2 %0, %1, %2;" : "=r"(least) : "r"(e), "r"(0x34003400u));
+  asm("set.gt.u32.bf16x2 %0, %1, %2;" : "=r"(above) : "r"(e), "r"(0x46004600u));
+  return (e & least) | above;
 }
 
 __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {

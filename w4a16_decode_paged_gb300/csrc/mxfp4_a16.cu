@@ -223,9 +223,12 @@ __global__ void __launch_bounds__(MA_THREADS, 1) w4pg_mxfp4_a16(const __grid_con
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);
         uint32_t v[64];
+        const uint32_t s01 = mx_weight_scales(__byte_perm(sc, 0, 0x4140)), s23 = mx_weight_scales(__byte_perm(sc, 0, 0x4342));
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const uint32_t sb = mx_scale_h2((sc >> (8 * b)) & 255u), cw[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
+          const uint32_t bf = b < 2 ? s01 : s23, cw[4] = {c[b].x, c[b].y, c[b].z, c[b].w};
+          const __half2 sh = __float2half2_rn(__uint_as_float(b & 1 ? bf & 0xFFFF0000u : bf << 16));
+          const uint32_t sb = *reinterpret_cast<const uint32_t*>(&sh);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint4 f = mx_values(cw[j]);

@@ -23,8 +23,8 @@
 //
 // What bounds it: a call of next to no bytes takes 2.4 us (one row, 512 x 3584:
 // launch, one chain of copies, the join); in the stream 138 instructions a unit of
-// 1088 bytes at 0.53 of the issue slots, 16 warps, no pipe full: 152064 x 3584 5.6
-// TB/s, one row of 18944 x 3584 twice 15.8 us, of 3584 x 18944 8.8 us.  Two chains
+// 1088 bytes at 0.53 of the issue slots, 16 warps, no pipe full: 152064 x 3584 5.5
+// TB/s, one row of 18944 x 3584 twice 16.0 us, of 3584 x 18944 9.0 us.  Two chains
 // of MMAs a unit lost 5 %.
 #include <algorithm>
 
@@ -84,10 +84,9 @@ __device__ __forceinline__ void cpa16_ca(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// two scale bytes as fp32 (255: NaN)
+// two scale bytes as fp32
 __device__ __forceinline__ float2 mv_scales(uint16_t bytes) {
-  uint32_t v;
-  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(v) : "h"(bytes));
+  const uint32_t v = mx_weight_scales(__byte_perm(bytes, 0, 0x4140));
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
