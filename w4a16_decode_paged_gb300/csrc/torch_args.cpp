@@ -11,9 +11,12 @@
 // No part of an operation is computed here.
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/TensorBody.h>
 #include <ATen/EmptyTensor.h>
+#include <ATen/PythonTorchFunctionTLS.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -341,8 +344,12 @@ Rows rows_of(PyObject* o) {
   return r;
 }
 // a new tensor on the current device, straight from torch's caching allocator (the
-// dispatcher's share of at::empty is 0.8 us)
+// dispatcher's share of at::empty is 0.8 us); where a mode wants to see it made, or new
+// memory is to be filled, the checked path makes it
 at::Tensor made(at::ScalarType type, c10::IntArrayRef shape) {
+  if (c10::impl::TorchDispatchModeTLS::any_modes_set() || at::impl::torch_function_mode_enabled() ||
+      (at::globalContext().deterministicAlgorithms() && at::globalContext().deterministicFillUninitializedMemory()))
+    throw NotPlain();
   return at::Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(),
                                               c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
 }
