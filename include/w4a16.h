@@ -181,7 +181,9 @@ W4A16_API size_t w4a16_gemm_workspace_size(int M, int K, int N, int silu);
  * call's sizes it may split as it likes, with less, or none, it splits less or
  * not at all.  Its first 8 KiB are left as they are, so that the split-K GEMMs
  * above, which keep their counters there, can have the same workspace in turn;
- * calls that overlap on the GPU need one each.
+ * calls that overlap on the GPU need one each.  The size that one call wants says
+ * nothing about another's (it may be 0 for many rows and not for few);
+ * mxfp4_workspace_size() is enough for every call of the three products.
  * err_flag: int32 device word or NULL: bit 1 is set if a bounded wait inside
  * a kernel gave up (its output is then not valid).
  * ------------------------------------------------------------------------ */
@@ -204,6 +206,7 @@ W4A16_API int w4a4_gemm_mxfp4(const uint32_t* x_codes, const uint8_t* x_scales, 
                               const uint32_t* codes, const uint8_t* scales, int N, const uint16_t* bias,
                               const uint16_t* residual, uint16_t* y, void* workspace, size_t workspace_bytes,
                               int32_t* err_flag, w4a16_stream_t stream);
+W4A16_API size_t mxfp4_workspace_size(void);
 W4A16_API size_t w4a16_gemm_mxfp4_workspace_size(int M, int K, int N, int silu);
 W4A16_API size_t w4a4_gemm_mxfp4_workspace_size(int M, int K, int N);
 

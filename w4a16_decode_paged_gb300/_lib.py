@@ -63,6 +63,7 @@ SIGNATURES = {
     "w4a16_gemm_mxfp4": (I32, [P, I32, I32, P, P, I32, P, P, P, P, SZ, P, P]),
     "w4a16_gemm_silu_mul_mxfp4": (I32, [P, I32, I32, P, P, P, P, I32, P, P, SZ, P, P]),
     "w4a4_gemm_mxfp4": (I32, [P, P, I32, I32, P, P, I32, P, P, P, P, SZ, P, P]),
+    "mxfp4_workspace_size": (SZ, []),
     "w4a16_gemm_mxfp4_workspace_size": (SZ, [I32, I32, I32, I32]),
     "w4a4_gemm_mxfp4_workspace_size": (SZ, [I32, I32, I32]),
     "w4a16_debug_mxfp4_plan": (I32, [I32, I32, I32, I32, SZ, I32, P]),

@@ -521,12 +521,21 @@ def mxfp4_dequantize(codes, scales, out=None, stream=None):
     return out
 
 
-def mxfp4_workspace(M, K, N, kind="a16", device="cuda"):
-    """A workspace for w4a16_gemm_mxfp4 (kind "a16"), w4a16_gemm_silu_mul_mxfp4
-    ("silu") or w4a4_gemm_mxfp4 ("a4") of these sizes; one serves every call that
-    does not overlap another on the GPU.  It is zeroed, so that the other split-K
-    calls may have it as well; these calls take any contents."""
-    return torch.zeros(_mx_workspace_bytes(M, K, N, kind), dtype=torch.uint8, device=device)
+def mxfp4_workspace(M=None, K=None, N=None, kind="a16", device="cuda"):
+    """A workspace for every call of the three MXFP4 products (30 MB): one serves all
+    that do not overlap on the GPU.  With sizes, one for calls of these sizes of
+    w4a16_gemm_mxfp4 (kind "a16"), w4a16_gemm_silu_mul_mxfp4 ("silu") or
+    w4a4_gemm_mxfp4 ("a4") only: other sizes or another kind may want more (also with
+    fewer rows) and split less with it, which costs time, not results.  It is zeroed,
+    so that the other split-K calls may have it as well; these calls take any contents."""
+    sizes = (M, K, N)
+    if all(s is None for s in sizes):
+        n = load().mxfp4_workspace_size()
+    elif any(s is None for s in sizes):
+        raise ValueError(f"M={M}, K={K}, N={N}: expected all three or none")
+    else:
+        n = _mx_workspace_bytes(M, K, N, kind)
+    return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def _mx_workspace_bytes(M, K, N, kind):

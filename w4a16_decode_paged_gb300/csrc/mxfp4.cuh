@@ -98,6 +98,8 @@ int launch_mxfp4_a16(const MxArgs& a, bool silu, cudaStream_t s);
 int launch_mxfp4_a4(const MxArgs& a, cudaStream_t s);
 size_t mxfp4_a4_workspace(int M, int N, int K);
 size_t mxfp4_a16_workspace(int M, int N, int K, bool silu);
+int mxfp4_a4_largest_tile();   // outputs
+int mxfp4_a16_largest_tile();
 // what w4a16_debug_mxfp4_plan tells
 void mxfp4_matvec_plan(int M, int N, int K, bool silu, int32_t* plan);
 void mxfp4_a16_plan(int M, int N, int K, bool silu, size_t bytes, int slots, int32_t* plan);

@@ -390,6 +390,8 @@ size_t mxfp4_a16_workspace(int M, int N, int K, bool silu) {
   return mt_workspace(ma_deal(M, N, K, silu, ~(size_t)0, ATW_SMS), ma_cols(M), 256);
 }
 
+int mxfp4_a16_largest_tile() { return 128 * 256; }
+
 void mxfp4_a16_plan(int M, int N, int K, bool silu, size_t bytes, int slots, int32_t* plan) {
   mt_tell(ma_deal(M, N, K, silu, bytes, slots), ma_cols(M), 256, slots, plan);
 }

@@ -381,6 +381,12 @@ size_t mxfp4_a4_workspace(int M, int N, int K) {
   return mt_workspace(b.d, 128 * b.na, b.nc);
 }
 
+int mxfp4_a4_largest_tile() {
+  int n = 0;
+  for (const MbTile& t : MB_TILES) n = std::max(n, 128 * t.na * t.nc);
+  return n;
+}
+
 void mxfp4_a4_plan(int M, int N, int K, size_t bytes, int slots, int32_t* plan) {
   const MbPlan b = mb_plan(M, N, K, bytes, slots);
   mt_tell(b.d, 128 * b.na, b.nc, slots, plan);

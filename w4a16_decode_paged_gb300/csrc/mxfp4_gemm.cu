@@ -143,6 +143,11 @@ extern "C" size_t w4a4_gemm_mxfp4_workspace_size(int M, int K, int N) {
   return M < 1 || K < 128 || N < 1 ? 0 : mxfp4_a4_workspace(M, N, K);
 }
 
+extern "C" size_t mxfp4_workspace_size(void) {
+  // a deal has at most as many parts as there are CTAs (mt_deal)
+  return TC_TICKET_BYTES + (size_t)ATW_SMS * std::max(mxfp4_a16_largest_tile(), mxfp4_a4_largest_tile()) * 4;
+}
+
 extern "C" int w4a16_gemm_mxfp4(const uint16_t* x, int M, int K, const uint32_t* codes, const uint8_t* scales, int N,
                                 const uint16_t* bias, const uint16_t* residual, uint16_t* y, void* workspace,
                                 size_t workspace_bytes, int32_t* err_flag, w4a16_stream_t stream) {
