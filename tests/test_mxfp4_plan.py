@@ -52,4 +52,8 @@ def test_tiles_and_workspace(lib):
 def test_refusals(lib):
     p = (ctypes.c_int32 * 7)()
     assert lib.w4a16_debug_mxfp4_plan(3, 1, 128, 1, 0, SMS, p) == 1 and lib.w4a16_debug_mxfp4_plan(0, 1, 128, 1, 0, SMS, None) == 1
-    assert lib.w4a16_debug_mxfp4_plan(2, 0, 128, 1, 0, SMS, p) == 1 and lib.w4a16_debug_mxfp4_plan(2, 1, 0, 1, 0, SMS, p) == 1
+    for m, k, n in ((0, 128, 1), (1, 0, 1), (1, 192, 1), (1, 128, 0), (1048577, 128, 1), (1, 131200, 1), (1, 128, 1048577)):
+        assert lib.w4a16_debug_mxfp4_plan(2, m, k, n, 0, SMS, p) == 3
+    for kind in (0, 2):                                            # the largest sizes: 22 and 34 million tiles
+        _, tm, tn, whole = plan(lib, kind, 1048576, 1048576, 131072, 0)[:4]
+        assert whole == -(-1048576 // tm) * -(-1048576 // tn) < 2 ** 31

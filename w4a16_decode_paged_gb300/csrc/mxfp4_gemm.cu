@@ -210,7 +210,10 @@ extern "C" int w4a4_gemm_mxfp4(const uint32_t* x_codes, const uint8_t* x_scales,
 }
 
 extern "C" int w4a16_debug_mxfp4_plan(int kind, int M, int K, int N, size_t workspace_bytes, int sms, int32_t* plan) {
-  W4_CHECK_ARG(plan && kind >= 0 && kind <= 2 && sms >= 0 && M >= 1 && N >= 1 && K >= 128, "w4a16_debug_mxfp4_plan: arguments");
+  W4_CHECK_ARG(plan && kind >= 0 && kind <= 2 && sms >= 0, "w4a16_debug_mxfp4_plan: arguments");
+  W4_CHECK_SHAPE(M >= 1 && M <= W4A16_MXFP4_MAX_ROWS && N >= 1 && N <= W4A16_MXFP4_MAX_ROWS && K >= 128 && K % 128 == 0 &&
+                     K <= W4A16_MXFP4_MAX_K,
+                 "w4a16_debug_mxfp4_plan: M=%d N=%d K=%d", M, N, K);
   const int slots = sms ? sms : num_sms();
   if (kind == 2) mxfp4_a4_plan(M, N, K, workspace_bytes, slots, plan);
   else if (mxfp4_matvec_serves(M, N, K, kind == 1)) mxfp4_matvec_plan(M, N, K, kind == 1, plan);
