@@ -185,7 +185,8 @@ W4A16_API size_t w4a16_gemm_workspace_size(int M, int K, int N, int silu);
  * nothing about another's (it may be 0 for many rows and not for few);
  * mxfp4_workspace_size() is enough for every call of the three products.
  * err_flag: int32 device word or NULL: bit 1 is set if a bounded wait inside
- * a kernel gave up (its output is then not valid).
+ * a kernel gave up (its output is then not valid; with NULL nothing tells).
+ * Outputs must not overlap inputs, but y may be the residual.
  * ------------------------------------------------------------------------ */
 #define W4A16_MXFP4_MAX_K 131072
 #define W4A16_MXFP4_MAX_ROWS 1048576

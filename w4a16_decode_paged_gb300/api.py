@@ -571,7 +571,9 @@ def w4a16_gemm_mxfp4(x, codes, scales, bias=None, residual=None, out=None, works
     with smaller ones count as zero, with larger ones as NaN), from one token to a
     prompt's rows.  Without a
     workspace (mxfp4_workspace) each call makes its own.  residual may be out; out must
-    not overlap x or the weights."""
+    not overlap x or the weights.  err_flag (int32, one word): bit 1 is set if a bounded
+    wait inside a kernel gave up, and the output is not valid then; without one nothing
+    tells.  (The same of the two calls below.)"""
     if stream is None and workspace is not None and _cuda(x) and (fast := native()) is not None:
         r = fast.mx_gemm16(x, codes, scales, bias, residual, out, workspace, err_flag)
         if r is not None:

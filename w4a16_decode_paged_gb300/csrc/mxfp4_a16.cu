@@ -21,12 +21,15 @@
 // that stores (and the residual's loads) are 16 bytes of a row of y.  Tiles are
 // dealt by mt_deal.
 //
-// What bounds it, by copies that leave work out: a stage of 32 rows of x takes 0.51 us,
-// 0.42 without the conversions, which is the DRAM's rate; of 64 rows 0.61, 0.54 without
+// What bounds it, by copies that leave work out: a stage of 32 rows of x takes 0.51 us in
+// a call of 28 stages (0.45 between 28 and 56, 5.9 TB/s),
+// 0.42 without the conversions, which is the DRAM's rate (38 conversions and more a clock
+// and SM would be 0.21 alone; no pipe is over 0.39, and the warps' largest stall is
+// waiting for shared and tensor memory, 2.8 of 9.2 cycles); of 64 rows 0.61, 0.54 without
 // the conversions and 0.48 without the stores as well; of 128 rows 0.80 to 0.83, 0.74
 // without both, where a bf16 product of that size takes 0.65 at the rate of a large one.
-// 32 rows, 18944 x 3584 twice, with SiLU 18.9 us; 2048 rows, 3584 x 3584 49.5 us, 18944
-// x 3584 198 us (1405 TFLOP/s).  A tile's first two stages under the one before's last
+// 32 rows, 18944 x 3584 twice, with SiLU 19.0 us; 2048 rows, 3584 x 3584 49.5 us, 18944
+// x 3584 199 us (1397 TFLOP/s).  A tile's first two stages under the one before's last
 // MMAs and ahead of its epilogue: 203.9 us to 198.1 there, 47.8 to 42.0 at 4096 rows, 8960
 // x 256; where a CTA has one tile only it costs up to 2 % (300 rows, 3584 x 3584 16.7 us to
 // 17.0).  A stage handed over by halves 0.67 (32 rows) and 0.83

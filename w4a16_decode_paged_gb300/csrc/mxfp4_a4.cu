@@ -15,13 +15,17 @@
 // columns further on in tensor memory (scales have to start on an even column, so
 // that NC is a multiple of 64).
 //
-// What bounds it, as far as a model tells, is shared memory: per 64 k an MMA reads 4 KB
-// of x and NC / 32 KB of weights, and as much is copied in (NA MMAs share the weights).
-// At 128 bytes a clock that is 4 to 12 % below the stages measured, 0.61 us at 2 x 192,
-// 0.42 at 1 x 256, 0.38 at 1 x 192.  It is a fit: the L1 data bank
-// counters are far from full, and may not count what the MMAs read.  (256 x 192 by pairs
-// of CTAs, each with half of the weight rows, took 0.38 us a stage, 0.30 two single
-// ones: not kept.)
+// What bounds it is not settled.  A stage takes 1170 to 1200 cycles at 2 x 192 (0.58 us,
+// 4096 x 3584 by two lengths of K, SM clock sampled at 2.02 to 2.07 GHz) and 690 to 720
+// at 1 x 192 (0.34 us); its MMAs at their nominal rate (128 x NC x 64 in NC / 2 cycles)
+// would be 768 and 384.  Two accounts fit all shapes: shared memory at 128 bytes a clock
+// (per 64 k an MMA reads 4 KB of x and NC / 32 KB of weights, and as much is copied in:
+// 1088 and 640 cycles), or the MMAs and a constant of 290 to 430 cycles, for which the scale
+// columns are a candidate: there is one set, so that a stage's copies into it wait for
+// the MMAs before them.  256 x 192 by pairs of CTAs, each with half of the weight rows,
+// has less to read and copy than 1 x 192 and took as long a stage (0.38 us where 1 x 192
+// took 0.38 as well; two CTAs of 2 x 192 get through as much in 0.30: not kept), which
+// speaks for the second.
 //
 // Roles: a producer lane, one warp that issues the scales' copies and the MMAs
 // (these run in the order issued, so one set of scale columns serves), 8 epilogue
@@ -335,10 +339,10 @@ __global__ void __launch_bounds__(MB_THREADS, 1) w4pg_mxfp4_a4(const __grid_cons
 // host
 // ---------------------------------------------------------------------------
 // A call's tile shape and deal: of the shapes built, and with and without the
-// split along K, the one whose busiest CTA has least to do, in cycles as measured
-// with every SM at work: a stage (in proportion to shared memory's traffic: NA MMAs
-// of 4 + NC / 32 KB read per 64 k, 4 NA + NC / 32 KB copied in), what a tile's
-// epilogue keeps the next one's MMAs from, and the join.
+// split along K, the one whose busiest CTA has least to do, in cycles with every SM at
+// work: a stage, what a tile's epilogue keeps the next one's MMAs from, and the join.
+// (Stages measured: see above; 1 x 128 680 at 1000 x 2432, where copies are not
+// shared by many CTAs.)
 struct MbTile {
   int na, nc, db;
   double stage, tail;

@@ -22,10 +22,15 @@
 // timing.
 //
 // What bounds it: a call of next to no bytes takes 2.4 us (one row, 512 x 3584:
-// launch, one chain of copies, the join); in the stream 138 instructions a unit of
-// 1088 bytes at 0.53 of the issue slots, 16 warps, no pipe full: 152064 x 3584 5.5
-// TB/s, one row of 18944 x 3584 twice 16.0 us, of 3584 x 18944 9.0 us.  Two chains
-// of MMAs a unit lost 5 %.
+// launch, one chain of copies, the join), and the stream behind that runs at 5.5 TB/s
+// (one row, 152064 x 3584, 52.4 us; a plain copy reaches 6.7): one row of 18944 x 3584
+// twice 16.0 us, of 3584 x 18944 9.0 us.  Why the stream stops there is not settled: of
+// 145 instructions a unit of 1088 bytes the warps issue at 0.53 of the slots, the
+// fullest pipe (integer, which the conversions share) is at 0.47, and no stall stands
+// out (13.7 cycles an instruction: 2.7 for the shared-memory queue, 2.2 not chosen, 1.8
+// fixed latencies, 1.7 copies).  The conversions alone would be 108 cycles at most of the
+// 273 that a unit takes its scheduler (38 and more a clock and SM, registers only).  Two
+// chains of MMAs a unit lost 5 %.
 #include <algorithm>
 
 #include "mxfp4.cuh"
@@ -352,7 +357,8 @@ static int mv_max_clusters(int csize, size_t smem) {
 // through the cluster.
 constexpr double MV_JOIN = 16;
 // From so many units per warp two CTAs share an SM instead of leaving room for the
-// next kernel's: b1 gate|up (28) 15.8 us against 16.4, down (14) 10.7 against 9.0.
+// next kernel's: b1 gate|up (28) 15.8 us against 16.4, down (14) 10.7 against 9.0
+// (before the scales below 104 and above 140 were told apart, 0.2 and 0.1 us).
 constexpr int MV_TWO = 20;
 
 template <int NW, int MS>
